@@ -279,7 +279,7 @@ def _plain_plan(st):
     pos = torch.where(real, ctx[b] + t - cu[b], -1)
     page = table[b, (pos // P).clamp(0, max_pages - 1)].long()
     slots = torch.where(real & ok[b], page * P + pos % P, -1)
-    head = torch.where(ok, end, st["head"].long()).amax().reshape(1)
+    head = st["head"].long() + torch.where(ok, need, 0).sum()
     return {"kv_lens": torch.where(ok, ctx + new, 0).int(), "cu_q": cu.int(), "slots": slots.int(), "positions": pos.int(),
             "table": table, "head": head.int()}
 
