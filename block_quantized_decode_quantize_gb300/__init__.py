@@ -7,6 +7,10 @@ library on the current torch CUDA stream.  Every step of the computation runs in
 library's sm_103a kernels; there is no fallback.  If the library has not been built
 (``block_quantized_decode_quantize_gb300.build.build()``) loading it raises.
 
+The decode step's other half is here too: the page plan of a step (memra_kv_plan), a paged
+KV cache in 8 bits (memra_kv_append_q8, memra_kv_read_q8), attention over it
+(memra_kv_attention_q8) and the routing to experts (memra_moe_route).
+
 Tensor conventions (all on one CUDA device, contiguous):
   wq  int8 [N, K]          Q8_0 quants            wd  float16 [N, K/32]  Q8_0 scales
   xq  int8 [M, K]          q8_1 quants            xd  float32 [M, K/32]  q8_1 scales
@@ -25,6 +29,7 @@ MEMRA_F32 = 1
 MAX_M = 16
 MAX_TOP_K = 64
 MOE_NOALLOC_SCRATCH_FLOATS = 65536
+KV_ATTENTION_WORKSPACE_BYTES = 33554432
 
 _STATUS = {0: "MEMRA_OK", 1: "MEMRA_ERR_INVALID_ARG", 2: "MEMRA_ERR_ALIGNMENT",
            3: "MEMRA_ERR_UNSUPPORTED", 4: "MEMRA_ERR_CUDA"}
@@ -89,6 +94,17 @@ _SIGS = {
                                    _p, _p],
     "memra_q8_0_block_dots": [_p, _i64, _i64, _p, _i64, _p, _p],
     "memra_debug_set_wait_test": [_i64, _i64],
+    "memra_kv_plan": [_p, _p, _i64, _i64, _p, _i64, _p, _p, _i64, _i64, _p, _p, _p, _p, _p, _p,
+                      _p],
+    "memra_kv_append_q8": [_p, _p, _i32, _i64, _i64, _i64, _p, _p, _p, _p, _p, _i64, _i64, _i64,
+                           _i64, _i64, _p, _p],
+    "memra_kv_read_q8": [_p, _i64, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _i32, _p, _p, _p,
+                         _p],
+    "memra_kv_attention_q8": [_p, _i32, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _i64, _i64, _i64,
+                              _i64, _i64, _p, _i64, _i64, _p, _p, ctypes.c_float, _i64, _p, _p,
+                              _p, _p, _p],
+    "memra_moe_route": [_p, _i32, _i64, _i64, _i64, _p, _i32, _i64, _i64, _i64, _i64, _i32,
+                        ctypes.c_float, _p, _p, _p],
 }
 
 
@@ -821,6 +837,258 @@ def memra_q8_0_block_dots(wq, xq, s=None):
         _check("memra_q8_0_block_dots",
                lib().memra_q8_0_block_dots(_ptr(wq), N, K, _ptr(xq), M, _ptr(s), _stream(wq)))
     return s
+
+
+# The entry points below run many times a decode step on small data, where the time of the
+# call itself counts: their checks try the whole condition first and look for what is wrong
+# only when it fails.
+
+def _ok(t, name, dtype, dev, shape):
+    """_need for a contiguous tensor on CUDA device number `dev`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+            and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, torch.device("cuda", dev), shape)
+
+
+def _rows(t, name, dev, ndim):
+    """dtype code of a bf16 / fp32 tensor whose last dimension is dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype is torch.bfloat16:
+        dt = MEMRA_BF16
+    elif t.dtype is torch.float32:
+        dt = MEMRA_F32
+    else:
+        raise TypeError("%s must be bfloat16 or float32" % name)
+    if t.get_device() != dev or dev < 0:
+        raise ValueError("%s must be a CUDA tensor on the other arguments' device" % name)
+    if t.dim() != ndim:
+        raise ValueError("%s must have %d dimensions, got %d" % (name, ndim, t.dim()))
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the last dimension of %s must be dense" % name)
+    return dt
+
+
+def _launch(name, dev, *args):
+    fn = getattr(_lib if _lib is not None else lib(), name)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st:
+        _check(name, st)
+
+
+def _addr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _cache(kq, kd, vq, vd):
+    """(device, n_pages, Hkv, page, D, block) of a cache's planes."""
+    if not isinstance(kq, torch.Tensor) or kq.dim() != 4 or not isinstance(kd, torch.Tensor) \
+            or kd.dim() != 3:
+        raise ValueError("the cache is kq, vq [pages, Hkv, page, D] and kd, vd [pages, Hkv, "
+                         "page / block]")
+    dev = kq.get_device()
+    n_pages, Hkv, page, D = shape = kq.shape
+    blocks = kd.shape[2]
+    if blocks < 1 or page % blocks:
+        raise ValueError("a page of %d tokens does not hold %d scale blocks" % (page, blocks))
+    if dev < 0:
+        raise ValueError("kq must be a CUDA tensor")
+    scales = (n_pages, Hkv, blocks)
+    _ok(kq, "kq", torch.int8, dev, shape)
+    _ok(vq, "vq", torch.int8, dev, shape)
+    _ok(kd, "kd", torch.float32, dev, scales)
+    _ok(vd, "vd", torch.float32, dev, scales)
+    return dev, n_pages, Hkv, page, D, page // blocks
+
+
+def memra_kv_plan(ctx_lens, new_lens, page_size, free_pages, block_table, num_tokens,
+                  free_head=None, kv_lens=None, cu_q=None, slots=None, positions=None,
+                  free_head_out=None, dev_status=None):
+    """The page plan of one step.  ctx_lens, new_lens int32 [B] (tokens in the cache, tokens
+    of this step), free_pages int32 [F], block_table int32 [B, max_pages] (its new entries
+    are written in place), free_head int32 [1] or None (start of the unused free pages).
+    Returns kv_lens [B], cu_q [B+1], slots [num_tokens], positions [num_tokens] and
+    free_head_out [1], all int32.  free_head_out may be free_head, to advance it in place."""
+    if not isinstance(ctx_lens, torch.Tensor) or not ctx_lens.is_cuda or ctx_lens.dim() != 1:
+        raise ValueError("ctx_lens must be a 1-D CUDA tensor")
+    dev, B, T = ctx_lens.get_device(), ctx_lens.shape[0], int(num_tokens)
+    if T < 0:
+        raise ValueError("num_tokens must not be negative")
+    i32 = torch.int32
+    _ok(ctx_lens, "ctx_lens", i32, dev, (B,))
+    _ok(new_lens, "new_lens", i32, dev, (B,))
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a 1-D tensor")
+    _ok(free_pages, "free_pages", i32, dev, free_pages.shape)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a 2-D tensor")
+    max_pages = block_table.shape[1]
+    _ok(block_table, "block_table", i32, dev, (B, max_pages))
+    if free_head is not None:
+        _ok(free_head, "free_head", i32, dev, (1,))
+    if kv_lens is None and cu_q is None and slots is None and positions is None \
+            and free_head_out is None:
+        # one allocation; slots and positions first, which keeps them 16-byte aligned
+        pad = -T % 4
+        buf = torch.empty(2 * (T + pad) + 2 * B + 2, dtype=i32, device=ctx_lens.device)
+        slots, _, positions, _, kv_lens, cu_q, free_head_out = buf.split_with_sizes(
+            (T, pad, T, pad, B, B + 1, 1))
+    else:
+        if kv_lens is None:
+            kv_lens = torch.empty((B,), dtype=i32, device=ctx_lens.device)
+        if cu_q is None:
+            cu_q = torch.empty((B + 1,), dtype=i32, device=ctx_lens.device)
+        if slots is None:
+            slots = torch.empty((T,), dtype=i32, device=ctx_lens.device)
+        if positions is None:
+            positions = torch.empty((T,), dtype=i32, device=ctx_lens.device)
+        if free_head_out is None:
+            free_head_out = torch.empty((1,), dtype=i32, device=ctx_lens.device)
+        _ok(kv_lens, "kv_lens", i32, dev, (B,))
+        _ok(cu_q, "cu_q", i32, dev, (B + 1,))
+        _ok(slots, "slots", i32, dev, (T,))
+        _ok(positions, "positions", i32, dev, (T,))
+        _ok(free_head_out, "free_head_out", i32, dev, (1,))
+    if dev_status is not None:
+        _ok(dev_status, "dev_status", i32, dev, (1,))
+    _launch("memra_kv_plan", dev, ctx_lens.data_ptr(), new_lens.data_ptr(), B, page_size,
+            free_pages.data_ptr(), free_pages.shape[0], _addr(free_head), block_table.data_ptr(),
+            max_pages, T, kv_lens.data_ptr(), cu_q.data_ptr(), slots.data_ptr(),
+            positions.data_ptr(), free_head_out.data_ptr(), _addr(dev_status))
+    return kv_lens, cu_q, slots, positions, free_head_out
+
+
+def memra_kv_append_q8(k, v, slots, kq, kd, vq, vd, dev_status=None):
+    """Write tokens into the cache: k, v [T, Hkv, D] (bf16 or fp32; any equal strides of 16
+    bytes' multiples with the last dimension dense, so columns of a fused projection's rows
+    will do), slots int32 [T] (-1: left out).  kq, vq int8 [pages, Hkv, page, D] and kd, vd
+    float32 [pages, Hkv, page / block] are updated in place."""
+    dev, n_pages, Hkv, page, D, block = _cache(kq, kd, vq, vd)
+    dt = _rows(k, "k", dev, 3)
+    T = k.shape[0]
+    if k.shape[1] != Hkv or k.shape[2] != D:
+        raise ValueError("k has shape %s, expected %s" % (tuple(k.shape), (T, Hkv, D)))
+    if _rows(v, "v", dev, 3) != dt or v.shape != k.shape or v.stride() != k.stride():
+        raise ValueError("v must have k's dtype, shape and strides")
+    _ok(slots, "slots", torch.int32, dev, (T,))
+    if dev_status is not None:
+        _ok(dev_status, "dev_status", torch.int32, dev, (1,))
+    stride_t, stride_h, _ = k.stride()
+    _launch("memra_kv_append_q8", dev, k.data_ptr(), v.data_ptr(), dt, T, stride_t, stride_h,
+            slots.data_ptr(), kq.data_ptr(), kd.data_ptr(), vq.data_ptr(), vd.data_ptr(), n_pages,
+            Hkv, page, D, block, _addr(dev_status))
+
+
+def memra_kv_read_q8(slots, kq, kd, vq, vd, dtype=torch.bfloat16, k=None, v=None,
+                     dev_status=None):
+    """Read cached tokens back as values: slots int32 [N] -> k, v [N, Hkv, D] of `dtype`
+    (bfloat16 or float32); zeros where a slot is -1."""
+    dev, n_pages, Hkv, page, D, block = _cache(kq, kd, vq, vd)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a 1-D tensor")
+    N = slots.shape[0]
+    _ok(slots, "slots", torch.int32, dev, (N,))
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError("dtype must be bfloat16 or float32")
+    if k is None and v is None:
+        k, v = torch.empty((2, N, Hkv, D), dtype=dtype, device=kq.device).unbind(0)
+    else:
+        if k is None:
+            k = torch.empty((N, Hkv, D), dtype=dtype, device=kq.device)
+        if v is None:
+            v = torch.empty((N, Hkv, D), dtype=dtype, device=kq.device)
+        _ok(k, "k", dtype, dev, (N, Hkv, D))
+        _ok(v, "v", dtype, dev, (N, Hkv, D))
+    if dev_status is not None:
+        _ok(dev_status, "dev_status", torch.int32, dev, (1,))
+    _launch("memra_kv_read_q8", dev, slots.data_ptr(), N, kq.data_ptr(), kd.data_ptr(),
+            vq.data_ptr(), vd.data_ptr(), n_pages, Hkv, page, D, block,
+            MEMRA_BF16 if dtype is torch.bfloat16 else MEMRA_F32, k.data_ptr(), v.data_ptr(),
+            _addr(dev_status))
+    return k, v
+
+
+def memra_kv_attention_q8(q, kq, kd, vq, vd, block_table, kv_lens, cu_q, scale=None, window=0,
+                          out=None, lse=None, workspace=None, dev_status=None):
+    """Causal attention of a step's queries over the cache.  q [T, Hq, D] (bf16 or fp32,
+    strided as for memra_kv_append_q8), rows cu_q[b] .. cu_q[b+1] the last tokens of
+    request b's kv_lens[b]; block_table int32 [B, max_pages], kv_lens int32 [B], cu_q int32
+    [B+1] (as memra_kv_plan gives them); scale defaults to D ** -0.5; window > 0 hides keys
+    `window` and more before the query.  Returns out [T, Hq, D] (q's dtype) and lse float32
+    [T, Hq].  `workspace` (uint8, KV_ATTENTION_WORKSPACE_BYTES, zeroed once before its first
+    use) should be kept from call to call, one a stream; without one a call takes and clears
+    its own."""
+    dev, n_pages, Hkv, page, D, block = _cache(kq, kd, vq, vd)
+    dt = _rows(q, "q", dev, 3)
+    T, Hq, qD = q.shape
+    if qD != D or Hq < 1 or Hq % Hkv:
+        raise ValueError("q has shape %s, expected [T, a multiple of %d, %d]"
+                         % (tuple(q.shape), Hkv, D))
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a 2-D tensor")
+    B, max_pages = block_table.shape
+    i32 = torch.int32
+    _ok(block_table, "block_table", i32, dev, (B, max_pages))
+    _ok(kv_lens, "kv_lens", i32, dev, (B,))
+    _ok(cu_q, "cu_q", i32, dev, (B + 1,))
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    else:
+        _ok(out, "out", q.dtype, dev, (T, Hq, D))
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _ok(lse, "lse", torch.float32, dev, (T, Hq))
+    if workspace is None:
+        workspace = torch.zeros(KV_ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device=q.device)
+    elif workspace.numel() < KV_ATTENTION_WORKSPACE_BYTES:
+        raise ValueError("workspace must hold %d bytes" % KV_ATTENTION_WORKSPACE_BYTES)
+    else:
+        _ok(workspace, "workspace", torch.uint8, dev, workspace.shape)
+    if dev_status is not None:
+        _ok(dev_status, "dev_status", i32, dev, (1,))
+    stride_t, stride_h, _ = q.stride()
+    _launch("memra_kv_attention_q8", dev, q.data_ptr(), dt, T, Hq, stride_t, stride_h,
+            kq.data_ptr(), kd.data_ptr(), vq.data_ptr(), vd.data_ptr(), n_pages, Hkv, page, D,
+            block, block_table.data_ptr(), B, max_pages, kv_lens.data_ptr(), cu_q.data_ptr(),
+            D ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(),
+            workspace.data_ptr(), _addr(dev_status))
+    return out, lse
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def memra_moe_route(logits, top_k, bias=None, score="softmax", n_groups=1, topk_groups=1,
+                    group_top=1, renormalize=True, scale=1.0, ids=None, gate_w=None):
+    """Routing: logits [T, E] (bf16 or fp32, the last dimension dense) -> ids int32 [T,
+    top_k] (descending rank, ties to the lowest index) and gate_w float32 [T, top_k], as the
+    routed products take them.  score "softmax" or "sigmoid"; bias float32 [E] is added for
+    the ranking only; with n_groups > 1 only the topk_groups best groups stay, a group
+    ranked by its group_top (1 or 2) best experts' sum."""
+    dev = logits.get_device() if isinstance(logits, torch.Tensor) else -1
+    dt = _rows(logits, "logits", dev, 2)
+    T, E = logits.shape
+    if score not in _SCORES:
+        raise ValueError("score must be softmax or sigmoid, got %r" % (score,))
+    if bias is not None:
+        _ok(bias, "bias", torch.float32, dev, (E,))
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    else:
+        _ok(ids, "ids", torch.int32, dev, (T, top_k))
+    if gate_w is None:
+        gate_w = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    else:
+        _ok(gate_w, "gate_w", torch.float32, dev, (T, top_k))
+    _launch("memra_moe_route", dev, logits.data_ptr(), dt, T, E, logits.stride(0), _addr(bias),
+            _SCORES[score], n_groups, topk_groups, group_top, top_k, 1 if renormalize else 0,
+            scale, ids.data_ptr(), gate_w.data_ptr())
+    return ids, gate_w
 
 
 def memra_debug_set_wait_test(wait_limit_cycles=0, stall_after_stages=-1):

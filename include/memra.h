@@ -488,6 +488,146 @@ memra_status memra_q8_0_moe_ffn_noalloc(const int8_t* gu_q, const uint16_t* gu_d
                                         cudaStream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * A sequence's state between the products: a paged KV cache held in 8 bits, the page
+ * plan of a step, attention over the cache, and the routing to experts.
+ *
+ * Cache.  Four planes over a pool of pages of P tokens:
+ *   kq, vq  int8 [n_pages][Hkv][P][D], kd, vd fp32 [n_pages][Hkv][P/S]:
+ *   one scale for each block of S consecutive tokens of a page and each head,
+ *   k ~= kd * kq.  P a multiple of 16, S a divisor of P, D 64, 128 or 256.
+ * A token's place is its slot = page * P + offset; n_pages * P <= 2^31 - 1.  Request b's
+ * token at position p lies in page block_table[b][p / P] at offset p % P.
+ * kq, vq, q, k, v, out: 16-byte aligned; all else 4 bytes.
+ *
+ * Device-side checks (lengths, slots and page numbers are device data): what is out of
+ * range is left out as described with each entry point and *dev_status (int32, may be
+ * NULL, never cleared by the library) is OR-ed with 1; 4 stands for an empty free list.
+ * Calls wait for the preceding kernel before they read anything but their arguments.
+ * ---------------------------------------------------------------------------
+ */
+#define MEMRA_MAX_KV_PAGE 1024       /* tokens a page */
+#define MEMRA_MAX_EXPERTS 1024       /* experts a routing chooses from */
+#define MEMRA_MAX_EXPERT_GROUPS 32
+/* Device memory an attention call takes for the parts of rows that several CTAs share. */
+#define MEMRA_KV_ATTENTION_WORKSPACE_BYTES 33554432
+
+/*
+ * The page plan of one step: which pages the step's new tokens take, and where each goes.
+ *   ctx_lens, new_lens  int32 [B]: request b's tokens in the cache and in this step.
+ *   free_pages          int32 [n_free]: page numbers, taken in order from *free_head on
+ *                       (free_head int32 [1], NULL: 0).
+ *   block_table         int32 [B][max_pages], in and out: the entries of the pages that
+ *                       request b has (ceil(ctx/P)) are read, those that it takes are
+ *                       written, the others are left.
+ *   T                   rows of slots and positions; the step's tokens fill the first ones,
+ *                       request after request.
+ * Out:
+ *   kv_lens   int32 [B]    ctx + new (0 for a refused request);
+ *   cu_q      int32 [B+1]  first row of each request, min(sum of new before it, T);
+ *   slots     int32 [T]    slot of each row's token (-1: a refused request's, or no token);
+ *   positions int32 [T]    its position in the sequence (-1: no token);
+ *   free_head_out int32 [1]  *free_head + pages taken; may be free_head itself.
+ * With need_b = ceil((ctx+new)/P) - ceil(ctx/P), request b takes the pages after those of
+ * all requests before it.  A request is refused, and takes no page, when a length is
+ * negative, its pages do not fit max_pages or its rows do not fit T (status 1), and, when
+ * it needs a page, if the pages of the requests up to it run past n_free (status 4): once
+ * one does not fit, none after it takes a page.
+ * B == 0 fills slots and positions with -1.
+ */
+memra_status memra_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t B,
+                           int64_t page_size, const int32_t* free_pages, int64_t n_free,
+                           const int32_t* free_head, int32_t* block_table, int64_t max_pages,
+                           int64_t T, int32_t* kv_lens, int32_t* cu_q, int32_t* slots,
+                           int32_t* positions, int32_t* free_head_out, int32_t* dev_status,
+                           cudaStream_t stream);
+
+/*
+ * Write T tokens into the cache.  k, v: [T][Hkv][D] of `dtype` (bf16 bits or fp32), token t
+ * of head h at t * stride_t + h * stride_h elements (k and v alike; the D values are
+ * consecutive; strides keep 16-byte alignment), slots int32 [T]: -1 leaves a token out.
+ * Consecutive rows whose slots lie in one scale block are one run; within a run the slots
+ * rise by one (as memra_kv_plan gives them), and the tokens at smaller offsets of the
+ * block are its older tokens.  For each run, head and plane:
+ *   d = max(d_old, amax / 127) over the run's values, d_old = 0 for a run that begins at
+ *   the block's first token; if d > d_old the older tokens' codes become
+ *   rha(q * (d_old / d)); the run's codes are clamp(rha(x / d), -127, 127).
+ * (IEEE fp32 division and product, rha: to nearest, halves away from zero; d = 0 gives
+ * codes 0.)  A repeated call with the same tokens changes nothing.  A slot beyond the pool
+ * is left out (status 1).  Inputs must be finite; no two runs may share a block.
+ */
+memra_status memra_kv_append_q8(const void* k, const void* v, int32_t dtype, int64_t T,
+                                int64_t stride_t, int64_t stride_h, const int32_t* slots,
+                                int8_t* kq, float* kd, int8_t* vq, float* vd, int64_t n_pages,
+                                int64_t Hkv, int64_t page_size, int64_t D, int64_t block,
+                                int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Read N tokens back as the values that they stand for: k, v [N][Hkv][D] of `dtype`
+ * (contiguous), k = d * q in fp32, rounded once to bf16 if asked.  slots int32 [N]; -1, or
+ * a slot beyond the pool (status 1), gives zeros.
+ */
+memra_status memra_kv_read_q8(const int32_t* slots, int64_t N, const int8_t* kq, const float* kd,
+                              const int8_t* vq, const float* vd, int64_t n_pages, int64_t Hkv,
+                              int64_t page_size, int64_t D, int64_t block, int32_t dtype, void* k,
+                              void* v, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Attention of the step's queries over the cache, causal, with grouped heads.  Request b's
+ * queries are rows cu_q[b] .. cu_q[b+1] of q (n_b of them; any number, ragged), the last
+ * n_b of its kv_lens[b] tokens (which are in the cache): query i stands at position
+ * pos = kv_lens[b] - n_b + i and sees keys j <= pos, with window > 0 only j > pos - window.
+ * Query head h reads cached head h / (Hq / Hkv).
+ *   s_j = scale * q . k_j,  out = sum_j softmax(s)_j v_j,  lse = ln sum_j exp(s_j).
+ *   q   [T][Hq][D] of `dtype`, row t, head h at t * stride_t + h * stride_h elements;
+ *   out [T][Hq][D] of `dtype`, contiguous; lse fp32 [T][Hq] or NULL.
+ * A row that sees no key (kv_lens 0, a position below 0, no request's row) gets out = 0 and
+ * lse = -inf.  Cache entries at and beyond kv_lens[b], and page entries that hold no
+ * visible key, are not used, whatever they hold.  A page number outside [0, n_pages) hides
+ * its tokens and kv_lens beyond max_pages * P are cut to it (status 1).
+ * Statistics and sums are fp32.
+ *   workspace: MEMRA_KV_ATTENTION_WORKSPACE_BYTES, 16-byte aligned, zeroed once by the
+ *   caller before its first use; every call leaves it fit for the next.  Calls that may
+ *   overlap on the GPU need one each.
+ */
+memra_status memra_kv_attention_q8(const void* q, int32_t dtype, int64_t T, int64_t Hq,
+                                   int64_t stride_t, int64_t stride_h, const int8_t* kq,
+                                   const float* kd, const int8_t* vq, const float* vd,
+                                   int64_t n_pages, int64_t Hkv, int64_t page_size, int64_t D,
+                                   int64_t block, const int32_t* block_table, int64_t B,
+                                   int64_t max_pages, const int32_t* kv_lens,
+                                   const int32_t* cu_q, float scale, int64_t window, void* out,
+                                   float* lse, void* workspace, int32_t* dev_status,
+                                   cudaStream_t stream);
+
+/*
+ * Routing to experts: ids int32 [T][top_k] and gate_w fp32 [T][top_k] as the routed
+ * products take them, from logits [T][E] of `dtype` (row t at t * stride_t elements).
+ *   score (MEMRA_SCORE_SOFTMAX)  s_e = exp(l_e - max l) / sum exp(l - max l)
+ *         (MEMRA_SCORE_SIGMOID)  s_e = 1 / (1 + exp(-l_e))
+ *   v_e = s_e + bias[e] (bias fp32 [E] or NULL) ranks the experts.  With n_groups > 1, E /
+ *   n_groups neighbouring experts make a group, its rank is the largest v in it (group_top
+ *   1) or the sum of the two largest (2), and only experts of the topk_groups first groups
+ *   stay.  ids: the top_k largest v, descending, ties to the lowest index (of groups too).
+ *   gate_w = s of the chosen, divided by their sum if renormalize (0 where that is 0), times
+ *   route_scale.
+ * Every fp32 operation is rounded once; exp is the one of memra_swiglu_quantize_q8_1, and
+ * the softmax sum is taken by 32 lanes, lane i adding experts 128c + 4i + j in ascending
+ * (c, j), joined pairwise at distances 16, 8, 4, 2, 1: equal inputs choose the same experts
+ * anywhere.  A logit of -inf or NaN masks an expert: s = 0, v = -inf; +inf counts as the
+ * largest finite value.  Where fewer than top_k experts are left, the remaining slots hold
+ * the lowest indexes not yet taken, with weight 0.
+ * E <= MEMRA_MAX_EXPERTS, top_k <= min(MEMRA_MAX_TOP_K, topk_groups * E / n_groups),
+ * n_groups <= MEMRA_MAX_EXPERT_GROUPS and a divisor of E, group_top <= E / n_groups.
+ */
+typedef enum memra_score { MEMRA_SCORE_SOFTMAX = 0, MEMRA_SCORE_SIGMOID = 1 } memra_score;
+memra_status memra_moe_route(const void* logits, int32_t dtype, int64_t T, int64_t E,
+                             int64_t stride_t, const float* bias, int32_t score,
+                             int64_t n_groups, int64_t topk_groups, int64_t group_top,
+                             int64_t top_k, int32_t renormalize, float route_scale, int32_t* ids,
+                             float* gate_w, cudaStream_t stream);
+
+/*
  * Exact int32 block sums s[m][n][b] = sum_{i<32} wq[n][32b+i] * xq[m][32b+i],
  * computed with the same dp4a block-dot routine as the product kernels.  For
  * verification of the integer stage.  s: int32 [M][N][K/32], 4-byte aligned.
