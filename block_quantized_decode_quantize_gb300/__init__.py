@@ -869,13 +869,19 @@ def _rows(t, name, dev, ndim):
     return dt
 
 
+# The current stream's handle without a Stream object around it (1 us less).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _launch(name, dev, *args):
     fn = getattr(_lib if _lib is not None else lib(), name)
+    stream = _raw_stream(dev)
     if torch.cuda.current_device() == dev:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, stream)
     if st:
         _check(name, st)
 

@@ -1,7 +1,23 @@
 // Attention over the paged 8-bit KV cache (layouts and arithmetic in memra.h).
 //
-// The simplest form: a CTA to a query row and head, a warp to every fourth key, one pass
-// with a running maximum and sum for each warp, joined at the end.
+// Work.  A unit is (request, cached head, group of 8 * kNT query rows); a row is a (query,
+// query head) pair that reads this cached head, so grouped heads share every byte.  The
+// keys of all units, in tiles of 128, form one list that is cut into equal parts for the
+// CTAs of one resident wave: every CTA streams the same number of bytes whatever the
+// lengths are.  The cut ends of a unit leave (maximum, sum, weighted values) in the
+// workspace, and the CTA that arrives last at the unit joins them in the order of the
+// keys, so results do not depend on timing.
+//
+// A CTA's eight warps take strips of 16 keys in turn, each with its own ring of
+// cp.async stages and its own running statistics; nothing in the loop crosses warps.
+// A strip is two products on the tensor cores with the keys (dims) in the 16-row operand,
+// so that 8 query rows waste nothing:
+//   S^T [16 keys x 8 rows]  = K [16 x D] * Q^T,   O^T [D x 8 rows] += V^T [D x 16] * P^T.
+// int8 codes become fp16 operands exactly, by setting the exponent of 1024 above the byte
+// and subtracting 1024 + 128 (2.5 instructions for two codes).  Scales never meet the
+// codes: kd multiplies the score, vd the weight.
+#include <atomic>
+
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -9,107 +25,766 @@
 namespace memra {
 namespace {
 
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStrip = 16;                 // keys of a warp's step
+constexpr int kTile = kWarps * kStrip;     // keys of a CTA's step, the unit of the work list
+constexpr int kMaxCtas = 512;              // arrival counters at the workspace's start
+
+// A weight enters the product as p * (vd / ref) * 2^8 in fp16, ref a running maximum of vd
+// kept within a factor 4, p = 2^(s - m) with m within 5 of the running maximum: at most
+// 2^(5 + 2 + 8) = 2^15, and down to 2^-33 of the largest before it rounds to zero.
+constexpr float kMaxSlack = 5.0f;
+constexpr float kRefSlack = 4.0f;
+constexpr float kWeightScale = 256.0f;
+
 struct AttnArgs {
   const void* q;
-  int64_t T, Hq, stride_t, stride_h;
+  int64_t T, stride_t, stride_h;
   const int8_t *kq, *vq;
   const float *kd, *vd;
-  int64_t n_pages, max_pages;
-  int Hkv, page, D, block;
   const int32_t *table, *kv_lens, *cu_q;
-  int64_t B, window;
+  int64_t B, max_pages, window;
+  int32_t n_pages;
+  int Hq, Hkv, G, page, block;
+  uint32_t block_magic;  // ceil(2^22 / block): off / block = off * magic >> 22, off < 1024
   float scale;
   void* out;
   float* lse;
+  int* arrived;   // [kMaxCtas], zero between calls
+  float* parts;   // [2 * CTAs][rows * (D + 2)]
   int32_t* status;
 };
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kN>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
+
+__device__ __forceinline__ void mma_16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Bytes 0 and 2 (1 and 3) of w, signed, as two fp16: byte ^ 0x80 under the exponent of
+// 1024 is 1024 + 128 + value.
+__device__ __forceinline__ uint32_t minus_1152(uint32_t h) {
+  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t even_bytes(uint32_t w) {
+  return minus_1152((w & 0x00ff00ffu) ^ 0x64806480u);
+}
+__device__ __forceinline__ uint32_t odd_bytes(uint32_t w) {
+  return minus_1152(((w >> 8) & 0x00ff00ffu) ^ 0x64806480u);
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_half(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// Which key of 8 sits in operand row i.  With 128-byte rows and more, keys i and i + 1 of a
+// 16-byte load's quarter-warp have to differ in bit 2 for the swizzle below to part them.
+template <int kD>
+__device__ __forceinline__ int key_of(int i) {
+  return kD == 64 ? i : (i >> 1) | ((i & 1) << 2);
+}
+// Byte offset of 16-byte chunk c of key k (0..15) in a stage's K or V part.
+template <int kD>
+__device__ __forceinline__ uint32_t k_place(int k, int c) {
+  if (kD == 64) return k * 64 + c * 16;
+  return k * kD + ((c ^ (k & 7)) << 4);
+}
+template <int kD>
+__device__ __forceinline__ uint32_t v_place(int k, int c) {
+  if (kD == 64)  // two keys to a 128-byte line
+    return (k >> 1) * 128 + (((((k & 1) << 2) | c) ^ (((k >> 1) & 3) << 1)) << 4);
+  return k * kD + ((c ^ (((k & 3) << 1) | ((k >> 2) & 1))) << 4);
+}
+
+template <typename T>
+struct Row;  // 16 bytes of a query row
+template <>
+struct Row<uint16_t> {
+  static constexpr bool kPair = false;  // bf16 has 8 significant bits: one fp16 holds them
+};
+template <>
+struct Row<float> {
+  static constexpr bool kPair = true;   // fp32: two fp16, 22 bits
+};
 __device__ __forceinline__ float value(const float* p) { return *p; }
 __device__ __forceinline__ float value(const uint16_t* p) {
   return __uint_as_float((uint32_t)*p << 16);
 }
-__device__ __forceinline__ void store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store(uint16_t* p, float v) {
-  *p = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(uint16_t* p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  uint2 u;
+  u.x = *reinterpret_cast<const uint32_t*>(&a);
+  u.y = *reinterpret_cast<const uint32_t*>(&b);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+template <typename T, int kD, int kNT>
+struct Shape {
+  static constexpr int kRows = 8 * kNT;
+  static constexpr bool kPair = Row<T>::kPair;
+  static constexpr int kCtas = kD <= 128 && kNT * kD <= 256 ? 2 : 1;  // a SM
+  static constexpr int kStage = 2 * kStrip * kD + 8 * kStrip;  // K, V, 16 kd, 16 vd
+  static constexpr int kStages = kD == 64 ? 5 : (kCtas == 2 ? 3 : (kD == 128 ? 6 : 3));
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kJoin = kWarps * kRows * kD * 4;  // reuses the ring
+  static constexpr int kBig = kRing > kJoin ? kRing : kJoin;
+  static constexpr int kQ = (kPair ? 2 : 1) * (kD / 16) * kNT * 32 * 8;
+  static constexpr int kStats = (2 * kWarps + 4) * kRows * 4;
+  static constexpr int kSmem = kBig + kQ + kStats;
+};
+
+// Where a request's part of the list lies, from its lengths.
+struct Request {
+  int len, n;        // tokens in the cache, queries
+  int lo;            // first key tile's start
+  int tiles, groups;
+};
+
+template <int kRows>
+__device__ __forceinline__ Request request_of(const AttnArgs& a, int64_t b) {
+  Request r;
+  const int64_t cap = a.max_pages * a.page;
+  int64_t len = a.kv_lens[b];
+  len = len < 0 ? 0 : (len > cap ? cap : len);
+  int64_t n = (int64_t)a.cu_q[b + 1] - a.cu_q[b];
+  n = n < 0 ? 0 : (n > a.T ? a.T : n);
+  r.len = (int)len;
+  r.n = (int)n;
+  int64_t lo = a.window > 0 ? len - n + 1 - a.window : 0;
+  lo = lo < 0 ? 0 : lo / kStrip * kStrip;
+  r.lo = (int)lo;
+  r.tiles = n > 0 && len > lo ? (int)((len - lo + kTile - 1) / kTile) : 0;
+  r.groups = (int)((n * a.G + kRows - 1) / kRows);
+  return r;
 }
 
 template <typename T, int kD>
-__global__ void __launch_bounds__(128) attention_rows_kernel(AttnArgs a) {
-  constexpr int kPer = kD / 32;
-  __shared__ float sm[4], sl[4], so[4][kD];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = blockIdx.x / a.Hq;
-  const int hq = (int)(blockIdx.x % a.Hq), h = hq / (int)(a.Hq / a.Hkv);
-  int64_t b = 0;
-  while (b < a.B && a.cu_q[b + 1] <= t) ++b;
-  int64_t lo = 0, hi = 0;
-  if (b < a.B) {
-    int64_t len = a.kv_lens[b];
-    if (len > a.max_pages * a.page) {
-      len = a.max_pages * a.page;
-      if (a.status != nullptr && threadIdx.x == 0) atomicOr(a.status, 1);
-    }
-    hi = len - (a.cu_q[b + 1] - t) + 1;
-    if (hi > len) hi = len;
-    if (a.window > 0 && hi > a.window) lo = hi - a.window;
-  }
-  const T* q = static_cast<const T*>(a.q) + t * a.stride_t + hq * a.stride_h;
-  float x[kPer], o[kPer];
-  for (int i = 0; i < kPer; ++i) {
-    x[i] = value(q + lane * kPer + i);
-    o[i] = 0.0f;
-  }
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t j = lo + warp; j < hi; j += 4) {
-    const int64_t page = a.table[b * a.max_pages + j / a.page];
-    if (page < 0 || page >= a.n_pages) {
-      if (a.status != nullptr && lane == 0) atomicOr(a.status, 1);
-      continue;
-    }
-    const int off = (int)(j % a.page);
-    const int64_t head = page * a.Hkv + h;
-    const int64_t row = (head * a.page + off) * kD + lane * kPer;
-    const int64_t sc = head * (a.page / a.block) + off / a.block;
-    float s = 0.0f;
-    for (int i = 0; i < kPer; ++i) s += x[i] * (float)a.kq[row + i];
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(kFullMask, s, w);
-    s *= a.kd[sc] * a.scale;
-    const float mn = fmaxf(m, s), keep = expf(m - mn), p = expf(s - mn);
-    const float pv = p * a.vd[sc];
-    l = l * keep + p;
-    m = mn;
-    for (int i = 0; i < kPer; ++i) o[i] = o[i] * keep + pv * (float)a.vq[row + i];
-  }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  for (int i = 0; i < kPer; ++i) so[warp][lane * kPer + i] = o[i];
-  __syncthreads();
-  const float mx = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float sum = 0.0f, f[4];
-  for (int w = 0; w < 4; ++w) {
-    f[w] = sm[w] == -INFINITY ? 0.0f : expf(sm[w] - mx);
-    sum += f[w] * sl[w];
-  }
-  T* out = static_cast<T*>(a.out) + (t * a.Hq + hq) * kD;
-  for (int i = threadIdx.x; i < kD; i += 128) {
-    float v = 0.0f;
-    for (int w = 0; w < 4; ++w) v += f[w] * so[w][i];
-    store(out + i, sum > 0.0f ? v / sum : 0.0f);
-  }
-  if (a.lse != nullptr && threadIdx.x == 0)
-    a.lse[t * a.Hq + hq] = sum > 0.0f ? mx + logf(sum) : -INFINITY;
+__device__ __forceinline__ void write_nothing(const AttnArgs& a, int64_t row0, int64_t row1,
+                                              int thread, int threads) {
+  T* out = static_cast<T*>(a.out);
+  row0 = row0 < 0 ? 0 : row0;
+  row1 = row1 > a.T ? a.T : row1;
+  for (int64_t i = row0 * a.Hq * kD / 4 + thread; i < row1 * a.Hq * kD / 4; i += threads)
+    store4(out + i * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+  if (a.lse != nullptr)
+    for (int64_t i = row0 * a.Hq + thread; i < row1 * a.Hq; i += threads)
+      a.lse[i] = __int_as_float(0xff800000);
 }
 
+template <typename T, int kD, int kNT>
+__global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attention_kernel(AttnArgs a) {
+  using Sh = Shape<T, kD, kNT>;
+  constexpr int kRows = Sh::kRows;
+  constexpr bool kPair = Sh::kPair;
+  constexpr int kSteps = kD / 16;          // k16 steps of S, m16 tiles of O
+  const float kInf = __int_as_float(0x7f800000);
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* ring = smem;
+  uint2* q_frag = reinterpret_cast<uint2*>(smem + Sh::kBig);  // [hi, lo][step][tile][lane]
+  float* stats = reinterpret_cast<float*>(smem + Sh::kBig + Sh::kQ);
+  float* warp_m = stats;                       // [kWarps][kRows]
+  float* warp_l = warp_m + kWarps * kRows;     // [kWarps][kRows]
+  float* row_m = warp_l + kWarps * kRows;      // [kRows]
+  float* row_l = row_m + kRows;
+  float* row_scale = row_l + kRows;
+  int* row_limit = reinterpret_cast<int*>(row_scale + kRows);
+  __shared__ int64_t scan[kWarps], found_at;
+  __shared__ int found_b, last_part;
+
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int cta = blockIdx.x;
+
+  // ---- the list: every CTA sums the requests' tiles and finds its own part ----
+  int64_t total = 0, first = 0, stop = 0;
+  int ctas = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t before = 0;
+    for (int64_t base = 0; base < a.B; base += kThreads) {
+      const int64_t b = base + tid;
+      int64_t w = 0;
+      bool empty = false;
+      if (b < a.B) {
+        const Request r = request_of<kRows>(a, b);
+        w = (int64_t)r.tiles * r.groups * a.Hkv;
+        empty = w == 0 && r.n > 0;
+        if (pass == 0 && cta == 0 && a.status != nullptr &&
+            a.kv_lens[b] > a.max_pages * a.page)
+          atomicOr(a.status, 1);
+      }
+      if (pass == 0) {  // rows of requests without keys, each request by one CTA
+        uint32_t todo = __ballot_sync(kFullMask, empty && b % gridDim.x == cta);
+        while (todo != 0) {
+          const int64_t e = base + warp * 32 + (__ffs(todo) - 1);
+          todo &= todo - 1;
+          write_nothing<T, kD>(a, a.cu_q[e], a.cu_q[e + 1], lane, 32);
+        }
+      }
+      int64_t sum = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(kFullMask, sum, o);
+        if (lane >= o) sum += u;
+      }
+      if (lane == 31) scan[warp] = sum;
+      __syncthreads();
+      int64_t chunk = 0;
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) sum += scan[i];
+        chunk += scan[i];
+      }
+      if (pass == 1 && w > 0 && before + sum - w <= first && first < before + sum) {
+        found_b = (int)b;
+        found_at = before + sum - w;
+      }
+      before += chunk;
+      __syncthreads();
+    }
+    if (pass == 0) {
+      total = before;
+      ctas = (int)min((int64_t)gridDim.x, total);
+      // rows that no request owns
+      for (int64_t row = (a.B > 0 ? a.cu_q[a.B] : 0) + cta; row < a.T; row += gridDim.x)
+        write_nothing<T, kD>(a, row, row + 1, tid, kThreads);
+      if (cta >= ctas) return;
+      first = total * cta / ctas;
+      stop = total * (cta + 1) / ctas;
+    }
+  }
+  int b = found_b;
+  int64_t at = found_at;  // list index of request b's first tile
+  Request req = request_of<kRows>(a, b);
+
+  const uint32_t my_ring = smem_addr(ring) + warp * Sh::kStages * Sh::kStage;
+  int64_t x = first;
+  while (x < stop) {
+    int64_t w = (int64_t)req.tiles * req.groups * a.Hkv;
+    while (x >= at + w) {
+      at += w;
+      req = request_of<kRows>(a, ++b);
+      w = (int64_t)req.tiles * req.groups * a.Hkv;
+    }
+    // ---- this unit: cached head h, rows [row0, row0 + kRows) of the request's n * G ----
+    const int unit = (int)((x - at) / req.tiles);
+    const int64_t unit_at = at + (int64_t)unit * req.tiles;
+    const int h = unit / req.groups, row0 = unit % req.groups * kRows;
+    const int64_t unit_stop = unit_at + req.tiles;
+    const int64_t x_stop = unit_stop < stop ? unit_stop : stop;
+    const int rows = min(kRows, req.n * a.G - row0);
+    const int token0 = a.cu_q[b];
+
+    // Queries to shared memory as B operands: row r of tile r / 8 is operand column r % 8;
+    // k index (2i, 2i+1, 2i+8, 2i+9) of step 4c+w is dim 64c + 16i + 4w + (0, 2, 1, 3).
+    // Each row is scaled by a power of two that brings its largest value to [2^13, 2^14).
+    for (int r = warp; r < kRows; r += kWarps) {
+      const int i = (row0 + r) / a.G, hq = h * a.G + (row0 + r) % a.G;
+      const bool real = r < rows && token0 + i >= 0 && token0 + i < a.T;
+      const T* src = static_cast<const T*>(a.q) + (real ? (token0 + i) * a.stride_t + hq * a.stride_h : 0);
+      constexpr int kPer = kD / 32;
+      float v[kPer], amax = 0.0f;
+      // lane's dims: those that its operand registers hold for steps kPer/2 ... (see below)
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        v[j] = real ? value(src + j * 32 + lane) : 0.0f;
+        amax = fmaxf(amax, fabsf(v[j]));
+      }
+      amax = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(amax)));
+      int e = (int)(__float_as_uint(amax) >> 23) - 127;
+      e = e < -100 ? -100 : e;
+      const float up = __int_as_float((13 - e + 127) << 23);  // 2^(13 - e), e in [-100, 128]
+      if (lane == 0) {
+        row_scale[r] = amax > 0.0f ? a.scale * 1.44269504088896341f * __int_as_float((e - 13 + 127) << 23)
+                                   : 0.0f;
+        row_limit[r] = min(req.len, req.len - req.n + i + 1);
+      }
+      __half* frag = reinterpret_cast<__half*>(q_frag);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int d = j * 32 + lane;
+        const int step = (d >> 6) * 4 + ((d >> 2) & 3), t = (d >> 4) & 3, y = d & 3;
+        // y 0, 2 -> register 0 halves 0, 1; y 1, 3 -> register 1 halves 0, 1
+        const int half = ((y & 1) << 1) | (y >> 1);
+        const int idx = (((step * kNT + (r >> 3)) * 32 + (r & 7) * 4 + t) << 2) + half;
+        const float s = v[j] * up;
+        const __half hi = __float2half_rn(s);
+        frag[idx] = hi;
+        if (kPair) frag[idx + kSteps * kNT * 32 * 4] = __float2half_rn(s - __half2float(hi));
+      }
+    }
+    __syncthreads();
+    float qs[kNT][2];
+    int limit[kNT][2];
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        qs[n][c] = row_scale[8 * n + 2 * t4 + c];
+        limit[n][c] = row_limit[8 * n + 2 * t4 + c];
+      }
+    const int limit_min = row_limit[0], limit_max = row_limit[rows - 1];
+    // keys below this are hidden from the last row (window)
+    const int low_max = a.window > 0 ? (int)max((int64_t)0, limit_max - a.window) : 0;
+
+    float o[kSteps][kNT][4];
+    float m[kNT][2], l[kNT][2], ref = 0.0f;
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[n][c] = -kInf;
+        l[n][c] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][n][c] = 0.0f;
+    }
+
+    // ---- the warp's strips: key0, key0 + kTile, ... below key_stop ----
+    const int key0 = req.lo + (int)(x - unit_at) * kTile + warp * kStrip;
+    const int key_stop = min(req.lo + (int)(x_stop - unit_at) * kTile, limit_max);
+    const int strips = key0 < key_stop ? (key_stop - key0 + kTile - 1) / kTile : 0;
+    const int32_t* pages = a.table + (int64_t)b * a.max_pages;
+    uint32_t hidden = 0;  // bit i: the stage i strips ahead has no page
+
+    auto page_of = [&](int s) { return s < strips ? pages[(key0 + s * kTile) / a.page] : 0; };
+    auto issue = [&](int s, int32_t page) {
+      if (s < strips) {
+        if ((uint32_t)page < (uint32_t)a.n_pages) {
+          const int key = key0 + s * kTile;
+          const int off = key % a.page;
+          const uint32_t dst = my_ring + s % Sh::kStages * Sh::kStage;
+          const int64_t head = (int64_t)page * a.Hkv + h;
+          const int64_t codes = (head * a.page + off) * kD;
+          constexpr int kChunks = kD / 16;
+#pragma unroll
+          for (int i = 0; i < kStrip * kChunks / 32; ++i) {
+            const int k = (i * 32 + lane) / kChunks, c = (i * 32 + lane) % kChunks;
+            cp16(dst + k_place<kD>(k, c), a.kq + codes + (i * 32 + lane) * 16);
+            cp16(dst + kStrip * kD + v_place<kD>(k, c), a.vq + codes + (i * 32 + lane) * 16);
+          }
+          const int64_t sc = head * (a.page / a.block) +
+                             (((uint32_t)(off + (lane & 15)) * a.block_magic) >> 22);
+          cp4(dst + 2 * kStrip * kD + lane * 4, (lane < 16 ? a.kd : a.vd) + sc);
+        } else {
+          hidden |= 1u << (s % Sh::kStages);
+          if (lane == 0 && a.status != nullptr) atomicOr(a.status, 1);
+        }
+      }
+      cp_commit();
+    };
+
+    int32_t next_page = page_of(0);
+#pragma unroll
+    for (int s = 0; s < Sh::kStages - 1; ++s) {
+      const int32_t p = next_page;
+      next_page = page_of(s + 1);
+      issue(s, p);
+    }
+
+    for (int s = 0; s < strips; ++s) {
+      cp_wait<Sh::kStages - 2>();
+      __syncwarp();
+      const int slot = s % Sh::kStages;
+      const uint32_t kbase = my_ring + slot * Sh::kStage, vbase = kbase + kStrip * kD;
+      const uint32_t dbase = kbase + 2 * kStrip * kD;
+      const int ka = key_of<kD>(g), kb = 8 + ka;
+
+      float c[kNT][4];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[n][i] = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kD / 64; ++q) {
+        const uint4 xa = lds_v4(kbase + k_place<kD>(ka, 4 * q + t4));
+        const uint4 xb = lds_v4(kbase + k_place<kD>(kb, 4 * q + t4));
+        const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int step = 4 * q + i;
+          const uint32_t a0 = even_bytes(wa[i]), a1 = even_bytes(wb[i]);
+          const uint32_t a2 = odd_bytes(wa[i]), a3 = odd_bytes(wb[i]);
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) {
+            const uint2 f = q_frag[(step * kNT + n) * 32 + lane];
+            mma_16816(c[n], a0, a1, a2, a3, f.x, f.y);
+            if (kPair) {
+              const uint2 lo = q_frag[((kSteps + step) * kNT + n) * 32 + lane];
+              mma_16816(c[n], a0, a1, a2, a3, lo.x, lo.y);
+            }
+          }
+        }
+      }
+
+      // c[n]: (key a, row 2t), (key a, row 2t+1), (key b, row 2t), (key b, row 2t+1)
+      float kda = lds_f32(dbase + ka * 4), kdb = lds_f32(dbase + kb * 4);
+      float vda = lds_f32(dbase + 64 + ka * 4), vdb = lds_f32(dbase + 64 + kb * 4);
+      const int key = key0 + s * kTile;
+      const bool no_page = (hidden >> slot) & 1u;
+      hidden &= ~(1u << slot);
+      const bool plain = key + kStrip <= limit_min && key >= low_max && !no_page;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        c[n][0] *= kda * qs[n][0];
+        c[n][1] *= kda * qs[n][1];
+        c[n][2] *= kdb * qs[n][0];
+        c[n][3] *= kdb * qs[n][1];
+      }
+      if (!plain) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = key + (i < 2 ? ka : kb), lim = limit[n][i & 1];
+            const bool seen = k < lim && (a.window == 0 || k >= lim - a.window) && !no_page;
+            c[n][i] = seen ? c[n][i] : -kInf;
+          }
+        vda = key + ka < limit_max && !no_page ? vda : 0.0f;
+        vdb = key + kb < limit_max && !no_page ? vdb : 0.0f;
+      }
+
+      // Running maxima: moved only when a score passes them by more than kMaxSlack.
+      bool move = fmaxf(vda, vdb) > kRefSlack * ref;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        move |= fmaxf(c[n][0], c[n][2]) > m[n][0] + kMaxSlack;
+        move |= fmaxf(c[n][1], c[n][3]) > m[n][1] + kMaxSlack;
+      }
+      if (__any_sync(kFullMask, move)) {
+        const float top = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(fmaxf(vda, vdb))));
+        const float new_ref = fmaxf(ref, top);
+        const float rescale = new_ref > 0.0f ? ref / new_ref : 1.0f;
+        ref = new_ref;
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float y = fmaxf(c[n][i], c[n][2 + i]);
+#pragma unroll
+            for (int w2 = 4; w2 < 32; w2 <<= 1) y = fmaxf(y, __shfl_xor_sync(kFullMask, y, w2));
+            const float new_m = fmaxf(m[n][i], y);
+            const float f = new_m == -kInf ? 1.0f : ex2(m[n][i] - new_m);
+            m[n][i] = new_m;
+            l[n][i] *= f;
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+              o[j][n][i] *= f * rescale;
+              o[j][n][2 + i] *= f * rescale;
+            }
+          }
+      }
+      const float wa2 = ref > 0.0f ? vda * (kWeightScale / ref) : 0.0f;
+      const float wb2 = ref > 0.0f ? vdb * (kWeightScale / ref) : 0.0f;
+      uint32_t p0[kNT], p1[kNT], e0[kNT], e1[kNT];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        const float m0 = m[n][0] == -kInf ? 0.0f : m[n][0], m1 = m[n][1] == -kInf ? 0.0f : m[n][1];
+        const float x0 = ex2(c[n][0] - m0), x1 = ex2(c[n][1] - m1);
+        const float x2 = ex2(c[n][2] - m0), x3 = ex2(c[n][3] - m1);
+        l[n][0] += x0 + x2;
+        l[n][1] += x1 + x3;
+        const float y0 = x0 * wa2, y1 = x1 * wa2, y2 = x2 * wb2, y3 = x3 * wb2;
+        const uint32_t h0 = pack_half(y0, y1), h1 = pack_half(y2, y3);
+        p0[n] = transpose_8x8(h0);
+        p1[n] = transpose_8x8(h1);
+        if (kPair) {
+          const float2 r0 = unpack_half(h0), r1 = unpack_half(h1);
+          e0[n] = transpose_8x8(pack_half(y0 - r0.x, y1 - r0.y));
+          e1[n] = transpose_8x8(pack_half(y2 - r1.x, y3 - r1.y));
+        }
+      }
+
+      // O^T: operand rows g, g + 8 of tile 2w (2w + 1) are dims 4w, 4w+1 (4w+2, 4w+3) of this
+      // lane's run of dims; keys 2t, 2t+1 of the operand are key_of(2t), key_of(2t+1).
+      const int k0 = key_of<kD>(2 * t4), k1 = key_of<kD>(2 * t4 + 1);
+#pragma unroll
+      for (int q = 0; q < (kD + 127) / 128; ++q) {
+        constexpr int kWords = kD == 64 ? 2 : 4;
+        uint32_t v[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = (i & 1 ? k1 : k0) + (i & 2 ? 8 : 0);
+          if (kD == 64) {
+            const uint32_t at2 = vbase + v_place<kD>(k, g >> 1) + (g & 1) * 8;
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(at2));
+          } else {
+            const uint4 y = lds_v4(vbase + v_place<kD>(k, 8 * q + g));
+            v[i][0] = y.x; v[i][1] = y.y; v[i][2] = y.z; v[i][3] = y.w;
+          }
+        }
+#pragma unroll
+        for (int w2 = 0; w2 < kWords; ++w2) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t sel = half ? 0x7632u : 0x5410u;
+            const uint32_t z0 = __byte_perm(v[0][w2], v[1][w2], sel);
+            const uint32_t z1 = __byte_perm(v[2][w2], v[3][w2], sel);
+            const uint32_t a0 = even_bytes(z0), a1 = odd_bytes(z0);
+            const uint32_t a2 = even_bytes(z1), a3 = odd_bytes(z1);
+            const int tile = (q * kWords + w2) * 2 + half;
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) {
+              mma_16816(o[tile][n], a0, a1, a2, a3, p0[n], p1[n]);
+              if (kPair) mma_16816(o[tile][n], a0, a1, a2, a3, e0[n], e1[n]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      const int32_t p = next_page;
+      next_page = page_of(s + Sh::kStages);
+      issue(s + Sh::kStages - 1, p);
+    }
+    cp_wait<0>();
+
+    // ---- join the warps ----
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int w2 = 4; w2 < 32; w2 <<= 1) l[n][i] += __shfl_xor_sync(kFullMask, l[n][i], w2);
+        if (g == 0) {
+          warp_m[warp * kRows + 8 * n + 2 * t4 + i] = m[n][i];
+          warp_l[warp * kRows + 8 * n + 2 * t4 + i] = l[n][i];
+        }
+      }
+    __syncthreads();  // also: every warp is done with its ring
+    for (int r = tid; r < kRows; r += kThreads) {
+      float top = -kInf, sum = 0.0f;
+      for (int i = 0; i < kWarps; ++i) top = fmaxf(top, warp_m[i * kRows + r]);
+      for (int i = 0; i < kWarps; ++i)
+        if (warp_m[i * kRows + r] > -kInf) sum += warp_l[i * kRows + r] * ex2(warp_m[i * kRows + r] - top);
+      row_m[r] = top;
+      row_l[r] = sum;
+    }
+    float* join = reinterpret_cast<float*>(ring) + warp * kRows * kD;
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * n + 2 * t4 + i;
+        float top = -kInf;
+        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, warp_m[k * kRows + r]);
+        const float f = m[n][i] > -kInf ? ex2(m[n][i] - top) * ref * (1.0f / kWeightScale) : 0.0f;
+        constexpr int kRun = kD == 64 ? 8 : 16;  // consecutive dims of a lane
+#pragma unroll
+        for (int j = 0; j < kSteps / 2; ++j) {
+          const float4 v = make_float4(o[2 * j][n][i] * f, o[2 * j][n][2 + i] * f,
+                                       o[2 * j + 1][n][i] * f, o[2 * j + 1][n][2 + i] * f);
+          const int d = (j / (kRun / 4)) * 128 + g * kRun + (j % (kRun / 4)) * 4;
+          *reinterpret_cast<float4*>(join + r * kD + d) = v;
+        }
+      }
+    __syncthreads();
+
+    const bool whole = x == unit_at && x_stop == unit_stop;
+    const int part_size = kRows * (kD + 2);
+    float* mine = a.parts + (int64_t)(2 * cta + (x == unit_at ? 1 : 0)) * part_size;
+    T* out = static_cast<T*>(a.out);
+    for (int i = tid; i < kRows * kD / 4; i += kThreads) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(ring) + k * kRows * kD + i * 4);
+        v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+      }
+      const int r = i * 4 / kD;
+      if (whole) {
+        const int64_t token = token0 + (row0 + r) / a.G;
+        if (r < rows && token >= 0 && token < a.T) {
+          const float f = row_l[r] > 0.0f ? 1.0f / row_l[r] : 0.0f;
+          const int64_t row = token * a.Hq + h * a.G + (row0 + r) % a.G;
+          store4(out + row * kD + i * 4 % kD, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+          if (a.lse != nullptr && i * 4 % kD == 0)
+            a.lse[row] = row_l[r] > 0.0f ? (row_m[r] + log2f(row_l[r])) * 0.693147180559945309f : -kInf;
+        }
+      } else {
+        __stcg(reinterpret_cast<float4*>(mine + 2 * kRows) + i, v);
+      }
+    }
+    if (!whole) {
+      if (tid < kRows) {
+        __stcg(mine + tid, row_m[tid]);
+        __stcg(mine + kRows + tid, row_l[tid]);
+      }
+      const int c0 = (int)(((unit_at + 1) * ctas - 1) / total), c1 = (int)((unit_stop * ctas - 1) / total);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int n = atomicAdd(a.arrived + c0, 1);
+        last_part = n == c1 - c0;
+        if (last_part) a.arrived[c0] = 0;
+      }
+      __syncthreads();
+      if (last_part) {
+        // ---- join the unit's parts: warps take parts in turn, then each other's sums ----
+        __threadfence();
+        const int parts = c1 - c0 + 1;
+        auto part = [&](int i) { return a.parts + (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * part_size; };
+        for (int r = warp; r < kRows; r += kWarps) {
+          float top = -kInf, sum = 0.0f;
+          for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(part(i) + r));
+#pragma unroll
+          for (int w2 = 16; w2 > 0; w2 >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, w2));
+          for (int i = lane; i < parts; i += 32) {
+            const float pm = __ldcg(part(i) + r);
+            if (pm > -kInf) sum += __ldcg(part(i) + kRows + r) * ex2(pm - top);
+          }
+#pragma unroll
+          for (int w2 = 16; w2 > 0; w2 >>= 1) sum += __shfl_xor_sync(kFullMask, sum, w2);
+          if (lane == 0) {
+            row_m[r] = top;
+            row_l[r] = sum;
+          }
+        }
+        __syncthreads();
+        constexpr int kPieces = 8;  // float4 a lane holds at once: 1024 values of a part
+        for (int base = 0; base < kRows * kD; base += kPieces * 128) {
+          float4 v[kPieces];
+#pragma unroll
+          for (int j = 0; j < kPieces; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int i = warp; i < parts; i += kWarps) {
+            const float* src = part(i);
+            float4 y[kPieces];
+            float f[kPieces];
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+              const int e = base + j * 128 + lane * 4;
+              if (e < kRows * kD) {
+                y[j] = __ldcg(reinterpret_cast<const float4*>(src + 2 * kRows + e));
+                f[j] = __ldcg(src + e / kD);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+              const int e = base + j * 128 + lane * 4;
+              if (e < kRows * kD) {
+                const float s2 = f[j] > -kInf ? ex2(f[j] - row_m[e / kD]) : 0.0f;
+                v[j].x += y[j].x * s2; v[j].y += y[j].y * s2; v[j].z += y[j].z * s2; v[j].w += y[j].w * s2;
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kPieces; ++j) {
+            const int e = base + j * 128 + lane * 4;
+            if (e < kRows * kD)
+              *reinterpret_cast<float4*>(reinterpret_cast<float*>(ring) + warp * kPieces * 128 + j * 128 + lane * 4) = v[j];
+          }
+          __syncthreads();
+          for (int i = tid; i < kPieces * 32; i += kThreads) {
+            const int e = base + i * 4;
+            if (e < kRows * kD) {
+              float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+              for (int k = 0; k < kWarps; ++k) {
+                const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(ring) + k * kPieces * 128 + i * 4);
+                s4.x += y.x; s4.y += y.y; s4.z += y.z; s4.w += y.w;
+              }
+              const int r = e / kD;
+              const int64_t token = token0 + (row0 + r) / a.G;
+              if (r < rows && token >= 0 && token < a.T) {
+                const float f = row_l[r] > 0.0f ? 1.0f / row_l[r] : 0.0f;
+                const int64_t row = token * a.Hq + h * a.G + (row0 + r) % a.G;
+                store4(out + row * kD + e % kD, make_float4(s4.x * f, s4.y * f, s4.z * f, s4.w * f));
+                if (a.lse != nullptr && e % kD == 0)
+                  a.lse[row] = row_l[r] > 0.0f ? (row_m[r] + log2f(row_l[r])) * 0.693147180559945309f : -kInf;
+              }
+            }
+          }
+          __syncthreads();
+        }
+      }
+    }
+    __syncthreads();  // the ring, the queries and the statistics are free again
+    x = x_stop;
+  }
+}
+
+template <typename T, int kD, int kNT>
+cudaError_t launch_shape(const AttnArgs& a, const DeviceInfo& info, int64_t max_tiles,
+                         cudaStream_t stream) {
+  using Sh = Shape<T, kD, kNT>;
+  static_assert(Sh::kSmem * Sh::kCtas <= 226 * 1024, "shared memory of the CTAs of an SM");
+  // The attribute is set once for each device: it stays with the function, whose size is
+  // always the same.
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !((ready.load() >> dev) & 1u)) {
+    e = cudaFuncSetAttribute(attention_kernel<T, kD, kNT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev);
+  }
+  int64_t ctas = (int64_t)info.sms * Sh::kCtas;
+  const int64_t fit = (MEMRA_KV_ATTENTION_WORKSPACE_BYTES - kMaxCtas * 4) /
+                      (2 * Sh::kRows * (kD + 2) * (int64_t)sizeof(float));
+  if (ctas > fit) ctas = fit;
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  const int64_t groups = (a.T * a.G + Sh::kRows - 1) / Sh::kRows + a.B;
+  const int64_t tiles = (max_tiles + 1) * groups * a.Hkv;  // what the list can hold at most
+  if (ctas > tiles) ctas = tiles;
+  if (ctas < 1) ctas = 1;
+  return launch_kernel(attention_kernel<T, kD, kNT>, dim3((unsigned)ctas), dim3(kThreads),
+                       (size_t)Sh::kSmem, stream, a);
+}
+
+// Query rows of a step: 8, 16 or 32, the fewest that hold an average request's (its keys
+// are read once for each step).
 template <typename T>
-cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
-  const dim3 grid((unsigned)(a.T * a.Hq)), block(128);
-  if (a.D == 64) return launch_kernel(attention_rows_kernel<T, 64>, grid, block, 0, stream, a);
-  if (a.D == 128) return launch_kernel(attention_rows_kernel<T, 128>, grid, block, 0, stream, a);
-  return launch_kernel(attention_rows_kernel<T, 256>, grid, block, 0, stream, a);
+cudaError_t launch_attention(const AttnArgs& a, int D, const DeviceInfo& info, cudaStream_t stream) {
+  const int64_t rows = a.B > 0 ? (a.T * a.G + a.B - 1) / a.B : 1;
+  const int64_t max_tiles = a.max_pages * a.page / kTile + 1;
+  if (D == 64) {
+    if (rows <= 8) return launch_shape<T, 64, 1>(a, info, max_tiles, stream);
+    if (rows <= 16) return launch_shape<T, 64, 2>(a, info, max_tiles, stream);
+    return launch_shape<T, 64, 4>(a, info, max_tiles, stream);
+  }
+  if (D == 128) {
+    if (rows <= 8) return launch_shape<T, 128, 1>(a, info, max_tiles, stream);
+    if (rows <= 16) return launch_shape<T, 128, 2>(a, info, max_tiles, stream);
+    return launch_shape<T, 128, 4>(a, info, max_tiles, stream);
+  }
+  if (rows <= 8) return launch_shape<T, 256, 1>(a, info, max_tiles, stream);
+  return launch_shape<T, 256, 2>(a, info, max_tiles, stream);
 }
 
 }  // namespace
@@ -145,33 +820,38 @@ extern "C" memra_status memra_kv_attention_q8(
   const void* words[] = {kd, vd, block_table, kv_lens, cu_q, lse, dev_status};
   for (const void* p : words)
     if (!aligned(p, 4)) return MEMRA_ERR_ALIGNMENT;
+  DeviceInfo info;
+  if (!device_info(&info)) return MEMRA_ERR_CUDA;
   AttnArgs a;
   a.q = q;
   a.T = T;
-  a.Hq = Hq;
   a.stride_t = stride_t;
   a.stride_h = stride_h;
   a.kq = kq;
   a.vq = vq;
   a.kd = kd;
   a.vd = vd;
-  a.n_pages = n_pages;
-  a.max_pages = max_pages;
-  a.Hkv = (int)Hkv;
-  a.page = (int)page_size;
-  a.D = (int)D;
-  a.block = (int)block;
   a.table = block_table;
   a.kv_lens = kv_lens;
   a.cu_q = cu_q;
   a.B = B;
+  a.max_pages = max_pages;
   a.window = window;
+  a.n_pages = (int32_t)n_pages;
+  a.Hq = (int)Hq;
+  a.Hkv = (int)Hkv;
+  a.G = (int)(Hq / Hkv);
+  a.page = (int)page_size;
+  a.block = (int)block;
+  a.block_magic = (uint32_t)(((1u << 22) + block - 1) / block);
   a.scale = scale;
   a.out = out;
   a.lse = lse;
+  a.arrived = static_cast<int*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMaxCtas * 4);
   a.status = dev_status;
-  const cudaError_t e =
-      dtype == MEMRA_BF16 ? launch_rows<uint16_t>(a, stream) : launch_rows<float>(a, stream);
+  const cudaError_t e = dtype == MEMRA_BF16 ? launch_attention<uint16_t>(a, (int)D, info, stream)
+                                            : launch_attention<float>(a, (int)D, info, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }
