@@ -13,14 +13,26 @@
 // A strip is two products on the tensor cores with the keys (dims) in the 16-row operand,
 // so that 8 query rows waste nothing:
 //   S^T [16 keys x 8 rows]  = K [16 x D] * Q^T,   O^T [D x 8 rows] += V^T [D x 16] * P^T.
-// int8 codes become fp16 operands exactly, by setting the exponent of 1024 above the byte
-// and subtracting 1024 + 128 (2.5 instructions for two codes).  Scales never meet the
-// codes: kd multiplies the score, vd the weight.
+// An int8 code c becomes an fp16 operand exactly and without arithmetic: the byte c + 128
+// (one xor) alone in an fp16's mantissa is the subnormal (c + 128) * 2^-24, which the
+// tensor cores take at full rate.  The 128 leaves S through its initial value, -128 sum q,
+// and O, for 8-row units of bf16 queries, through a second product of a constant -128
+// matrix with the same weights, so the two parts cancel within a strip; elsewhere codes of
+// V are made as 1024 + 128 + c and an fp16 subtraction, which is exact and costs the
+// arithmetic pipe instead.  Scales never meet the codes: kd multiplies the score, vd the
+// weight.
 #include <atomic>
 
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+
+#ifndef MEMRA_ATTN_UNIT_COST
+#define MEMRA_ATTN_UNIT_COST 3
+#endif
+#ifndef MEMRA_ATTN_MIN_SHARE
+#define MEMRA_ATTN_MIN_SHARE 1
+#endif
 
 namespace memra {
 namespace {
@@ -30,6 +42,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStrip = 16;                 // keys of a warp's step
 constexpr int kTile = kWarps * kStrip;     // keys of a CTA's step, the unit of the work list
 constexpr int kMaxCtas = 512;              // arrival counters at the workspace's start
+constexpr int kUnitCost = MEMRA_ATTN_UNIT_COST;  // list entries that stand for a unit's fixed time
+constexpr int kMinShare = MEMRA_ATTN_MIN_SHARE;  // list entries that a CTA gets at least
 
 // A weight enters the product as p * (vd / ref) * 2^8 in fp16, ref a running maximum of vd
 // kept within a factor 4, p = 2^(s - m) with m within 5 of the running maximum: at most
@@ -48,6 +62,8 @@ struct AttnArgs {
   int32_t n_pages;
   int Hq, Hkv, G, page, block;
   uint32_t block_magic;  // ceil(2^22 / block): off / block = off * magic >> 22, off < 1024
+  uint32_t page_bytes, page_scales;  // of one page in a plane, all heads
+  int step_pages, step_off;          // kTile = step_pages * page + step_off
   float scale;
   void* out;
   float* lse;
@@ -83,8 +99,12 @@ __device__ __forceinline__ void mma_16816(float c[4], uint32_t a0, uint32_t a1, 
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Bytes 0 and 2 (1 and 3) of w, signed, as two fp16: byte ^ 0x80 under the exponent of
-// 1024 is 1024 + 128 + value.
+// Codes 0 and 2 (1 and 3) of w plus 128, times 2^-24, as two fp16.
+__device__ __forceinline__ uint32_t even_raised(uint32_t w) { return (w & 0x00ff00ffu) ^ 0x00800080u; }
+__device__ __forceinline__ uint32_t odd_raised(uint32_t w) {
+  return ((w >> 8) & 0x00ff00ffu) ^ 0x00800080u;
+}
+// The codes themselves: the byte under the exponent of 1024 is 1024 + 128 + code.
 __device__ __forceinline__ uint32_t minus_1152(uint32_t h) {
   const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x6480)));
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -155,6 +175,7 @@ template <typename T, int kD, int kNT>
 struct Shape {
   static constexpr int kRows = 8 * kNT;
   static constexpr bool kPair = Row<T>::kPair;
+  static constexpr bool kRaisedV = !kPair && kNT == 1;
   static constexpr int kCtas = kD <= 128 && kNT * kD <= 256 ? 2 : 1;  // a SM
   static constexpr int kStage = 2 * kStrip * kD + 8 * kStrip;  // K, V, 16 kd, 16 vd
   static constexpr int kStages = kD == 64 ? 5 : (kCtas == 2 ? 3 : (kD == 128 ? 6 : 3));
@@ -162,7 +183,7 @@ struct Shape {
   static constexpr int kJoin = kWarps * kRows * kD * 4;  // reuses the ring
   static constexpr int kBig = kRing > kJoin ? kRing : kJoin;
   static constexpr int kQ = (kPair ? 2 : 1) * (kD / 16) * kNT * 32 * 8;
-  static constexpr int kStats = (2 * kWarps + 4) * kRows * 4;
+  static constexpr int kStats = (2 * kWarps + 5) * kRows * 4;
   static constexpr int kSmem = kBig + kQ + kStats;
 };
 
@@ -220,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
   float* row_m = warp_l + kWarps * kRows;      // [kRows]
   float* row_l = row_m + kRows;
   float* row_scale = row_l + kRows;
-  int* row_limit = reinterpret_cast<int*>(row_scale + kRows);
+  float* row_raise = row_scale + kRows;
+  int* row_limit = reinterpret_cast<int*>(row_raise + kRows);
   __shared__ int64_t scan[kWarps], found_at;
   __shared__ int found_b, last_part;
 
@@ -230,54 +252,61 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
   const int g = lane >> 2, t4 = lane & 3;
   const int cta = blockIdx.x;
 
-  // ---- the list: every CTA sums the requests' tiles and finds its own part ----
-  int64_t total = 0, first = 0, stop = 0;
+  // ---- the list: every CTA sums the requests' entries and finds its own part ----
+  // A unit takes kUnitCost entries and one for each tile.
+  auto entries_of = [&](const Request& r) {
+    return r.tiles > 0 ? (int64_t)(r.tiles + kUnitCost) * r.groups * a.Hkv : (int64_t)0;
+  };
+  int64_t total = 0, first = 0, stop = 0, w = 0, sum = 0;
   int ctas = 0;
   for (int pass = 0; pass < 2; ++pass) {
     int64_t before = 0;
     for (int64_t base = 0; base < a.B; base += kThreads) {
       const int64_t b = base + tid;
-      int64_t w = 0;
-      bool empty = false;
-      if (b < a.B) {
-        const Request r = request_of<kRows>(a, b);
-        w = (int64_t)r.tiles * r.groups * a.Hkv;
-        empty = w == 0 && r.n > 0;
-        if (pass == 0 && cta == 0 && a.status != nullptr &&
-            a.kv_lens[b] > a.max_pages * a.page)
-          atomicOr(a.status, 1);
-      }
-      if (pass == 0) {  // rows of requests without keys, each request by one CTA
-        uint32_t todo = __ballot_sync(kFullMask, empty && b % gridDim.x == cta);
-        while (todo != 0) {
-          const int64_t e = base + warp * 32 + (__ffs(todo) - 1);
-          todo &= todo - 1;
-          write_nothing<T, kD>(a, a.cu_q[e], a.cu_q[e + 1], lane, 32);
+      if (pass == 0 || a.B > kThreads) {  // one chunk's sums stay in registers
+        w = 0;
+        bool empty = false;
+        if (b < a.B) {
+          const Request r = request_of<kRows>(a, b);
+          w = entries_of(r);
+          empty = w == 0 && r.n > 0;
+          if (pass == 0 && cta == 0 && a.status != nullptr &&
+              a.kv_lens[b] > a.max_pages * a.page)
+            atomicOr(a.status, 1);
         }
-      }
-      int64_t sum = w;
+        if (pass == 0) {  // rows of requests without keys, each request by one CTA
+          uint32_t todo = __ballot_sync(kFullMask, empty && b % gridDim.x == cta);
+          while (todo != 0) {
+            const int64_t e = base + warp * 32 + (__ffs(todo) - 1);
+            todo &= todo - 1;
+            write_nothing<T, kD>(a, a.cu_q[e], a.cu_q[e + 1], lane, 32);
+          }
+        }
+        sum = w;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(kFullMask, sum, o);
-        if (lane >= o) sum += u;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t u = __shfl_up_sync(kFullMask, sum, o);
+          if (lane >= o) sum += u;
+        }
+        if (lane == 31) scan[warp] = sum;
+        __syncthreads();
+        int64_t chunk = 0;
+        for (int i = 0; i < kWarps; ++i) {
+          if (i < warp) sum += scan[i];
+          chunk += scan[i];
+        }
+        sum += before;
+        before += chunk;
       }
-      if (lane == 31) scan[warp] = sum;
-      __syncthreads();
-      int64_t chunk = 0;
-      for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) sum += scan[i];
-        chunk += scan[i];
-      }
-      if (pass == 1 && w > 0 && before + sum - w <= first && first < before + sum) {
+      if (pass == 1 && w > 0 && sum - w <= first && first < sum) {
         found_b = (int)b;
-        found_at = before + sum - w;
+        found_at = sum - w;
       }
-      before += chunk;
       __syncthreads();
     }
     if (pass == 0) {
       total = before;
-      ctas = (int)min((int64_t)gridDim.x, total);
+      ctas = (int)min((int64_t)gridDim.x, (total + kMinShare - 1) / kMinShare);
       // rows that no request owns
       for (int64_t row = (a.B > 0 ? a.cu_q[a.B] : 0) + cta; row < a.T; row += gridDim.x)
         write_nothing<T, kD>(a, row, row + 1, tid, kThreads);
@@ -291,20 +320,37 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
   Request req = request_of<kRows>(a, b);
 
   const uint32_t my_ring = smem_addr(ring) + warp * Sh::kStages * Sh::kStage;
+  // Lane constants of the ring: where this lane's 16 bytes of a copy go (row i * 512 bytes
+  // further on differs by a constant exclusive-or in bits 4..6), and where it reads.
+  constexpr int kChunks = kD / 16;
+  const uint32_t k_dst = k_place<kD>(lane / kChunks, lane % kChunks);
+  const uint32_t v_dst = kStrip * kD + v_place<kD>(lane / kChunks, lane % kChunks);
+  const int ka = key_of<kD>(g), kb = 8 + ka;
+  const uint32_t k_src = k_place<kD>(ka, t4);
+  const int vk0 = key_of<kD>(2 * t4), vk1 = key_of<kD>(2 * t4 + 1);
+  const uint32_t v_src0 = kStrip * kD + (kD == 64 ? v_place<kD>(vk0, g >> 1) + (g & 1) * 8 : v_place<kD>(vk0, g));
+  const uint32_t v_src1 = kStrip * kD + (kD == 64 ? v_place<kD>(vk1, g >> 1) + (g & 1) * 8 : v_place<kD>(vk1, g));
+  const int64_t v_minus_k = a.vq - a.kq;
+
   int64_t x = first;
   while (x < stop) {
-    int64_t w = (int64_t)req.tiles * req.groups * a.Hkv;
+    w = entries_of(req);
     while (x >= at + w) {
       at += w;
       req = request_of<kRows>(a, ++b);
-      w = (int64_t)req.tiles * req.groups * a.Hkv;
+      w = entries_of(req);
     }
     // ---- this unit: cached head h, rows [row0, row0 + kRows) of the request's n * G ----
-    const int unit = (int)((x - at) / req.tiles);
-    const int64_t unit_at = at + (int64_t)unit * req.tiles;
-    const int h = unit / req.groups, row0 = unit % req.groups * kRows;
-    const int64_t unit_stop = unit_at + req.tiles;
+    const int unit_size = req.tiles + kUnitCost;
+    const int unit = (int)((x - at) / unit_size);
+    const int64_t unit_at = at + (int64_t)unit * unit_size;
+    const int64_t unit_stop = unit_at + unit_size;
     const int64_t x_stop = unit_stop < stop ? unit_stop : stop;
+    const int tile0 = max((int)(x - unit_at) - kUnitCost, 0);
+    const int tile1 = (int)(x_stop - unit_at) - kUnitCost;
+    if (tile1 <= 0) break;  // this part ends within the unit's fixed entries
+    const bool begins = tile0 == 0;
+    const int h = unit / req.groups, row0 = unit % req.groups * kRows;
     const int rows = min(kRows, req.n * a.G - row0);
     const int token0 = a.cu_q[b];
 
@@ -317,7 +363,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
       const T* src = static_cast<const T*>(a.q) + (real ? (token0 + i) * a.stride_t + hq * a.stride_h : 0);
       constexpr int kPer = kD / 32;
       float v[kPer], amax = 0.0f;
-      // lane's dims: those that its operand registers hold for steps kPer/2 ... (see below)
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         v[j] = real ? value(src + j * 32 + lane) : 0.0f;
@@ -327,12 +372,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
       int e = (int)(__float_as_uint(amax) >> 23) - 127;
       e = e < -100 ? -100 : e;
       const float up = __int_as_float((13 - e + 127) << 23);  // 2^(13 - e), e in [-100, 128]
-      if (lane == 0) {
-        row_scale[r] = amax > 0.0f ? a.scale * 1.44269504088896341f * __int_as_float((e - 13 + 127) << 23)
+      if (lane == 0) {  // the codes' 2^-24 goes back in here
+        row_scale[r] = amax > 0.0f ? a.scale * (0x1p24f * 1.44269504088896341f) *
+                                         __int_as_float((e - 13 + 127) << 23)
                                    : 0.0f;
         row_limit[r] = min(req.len, req.len - req.n + i + 1);
       }
       __half* frag = reinterpret_cast<__half*>(q_frag);
+      float sum_q = 0.0f;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int d = j * 32 + lane;
@@ -343,30 +390,42 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         const float s = v[j] * up;
         const __half hi = __float2half_rn(s);
         frag[idx] = hi;
-        if (kPair) frag[idx + kSteps * kNT * 32 * 4] = __float2half_rn(s - __half2float(hi));
+        sum_q += __half2float(hi);
+        if (kPair) {
+          const __half lo = __float2half_rn(s - __half2float(hi));
+          frag[idx + kSteps * kNT * 32 * 4] = lo;
+          sum_q += __half2float(lo);
+        }
       }
+#pragma unroll
+      for (int w2 = 16; w2 > 0; w2 >>= 1) sum_q += __shfl_xor_sync(kFullMask, sum_q, w2);
+      if (lane == 0) row_raise[r] = -128.0f * 0x1p-24f * sum_q;
     }
     __syncthreads();
-    float qs[kNT][2];
+    float qs[kNT][2], raise[kNT][2];
     int limit[kNT][2];
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         qs[n][c] = row_scale[8 * n + 2 * t4 + c];
+        raise[n][c] = row_raise[8 * n + 2 * t4 + c];
         limit[n][c] = row_limit[8 * n + 2 * t4 + c];
       }
     const int limit_min = row_limit[0], limit_max = row_limit[rows - 1];
     // keys below this are hidden from the last row (window)
     const int low_max = a.window > 0 ? (int)max((int64_t)0, limit_max - a.window) : 0;
 
+    // m: the reference that weights are taken against (0 while a row has seen no key);
+    // bar: m + kMaxSlack (-inf then).
     float o[kSteps][kNT][4];
-    float m[kNT][2], l[kNT][2], ref = 0.0f;
+    float m[kNT][2], bar[kNT][2], l[kNT][2], ref = 0.0f, inv_ref = 0.0f;
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        m[n][c] = -kInf;
+        m[n][c] = 0.0f;
+        bar[n][c] = -kInf;
         l[n][c] = 0.0f;
       }
 #pragma unroll
@@ -375,71 +434,91 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         for (int c = 0; c < 4; ++c) o[i][n][c] = 0.0f;
     }
 
-    // ---- the warp's strips: key0, key0 + kTile, ... below key_stop ----
-    const int key0 = req.lo + (int)(x - unit_at) * kTile + warp * kStrip;
-    const int key_stop = min(req.lo + (int)(x_stop - unit_at) * kTile, limit_max);
-    const int strips = key0 < key_stop ? (key_stop - key0 + kTile - 1) / kTile : 0;
+    // ---- the warp's strips: keys key, key + kTile, ... below key_stop ----
+    int key = req.lo + tile0 * kTile + warp * kStrip;
+    const int key_stop = min(req.lo + tile1 * kTile, limit_max);
+    const int strips = key < key_stop ? (key_stop - key + kTile - 1) / kTile : 0;
     const int32_t* pages = a.table + (int64_t)b * a.max_pages;
-    uint32_t hidden = 0;  // bit i: the stage i strips ahead has no page
+    const int8_t* k_head = a.kq + (int64_t)h * a.page * kD + lane * 16;
+    const float* scale_head = (lane < 16 ? a.kd : a.vd) + (int64_t)h * (a.page / a.block);
+    uint32_t hidden = 0;  // bit i: stage i's strip has no page
+    // The page of a strip is looked up one strip before its copies are issued.
+    int look = 0, look_at = key / a.page, look_off = key % a.page;
+    int issue_off = 0, write_slot = 0;
+    uint32_t write_at = my_ring;
+    int32_t page = 0;
 
-    auto page_of = [&](int s) { return s < strips ? pages[(key0 + s * kTile) / a.page] : 0; };
-    auto issue = [&](int s, int32_t page) {
-      if (s < strips) {
+    auto look_up = [&]() {
+      issue_off = look_off;
+      if (look < strips) page = pages[look_at];
+      ++look;
+      look_at += a.step_pages;
+      look_off += a.step_off;
+      if (look_off >= a.page) {
+        look_off -= a.page;
+        ++look_at;
+      }
+    };
+    auto issue = [&]() {  // the strip looked up last, if there was one
+      if (look <= strips) {
         if ((uint32_t)page < (uint32_t)a.n_pages) {
-          const int key = key0 + s * kTile;
-          const int off = key % a.page;
-          const uint32_t dst = my_ring + s % Sh::kStages * Sh::kStage;
-          const int64_t head = (int64_t)page * a.Hkv + h;
-          const int64_t codes = (head * a.page + off) * kD;
-          constexpr int kChunks = kD / 16;
+          const int8_t* src = k_head + (uint64_t)(uint32_t)page * a.page_bytes + issue_off * kD;
+          const int8_t* src_v = src + v_minus_k;
+          const uint32_t kd0 = write_at + k_dst, vd0 = write_at + v_dst;
 #pragma unroll
           for (int i = 0; i < kStrip * kChunks / 32; ++i) {
-            const int k = (i * 32 + lane) / kChunks, c = (i * 32 + lane) % kChunks;
-            cp16(dst + k_place<kD>(k, c), a.kq + codes + (i * 32 + lane) * 16);
-            cp16(dst + kStrip * kD + v_place<kD>(k, c), a.vq + codes + (i * 32 + lane) * 16);
+            constexpr uint32_t kNone = 0;
+            const uint32_t xk = kD == 64 ? kNone : kD == 128 ? (i & 1) * 64u : (i & 3) * 32u;
+            const uint32_t xv = kD == 64 ? kNone
+                                         : kD == 128 ? (i & 1) * 16u
+                                                     : ((i & 1) * 4u + ((i >> 1) & 1)) * 16u;
+            cp16((kd0 ^ xk) + i * 512, src + i * 512);
+            cp16((vd0 ^ xv) + i * 512, src_v + i * 512);
           }
-          const int64_t sc = head * (a.page / a.block) +
-                             (((uint32_t)(off + (lane & 15)) * a.block_magic) >> 22);
-          cp4(dst + 2 * kStrip * kD + lane * 4, (lane < 16 ? a.kd : a.vd) + sc);
+          cp4(write_at + 2 * kStrip * kD + lane * 4,
+              scale_head + (uint64_t)(uint32_t)page * a.page_scales +
+                  (((uint32_t)(issue_off + (lane & 15)) * a.block_magic) >> 22));
         } else {
-          hidden |= 1u << (s % Sh::kStages);
+          hidden |= 1u << write_slot;
           if (lane == 0 && a.status != nullptr) atomicOr(a.status, 1);
         }
       }
       cp_commit();
+      write_at += Sh::kStage;
+      if (++write_slot == Sh::kStages) {
+        write_slot = 0;
+        write_at = my_ring;
+      }
     };
 
-    int32_t next_page = page_of(0);
+    look_up();
 #pragma unroll
     for (int s = 0; s < Sh::kStages - 1; ++s) {
-      const int32_t p = next_page;
-      next_page = page_of(s + 1);
-      issue(s, p);
+      issue();
+      look_up();
     }
 
+    uint32_t read_at = my_ring;
+    int read_slot = 0;
     for (int s = 0; s < strips; ++s) {
       cp_wait<Sh::kStages - 2>();
       __syncwarp();
-      const int slot = s % Sh::kStages;
-      const uint32_t kbase = my_ring + slot * Sh::kStage, vbase = kbase + kStrip * kD;
-      const uint32_t dbase = kbase + 2 * kStrip * kD;
-      const int ka = key_of<kD>(g), kb = 8 + ka;
-
       float c[kNT][4];
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[n][i] = 0.0f;
+      for (int n = 0; n < kNT; ++n) {
+        c[n][0] = c[n][2] = raise[n][0];
+        c[n][1] = c[n][3] = raise[n][1];
+      }
 #pragma unroll
       for (int q = 0; q < kD / 64; ++q) {
-        const uint4 xa = lds_v4(kbase + k_place<kD>(ka, 4 * q + t4));
-        const uint4 xb = lds_v4(kbase + k_place<kD>(kb, 4 * q + t4));
+        const uint32_t from = ((read_at + k_src) ^ (kD == 64 ? 0u : (q & 1) * 64u)) + (q >> 1) * 128;
+        const uint4 xa = lds_v4(from), xb = lds_v4(from + 8 * kD);
         const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int step = 4 * q + i;
-          const uint32_t a0 = even_bytes(wa[i]), a1 = even_bytes(wb[i]);
-          const uint32_t a2 = odd_bytes(wa[i]), a3 = odd_bytes(wb[i]);
+          const uint32_t a0 = even_raised(wa[i]), a1 = even_raised(wb[i]);
+          const uint32_t a2 = odd_raised(wa[i]), a3 = odd_raised(wb[i]);
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
             const uint2 f = q_frag[(step * kNT + n) * 32 + lane];
@@ -453,12 +532,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
       }
 
       // c[n]: (key a, row 2t), (key a, row 2t+1), (key b, row 2t), (key b, row 2t+1)
-      float kda = lds_f32(dbase + ka * 4), kdb = lds_f32(dbase + kb * 4);
-      float vda = lds_f32(dbase + 64 + ka * 4), vdb = lds_f32(dbase + 64 + kb * 4);
-      const int key = key0 + s * kTile;
-      const bool no_page = (hidden >> slot) & 1u;
-      hidden &= ~(1u << slot);
-      const bool plain = key + kStrip <= limit_min && key >= low_max && !no_page;
+      const uint32_t d_at = read_at + 2 * kStrip * kD + ka * 4;
+      const float kda = lds_f32(d_at), kdb = lds_f32(d_at + 32);
+      float vda = lds_f32(d_at + 64), vdb = lds_f32(d_at + 96);
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         c[n][0] *= kda * qs[n][0];
@@ -466,7 +542,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         c[n][2] *= kdb * qs[n][0];
         c[n][3] *= kdb * qs[n][1];
       }
-      if (!plain) {
+      const bool no_page = (hidden >> read_slot) & 1u;
+      if (key + kStrip > limit_min || key < low_max || no_page) {
+        hidden &= ~(1u << read_slot);
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
@@ -479,18 +557,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         vdb = key + kb < limit_max && !no_page ? vdb : 0.0f;
       }
 
-      // Running maxima: moved only when a score passes them by more than kMaxSlack.
+      // The references move only when a score (a scale) passes them by more than the slack.
       bool move = fmaxf(vda, vdb) > kRefSlack * ref;
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        move |= fmaxf(c[n][0], c[n][2]) > m[n][0] + kMaxSlack;
-        move |= fmaxf(c[n][1], c[n][3]) > m[n][1] + kMaxSlack;
+        move |= fmaxf(c[n][0], c[n][2]) > bar[n][0];
+        move |= fmaxf(c[n][1], c[n][3]) > bar[n][1];
       }
       if (__any_sync(kFullMask, move)) {
         const float top = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(fmaxf(vda, vdb))));
         const float new_ref = fmaxf(ref, top);
         const float rescale = new_ref > 0.0f ? ref / new_ref : 1.0f;
         ref = new_ref;
+        inv_ref = ref > 0.0f ? kWeightScale / ref : 0.0f;
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
@@ -498,9 +577,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
             float y = fmaxf(c[n][i], c[n][2 + i]);
 #pragma unroll
             for (int w2 = 4; w2 < 32; w2 <<= 1) y = fmaxf(y, __shfl_xor_sync(kFullMask, y, w2));
-            const float new_m = fmaxf(m[n][i], y);
-            const float f = new_m == -kInf ? 1.0f : ex2(m[n][i] - new_m);
-            m[n][i] = new_m;
+            float f = 1.0f;
+            if (y > bar[n][i] - kMaxSlack) {  // new maximum (bar - slack is -inf at first)
+              f = bar[n][i] == -kInf ? 0.0f : ex2(m[n][i] - y);
+              m[n][i] = y;
+              bar[n][i] = y + kMaxSlack;
+            }
             l[n][i] *= f;
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
@@ -509,14 +591,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
             }
           }
       }
-      const float wa2 = ref > 0.0f ? vda * (kWeightScale / ref) : 0.0f;
-      const float wb2 = ref > 0.0f ? vdb * (kWeightScale / ref) : 0.0f;
+      const float wa2 = vda * inv_ref, wb2 = vdb * inv_ref;
       uint32_t p0[kNT], p1[kNT], e0[kNT], e1[kNT];
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        const float m0 = m[n][0] == -kInf ? 0.0f : m[n][0], m1 = m[n][1] == -kInf ? 0.0f : m[n][1];
-        const float x0 = ex2(c[n][0] - m0), x1 = ex2(c[n][1] - m1);
-        const float x2 = ex2(c[n][2] - m0), x3 = ex2(c[n][3] - m1);
+        const float x0 = ex2(c[n][0] - m[n][0]), x1 = ex2(c[n][1] - m[n][1]);
+        const float x2 = ex2(c[n][2] - m[n][0]), x3 = ex2(c[n][3] - m[n][1]);
         l[n][0] += x0 + x2;
         l[n][1] += x1 + x3;
         const float y0 = x0 * wa2, y1 = x1 * wa2, y2 = x2 * wb2, y3 = x3 * wb2;
@@ -532,19 +612,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
 
       // O^T: operand rows g, g + 8 of tile 2w (2w + 1) are dims 4w, 4w+1 (4w+2, 4w+3) of this
       // lane's run of dims; keys 2t, 2t+1 of the operand are key_of(2t), key_of(2t+1).
-      const int k0 = key_of<kD>(2 * t4), k1 = key_of<kD>(2 * t4 + 1);
 #pragma unroll
       for (int q = 0; q < (kD + 127) / 128; ++q) {
         constexpr int kWords = kD == 64 ? 2 : 4;
         uint32_t v[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int k = (i & 1 ? k1 : k0) + (i & 2 ? 8 : 0);
+          const uint32_t from = read_at + (i & 1 ? v_src1 : v_src0) + (i & 2 ? 8 * kD : 0) + q * 128;
           if (kD == 64) {
-            const uint32_t at2 = vbase + v_place<kD>(k, g >> 1) + (g & 1) * 8;
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(at2));
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(from));
           } else {
-            const uint4 y = lds_v4(vbase + v_place<kD>(k, 8 * q + g));
+            const uint4 y = lds_v4(from);
             v[i][0] = y.x; v[i][1] = y.y; v[i][2] = y.z; v[i][3] = y.w;
           }
         }
@@ -555,21 +633,33 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
             const uint32_t sel = half ? 0x7632u : 0x5410u;
             const uint32_t z0 = __byte_perm(v[0][w2], v[1][w2], sel);
             const uint32_t z1 = __byte_perm(v[2][w2], v[3][w2], sel);
-            const uint32_t a0 = even_bytes(z0), a1 = odd_bytes(z0);
-            const uint32_t a2 = even_bytes(z1), a3 = odd_bytes(z1);
             const int tile = (q * kWords + w2) * 2 + half;
+            if (Sh::kRaisedV) {
+              constexpr uint32_t kLower = 0x80808080u;  // -128 * 2^-24, twice
+              mma_16816(o[tile][0], kLower, kLower, kLower, kLower, p0[0], p1[0]);
+              mma_16816(o[tile][0], even_raised(z0), odd_raised(z0), even_raised(z1), odd_raised(z1),
+                        p0[0], p1[0]);
+            } else {
+              const uint32_t a0 = even_bytes(z0), a1 = odd_bytes(z0);
+              const uint32_t a2 = even_bytes(z1), a3 = odd_bytes(z1);
 #pragma unroll
-            for (int n = 0; n < kNT; ++n) {
-              mma_16816(o[tile][n], a0, a1, a2, a3, p0[n], p1[n]);
-              if (kPair) mma_16816(o[tile][n], a0, a1, a2, a3, e0[n], e1[n]);
+              for (int n = 0; n < kNT; ++n) {
+                mma_16816(o[tile][n], a0, a1, a2, a3, p0[n], p1[n]);
+                if (kPair) mma_16816(o[tile][n], a0, a1, a2, a3, e0[n], e1[n]);
+              }
             }
           }
         }
       }
       __syncwarp();
-      const int32_t p = next_page;
-      next_page = page_of(s + Sh::kStages);
-      issue(s + Sh::kStages - 1, p);
+      issue();
+      look_up();
+      key += kTile;
+      read_at += Sh::kStage;
+      if (++read_slot == Sh::kStages) {
+        read_slot = 0;
+        read_at = my_ring;
+      }
     }
     cp_wait<0>();
 
@@ -581,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
 #pragma unroll
         for (int w2 = 4; w2 < 32; w2 <<= 1) l[n][i] += __shfl_xor_sync(kFullMask, l[n][i], w2);
         if (g == 0) {
-          warp_m[warp * kRows + 8 * n + 2 * t4 + i] = m[n][i];
+          warp_m[warp * kRows + 8 * n + 2 * t4 + i] = bar[n][i] == -kInf ? -kInf : m[n][i];
           warp_l[warp * kRows + 8 * n + 2 * t4 + i] = l[n][i];
         }
       }
@@ -602,7 +692,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         const int r = 8 * n + 2 * t4 + i;
         float top = -kInf;
         for (int k = 0; k < kWarps; ++k) top = fmaxf(top, warp_m[k * kRows + r]);
-        const float f = m[n][i] > -kInf ? ex2(m[n][i] - top) * ref * (1.0f / kWeightScale) : 0.0f;
+        const float f = bar[n][i] == -kInf ? 0.0f
+                                            : ex2(m[n][i] - top) * ref *
+                                                  ((Sh::kRaisedV ? 0x1p24f : 1.0f) / kWeightScale);
         constexpr int kRun = kD == 64 ? 8 : 16;  // consecutive dims of a lane
 #pragma unroll
         for (int j = 0; j < kSteps / 2; ++j) {
@@ -614,9 +706,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
       }
     __syncthreads();
 
-    const bool whole = x == unit_at && x_stop == unit_stop;
+    const bool whole = begins && x_stop == unit_stop;
     const int part_size = kRows * (kD + 2);
-    float* mine = a.parts + (int64_t)(2 * cta + (x == unit_at ? 1 : 0)) * part_size;
+    float* mine = a.parts + (int64_t)(2 * cta + (begins ? 1 : 0)) * part_size;
     T* out = static_cast<T*>(a.out);
     for (int i = tid; i < kRows * kD / 4; i += kThreads) {
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -644,7 +736,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         __stcg(mine + tid, row_m[tid]);
         __stcg(mine + kRows + tid, row_l[tid]);
       }
-      const int c0 = (int)(((unit_at + 1) * ctas - 1) / total), c1 = (int)((unit_stop * ctas - 1) / total);
+      // the CTAs that hold the unit's first and last tile
+      const int c0 = (int)(((unit_at + kUnitCost + 1) * ctas - 1) / total), c1 = (int)((unit_stop * ctas - 1) / total);
       __threadfence();
       __syncthreads();
       if (tid == 0) {
@@ -772,7 +865,7 @@ cudaError_t launch_shape(const AttnArgs& a, const DeviceInfo& info, int64_t max_
 template <typename T>
 cudaError_t launch_attention(const AttnArgs& a, int D, const DeviceInfo& info, cudaStream_t stream) {
   const int64_t rows = a.B > 0 ? (a.T * a.G + a.B - 1) / a.B : 1;
-  const int64_t max_tiles = a.max_pages * a.page / kTile + 1;
+  const int64_t max_tiles = a.max_pages * a.page / kTile + 1 + kUnitCost;
   if (D == 64) {
     if (rows <= 8) return launch_shape<T, 64, 1>(a, info, max_tiles, stream);
     if (rows <= 16) return launch_shape<T, 64, 2>(a, info, max_tiles, stream);
@@ -809,6 +902,7 @@ extern "C" memra_status memra_kv_attention_q8(
   if (page_size > MEMRA_MAX_KV_PAGE || Hkv > 65535 || n_pages > INT32_MAX / page_size ||
       max_pages > INT32_MAX / page_size || T > INT32_MAX / Hq || B > (1 << 24))
     return MEMRA_ERR_UNSUPPORTED;
+  if (Hkv * page_size * D > (int64_t)UINT32_MAX) return MEMRA_ERR_UNSUPPORTED;
   if (T == 0) return MEMRA_OK;
   if (!q || !out || !workspace || !cu_q) return MEMRA_ERR_INVALID_ARG;
   if (B > 0 && (!kv_lens || (max_pages > 0 && !block_table))) return MEMRA_ERR_INVALID_ARG;
@@ -844,6 +938,10 @@ extern "C" memra_status memra_kv_attention_q8(
   a.page = (int)page_size;
   a.block = (int)block;
   a.block_magic = (uint32_t)(((1u << 22) + block - 1) / block);
+  a.page_bytes = (uint32_t)(Hkv * page_size * D);
+  a.page_scales = (uint32_t)(Hkv * (page_size / block));
+  a.step_pages = kTile / (int)page_size;
+  a.step_off = kTile % (int)page_size;
   a.scale = scale;
   a.out = out;
   a.lse = lse;
