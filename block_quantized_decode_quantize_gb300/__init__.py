@@ -17,6 +17,7 @@ Tensor conventions (all on one CUDA device, contiguous):
   y   float32 [M, N]       (the GEMV takes and returns 1-D x / y)
 """
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -840,8 +841,29 @@ def memra_q8_0_block_dots(wq, xq, s=None):
 
 
 # The entry points below run many times a decode step on small data, where the time of the
-# call itself counts: their checks try the whole condition first and look for what is wrong
-# only when it fails.
+# call itself counts.  Each goes through the extension module _memra_binding first
+# (csrc/binding.cpp), which makes the same checks in C++ and calls the same C entry point;
+# where that finds anything unusual it returns None, and the long way here names the error
+# or handles the case.
+
+_fast = None
+
+
+def _binding():
+    """The extension module with the quick paths (built and loaded with the library)."""
+    global _fast
+    if _fast is None:
+        lib()
+        path = _build.BINDING
+        if not os.path.exists(path):
+            raise RuntimeError("_memra_binding.so is not built (expected at %s); run "
+                               "block_quantized_decode_quantize_gb300.build.build()" % path)
+        spec = importlib.util.spec_from_file_location("_memra_binding", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _fast = mod
+    return _fast
+
 
 def _ok(t, name, dtype, dev, shape):
     """_need for a contiguous tensor on CUDA device number `dev`."""
@@ -919,6 +941,11 @@ def memra_kv_plan(ctx_lens, new_lens, page_size, free_pages, block_table, num_to
     are written in place), free_head int32 [1] or None (start of the unused free pages).
     Returns kv_lens [B], cu_q [B+1], slots [num_tokens], positions [num_tokens] and
     free_head_out [1], all int32.  free_head_out may be free_head, to advance it in place."""
+    if kv_lens is None and cu_q is None and slots is None and positions is None:
+        done = (_fast or _binding()).plan(ctx_lens, new_lens, page_size, free_pages, block_table,
+                                          num_tokens, free_head, free_head_out, dev_status)
+        if done is not None:
+            return done
     if not isinstance(ctx_lens, torch.Tensor) or not ctx_lens.is_cuda or ctx_lens.dim() != 1:
         raise ValueError("ctx_lens must be a 1-D CUDA tensor")
     dev, B, T = ctx_lens.get_device(), ctx_lens.shape[0], int(num_tokens)
@@ -973,6 +1000,8 @@ def memra_kv_append_q8(k, v, slots, kq, kd, vq, vd, dev_status=None):
     bytes' multiples with the last dimension dense, so columns of a fused projection's rows
     will do), slots int32 [T] (-1: left out).  kq, vq int8 [pages, Hkv, page, D] and kd, vd
     float32 [pages, Hkv, page / block] are updated in place."""
+    if (_fast or _binding()).append(k, v, slots, kq, kd, vq, vd, dev_status):
+        return
     dev, n_pages, Hkv, page, D, block = _cache(kq, kd, vq, vd)
     dt = _rows(k, "k", dev, 3)
     T = k.shape[0]
@@ -993,6 +1022,11 @@ def memra_kv_read_q8(slots, kq, kd, vq, vd, dtype=torch.bfloat16, k=None, v=None
                      dev_status=None):
     """Read cached tokens back as values: slots int32 [N] -> k, v [N, Hkv, D] of `dtype`
     (bfloat16 or float32); zeros where a slot is -1."""
+    if k is None and v is None and (dtype is torch.bfloat16 or dtype is torch.float32):
+        done = (_fast or _binding()).read(slots, kq, kd, vq, vd, dtype is torch.bfloat16,
+                                          dev_status)
+        if done is not None:
+            return done
     dev, n_pages, Hkv, page, D, block = _cache(kq, kd, vq, vd)
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a 1-D tensor")
@@ -1028,6 +1062,11 @@ def memra_kv_attention_q8(q, kq, kd, vq, vd, block_table, kv_lens, cu_q, scale=N
     [T, Hq].  `workspace` (uint8, KV_ATTENTION_WORKSPACE_BYTES, zeroed once before its first
     use) should be kept from call to call, one a stream; without one a call takes and clears
     its own."""
+    if out is None and lse is None and workspace is not None and scale is not None:
+        done = (_fast or _binding()).attention(q, kq, kd, vq, vd, block_table, kv_lens, cu_q,
+                                               scale, window, workspace, dev_status)
+        if done is not None:
+            return done
     dev, n_pages, Hkv, page, D, block = _cache(kq, kd, vq, vd)
     dt = _rows(q, "q", dev, 3)
     T, Hq, qD = q.shape
@@ -1076,6 +1115,11 @@ def memra_moe_route(logits, top_k, bias=None, score="softmax", n_groups=1, topk_
     routed products take them.  score "softmax" or "sigmoid"; bias float32 [E] is added for
     the ranking only; with n_groups > 1 only the topk_groups best groups stay, a group
     ranked by its group_top (1 or 2) best experts' sum."""
+    if ids is None and gate_w is None:
+        done = (_fast or _binding()).route(logits, top_k, bias, _SCORES.get(score, -1), n_groups,
+                                           topk_groups, group_top, renormalize, scale)
+        if done is not None:
+            return done
     dev = logits.get_device() if isinstance(logits, torch.Tensor) else -1
     dt = _rows(logits, "logits", dev, 2)
     T, E = logits.shape

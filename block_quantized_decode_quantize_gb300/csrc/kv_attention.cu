@@ -45,6 +45,11 @@ constexpr int kMaxCtas = 512;              // arrival counters at the workspace'
 constexpr int kUnitCost = MEMRA_ATTN_UNIT_COST;  // list entries that stand for a unit's fixed time
 constexpr int kMinShare = MEMRA_ATTN_MIN_SHARE;  // list entries that a CTA gets at least
 
+#ifndef MEMRA_ATTN_MAX_PARTS
+#define MEMRA_ATTN_MAX_PARTS 64
+#endif
+constexpr int kMaxParts = MEMRA_ATTN_MAX_PARTS;  // CTAs to a unit, on average
+
 // A weight enters the product as p * (vd / ref) * 2^8 in fp16, ref a running maximum of vd
 // kept within a factor 4, p = 2^(s - m) with m within 5 of the running maximum: at most
 // 2^(5 + 2 + 8) = 2^15, and down to 2^-33 of the largest before it rounds to zero.
@@ -68,7 +73,7 @@ struct AttnArgs {
   void* out;
   float* lse;
   int* arrived;   // [kMaxCtas], zero between calls
-  float* parts;   // [2 * CTAs][rows * (D + 2)]
+  float* parts;   // [2][CTAs][rows * (D + 2)]
   int32_t* status;
 };
 
@@ -190,8 +195,10 @@ struct Shape {
 // Where a request's part of the list lies, from its lengths.
 struct Request {
   int len, n;        // tokens in the cache, queries
+  int row;           // the first query's row of q
   int lo;            // first key tile's start
   int tiles, groups;
+  bool over;         // longer than its row of the block table
 };
 
 template <int kRows>
@@ -199,11 +206,14 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int64_t b) {
   Request r;
   const int64_t cap = a.max_pages * a.page;
   int64_t len = a.kv_lens[b];
+  const int row = a.cu_q[b];
+  r.over = len > cap;
   len = len < 0 ? 0 : (len > cap ? cap : len);
-  int64_t n = (int64_t)a.cu_q[b + 1] - a.cu_q[b];
+  int64_t n = (int64_t)a.cu_q[b + 1] - row;
   n = n < 0 ? 0 : (n > a.T ? a.T : n);
   r.len = (int)len;
   r.n = (int)n;
+  r.row = row;
   int64_t lo = a.window > 0 ? len - n + 1 - a.window : 0;
   lo = lo < 0 ? 0 : lo / kStrip * kStrip;
   r.lo = (int)lo;
@@ -211,6 +221,34 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int64_t b) {
   r.groups = (int)((n * a.G + kRows - 1) / kRows);
   return r;
 }
+
+// total entries in ctas equal parts (the first ones one longer): where part c begins, and
+// which part holds entry x.
+struct Cut {
+  int64_t total, q, r;
+  static __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+  }
+  __device__ __forceinline__ Cut(int64_t t, int ctas) : total(t), q(divide(t, ctas)), r(t - q * ctas) {}
+  __device__ __forceinline__ int64_t begin(int c) const { return c * q + min((int64_t)c, r); }
+  __device__ __forceinline__ int part_of(int64_t x) const {
+    const int64_t longer = r * (q + 1);
+    return (int)(x < longer ? divide(x, q + 1) : r + divide(x - longer, q));
+  }
+};
+
+// What a CTA keeps in shared memory while its strips want the registers: where it stands in
+// the list, and the unit at hand.
+struct Walk {
+  int64_t x, at, stop;
+  int b;
+  Request req;
+};
+struct Unit {
+  int h, row0, rows, token0;
+  int first_cta, parts;  // CTAs that hold a part of it
+  int begins, whole;
+};
 
 template <typename T, int kD>
 __device__ __forceinline__ void write_nothing(const AttnArgs& a, int64_t row0, int64_t row1,
@@ -245,6 +283,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
   int* row_limit = reinterpret_cast<int*>(row_raise + kRows);
   __shared__ int64_t scan[kWarps], found_at;
   __shared__ int found_b, last_part;
+  __shared__ Request found;
+  __shared__ Walk walk;
+  __shared__ Unit unit_at_hand;
 
   pdl_launch_dependents();
   pdl_wait();
@@ -257,67 +298,111 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
   auto entries_of = [&](const Request& r) {
     return r.tiles > 0 ? (int64_t)(r.tiles + kUnitCost) * r.groups * a.Hkv : (int64_t)0;
   };
-  int64_t total = 0, first = 0, stop = 0, w = 0, sum = 0;
+  int64_t total = 0, first = 0, w = 0, sum = 0;
   int ctas = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t before = 0;
-    for (int64_t base = 0; base < a.B; base += kThreads) {
-      const int64_t b = base + tid;
-      if (pass == 0 || a.B > kThreads) {  // one chunk's sums stay in registers
-        w = 0;
-        bool empty = false;
-        if (b < a.B) {
-          const Request r = request_of<kRows>(a, b);
-          w = entries_of(r);
-          empty = w == 0 && r.n > 0;
-          if (pass == 0 && cta == 0 && a.status != nullptr &&
-              a.kv_lens[b] > a.max_pages * a.page)
-            atomicOr(a.status, 1);
-        }
-        if (pass == 0) {  // rows of requests without keys, each request by one CTA
-          uint32_t todo = __ballot_sync(kFullMask, empty && b % gridDim.x == cta);
-          while (todo != 0) {
-            const int64_t e = base + warp * 32 + (__ffs(todo) - 1);
-            todo &= todo - 1;
-            write_nothing<T, kD>(a, a.cu_q[e], a.cu_q[e + 1], lane, 32);
-          }
-        }
-        sum = w;
+  Request r{};
+  int64_t no_row = a.B > 0 ? a.cu_q[a.B] : 0;  // first row that no request owns
+  int b;
+  int64_t at;  // list index of request b's first entry
+  Request req;
+  if (a.B <= 32) {
+    // a lane to a request, every warp for itself: no barrier
+    if (lane < a.B) {
+      r = request_of<kRows>(a, lane);
+      w = entries_of(r);
+      if (cta == 0 && warp == 0 && r.over && a.status != nullptr) atomicOr(a.status, 1);
+    }
+    sum = w;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t u = __shfl_up_sync(kFullMask, sum, o);
-          if (lane >= o) sum += u;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(kFullMask, sum, o);
+      if (lane >= o) sum += u;
+    }
+    total = __shfl_sync(kFullMask, sum, 31);
+    const uint32_t empty = __ballot_sync(kFullMask, w == 0 && r.n > 0);
+    for (uint32_t todo = empty; todo != 0; todo &= todo - 1) {
+      const int e = __ffs(todo) - 1;
+      if (e % gridDim.x == cta) write_nothing<T, kD>(a, a.cu_q[e], a.cu_q[e + 1], tid, kThreads);
+    }
+    ctas = (int)min((int64_t)gridDim.x, (total + kMinShare - 1) / kMinShare);
+    for (no_row += cta; no_row < a.T; no_row += gridDim.x)
+      write_nothing<T, kD>(a, no_row, no_row + 1, tid, kThreads);
+    if (cta >= ctas) return;
+    first = Cut(total, ctas).begin(cta);
+    b = __ffs(__ballot_sync(kFullMask, w > 0 && sum - w <= first && first < sum)) - 1;
+    at = __shfl_sync(kFullMask, sum - w, b);
+    req.len = __shfl_sync(kFullMask, r.len, b);
+    req.n = __shfl_sync(kFullMask, r.n, b);
+    req.row = __shfl_sync(kFullMask, r.row, b);
+    req.lo = __shfl_sync(kFullMask, r.lo, b);
+    req.tiles = __shfl_sync(kFullMask, r.tiles, b);
+    req.groups = __shfl_sync(kFullMask, r.groups, b);
+  } else {
+    for (int pass = 0; pass < 2; ++pass) {
+      int64_t before = 0;
+      for (int64_t base = 0; base < a.B; base += kThreads) {
+        const int64_t b = base + tid;
+        if (pass == 0 || a.B > kThreads) {  // one chunk's sums stay in registers
+          w = 0;
+          bool empty = false;
+          if (b < a.B) {
+            r = request_of<kRows>(a, b);
+            w = entries_of(r);
+            empty = w == 0 && r.n > 0;
+            if (pass == 0 && cta == 0 && r.over && a.status != nullptr) atomicOr(a.status, 1);
+          }
+          if (pass == 0) {  // rows of requests without keys, each request by one CTA
+            uint32_t todo = __ballot_sync(kFullMask, empty && b % gridDim.x == cta);
+            while (todo != 0) {
+              const int64_t e = base + warp * 32 + (__ffs(todo) - 1);
+              todo &= todo - 1;
+              write_nothing<T, kD>(a, a.cu_q[e], a.cu_q[e + 1], lane, 32);
+            }
+          }
+          sum = w;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(kFullMask, sum, o);
+            if (lane >= o) sum += u;
+          }
+          if (lane == 31) scan[warp] = sum;
+          __syncthreads();
+          int64_t chunk = 0;
+          for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) sum += scan[i];
+            chunk += scan[i];
+          }
+          sum += before;
+          before += chunk;
         }
-        if (lane == 31) scan[warp] = sum;
+        if (pass == 1 && w > 0 && sum - w <= first && first < sum) {
+          found_b = (int)b;
+          found_at = sum - w;
+          found = r;
+        }
         __syncthreads();
-        int64_t chunk = 0;
-        for (int i = 0; i < kWarps; ++i) {
-          if (i < warp) sum += scan[i];
-          chunk += scan[i];
-        }
-        sum += before;
-        before += chunk;
       }
-      if (pass == 1 && w > 0 && sum - w <= first && first < sum) {
-        found_b = (int)b;
-        found_at = sum - w;
+      if (pass == 0) {
+        total = before;
+        ctas = (int)min((int64_t)gridDim.x, (total + kMinShare - 1) / kMinShare);
+        // rows that no request owns
+        for (no_row += cta; no_row < a.T; no_row += gridDim.x)
+          write_nothing<T, kD>(a, no_row, no_row + 1, tid, kThreads);
+        if (cta >= ctas) return;
+        first = Cut(total, ctas).begin(cta);
       }
-      __syncthreads();
     }
-    if (pass == 0) {
-      total = before;
-      ctas = (int)min((int64_t)gridDim.x, (total + kMinShare - 1) / kMinShare);
-      // rows that no request owns
-      for (int64_t row = (a.B > 0 ? a.cu_q[a.B] : 0) + cta; row < a.T; row += gridDim.x)
-        write_nothing<T, kD>(a, row, row + 1, tid, kThreads);
-      if (cta >= ctas) return;
-      first = total * cta / ctas;
-      stop = total * (cta + 1) / ctas;
-    }
+    b = found_b;
+    at = found_at;
+    req = found;
   }
-  int b = found_b;
-  int64_t at = found_at;  // list index of request b's first tile
-  Request req = request_of<kRows>(a, b);
+  if (tid == 0) {
+    walk.x = first;
+    walk.at = at;
+    walk.stop = Cut(total, ctas).begin(cta + 1);
+    walk.b = b;
+    walk.req = req;
+  }
 
   const uint32_t my_ring = smem_addr(ring) + warp * Sh::kStages * Sh::kStage;
   // Lane constants of the ring: where this lane's 16 bytes of a copy go (row i * 512 bytes
@@ -332,8 +417,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
   const uint32_t v_src1 = kStrip * kD + (kD == 64 ? v_place<kD>(vk1, g >> 1) + (g & 1) * 8 : v_place<kD>(vk1, g));
   const int64_t v_minus_k = a.vq - a.kq;
 
-  int64_t x = first;
-  while (x < stop) {
+  for (;;) {
+    __syncthreads();  // the ring, the queries and the statistics are free again
+    const int64_t x = walk.x, stop = walk.stop;
+    if (x >= stop) break;
+    at = walk.at;
+    b = walk.b;
+    req = walk.req;
     w = entries_of(req);
     while (x >= at + w) {
       at += w;
@@ -342,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
     }
     // ---- this unit: cached head h, rows [row0, row0 + kRows) of the request's n * G ----
     const int unit_size = req.tiles + kUnitCost;
-    const int unit = (int)((x - at) / unit_size);
+    const int unit = (int)Cut::divide(x - at, unit_size);
     const int64_t unit_at = at + (int64_t)unit * unit_size;
     const int64_t unit_stop = unit_at + unit_size;
     const int64_t x_stop = unit_stop < stop ? unit_stop : stop;
@@ -352,22 +442,103 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
     const bool begins = tile0 == 0;
     const int h = unit / req.groups, row0 = unit % req.groups * kRows;
     const int rows = min(kRows, req.n * a.G - row0);
-    const int token0 = a.cu_q[b];
+    const int token0 = req.row;
+    // Keys that the first and the last row see end here; those below low_max are hidden
+    // from the last row (window).
+    const int limit_min = min(req.len, req.len - req.n + row0 / a.G + 1);
+    const int limit_max = min(req.len, req.len - req.n + (row0 + rows - 1) / a.G + 1);
+    const int low_max = a.window > 0 ? (int)max((int64_t)0, limit_max - a.window) : 0;
+
+    // This warp's query rows (row r = warp + 8 j) on their way to registers.
+    constexpr int kPer = kD / 32;
+    float qv[kNT][kPer];
+#pragma unroll
+    for (int j = 0; j < kNT; ++j) {
+      const int r = warp + kWarps * j;
+      const int64_t token = token0 + (row0 + r) / a.G;
+      const bool real = r < rows && token >= 0 && token < a.T;
+      const T* src = static_cast<const T*>(a.q) +
+                     (real ? token * a.stride_t + (h * a.G + (row0 + r) % a.G) * a.stride_h : 0);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) qv[j][k] = real ? value(src + k * 32 + lane) : 0.0f;
+    }
+
+    // ---- the warp's strips: keys key, key + kTile, ... below key_stop ----
+    int key = req.lo + tile0 * kTile + warp * kStrip;
+    const int key_stop = min(req.lo + tile1 * kTile, limit_max);
+    const int strips = key < key_stop ? (key_stop - key + kTile - 1) / kTile : 0;
+    const int32_t* pages = a.table + (int64_t)b * a.max_pages;
+    const int8_t* k_head = a.kq + (int64_t)h * a.page * kD + lane * 16;
+    const float* scale_head = (lane < 16 ? a.kd : a.vd) + (int64_t)h * (a.page / a.block);
+    uint32_t hidden = 0;  // bit i: stage i's strip has no page
+    // The page of a strip is looked up one strip before its copies are issued (those of the
+    // first strips at once).
+    int look = 0, look_at = key / a.page, look_off = key % a.page;
+    int issued = 0, write_slot = 0;
+    uint32_t write_at = my_ring;
+
+    auto look_up = [&](int32_t& page, int& off) {
+      off = look_off;
+      page = look < strips ? pages[look_at] : 0;
+      ++look;
+      look_at += a.step_pages;
+      look_off += a.step_off;
+      if (look_off >= a.page) {
+        look_off -= a.page;
+        ++look_at;
+      }
+    };
+    auto issue = [&](int32_t page, int off) {
+      if (issued++ < strips) {
+        if ((uint32_t)page < (uint32_t)a.n_pages) {
+          const int8_t* src = k_head + (uint64_t)(uint32_t)page * a.page_bytes + off * kD;
+          const int8_t* src_v = src + v_minus_k;
+          const uint32_t kd0 = write_at + k_dst, vd0 = write_at + v_dst;
+#pragma unroll
+          for (int i = 0; i < kStrip * kChunks / 32; ++i) {
+            constexpr uint32_t kNone = 0;
+            const uint32_t xk = kD == 64 ? kNone : kD == 128 ? (i & 1) * 64u : (i & 3) * 32u;
+            const uint32_t xv = kD == 64 ? kNone
+                                         : kD == 128 ? (i & 1) * 16u
+                                                     : ((i & 1) * 4u + ((i >> 1) & 1)) * 16u;
+            cp16((kd0 ^ xk) + i * 512, src + i * 512);
+            cp16((vd0 ^ xv) + i * 512, src_v + i * 512);
+          }
+          cp4(write_at + 2 * kStrip * kD + lane * 4,
+              scale_head + (uint64_t)(uint32_t)page * a.page_scales +
+                  (((uint32_t)(off + (lane & 15)) * a.block_magic) >> 22));
+        } else {
+          hidden |= 1u << write_slot;
+          if (lane == 0 && a.status != nullptr) atomicOr(a.status, 1);
+        }
+      }
+      cp_commit();
+      write_at += Sh::kStage;
+      if (++write_slot == Sh::kStages) {
+        write_slot = 0;
+        write_at = my_ring;
+      }
+    };
+
+    int32_t page[Sh::kStages];
+    int off[Sh::kStages];
+#pragma unroll
+    for (int s = 0; s < Sh::kStages; ++s) look_up(page[s], off[s]);
+#pragma unroll
+    for (int s = 0; s < Sh::kStages - 1; ++s) issue(page[s], off[s]);
+    int32_t next_page = page[Sh::kStages - 1];
+    int next_off = off[Sh::kStages - 1];
 
     // Queries to shared memory as B operands: row r of tile r / 8 is operand column r % 8;
     // k index (2i, 2i+1, 2i+8, 2i+9) of step 4c+w is dim 64c + 16i + 4w + (0, 2, 1, 3).
     // Each row is scaled by a power of two that brings its largest value to [2^13, 2^14).
-    for (int r = warp; r < kRows; r += kWarps) {
-      const int i = (row0 + r) / a.G, hq = h * a.G + (row0 + r) % a.G;
-      const bool real = r < rows && token0 + i >= 0 && token0 + i < a.T;
-      const T* src = static_cast<const T*>(a.q) + (real ? (token0 + i) * a.stride_t + hq * a.stride_h : 0);
-      constexpr int kPer = kD / 32;
-      float v[kPer], amax = 0.0f;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        v[j] = real ? value(src + j * 32 + lane) : 0.0f;
-        amax = fmaxf(amax, fabsf(v[j]));
-      }
+    for (int row_step = 0; row_step < kNT; ++row_step) {
+      const int r = warp + kWarps * row_step, i = (row0 + r) / a.G;
+      const float* v = qv[row_step];
+      float amax = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) amax = fmaxf(amax, fabsf(v[j]));
       amax = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(amax)));
       int e = (int)(__float_as_uint(amax) >> 23) - 127;
       e = e < -100 ? -100 : e;
@@ -402,6 +573,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
       if (lane == 0) row_raise[r] = -128.0f * 0x1p-24f * sum_q;
     }
     __syncthreads();
+    if (tid == 0) {
+      const Cut cut(total, ctas);
+      const bool whole = begins && x_stop == unit_stop;
+      const int c0 = whole ? cta : cut.part_of(unit_at + kUnitCost);
+      const int c1 = whole ? cta : cut.part_of(unit_stop - 1);
+      unit_at_hand = {h, row0, rows, token0, c0, c1 - c0 + 1, begins, whole};
+      walk.x = x_stop;
+      walk.at = at;
+      walk.b = b;
+      walk.req = req;
+    }
     float qs[kNT][2], raise[kNT][2];
     int limit[kNT][2];
 #pragma unroll
@@ -412,9 +594,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         raise[n][c] = row_raise[8 * n + 2 * t4 + c];
         limit[n][c] = row_limit[8 * n + 2 * t4 + c];
       }
-    const int limit_min = row_limit[0], limit_max = row_limit[rows - 1];
-    // keys below this are hidden from the last row (window)
-    const int low_max = a.window > 0 ? (int)max((int64_t)0, limit_max - a.window) : 0;
 
     // m: the reference that weights are taken against (0 while a row has seen no key);
     // bar: m + kMaxSlack (-inf then).
@@ -434,70 +613,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         for (int c = 0; c < 4; ++c) o[i][n][c] = 0.0f;
     }
 
-    // ---- the warp's strips: keys key, key + kTile, ... below key_stop ----
-    int key = req.lo + tile0 * kTile + warp * kStrip;
-    const int key_stop = min(req.lo + tile1 * kTile, limit_max);
-    const int strips = key < key_stop ? (key_stop - key + kTile - 1) / kTile : 0;
-    const int32_t* pages = a.table + (int64_t)b * a.max_pages;
-    const int8_t* k_head = a.kq + (int64_t)h * a.page * kD + lane * 16;
-    const float* scale_head = (lane < 16 ? a.kd : a.vd) + (int64_t)h * (a.page / a.block);
-    uint32_t hidden = 0;  // bit i: stage i's strip has no page
-    // The page of a strip is looked up one strip before its copies are issued.
-    int look = 0, look_at = key / a.page, look_off = key % a.page;
-    int issue_off = 0, write_slot = 0;
-    uint32_t write_at = my_ring;
-    int32_t page = 0;
-
-    auto look_up = [&]() {
-      issue_off = look_off;
-      if (look < strips) page = pages[look_at];
-      ++look;
-      look_at += a.step_pages;
-      look_off += a.step_off;
-      if (look_off >= a.page) {
-        look_off -= a.page;
-        ++look_at;
-      }
-    };
-    auto issue = [&]() {  // the strip looked up last, if there was one
-      if (look <= strips) {
-        if ((uint32_t)page < (uint32_t)a.n_pages) {
-          const int8_t* src = k_head + (uint64_t)(uint32_t)page * a.page_bytes + issue_off * kD;
-          const int8_t* src_v = src + v_minus_k;
-          const uint32_t kd0 = write_at + k_dst, vd0 = write_at + v_dst;
-#pragma unroll
-          for (int i = 0; i < kStrip * kChunks / 32; ++i) {
-            constexpr uint32_t kNone = 0;
-            const uint32_t xk = kD == 64 ? kNone : kD == 128 ? (i & 1) * 64u : (i & 3) * 32u;
-            const uint32_t xv = kD == 64 ? kNone
-                                         : kD == 128 ? (i & 1) * 16u
-                                                     : ((i & 1) * 4u + ((i >> 1) & 1)) * 16u;
-            cp16((kd0 ^ xk) + i * 512, src + i * 512);
-            cp16((vd0 ^ xv) + i * 512, src_v + i * 512);
-          }
-          cp4(write_at + 2 * kStrip * kD + lane * 4,
-              scale_head + (uint64_t)(uint32_t)page * a.page_scales +
-                  (((uint32_t)(issue_off + (lane & 15)) * a.block_magic) >> 22));
-        } else {
-          hidden |= 1u << write_slot;
-          if (lane == 0 && a.status != nullptr) atomicOr(a.status, 1);
-        }
-      }
-      cp_commit();
-      write_at += Sh::kStage;
-      if (++write_slot == Sh::kStages) {
-        write_slot = 0;
-        write_at = my_ring;
-      }
-    };
-
-    look_up();
-#pragma unroll
-    for (int s = 0; s < Sh::kStages - 1; ++s) {
-      issue();
-      look_up();
-    }
-
     uint32_t read_at = my_ring;
     int read_slot = 0;
     for (int s = 0; s < strips; ++s) {
@@ -509,6 +624,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         c[n][0] = c[n][2] = raise[n][0];
         c[n][1] = c[n][3] = raise[n][1];
       }
+      // with one tile of rows, odd steps sum apart: two chains of products instead of one
+      float c2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int q = 0; q < kD / 64; ++q) {
         const uint32_t from = ((read_at + k_src) ^ (kD == 64 ? 0u : (q & 1) * 64u)) + (q >> 1) * 128;
@@ -522,13 +639,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
             const uint2 f = q_frag[(step * kNT + n) * 32 + lane];
-            mma_16816(c[n], a0, a1, a2, a3, f.x, f.y);
+            float* to = kNT == 1 && (i & 1) ? c2 : c[n];
+            mma_16816(to, a0, a1, a2, a3, f.x, f.y);
             if (kPair) {
               const uint2 lo = q_frag[((kSteps + step) * kNT + n) * 32 + lane];
-              mma_16816(c[n], a0, a1, a2, a3, lo.x, lo.y);
+              mma_16816(to, a0, a1, a2, a3, lo.x, lo.y);
             }
           }
         }
+      }
+
+      if (kNT == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[0][i] += c2[i];
       }
 
       // c[n]: (key a, row 2t), (key a, row 2t+1), (key b, row 2t), (key b, row 2t+1)
@@ -652,8 +775,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         }
       }
       __syncwarp();
-      issue();
-      look_up();
+      issue(next_page, next_off);
+      look_up(next_page, next_off);
       key += kTile;
       read_at += Sh::kStage;
       if (++read_slot == Sh::kStages) {
@@ -706,127 +829,117 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
       }
     __syncthreads();
 
-    const bool whole = begins && x_stop == unit_stop;
-    const int part_size = kRows * (kD + 2);
-    float* mine = a.parts + (int64_t)(2 * cta + (begins ? 1 : 0)) * part_size;
-    T* out = static_cast<T*>(a.out);
-    for (int i = tid; i < kRows * kD / 4; i += kThreads) {
+    const Unit u = unit_at_hand;
+    // Values 4i .. 4i+3 of the unit's rows, divided by their sums, to their place.
+    auto finish = [&](int i, float4 v) {
+      const int r = i * 4 / kD, d = i * 4 % kD;
+      const int64_t token = u.token0 + (u.row0 + r) / a.G;
+      if (r >= u.rows || token < 0 || token >= a.T) return;
+      const float sum_l = row_l[r], f = sum_l > 0.0f ? 1.0f / sum_l : 0.0f;
+      const int64_t row = token * a.Hq + u.h * a.G + (u.row0 + r) % a.G;
+      store4(static_cast<T*>(a.out) + row * kD + d, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+      if (a.lse != nullptr && d == 0)
+        a.lse[row] = sum_l > 0.0f ? (row_m[r] + log2f(sum_l)) * 0.693147180559945309f : -kInf;
+    };
+    constexpr int kItems = kRows * kD / 4;
+    constexpr int kPart = kRows * (kD + 2);  // m, l, values
+    float* mine = a.parts + (int64_t)((u.begins ? gridDim.x : 0) + cta) * kPart;
+    for (int i = tid; i < kItems; i += kThreads) {
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
-        const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(ring) + k * kRows * kD + i * 4);
+        const float4 y = reinterpret_cast<const float4*>(ring)[k * kItems + i];
         v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
       }
-      const int r = i * 4 / kD;
-      if (whole) {
-        const int64_t token = token0 + (row0 + r) / a.G;
-        if (r < rows && token >= 0 && token < a.T) {
-          const float f = row_l[r] > 0.0f ? 1.0f / row_l[r] : 0.0f;
-          const int64_t row = token * a.Hq + h * a.G + (row0 + r) % a.G;
-          store4(out + row * kD + i * 4 % kD, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-          if (a.lse != nullptr && i * 4 % kD == 0)
-            a.lse[row] = row_l[r] > 0.0f ? (row_m[r] + log2f(row_l[r])) * 0.693147180559945309f : -kInf;
-        }
-      } else {
-        __stcg(reinterpret_cast<float4*>(mine + 2 * kRows) + i, v);
-      }
+      if (u.whole) finish(i, v);
+      else __stcg(reinterpret_cast<float4*>(mine + 2 * kRows) + i, v);
     }
-    if (!whole) {
+    if (!u.whole) {
       if (tid < kRows) {
         __stcg(mine + tid, row_m[tid]);
         __stcg(mine + kRows + tid, row_l[tid]);
       }
-      // the CTAs that hold the unit's first and last tile
-      const int c0 = (int)(((unit_at + kUnitCost + 1) * ctas - 1) / total), c1 = (int)((unit_stop * ctas - 1) / total);
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
-        const int n = atomicAdd(a.arrived + c0, 1);
-        last_part = n == c1 - c0;
-        if (last_part) a.arrived[c0] = 0;
+        // releases the CTA's part (ordered before by the barrier), acquires the others'
+        int n;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                     : "=r"(n) : "l"(a.arrived + u.first_cta) : "memory");
+        last_part = n == u.parts - 1;
+        if (last_part) a.arrived[u.first_cta] = 0;
       }
       __syncthreads();
       if (last_part) {
-        // ---- join the unit's parts: warps take parts in turn, then each other's sums ----
-        __threadfence();
-        const int parts = c1 - c0 + 1;
-        auto part = [&](int i) { return a.parts + (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * part_size; };
+        // ---- join the unit's parts, in the order of the keys ----
+        // Part 0 is the second one of its CTA, the others are the first ones of theirs.
+        const int parts = u.parts;
+        const float* part0 = a.parts + (int64_t)(gridDim.x + u.first_cta) * kPart;
+        const float* part1 = a.parts + (int64_t)u.first_cta * kPart;
+        float* fac = reinterpret_cast<float*>(ring);  // [parts][kRows]: m, then the factor
+        float* sum_of = fac + parts * kRows;          // [parts][kRows]: l
+        // The values follow through shared memory, each thread's own ones, as many parts at a
+        // time as fit; the first are on their way while the factors are made.
+        float4* values = reinterpret_cast<float4*>(fac + (2 * parts * kRows + 3) / 4 * 4);
+        const int batch = (Sh::kBig - (2 * parts * kRows + 3) / 4 * 16) / (kItems * 16);
+        auto fetch = [&](int first_part) {
+          const int n = min(batch, parts - first_part);
+          for (int i = tid; i < kItems; i += kThreads) {
+            const uint32_t dst = smem_addr(values + i);
+            const float* src = part1 + 2 * kRows + i * 4;
+            for (int k = 0; k < n; ++k)
+              cp16(dst + k * kItems * 16,
+                   first_part + k == 0 ? part0 + 2 * kRows + i * 4 : src + (int64_t)(first_part + k) * kPart);
+          }
+          cp_commit();
+        };
+        fetch(0);
+        for (int i = tid; i < parts * kRows; i += kThreads) {
+          const float* src = (i < kRows ? part0 : part1 + (int64_t)(i / kRows) * kPart) + i % kRows;
+          fac[i] = __ldcg(src);
+          sum_of[i] = __ldcg(src + kRows);
+        }
+        __syncthreads();
         for (int r = warp; r < kRows; r += kWarps) {
-          float top = -kInf, sum = 0.0f;
-          for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(part(i) + r));
+          float top = -kInf, total_l = 0.0f;
+          for (int i = lane; i < parts; i += 32) top = fmaxf(top, fac[i * kRows + r]);
 #pragma unroll
           for (int w2 = 16; w2 > 0; w2 >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, w2));
           for (int i = lane; i < parts; i += 32) {
-            const float pm = __ldcg(part(i) + r);
-            if (pm > -kInf) sum += __ldcg(part(i) + kRows + r) * ex2(pm - top);
+            const float pm = fac[i * kRows + r];
+            const float f = pm > -kInf ? ex2(pm - top) : 0.0f;
+            fac[i * kRows + r] = f;
+            total_l += f * sum_of[i * kRows + r];
           }
 #pragma unroll
-          for (int w2 = 16; w2 > 0; w2 >>= 1) sum += __shfl_xor_sync(kFullMask, sum, w2);
+          for (int w2 = 16; w2 > 0; w2 >>= 1) total_l += __shfl_xor_sync(kFullMask, total_l, w2);
           if (lane == 0) {
             row_m[r] = top;
-            row_l[r] = sum;
+            row_l[r] = total_l;
           }
         }
         __syncthreads();
-        constexpr int kPieces = 8;  // float4 a lane holds at once: 1024 values of a part
-        for (int base = 0; base < kRows * kD; base += kPieces * 128) {
-          float4 v[kPieces];
+        float4 v[(kItems + kThreads - 1) / kThreads] = {};
+        for (int first_part = 0; first_part < parts; first_part += batch) {
+          if (first_part > 0) fetch(first_part);
+          cp_wait<0>();
+          const int n = min(batch, parts - first_part);
 #pragma unroll
-          for (int j = 0; j < kPieces; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int i = warp; i < parts; i += kWarps) {
-            const float* src = part(i);
-            float4 y[kPieces];
-            float f[kPieces];
-#pragma unroll
-            for (int j = 0; j < kPieces; ++j) {
-              const int e = base + j * 128 + lane * 4;
-              if (e < kRows * kD) {
-                y[j] = __ldcg(reinterpret_cast<const float4*>(src + 2 * kRows + e));
-                f[j] = __ldcg(src + e / kD);
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < kPieces; ++j) {
-              const int e = base + j * 128 + lane * 4;
-              if (e < kRows * kD) {
-                const float s2 = f[j] > -kInf ? ex2(f[j] - row_m[e / kD]) : 0.0f;
-                v[j].x += y[j].x * s2; v[j].y += y[j].y * s2; v[j].z += y[j].z * s2; v[j].w += y[j].w * s2;
-              }
+          for (int j = 0; j < (kItems + kThreads - 1) / kThreads; ++j) {
+            const int i = tid + j * kThreads;
+            if (i >= kItems) continue;
+#pragma unroll 2
+            for (int k = 0; k < n; ++k) {
+              const float4 y = values[k * kItems + i];
+              const float f = fac[(first_part + k) * kRows + i * 4 / kD];
+              v[j].x += y.x * f; v[j].y += y.y * f; v[j].z += y.z * f; v[j].w += y.w * f;
             }
           }
-#pragma unroll
-          for (int j = 0; j < kPieces; ++j) {
-            const int e = base + j * 128 + lane * 4;
-            if (e < kRows * kD)
-              *reinterpret_cast<float4*>(reinterpret_cast<float*>(ring) + warp * kPieces * 128 + j * 128 + lane * 4) = v[j];
-          }
-          __syncthreads();
-          for (int i = tid; i < kPieces * 32; i += kThreads) {
-            const int e = base + i * 4;
-            if (e < kRows * kD) {
-              float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-              for (int k = 0; k < kWarps; ++k) {
-                const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(ring) + k * kPieces * 128 + i * 4);
-                s4.x += y.x; s4.y += y.y; s4.z += y.z; s4.w += y.w;
-              }
-              const int r = e / kD;
-              const int64_t token = token0 + (row0 + r) / a.G;
-              if (r < rows && token >= 0 && token < a.T) {
-                const float f = row_l[r] > 0.0f ? 1.0f / row_l[r] : 0.0f;
-                const int64_t row = token * a.Hq + h * a.G + (row0 + r) % a.G;
-                store4(out + row * kD + e % kD, make_float4(s4.x * f, s4.y * f, s4.z * f, s4.w * f));
-                if (a.lse != nullptr && e % kD == 0)
-                  a.lse[row] = row_l[r] > 0.0f ? (row_m[r] + log2f(row_l[r])) * 0.693147180559945309f : -kInf;
-              }
-            }
-          }
-          __syncthreads();
         }
+#pragma unroll
+        for (int j = 0; j < (kItems + kThreads - 1) / kThreads; ++j)
+          if (tid + j * kThreads < kItems) finish(tid + j * kThreads, v[j]);
       }
     }
-    __syncthreads();  // the ring, the queries and the statistics are free again
-    x = x_stop;
   }
 }
 
@@ -852,6 +965,14 @@ cudaError_t launch_shape(const AttnArgs& a, const DeviceInfo& info, int64_t max_
                       (2 * Sh::kRows * (kD + 2) * (int64_t)sizeof(float));
   if (ctas > fit) ctas = fit;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
+  // a unit may have as many parts: their factors and one part's values at a time fit the ring
+  constexpr int kMost = (Sh::kBig - Sh::kRows * kD * 4 - 16) / (Sh::kRows * 8);
+  static_assert(kMost >= 64, "parts that can be joined");
+  if (ctas > kMost) ctas = kMost;
+  // One CTA joins a unit's parts at the rate of one SM, so few units are cut less finely.
+  const int64_t batch_rows = (a.B > 0 ? a.B : 1) * Sh::kRows;
+  const int64_t units = batch_rows / Sh::kRows * a.Hkv * ((a.T * a.G + batch_rows - 1) / batch_rows);
+  if (ctas > units * kMaxParts) ctas = units * kMaxParts;
   const int64_t groups = (a.T * a.G + Sh::kRows - 1) / Sh::kRows + a.B;
   const int64_t tiles = (max_tiles + 1) * groups * a.Hkv;  // what the list can hold at most
   if (ctas > tiles) ctas = tiles;
