@@ -8,10 +8,12 @@ namespace memra {
 namespace {
 
 // ---------------------------------------------------------------------------
-// The page plan.  One CTA scans the requests in chunks of its size (tokens and pages
-// before each request), writes the per-request outputs and the chunk's new table entries,
-// and, when the step is small, the rows' slots too; a second kernel over the whole GPU
-// fills the rows of a large step by searching cu_q.
+// The page plan.  Every CTA sums the requests' rows and pages for itself, a chunk of its
+// size at a time (two scans; the lengths come from L2, 8 bytes a request), and then fills
+// its own share of the chunk's table entries and rows: a thread finds the request of its
+// entry, or of its four rows, by bisection in shared memory.  Nothing passes between CTAs,
+// so one launch does for any size, and what bounds it is latency: launch, one read of the
+// lengths, two scans, one read of pages, one write.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 
@@ -23,48 +25,31 @@ struct PlanArgs {
   int32_t *table, *kv_lens, *cu_q, *slots, *positions, *free_head_out, *status;
 };
 
-// Inclusive sums of a and b over the CTA's threads; *ta, *tb receive the totals.
-__device__ __forceinline__ void scan2(int64_t& a, int64_t& b, int64_t* sa, int64_t* sb,
-                                      int64_t* ta, int64_t* tb) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive sum of v over the CTA's threads; *total receives the CTA's.
+__device__ __forceinline__ int64_t scan(int64_t v, int64_t* warp_sum, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t ua = __shfl_up_sync(kFullMask, a, o), ub = __shfl_up_sync(kFullMask, b, o);
-    if (lane >= o) {
-      a += ua;
-      b += ub;
-    }
+    const int64_t u = __shfl_up_sync(kFullMask, v, o);
+    if (lane >= o) v += u;
   }
-  if (lane == 31) {
-    sa[warp] = a;
-    sb[warp] = b;
-  }
+  if (lane == 31) warp_sum[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    int64_t wa = sa[lane], wb = sb[lane];
+  // every warp sums the warps' totals for itself
+  int64_t w = lane < warps ? warp_sum[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t ua = __shfl_up_sync(kFullMask, wa, o), ub = __shfl_up_sync(kFullMask, wb, o);
-      if (lane >= o) {
-        wa += ua;
-        wb += ub;
-      }
-    }
-    sa[lane] = wa;
-    sb[lane] = wb;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(kFullMask, w, o);
+    if (lane >= o) w += u;
   }
-  __syncthreads();
-  if (warp > 0) {
-    a += sa[warp - 1];
-    b += sb[warp - 1];
-  }
-  *ta = sa[31];
-  *tb = sb[31];
+  *total = __shfl_sync(kFullMask, w, 31);
+  const int64_t before = __shfl_sync(kFullMask, w, (warp + 31) & 31);
+  return warp > 0 ? v + before : v;
 }
 
-// Last i in [lo, hi) with a[i] <= x, given a[lo] <= x (a ascending).
-template <typename V>
-__device__ __forceinline__ int last_at_most(const V* a, int lo, int hi, V x) {
+// Last i in [0, n) with a[i] <= x, given a[0] <= x (a ascending).
+__device__ __forceinline__ int last_at_most(const int64_t* a, int n, int64_t x) {
+  int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (a[mid] <= x) lo = mid;
@@ -73,147 +58,117 @@ __device__ __forceinline__ int last_at_most(const V* a, int lo, int hi, V x) {
   return lo;
 }
 
-template <bool kFill>
+// kHeadOnly: *free_head_out alone, for a plan that advances its own free_head (no CTA of
+// the plan itself may write what another still reads).
+template <bool kHeadOnly>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
-  __shared__ int64_t sa[32], sb[32];
+  __shared__ int64_t sum_a[32], sum_b[32];
   __shared__ int64_t first_row[kPlanThreads], first_page[kPlanThreads];
   __shared__ int32_t have_of[kPlanThreads], ctx_of[kPlanThreads];
+  __shared__ uint32_t refused[kPlanThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int cta = blockIdx.x, ctas = gridDim.x;
   int64_t head = a.free_head != nullptr ? *a.free_head : 0;
   if (head < 0) head = 0;
-  const int64_t head0 = head;
-  int64_t row0 = 0, taken = 0;
+  int64_t row0 = 0, last_end = head;
   int bits = 0;
-  if (tid == 0) a.cu_q[0] = 0;
-  for (int64_t base = 0; base < a.B; base += kPlanThreads) {
+  if (!kHeadOnly && cta == 0 && tid == 0) a.cu_q[0] = 0;
+  const bool wide = (((uintptr_t)a.slots | (uintptr_t)a.positions) & 15) == 0;
+  for (int64_t base = 0; base < a.B; base += threads) {
     const int64_t b = base + tid;
-    const int count = (int)min((int64_t)kPlanThreads, a.B - base);
-    int64_t ctx = 0, add = 0;
-    bool fits = b < a.B;
-    if (fits) {
-      ctx = a.ctx[b];
-      add = a.add[b];
-      if (ctx < 0 || add < 0) {
-        fits = false;
-        ctx = ctx < 0 ? 0 : ctx;
-        add = add < 0 ? 0 : add;
-      }
-    }
-    const int64_t have = (ctx + a.page - 1) / a.page, after = (ctx + add + a.page - 1) / a.page;
-    int64_t rows = add, unused = 0, total_rows, total_pages, total_unused;
-    // The rows decide who fits, so they are summed before the pages.
-    scan2(rows, unused, sa, sb, &total_rows, &total_unused);
-    const int64_t upto = row0 + rows;
-    const bool counted = b < a.B;
+    const int count = (int)min((int64_t)threads, a.B - base);
+    const bool mine = b < a.B;
+    int64_t ctx = mine ? a.ctx[b] : 0, add = mine ? a.add[b] : 0;
+    bool fits = mine && ctx >= 0 && add >= 0;
+    ctx = ctx < 0 ? 0 : ctx;
+    add = add < 0 ? 0 : add;
+    const int have = (int)((uint32_t)(ctx + a.page - 1) / (uint32_t)a.page);
+    const int after = (int)((uint32_t)(ctx + add + a.page - 1) / (uint32_t)a.page);
+    int64_t rows, pages;
+    const int64_t upto = row0 + scan(add, sum_a, &rows);
     fits = fits && after <= a.max_pages && ctx + add <= INT32_MAX && upto <= a.T;
-    if (counted && !fits) bits |= 1;
-    __syncthreads();
     const int64_t need = fits ? after - have : 0;
-    int64_t pages = need;
-    scan2(pages, unused, sa, sb, &total_pages, &total_unused);
-    const int64_t end = head + pages;
+    const int64_t end = head + scan(need, sum_b, &pages);
     const bool ok = fits && (need == 0 || end <= a.n_free);
+    if (ok && need > 0) last_end = end;  // those that take pages come before those refused them
+    if (mine && !fits) bits |= 1;
     if (fits && !ok) bits |= 4;
-    const int64_t got = ok ? need : 0;
-    first_row[tid] = min(upto - add, a.T);
-    first_page[tid] = ok ? pages - need : -1;
-    have_of[tid] = (int32_t)have;
-    ctx_of[tid] = (int32_t)ctx;
-    if (counted) {
-      a.kv_lens[b] = ok ? (int32_t)(ctx + add) : 0;
-      a.cu_q[b + 1] = (int32_t)min(upto, a.T);
-    }
-    __syncthreads();
-    // New table entries, a warp to a request: its lanes take neighbouring pages.
-    for (int r = tid >> 5; r < count; r += kPlanThreads / 32) {
-      const int64_t f = first_page[r];
-      if (f < 0) continue;
-      const int64_t c = ctx_of[r], h = have_of[r];
-      const int64_t n = a.add[base + r];
-      const int64_t m = (c + n + a.page - 1) / a.page - h;
-      for (int64_t i = tid & 31; i < m; i += 32)
-        a.table[(base + r) * a.max_pages + h + i] = a.free_pages[head + f + i];
-    }
-    if (kFill) {
-      const int64_t stop = min(row0 + total_rows, a.T);
-      for (int64_t t = min(row0, a.T) + tid; t < stop; t += kPlanThreads) {
-        const int r = last_at_most(first_row, 0, count, t);
-        const int64_t pos = ctx_of[r] + t - first_row[r];
-        int32_t slot = -1;
-        if (first_page[r] >= 0) {
-          const int64_t p = pos / a.page;
-          const int64_t page = p < have_of[r]
-                                   ? a.table[(base + r) * a.max_pages + p]
-                                   : a.free_pages[head + first_page[r] + p - have_of[r]];
-          slot = (int32_t)(page * a.page + pos % a.page);
+    if (!kHeadOnly) {
+      first_row[tid] = min(upto - add, a.T);
+      first_page[tid] = end - need;
+      have_of[tid] = have;
+      ctx_of[tid] = (int32_t)ctx;
+      const uint32_t no = __ballot_sync(kFullMask, !ok);
+      if ((tid & 31) == 0) refused[tid >> 5] = no;
+      if (mine && cta == 0) {
+        a.kv_lens[b] = ok ? (int32_t)(ctx + add) : 0;
+        a.cu_q[b + 1] = (int32_t)min(upto, a.T);
+      }
+      __syncthreads();
+      // new table entries: pages head .. of the chunk that the free list holds
+      const int64_t last = min(head + pages, a.n_free);
+      for (int64_t p = head + (int64_t)cta * threads + tid; p < last; p += (int64_t)ctas * threads) {
+        const int r = last_at_most(first_page, count, p);
+        if (!((refused[r >> 5] >> (r & 31)) & 1u))
+          a.table[(base + r) * a.max_pages + have_of[r] + (p - first_page[r])] = a.free_pages[p];
+      }
+      // rows, four neighbours to a thread
+      const int64_t from = min(row0, a.T), to = min(row0 + rows, a.T);
+      for (int64_t t0 = from / 4 * 4 + ((int64_t)cta * threads + tid) * 4; t0 < to;
+           t0 += (int64_t)ctas * threads * 4) {
+        const int64_t lo = max(t0, from), hi = min(t0 + 4, to);
+        int r = last_at_most(first_row, count, lo);
+        int32_t slot[4], pos[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t t = t0 + i;
+          slot[i] = pos[i] = -1;
+          if (t < lo || t >= hi) continue;
+          while (r + 1 < count && first_row[r + 1] <= t) ++r;
+          const uint32_t at = (uint32_t)ctx_of[r] + (uint32_t)(t - first_row[r]);
+          pos[i] = (int32_t)at;
+          if ((refused[r >> 5] >> (r & 31)) & 1u) continue;
+          const int p = (int)(at / (uint32_t)a.page);
+          const int64_t page = p < have_of[r] ? a.table[(base + r) * a.max_pages + p]
+                                              : a.free_pages[first_page[r] + (p - have_of[r])];
+          slot[i] = (int32_t)(page * a.page + (at - (uint32_t)p * (uint32_t)a.page));
         }
-        a.slots[t] = slot;
-        a.positions[t] = (int32_t)pos;
+        if (wide && hi - lo == 4) {
+          *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+          *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (t0 + i >= lo && t0 + i < hi) {
+              a.slots[t0 + i] = slot[i];
+              a.positions[t0 + i] = pos[i];
+            }
+        }
       }
     }
-    __syncthreads();
-    // Pages granted in this chunk (the requests that were refused took none).
-    int64_t granted = got, total_granted;
-    scan2(granted, unused, sa, sb, &total_granted, &total_unused);
-    taken += total_granted;
-    head += total_pages;
-    row0 += total_rows;
+    head += pages;
+    row0 += rows;
     __syncthreads();
   }
-  if (kFill) {
-    for (int64_t t = min(row0, a.T) + tid; t < a.T; t += kPlanThreads) {
+  if (!kHeadOnly)
+    for (int64_t t = min(row0, a.T) + (int64_t)cta * threads + tid; t < a.T; t += (int64_t)ctas * threads) {
       a.slots[t] = -1;
       a.positions[t] = -1;
     }
-  }
-  if (tid == 0) *a.free_head_out = (int32_t)(head0 + taken);
-  if (bits != 0 && a.status != nullptr) atomicOr(a.status, bits);
-}
-
-// Rows of a large step: thread by thread four consecutive rows, the request found in cu_q.
-// kv_lens tells a refused request (it has rows and kv_lens 0).
-__global__ void __launch_bounds__(256) plan_fill_kernel(PlanArgs a) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int64_t t0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
-  if (t0 >= a.T) return;
-  int r = last_at_most(a.cu_q, 0, (int)a.B + 1, (int32_t)t0);
-  int32_t slot[4], posn[4];
-  int32_t next = r < a.B ? a.cu_q[r + 1] : INT32_MAX;
-  int32_t first = r < a.B ? a.cu_q[r] : 0, ctx = r < a.B ? max(a.ctx[r], 0) : 0;
-  bool ok = r < a.B && a.kv_lens[r] > 0;
+  if (cta == 0 && (kHeadOnly || a.free_head_out != nullptr)) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int32_t t = (int32_t)(t0 + i);
-    while (t >= next) {
-      ++r;
-      next = r < a.B ? a.cu_q[r + 1] : INT32_MAX;
-      first = r < a.B ? a.cu_q[r] : 0;
-      ctx = r < a.B ? max(a.ctx[r], 0) : 0;
-      ok = r < a.B && a.kv_lens[r] > 0;
-    }
-    const int32_t pos = r < a.B ? ctx + (t - first) : -1;
-    posn[i] = pos;
-    slot[i] = -1;
-    if (ok && t < a.T)
-      slot[i] = (int32_t)((int64_t)a.table[(int64_t)r * a.max_pages + pos / a.page] * a.page +
-                          pos % a.page);
-  }
-  if (t0 + 4 <= a.T && (((uintptr_t)a.slots | (uintptr_t)a.positions) & 15) == 0) {
-    *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-    *reinterpret_cast<int4*>(a.positions + t0) = make_int4(posn[0], posn[1], posn[2], posn[3]);
-  } else {
-    for (int i = 0; i < 4 && t0 + i < a.T; ++i) {
-      a.slots[t0 + i] = slot[i];
-      a.positions[t0 + i] = posn[i];
+    for (int o = 16; o > 0; o >>= 1) last_end = max(last_end, (int64_t)__shfl_xor_sync(kFullMask, last_end, o));
+    if ((tid & 31) == 0) sum_a[tid >> 5] = last_end;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 1; w < threads / 32; ++w) last_end = max(last_end, sum_a[w]);
+      *a.free_head_out = (int32_t)last_end;
     }
   }
+  if (!kHeadOnly && cta == 0 && bits != 0 && a.status != nullptr) atomicOr(a.status, bits);
 }
-
-// Steps up to this many rows are filled by the scanning CTA itself.
-constexpr int64_t kPlanFillRows = 4096;
 
 // ---------------------------------------------------------------------------
 // The write.  A warp takes one run of tokens (one scale block) of one head and plane: the
@@ -238,88 +193,139 @@ struct AppendArgs {
   int32_t* status;
 };
 
-// Place of a slot's codes (of head h) and of its scale.
-__device__ __forceinline__ int64_t code_at(const CacheArgs& c, int64_t slot, int h) {
-  const int64_t page = slot / c.page, off = slot % c.page;
-  return ((page * c.Hkv + h) * c.page + off) * c.D;
-}
-__device__ __forceinline__ int64_t scale_at(const CacheArgs& c, int64_t slot, int h) {
-  const int64_t page = slot / c.page, off = slot % c.page;
-  return (page * c.Hkv + h) * (c.page / c.block) + off / c.block;
-}
-
 template <typename T>
 struct Vec;  // 16 bytes of input
 template <>
 struct Vec<float> {
   static constexpr int kN = 4;
-  static __device__ __forceinline__ void load(const float* p, float v[4]) {
-    const float4 x = *reinterpret_cast<const float4*>(p);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  static __device__ __forceinline__ void unpack(const uint4& u, float* v) {
+    v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
   }
 };
 template <>
 struct Vec<uint16_t> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ void load(const uint16_t* p, float v[8]) { load8_bf16(p, v); }
+  static __device__ __forceinline__ void unpack(const uint4& u, float* v) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
 };
 
-template <typename T>
+// Codes of kN values with scale d (inv = 1 / d): the integers of quant_value, by the
+// reasoning of quant8_fast (v * inv is within 5e-5 of the IEEE quotient), but rounded by
+// adding 1.5 * 2^23, which leaves the code in the sum's low byte.  Values within 1e-4 of a
+// half take the quotient itself.
+template <int kN>
+__device__ __forceinline__ void codes_of(const float* v, float d, float inv, uint32_t* out) {
+  constexpr float kMagic = 12582912.0f;
+  uint32_t y[kN];
+  bool near = false;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const float r = __fmul_rn(v[i], inv), z = __fadd_rn(r, kMagic);
+    near |= fabsf(__fsub_rn(r, __fsub_rn(z, kMagic))) > 0.4999f;
+    y[i] = __float_as_uint(z);
+  }
+  if (near) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) y[i] = (uint32_t)quant_value(v[i], d);
+  }
+#pragma unroll
+  for (int i = 0; i < kN; i += 4)
+    out[i / 4] = __byte_perm(__byte_perm(y[i], y[i + 1], 0x0040), __byte_perm(y[i + 2], y[i + 3], 0x0040), 0x5410);
+}
+
+template <typename T, int kD>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendArgs a) {
   constexpr int kN = Vec<T>::kN;
+  constexpr int kLanes = kD / kN;                       // 16-byte pieces of a row
+  constexpr int kStepRows = kLanes < 32 ? 32 / kLanes : 1;
+  constexpr int kPieces = kLanes < 32 ? 1 : kLanes / 32;
+  constexpr int kHeld = 8 / kPieces;                    // steps of a run that stay in registers
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-  const int planes = 2 * a.c.Hkv;
-  const int64_t tiles = (a.T + a.tile - 1) / a.tile;
-  if (item >= tiles * planes) return;
-  const int plane = (int)(item % planes);
-  const int h = plane >> 1;
+  const uint32_t item = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  const uint32_t planes = 2 * a.c.Hkv;
+  const uint32_t t0 = item / planes * a.tile;
+  if (t0 >= a.T) return;
+  const int plane = (int)(item % planes), h = plane >> 1;
   const bool is_v = plane & 1;
-  const T* x = static_cast<const T*>(is_v ? a.v : a.k) + h * a.stride_h;
-  int8_t* codes = is_v ? a.c.vq : a.c.kq;
-  float* scales = is_v ? a.c.vd : a.c.kd;
-  const int D = a.c.D, S = a.c.block;
-  const int per_row = D / kN;            // lanes to a row (8 .. 64)
-  const int64_t t_end = min((item / planes + 1) * a.tile, a.T);
-  for (int64_t t = item / planes * a.tile; t < t_end; ++t) {
-    const int64_t slot = a.slots[t];
-    if (slot < 0) continue;
-    if (slot >= a.c.slots_in_pool) {
-      if (a.status != nullptr && plane == 0 && lane == 0) atomicOr(a.status, 1);
-      continue;
-    }
-    const int64_t blk = slot / S;
-    if (t > 0) {
-      const int64_t before = a.slots[t - 1];
-      if (before >= 0 && before / S == blk) continue;  // not the run's first token
-    }
-    const int first = (int)(slot - blk * S);
-    int n = 1;
-    while (first + n < S && t + n < a.T) {
-      const int64_t next = a.slots[t + n];
-      if (next < 0 || next / S != blk) break;
-      ++n;
-    }
+  // Slots of rows t0 - 1 .. t0 + 30, one a lane; blk: which scale block, -1 for none.
+  const uint32_t S = a.c.block;
+  const int64_t row = (int64_t)t0 - 1 + lane;
+  const int32_t slot = row >= 0 && row < a.T ? a.slots[row] : -1;
+  const bool beyond = slot >= a.c.slots_in_pool;
+  int32_t blk = slot >= 0 && !beyond ? (int32_t)((uint32_t)slot / S) : -1;
+  const int32_t blk_before = __shfl_up_sync(kFullMask, blk, 1);
+  const bool in_tile = lane >= 1 && lane <= a.tile;
+  if (beyond && in_tile && plane == 0 && a.status != nullptr) atomicOr(a.status, 1);
+  uint32_t leaders = __ballot_sync(kFullMask, in_tile && blk >= 0 && blk != blk_before);
+
+  const int lane_row = kLanes < 32 ? lane / kLanes : 0;
+  const T* x = static_cast<const T*>(is_v ? a.v : a.k) + h * a.stride_h + (lane % kLanes) * kN;
+  int8_t* planes_codes = is_v ? a.c.vq : a.c.kq;
+  float* planes_scales = is_v ? a.c.vd : a.c.kd;
+  for (; leaders != 0; leaders &= leaders - 1) {
+    const int lead = __ffs(leaders) - 1;
+    const int32_t my_blk = __shfl_sync(kFullMask, blk, lead);
+    const uint32_t my_slot = (uint32_t)__shfl_sync(kFullMask, slot, lead);
+    const int first = (int)(my_slot - (uint32_t)my_blk * S);
+    const int64_t t = (int64_t)t0 - 1 + lead;
+    // the run: rows of the same block that follow, at most to the block's end
+    const uint32_t same = __ballot_sync(kFullMask, blk == my_blk) >> lead;
+    int n = __ffs(~same) - 1;
+    n = n < 0 ? 32 : n;
+    if (n == 32 - lead)  // it reaches the last row looked at
+      while (t + n < a.T && first + n < (int)S) {
+        const int64_t next = a.slots[t + n];
+        if (next < 0 || next >= a.c.slots_in_pool || next / S != my_blk) break;
+        ++n;
+      }
+    n = min(n, (int)S - first);
     const T* rows = x + t * a.stride_t;
-    const int total = n * per_row;
+    const uint32_t page = my_slot / (uint32_t)a.c.page;
+    const uint32_t off = my_slot - page * (uint32_t)a.c.page;
+    const int64_t head = (int64_t)page * a.c.Hkv + h;
+    float* scale = planes_scales + head * (a.c.page / (int)S) + off / S;
+    int8_t* block_codes = planes_codes + (head * a.c.page + off - first) * kD;
+    const float d_old = first > 0 ? *scale : 0.0f;
+
+    uint4 held[kHeld][kPieces];
     float amax = 0.0f;
-    for (int i = lane; i < total; i += 32) {
+    auto take = [&](const uint4& u) {
       float v[kN];
-      Vec<T>::load(rows + (int64_t)(i / per_row) * a.stride_t + (i % per_row) * kN, v);
+      Vec<T>::unpack(u, v);
 #pragma unroll
       for (int j = 0; j < kN; ++j) amax = fmaxf(amax, fabsf(v[j]));
-    }
+    };
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, o));
-    float* scale = scales + scale_at(a.c, slot, h);
-    const float d_old = first > 0 ? *scale : 0.0f;
+    for (int s = 0; s < kHeld; ++s)
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) {
+        const int r = s * kStepRows + lane_row;
+        held[s][p] = r < n ? *reinterpret_cast<const uint4*>(rows + r * a.stride_t + p * 32 * kN)
+                           : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+    for (int s = 0; s < kHeld; ++s)
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p) take(held[s][p]);
+    for (int r = kHeld * kStepRows + lane_row; r < n; r += kStepRows)
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+        take(*reinterpret_cast<const uint4*>(rows + r * a.stride_t + p * 32 * kN));
+    amax = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(amax)));
     const float d = fmaxf(d_old, amax / 127.0f);
-    int8_t* block_codes = codes + code_at(a.c, blk * S, h);
+
     if (first > 0 && d > d_old) {
       const float ratio = d_old / d;
-      for (int i = lane * 4; i < first * D; i += 128) {
+      for (int i = lane * 4; i < first * kD; i += 128) {
         const char4 q = *reinterpret_cast<const char4*>(block_codes + i);
         char4 r;
         r.x = (signed char)(int)roundf(__fmul_rn((float)q.x, ratio));
@@ -329,17 +335,37 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendArgs a)
         *reinterpret_cast<char4*>(block_codes + i) = r;
       }
     }
-    for (int i = lane; i < total; i += 32) {
+    // 1 / d is of use for scales that are normal by a margin; the others are divided by
+    const bool quick = d > 1e-30f;
+    const float inv = quick ? 1.0f / d : 0.0f;
+    int8_t* to = block_codes + (int64_t)first * kD + (lane % kLanes) * kN;
+    auto put = [&](const uint4& u, int r, int p) {
       float v[kN];
-      Vec<T>::load(rows + (int64_t)(i / per_row) * a.stride_t + (i % per_row) * kN, v);
-      int8_t* to = block_codes + (int64_t)(first + i / per_row) * D + (i % per_row) * kN;
+      uint32_t w[kN / 4];
+      Vec<T>::unpack(u, v);
+      if (quick) {
+        codes_of<kN>(v, d, inv, w);
+      } else {
 #pragma unroll
-      for (int j = 0; j < kN; j += 4)
-        *reinterpret_cast<uint32_t*>(to + j) =
-            pack4(quant_value(v[j], d), quant_value(v[j + 1], d), quant_value(v[j + 2], d),
-                  quant_value(v[j + 3], d));
+        for (int j = 0; j < kN; j += 4)
+          w[j / 4] = pack4(quant_value(v[j], d), quant_value(v[j + 1], d), quant_value(v[j + 2], d),
+                           quant_value(v[j + 3], d));
+      }
+      int8_t* dst = to + (int64_t)r * kD + p * 32 * kN;
+      if (kN == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[kN / 4 - 1]);
+      else *reinterpret_cast<uint32_t*>(dst) = w[0];
+    };
+#pragma unroll
+    for (int s = 0; s < kHeld; ++s) {
+      const int r = s * kStepRows + lane_row;
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+        if (r < n) put(held[s][p], r, p);
     }
-    __syncwarp();
+    for (int r = kHeld * kStepRows + lane_row; r < n; r += kStepRows)
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+        put(*reinterpret_cast<const uint4*>(rows + r * a.stride_t + p * 32 * kN), r, p);
     if (lane == 0) *scale = d;
   }
 }
@@ -360,49 +386,71 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+constexpr int kReadWarps = 8;
+constexpr int kReadPieces = 4;  // 16-byte pieces of output a lane
+
+// A warp takes 128 pieces of one token's K or V row (all heads lie one after another in the
+// output); the slot is looked up and divided once for all of them.
 template <typename T>
-__global__ void __launch_bounds__(256) read_kernel(ReadArgs a) {
+__global__ void __launch_bounds__(kReadWarps * 32) read_kernel(ReadArgs a, uint32_t groups) {
   constexpr int kN = Vec<T>::kN;
   pdl_launch_dependents();
   pdl_wait();
-  const int per_row = a.c.D / kN;
-  const int64_t per_token = (int64_t)a.c.Hkv * per_row, total = 2 * a.N * per_token;
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
-    const bool is_v = i >= a.N * per_token;
-    const int64_t j = is_v ? i - a.N * per_token : i;
-    const int64_t n = j / per_token;
-    const int at = (int)(j % per_token), h = at / per_row, e = at % per_row * kN;
-    const int64_t slot = a.slots[n];
-    T* out = static_cast<T*>(is_v ? a.v : a.k) + j * kN;
-    const bool have = slot >= 0 && slot < a.c.slots_in_pool;
-    if (slot >= a.c.slots_in_pool && a.status != nullptr && at == 0 && !is_v)
-      atomicOr(a.status, 1);
-    float d = 0.0f;
-    uint32_t w[kN / 4] = {};
-    if (have) {
-      d = (is_v ? a.c.vd : a.c.kd)[scale_at(a.c, slot, h)];
-      const int8_t* q = (is_v ? a.c.vq : a.c.kq) + code_at(a.c, slot, h) + e;
+  const uint32_t item = blockIdx.x * kReadWarps + (threadIdx.x >> 5);
+  const uint32_t n = item / (2 * groups);
+  if (n >= a.N) return;
+  const bool is_v = (item / groups) & 1;
+  const int lane = threadIdx.x & 31;
+  const int per_head = a.c.D / kN, total = a.c.Hkv * per_head;
+  const int32_t slot = a.slots[n];
+  const bool have = slot >= 0 && slot < a.c.slots_in_pool;
+  if (slot >= a.c.slots_in_pool && a.status != nullptr && lane == 0) atomicOr(a.status, 1);
+  const uint32_t page = have ? (uint32_t)slot / (uint32_t)a.c.page : 0;
+  const uint32_t off = have ? (uint32_t)slot - page * (uint32_t)a.c.page : 0;
+  const int64_t head0 = (int64_t)page * a.c.Hkv;
+  const int8_t* codes = (is_v ? a.c.vq : a.c.kq) + (head0 * a.c.page + off) * a.c.D;
+  const float* scales = (is_v ? a.c.vd : a.c.kd) + head0 * (a.c.page / a.c.block) + off / (uint32_t)a.c.block;
+  T* out = static_cast<T*>(is_v ? a.v : a.k) + (int64_t)n * total * kN;
+  float d[kReadPieces];
+  uint2 w[kReadPieces];
 #pragma unroll
-      for (int x = 0; x < kN / 4; ++x) w[x] = *reinterpret_cast<const uint32_t*>(q + 4 * x);
+  for (int i = 0; i < kReadPieces; ++i) {
+    const int piece = (int)(item % groups) * (32 * kReadPieces) + i * 32 + lane;
+    d[i] = 0.0f;
+    w[i] = make_uint2(0, 0);
+    if (have && piece < total) {
+      const int h = piece / per_head, e = piece % per_head * kN;
+      const int8_t* q = codes + (int64_t)h * a.c.page * a.c.D + e;
+      d[i] = scales[h * (a.c.page / a.c.block)];
+      if (kN == 8) w[i] = *reinterpret_cast<const uint2*>(q);
+      else w[i].x = *reinterpret_cast<const uint32_t*>(q);
     }
-    float v[kN];
+  }
 #pragma unroll
-    for (int x = 0; x < kN; ++x)
-      v[x] = __fmul_rn((float)(int8_t)(w[x / 4] >> (8 * (x % 4))), d);
+  for (int i = 0; i < kReadPieces; ++i) {
+    const int piece = (int)(item % groups) * (32 * kReadPieces) + i * 32 + lane;
+    if (piece >= total) continue;
+    float v[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      v[x] = __fmul_rn((float)(int8_t)((x < 4 ? w[i].x : w[i].y) >> (8 * (x % 4))), d[i]);
     uint4 o;
-    if (kN == 4) {
+    if (kN == 4)
       o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                      __float_as_uint(v[3]));
-    } else {
-      uint32_t p[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        p[x] = bf16_pair(v[(2 * x) % kN], v[(2 * x + 1) % kN]);
-      o = make_uint4(p[0], p[1], p[2], p[3]);
-    }
-    *reinterpret_cast<uint4*>(out) = o;
+    else
+      o = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                     bf16_pair(v[6], v[7]));
+    *reinterpret_cast<uint4*>(out + (int64_t)piece * kN) = o;
   }
+}
+
+template <typename T>
+cudaError_t launch_append(const AppendArgs& a, dim3 grid, cudaStream_t stream) {
+  const dim3 block(kAppendWarps * 32);
+  if (a.c.D == 64) return launch_kernel(append_kernel<T, 64>, grid, block, 0, stream, a);
+  if (a.c.D == 128) return launch_kernel(append_kernel<T, 128>, grid, block, 0, stream, a);
+  return launch_kernel(append_kernel<T, 256>, grid, block, 0, stream, a);
 }
 
 }  // namespace
@@ -447,16 +495,21 @@ extern "C" memra_status memra_kv_plan(const int32_t* ctx_lens, const int32_t* ne
   a.positions = positions;
   a.free_head_out = free_head_out;
   a.status = dev_status;
-  cudaError_t e;
-  if (T <= kPlanFillRows) {
+  DeviceInfo info;
+  if (!device_info(&info)) return MEMRA_ERR_CUDA;
+  // A CTA for every 4096 rows, up to one an SM; small plans take a small CTA, whose barriers
+  // cost less.
+  const bool small = B <= 256 && T <= 1024;
+  int64_t ctas = (T + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  ctas = ctas < 1 ? 1 : (ctas > info.sms ? info.sms : ctas);
+  const bool in_place = ctas > 1 && free_head == free_head_out;
+  if (in_place) a.free_head_out = nullptr;
+  cudaError_t e = launch_kernel(plan_kernel<false>, dim3((unsigned)ctas),
+                                dim3(small ? 256 : kPlanThreads), 0, stream, a);
+  if (e == cudaSuccess && in_place) {
+    a.free_head_out = free_head_out;
     e = launch_kernel(plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, stream, a);
-    if (e != cudaSuccess) return cuda_fail(e);
-    return MEMRA_OK;
   }
-  e = launch_kernel(plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, stream, a);
-  if (e != cudaSuccess) return cuda_fail(e);
-  const int64_t blocks = (T + 1023) / 1024;
-  e = launch_kernel(plan_fill_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }
@@ -518,11 +571,10 @@ extern "C" memra_status memra_kv_append_q8(const void* k, const void* v, int32_t
   a.tile = T * 2 * Hkv <= (int64_t)info.sms * 64 ? 1 : 16;
   const int64_t items = (T + a.tile - 1) / a.tile * 2 * Hkv;
   const int64_t blocks = (items + kAppendWarps - 1) / kAppendWarps;
-  if (blocks > INT32_MAX) return MEMRA_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks), threads(kAppendWarps * 32);
-  const cudaError_t e = dtype == MEMRA_BF16
-                            ? launch_kernel(append_kernel<uint16_t>, grid, threads, 0, stream, a)
-                            : launch_kernel(append_kernel<float>, grid, threads, 0, stream, a);
+  if (blocks > INT32_MAX / kAppendWarps) return MEMRA_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks);
+  const cudaError_t e = dtype == MEMRA_BF16 ? launch_append<uint16_t>(a, grid, stream)
+                                            : launch_append<float>(a, grid, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }
@@ -551,13 +603,14 @@ extern "C" memra_status memra_kv_read_q8(const int32_t* slots, int64_t N, const 
   a.k = k;
   a.v = v;
   a.status = dev_status;
-  const int64_t items = 2 * N * Hkv * (D / (dtype == MEMRA_BF16 ? 8 : 4));
-  int64_t blocks = (items + 255) / 256;
-  if (blocks > (int64_t)info.sms * 8) blocks = (int64_t)info.sms * 8;
-  const dim3 grid((unsigned)blocks), threads(256);
+  const int64_t pieces = Hkv * (D / (dtype == MEMRA_BF16 ? 8 : 4));
+  const int64_t groups = (pieces + 32 * kReadPieces - 1) / (32 * kReadPieces);
+  const int64_t blocks = (2 * N * groups + kReadWarps - 1) / kReadWarps;
+  if (blocks > INT32_MAX / kReadWarps) return MEMRA_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks), threads(kReadWarps * 32);
   const cudaError_t e = dtype == MEMRA_BF16
-                            ? launch_kernel(read_kernel<uint16_t>, grid, threads, 0, stream, a)
-                            : launch_kernel(read_kernel<float>, grid, threads, 0, stream, a);
+                            ? launch_kernel(read_kernel<uint16_t>, grid, threads, 0, stream, a, (uint32_t)groups)
+                            : launch_kernel(read_kernel<float>, grid, threads, 0, stream, a, (uint32_t)groups);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }
