@@ -177,11 +177,28 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
 
+// x / n for x < 2^31 by a product: with 2^l >= n > 2^(l-1) and m = ceil(2^(31+l) / n) the
+// product is above x * 2^(31+l) / n by less than x * n / n < 2^31 parts of 2^(31+l), too
+// little to reach the next whole quotient.
+struct Divider {
+  uint32_t m, shift;
+  explicit Divider(uint32_t n = 1) {
+    uint32_t l = 0;
+    while ((1u << l) < n) ++l;
+    m = (uint32_t)(((1ull << (31 + l)) + n - 1) / n);
+    shift = 31 + l;
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
+    return (uint32_t)(((uint64_t)x * m) >> shift);
+  }
+};
+
 struct CacheArgs {
   int8_t *kq, *vq;
   float *kd, *vd;
   int64_t slots_in_pool;
   int Hkv, page, D, block;
+  Divider by_page, by_block;
 };
 
 struct AppendArgs {
@@ -202,6 +219,14 @@ struct Vec<float> {
     v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
     v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
   }
+  struct Largest {  // the largest magnitude of the pieces taken
+    float m = 0.0f;
+    __device__ __forceinline__ void take(const uint4& u) {
+      m = fmaxf(fmaxf(m, fmaxf(fabsf(__uint_as_float(u.x)), fabsf(__uint_as_float(u.y)))),
+                fmaxf(fabsf(__uint_as_float(u.z)), fabsf(__uint_as_float(u.w))));
+    }
+    __device__ __forceinline__ float value() const { return m; }
+  };
 };
 template <>
 struct Vec<uint16_t> {
@@ -214,26 +239,36 @@ struct Vec<uint16_t> {
       v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  struct Largest {
+    uint32_t m = 0;  // two bf16
+    __device__ __forceinline__ void take(const uint4& u) {
+      m = most(m, most(most(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), most(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+    }
+    static __device__ __forceinline__ uint32_t most(uint32_t a, uint32_t b) {
+      const __nv_bfloat162 x = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&b));
+      return *reinterpret_cast<const uint32_t*>(&x);
+    }
+    __device__ __forceinline__ float value() const {
+      return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
+  };
 };
 
-// Codes of kN values with scale d (inv = 1 / d): the integers of quant_value, by the
-// reasoning of quant8_fast (v * inv is within 5e-5 of the IEEE quotient), but rounded by
-// adding 1.5 * 2^23, which leaves the code in the sum's low byte.  Values within 1e-4 of a
-// half take the quotient itself.
+// Codes of kN values with scale d, the integers of quant_value: v * inv with inv = 1 / d
+// rounded, corrected once by its remainder, is the IEEE quotient (Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990; no underflow for
+// d above 1e-30 but where the code is 0 anyway), and a half added towards its sign and cut
+// off rounds halves away from zero.  A bf16 value is often an exact half of its block's
+// scale, so a shortcut that leaves halves to a division would take it all the time.
 template <int kN>
 __device__ __forceinline__ void codes_of(const float* v, float d, float inv, uint32_t* out) {
-  constexpr float kMagic = 12582912.0f;
   uint32_t y[kN];
-  bool near = false;
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
-    const float r = __fmul_rn(v[i], inv), z = __fadd_rn(r, kMagic);
-    near |= fabsf(__fsub_rn(r, __fsub_rn(z, kMagic))) > 0.4999f;
-    y[i] = __float_as_uint(z);
-  }
-  if (near) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) y[i] = (uint32_t)quant_value(v[i], d);
+    float q = __fmul_rn(v[i], inv);
+    q = __fmaf_rn(__fmaf_rn(-q, d, v[i]), inv, q);
+    y[i] = (uint32_t)__float2int_rz(__fadd_rz(q, copysignf(0.5f, q)));
   }
 #pragma unroll
   for (int i = 0; i < kN; i += 4)
@@ -241,7 +276,7 @@ __device__ __forceinline__ void codes_of(const float* v, float d, float inv, uin
 }
 
 template <typename T, int kD>
-__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kAppendWarps * 32, 8) append_kernel(AppendArgs a) {
   constexpr int kN = Vec<T>::kN;
   constexpr int kLanes = kD / kN;                       // 16-byte pieces of a row
   constexpr int kStepRows = kLanes < 32 ? 32 / kLanes : 1;
@@ -250,25 +285,24 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendArgs a)
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const uint32_t item = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
-  const uint32_t planes = 2 * a.c.Hkv;
-  const uint32_t t0 = item / planes * a.tile;
+  // grid: x tiles of rows, y planes
+  const int64_t t0 = ((int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5)) * a.tile;
   if (t0 >= a.T) return;
-  const int plane = (int)(item % planes), h = plane >> 1;
-  const bool is_v = plane & 1;
+  const bool is_v = blockIdx.y & 1;
+  const int h = (int)(blockIdx.y >> 1);
   // Slots of rows t0 - 1 .. t0 + 30, one a lane; blk: which scale block, -1 for none.
   const uint32_t S = a.c.block;
-  const int64_t row = (int64_t)t0 - 1 + lane;
+  const int64_t row = t0 - 1 + lane;
   const int32_t slot = row >= 0 && row < a.T ? a.slots[row] : -1;
   const bool beyond = slot >= a.c.slots_in_pool;
-  int32_t blk = slot >= 0 && !beyond ? (int32_t)((uint32_t)slot / S) : -1;
+  int32_t blk = slot >= 0 && !beyond ? (int32_t)a.c.by_block((uint32_t)slot) : -1;
   const int32_t blk_before = __shfl_up_sync(kFullMask, blk, 1);
   const bool in_tile = lane >= 1 && lane <= a.tile;
-  if (beyond && in_tile && plane == 0 && a.status != nullptr) atomicOr(a.status, 1);
+  if (beyond && in_tile && blockIdx.y == 0 && a.status != nullptr) atomicOr(a.status, 1);
   uint32_t leaders = __ballot_sync(kFullMask, in_tile && blk >= 0 && blk != blk_before);
 
   const int lane_row = kLanes < 32 ? lane / kLanes : 0;
-  const T* x = static_cast<const T*>(is_v ? a.v : a.k) + h * a.stride_h + (lane % kLanes) * kN;
+  const T* x = static_cast<const T*>(is_v ? a.v : a.k) + (lane % kLanes) * kN;
   int8_t* planes_codes = is_v ? a.c.vq : a.c.kq;
   float* planes_scales = is_v ? a.c.vd : a.c.kd;
   for (; leaders != 0; leaders &= leaders - 1) {
@@ -276,7 +310,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendArgs a)
     const int32_t my_blk = __shfl_sync(kFullMask, blk, lead);
     const uint32_t my_slot = (uint32_t)__shfl_sync(kFullMask, slot, lead);
     const int first = (int)(my_slot - (uint32_t)my_blk * S);
-    const int64_t t = (int64_t)t0 - 1 + lead;
+    const int64_t t = t0 - 1 + lead;
     // the run: rows of the same block that follow, at most to the block's end
     const uint32_t same = __ballot_sync(kFullMask, blk == my_blk) >> lead;
     int n = __ffs(~same) - 1;
@@ -284,26 +318,21 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendArgs a)
     if (n == 32 - lead)  // it reaches the last row looked at
       while (t + n < a.T && first + n < (int)S) {
         const int64_t next = a.slots[t + n];
-        if (next < 0 || next >= a.c.slots_in_pool || next / S != my_blk) break;
+        if (next < 0 || next >= a.c.slots_in_pool || a.c.by_block((uint32_t)next) != (uint32_t)my_blk) break;
         ++n;
       }
     n = min(n, (int)S - first);
-    const T* rows = x + t * a.stride_t;
-    const uint32_t page = my_slot / (uint32_t)a.c.page;
+    const uint32_t page = a.c.by_page(my_slot);
     const uint32_t off = my_slot - page * (uint32_t)a.c.page;
+    const uint32_t block_in_page = a.c.by_block(off);
+    const T* rows = x + t * a.stride_t + h * a.stride_h;
     const int64_t head = (int64_t)page * a.c.Hkv + h;
-    float* scale = planes_scales + head * (a.c.page / (int)S) + off / S;
+    float* scale = planes_scales + head * (a.c.page / (int)S) + block_in_page;
     int8_t* block_codes = planes_codes + (head * a.c.page + off - first) * kD;
     const float d_old = first > 0 ? *scale : 0.0f;
 
     uint4 held[kHeld][kPieces];
-    float amax = 0.0f;
-    auto take = [&](const uint4& u) {
-      float v[kN];
-      Vec<T>::unpack(u, v);
-#pragma unroll
-      for (int j = 0; j < kN; ++j) amax = fmaxf(amax, fabsf(v[j]));
-    };
+    typename Vec<T>::Largest largest;
 #pragma unroll
     for (int s = 0; s < kHeld; ++s)
 #pragma unroll
@@ -315,11 +344,12 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendArgs a)
 #pragma unroll
     for (int s = 0; s < kHeld; ++s)
 #pragma unroll
-      for (int p = 0; p < kPieces; ++p) take(held[s][p]);
+      for (int p = 0; p < kPieces; ++p) largest.take(held[s][p]);
     for (int r = kHeld * kStepRows + lane_row; r < n; r += kStepRows)
 #pragma unroll
       for (int p = 0; p < kPieces; ++p)
-        take(*reinterpret_cast<const uint4*>(rows + r * a.stride_t + p * 32 * kN));
+        largest.take(*reinterpret_cast<const uint4*>(rows + r * a.stride_t + p * 32 * kN));
+    float amax = largest.value();
     amax = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(amax)));
     const float d = fmaxf(d_old, amax / 127.0f);
 
@@ -335,37 +365,48 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendArgs a)
         *reinterpret_cast<char4*>(block_codes + i) = r;
       }
     }
-    // 1 / d is of use for scales that are normal by a margin; the others are divided by
-    const bool quick = d > 1e-30f;
-    const float inv = quick ? 1.0f / d : 0.0f;
     int8_t* to = block_codes + (int64_t)first * kD + (lane % kLanes) * kN;
-    auto put = [&](const uint4& u, int r, int p) {
-      float v[kN];
-      uint32_t w[kN / 4];
-      Vec<T>::unpack(u, v);
-      if (quick) {
-        codes_of<kN>(v, d, inv, w);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kN; j += 4)
-          w[j / 4] = pack4(quant_value(v[j], d), quant_value(v[j + 1], d), quant_value(v[j + 2], d),
-                           quant_value(v[j + 3], d));
-      }
+    auto write = [&](int r, int p, const uint32_t* w) {
       int8_t* dst = to + (int64_t)r * kD + p * 32 * kN;
       if (kN == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[kN / 4 - 1]);
       else *reinterpret_cast<uint32_t*>(dst) = w[0];
     };
+    float v[kN];
+    uint32_t w[kN / 4];
+    if (d > 1e-30f) {
+      const float inv = 1.0f / d;
 #pragma unroll
-    for (int s = 0; s < kHeld; ++s) {
-      const int r = s * kStepRows + lane_row;
+      for (int s = 0; s < kHeld; ++s) {
+        const int r = s * kStepRows + lane_row;
 #pragma unroll
-      for (int p = 0; p < kPieces; ++p)
-        if (r < n) put(held[s][p], r, p);
+        for (int p = 0; p < kPieces; ++p)
+          if (r < n) {
+            Vec<T>::unpack(held[s][p], v);
+            codes_of<kN>(v, d, inv, w);
+            write(r, p, w);
+          }
+      }
+#pragma unroll 1
+      for (int r = kHeld * kStepRows + lane_row; r < n; r += kStepRows)
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+          Vec<T>::unpack(*reinterpret_cast<const uint4*>(rows + r * a.stride_t + p * 32 * kN), v);
+          codes_of<kN>(v, d, inv, w);
+          write(r, p, w);
+        }
+    } else {  // zeros, or next to nothing: divide
+#pragma unroll 1
+      for (int r = lane_row; r < n; r += kStepRows)
+#pragma unroll 1
+        for (int p = 0; p < kPieces; ++p) {
+          Vec<T>::unpack(*reinterpret_cast<const uint4*>(rows + r * a.stride_t + p * 32 * kN), v);
+#pragma unroll
+          for (int j = 0; j < kN; j += 4)
+            w[j / 4] = pack4(quant_value(v[j], d), quant_value(v[j + 1], d), quant_value(v[j + 2], d),
+                             quant_value(v[j + 3], d));
+          write(r, p, w);
+        }
     }
-    for (int r = kHeld * kStepRows + lane_row; r < n; r += kStepRows)
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p)
-        put(*reinterpret_cast<const uint4*>(rows + r * a.stride_t + p * 32 * kN), r, p);
     if (lane == 0) *scale = d;
   }
 }
@@ -388,61 +429,89 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 
 constexpr int kReadWarps = 8;
 constexpr int kReadPieces = 4;  // 16-byte pieces of output a lane
+constexpr int kReadTokens = 4;  // tokens a warp, where there are many (with 2: 23.7 us for 20.3)
 
-// A warp takes 128 pieces of one token's K or V row (all heads lie one after another in the
-// output); the slot is looked up and divided once for all of them.
-template <typename T>
-__global__ void __launch_bounds__(kReadWarps * 32) read_kernel(ReadArgs a, uint32_t groups) {
+// A warp takes 128 pieces of the K or V rows of kTokens tokens (all heads lie one after
+// another in the output); a slot is looked up and divided once for all of them, and the
+// tokens' codes are on their way together.
+template <typename T, int kTokens>
+__global__ void __launch_bounds__(kReadWarps * 32) read_kernel(ReadArgs a, int head_bits) {
   constexpr int kN = Vec<T>::kN;
   pdl_launch_dependents();
   pdl_wait();
-  const uint32_t item = blockIdx.x * kReadWarps + (threadIdx.x >> 5);
-  const uint32_t n = item / (2 * groups);
-  if (n >= a.N) return;
-  const bool is_v = (item / groups) & 1;
+  // grid: x tokens, y K or V, z 128 pieces
+  const int64_t n0 = ((int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5)) * kTokens;
+  const bool is_v = blockIdx.y;
   const int lane = threadIdx.x & 31;
-  const int per_head = a.c.D / kN, total = a.c.Hkv * per_head;
-  const int32_t slot = a.slots[n];
-  const bool have = slot >= 0 && slot < a.c.slots_in_pool;
-  if (slot >= a.c.slots_in_pool && a.status != nullptr && lane == 0) atomicOr(a.status, 1);
-  const uint32_t page = have ? (uint32_t)slot / (uint32_t)a.c.page : 0;
-  const uint32_t off = have ? (uint32_t)slot - page * (uint32_t)a.c.page : 0;
-  const int64_t head0 = (int64_t)page * a.c.Hkv;
-  const int8_t* codes = (is_v ? a.c.vq : a.c.kq) + (head0 * a.c.page + off) * a.c.D;
-  const float* scales = (is_v ? a.c.vd : a.c.kd) + head0 * (a.c.page / a.c.block) + off / (uint32_t)a.c.block;
-  T* out = static_cast<T*>(is_v ? a.v : a.k) + (int64_t)n * total * kN;
-  float d[kReadPieces];
-  uint2 w[kReadPieces];
+  const int total = a.c.Hkv << head_bits;  // pieces of a row, 2^head_bits of a head
+  const int blocks = (int)a.c.by_block((uint32_t)a.c.page);
+  const int8_t* codes = is_v ? a.c.vq : a.c.kq;
+  const float* scales = is_v ? a.c.vd : a.c.kd;
+  int32_t slot[kTokens];
 #pragma unroll
-  for (int i = 0; i < kReadPieces; ++i) {
-    const int piece = (int)(item % groups) * (32 * kReadPieces) + i * 32 + lane;
-    d[i] = 0.0f;
-    w[i] = make_uint2(0, 0);
-    if (have && piece < total) {
-      const int h = piece / per_head, e = piece % per_head * kN;
-      const int8_t* q = codes + (int64_t)h * a.c.page * a.c.D + e;
-      d[i] = scales[h * (a.c.page / a.c.block)];
-      if (kN == 8) w[i] = *reinterpret_cast<const uint2*>(q);
-      else w[i].x = *reinterpret_cast<const uint32_t*>(q);
+  for (int k = 0; k < kTokens; ++k) slot[k] = n0 + k < a.N ? a.slots[n0 + k] : -1;
+  float d[kTokens][kReadPieces];
+  uint2 w[kTokens][kReadPieces];
+#pragma unroll
+  for (int k = 0; k < kTokens; ++k) {
+    const bool have = slot[k] >= 0 && slot[k] < a.c.slots_in_pool;
+    if (slot[k] >= a.c.slots_in_pool && a.status != nullptr && lane == 0) atomicOr(a.status, 1);
+    const uint32_t page = have ? a.c.by_page((uint32_t)slot[k]) : 0;
+    const uint32_t off = have ? (uint32_t)slot[k] - page * (uint32_t)a.c.page : 0;
+    const int64_t head0 = (int64_t)page * a.c.Hkv;
+    const int8_t* q0 = codes + (head0 * a.c.page + off) * a.c.D;
+    const float* d0 = scales + head0 * blocks + a.c.by_block(off);
+#pragma unroll
+    for (int i = 0; i < kReadPieces; ++i) {
+      const int piece = (int)blockIdx.z * (32 * kReadPieces) + i * 32 + lane;
+      d[k][i] = 0.0f;
+      w[k][i] = make_uint2(0, 0);
+      if (have && piece < total) {
+        const int h = piece >> head_bits, e = (piece & ((1 << head_bits) - 1)) * kN;
+        const int8_t* q = q0 + (int64_t)h * a.c.page * a.c.D + e;
+        d[k][i] = d0[h * blocks];
+        if (kN == 8) w[k][i] = *reinterpret_cast<const uint2*>(q);
+        else w[k][i].x = *reinterpret_cast<const uint32_t*>(q);
+      }
     }
   }
+  T* out = static_cast<T*>(is_v ? a.v : a.k);
 #pragma unroll
-  for (int i = 0; i < kReadPieces; ++i) {
-    const int piece = (int)(item % groups) * (32 * kReadPieces) + i * 32 + lane;
-    if (piece >= total) continue;
-    float v[8];
+  for (int k = 0; k < kTokens; ++k) {
+    if (n0 + k >= a.N) break;
 #pragma unroll
-    for (int x = 0; x < 8; ++x)
-      v[x] = __fmul_rn((float)(int8_t)((x < 4 ? w[i].x : w[i].y) >> (8 * (x % 4))), d[i]);
-    uint4 o;
-    if (kN == 4)
-      o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                     __float_as_uint(v[3]));
-    else
-      o = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
-                     bf16_pair(v[6], v[7]));
-    *reinterpret_cast<uint4*>(out + (int64_t)piece * kN) = o;
+    for (int i = 0; i < kReadPieces; ++i) {
+      const int piece = (int)blockIdx.z * (32 * kReadPieces) + i * 32 + lane;
+      if (piece >= total) continue;
+      // a code q as the float 2^23 + 128 + q (its byte under that exponent), less 2^23 + 128
+      const uint32_t raised[2] = {w[k][i].x ^ 0x80808080u, w[k][i].y ^ 0x80808080u};
+      float v[8];
+#pragma unroll
+      for (int x = 0; x < kN; ++x)
+        v[x] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(raised[x / 4], 0x4b000000u, 0x7440 | (x % 4))),
+                                   8388736.0f), d[k][i]);
+      uint4 o;
+      if (kN == 4)
+        o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                       __float_as_uint(v[3]));
+      else
+        o = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                       bf16_pair(v[6], v[7]));
+      *reinterpret_cast<uint4*>(out + ((n0 + k) * total + piece) * kN) = o;
+    }
   }
+}
+
+template <typename T>
+cudaError_t launch_read(const ReadArgs& a, int head_bits, unsigned groups, const DeviceInfo& info,
+                        cudaStream_t stream) {
+  // Several tokens a warp where that leaves 32 warps to an SM.
+  const int tokens = 2 * a.N * groups >= (int64_t)info.sms * 32 * kReadTokens ? kReadTokens : 1;
+  const dim3 grid((unsigned)((a.N + kReadWarps * tokens - 1) / (kReadWarps * tokens)), 2, groups);
+  const dim3 block(kReadWarps * 32);
+  if (tokens > 1)
+    return launch_kernel(read_kernel<T, kReadTokens>, grid, block, 0, stream, a, head_bits);
+  return launch_kernel(read_kernel<T, 1>, grid, block, 0, stream, a, head_bits);
 }
 
 template <typename T>
@@ -522,7 +591,7 @@ static memra_status cache_args(int8_t* kq, float* kd, int8_t* vq, float* vd, int
   if (page_size < 16 || page_size % 16 != 0 || block < 1 || page_size % block != 0)
     return MEMRA_ERR_INVALID_ARG;
   if (D != 64 && D != 128 && D != 256) return MEMRA_ERR_UNSUPPORTED;
-  if (page_size > MEMRA_MAX_KV_PAGE || Hkv > 65535 || n_pages > INT32_MAX / page_size)
+  if (page_size > MEMRA_MAX_KV_PAGE || Hkv > 32767 || n_pages > INT32_MAX / page_size)
     return MEMRA_ERR_UNSUPPORTED;
   if (n_pages > 0 && (!kq || !kd || !vq || !vd)) return MEMRA_ERR_INVALID_ARG;
   if (!aligned(kq, 16) || !aligned(vq, 16) || !aligned(kd, 4) || !aligned(vd, 4))
@@ -536,6 +605,8 @@ static memra_status cache_args(int8_t* kq, float* kd, int8_t* vq, float* vd, int
   c->page = (int)page_size;
   c->D = (int)D;
   c->block = (int)block;
+  c->by_page = Divider((uint32_t)page_size);
+  c->by_block = Divider((uint32_t)block);
   return MEMRA_OK;
 }
 
@@ -567,12 +638,11 @@ extern "C" memra_status memra_kv_append_q8(const void* k, const void* v, int32_t
   a.stride_h = stride_h;
   a.status = dev_status;
   // A warp looks at one row where the rows leave warps to spare, at 16 of them otherwise
-  // (most rows of a long run begin none).
+  // (most rows of a long run begin none).  Taking several heads in one warp, to look at the
+  // slots once, was slower (8191 rows: 31 us with four heads, 30 with one).
   a.tile = T * 2 * Hkv <= (int64_t)info.sms * 64 ? 1 : 16;
-  const int64_t items = (T + a.tile - 1) / a.tile * 2 * Hkv;
-  const int64_t blocks = (items + kAppendWarps - 1) / kAppendWarps;
-  if (blocks > INT32_MAX / kAppendWarps) return MEMRA_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks);
+  const int64_t tiles = (T + a.tile - 1) / a.tile;
+  const dim3 grid((unsigned)((tiles + kAppendWarps - 1) / kAppendWarps), (unsigned)(2 * Hkv));
   const cudaError_t e = dtype == MEMRA_BF16 ? launch_append<uint16_t>(a, grid, stream)
                                             : launch_append<float>(a, grid, stream);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -603,14 +673,14 @@ extern "C" memra_status memra_kv_read_q8(const int32_t* slots, int64_t N, const 
   a.k = k;
   a.v = v;
   a.status = dev_status;
-  const int64_t pieces = Hkv * (D / (dtype == MEMRA_BF16 ? 8 : 4));
+  int head_bits = 0;
+  while ((1 << head_bits) < D / (dtype == MEMRA_BF16 ? 8 : 4)) ++head_bits;
+  const int64_t pieces = Hkv << head_bits;
   const int64_t groups = (pieces + 32 * kReadPieces - 1) / (32 * kReadPieces);
-  const int64_t blocks = (2 * N * groups + kReadWarps - 1) / kReadWarps;
-  if (blocks > INT32_MAX / kReadWarps) return MEMRA_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks), threads(kReadWarps * 32);
+  if (groups > 65535) return MEMRA_ERR_UNSUPPORTED;
   const cudaError_t e = dtype == MEMRA_BF16
-                            ? launch_kernel(read_kernel<uint16_t>, grid, threads, 0, stream, a, (uint32_t)groups)
-                            : launch_kernel(read_kernel<float>, grid, threads, 0, stream, a, (uint32_t)groups);
+                            ? launch_read<uint16_t>(a, head_bits, (unsigned)groups, info, stream)
+                            : launch_read<float>(a, head_bits, (unsigned)groups, info, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }
