@@ -177,22 +177,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
 
-// x / n for x < 2^31 by a product: with 2^l >= n > 2^(l-1) and m = ceil(2^(31+l) / n) the
-// product is above x * 2^(31+l) / n by less than x * n / n < 2^31 parts of 2^(31+l), too
-// little to reach the next whole quotient.
-struct Divider {
-  uint32_t m, shift;
-  explicit Divider(uint32_t n = 1) {
-    uint32_t l = 0;
-    while ((1u << l) < n) ++l;
-    m = (uint32_t)(((1ull << (31 + l)) + n - 1) / n);
-    shift = 31 + l;
-  }
-  __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
-    return (uint32_t)(((uint64_t)x * m) >> shift);
-  }
-};
-
 struct CacheArgs {
   int8_t *kq, *vq;
   float *kd, *vd;

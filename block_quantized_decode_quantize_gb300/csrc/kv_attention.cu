@@ -1,12 +1,8 @@
 // Attention over the paged 8-bit KV cache (layouts and arithmetic in memra.h).
 //
-// Work.  A unit is (request, cached head, group of 8 * kNT query rows); a row is a (query,
-// query head) pair that reads this cached head, so grouped heads share every byte.  The
-// keys of all units, in tiles of 128, form one list that is cut into equal parts for the
-// CTAs of one resident wave: every CTA streams the same number of bytes whatever the
-// lengths are.  The cut ends of a unit leave (maximum, sum, weighted values) in the
-// workspace, and the CTA that arrives last at the unit joins them in the order of the
-// keys, so results do not depend on timing.
+// The work list is that of kv_attention.cuh.  The cut ends of a unit leave (maximum, sum,
+// weighted values) in the workspace, and the CTA that arrives last at the unit joins them
+// in the order of the keys, so results do not depend on timing.
 //
 // A CTA's eight warps take strips of 16 keys in turn, each with its own ring of
 // cp.async stages and its own running statistics; nothing in the loop crosses warps.
@@ -23,65 +19,21 @@
 // weight.
 #include <atomic>
 
-#include <cuda_bf16.h>
-
-#include "common.cuh"
-
-#ifndef MEMRA_ATTN_UNIT_COST
-#define MEMRA_ATTN_UNIT_COST 3
-#endif
-#ifndef MEMRA_ATTN_MIN_SHARE
-#define MEMRA_ATTN_MIN_SHARE 1
-#endif
+#include "kv_attention.cuh"
 
 namespace memra {
 namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStrip = 16;                 // keys of a warp's step
-constexpr int kTile = kWarps * kStrip;     // keys of a CTA's step, the unit of the work list
-constexpr int kMaxCtas = 512;              // arrival counters at the workspace's start
-constexpr int kUnitCost = MEMRA_ATTN_UNIT_COST;  // list entries that stand for a unit's fixed time
-constexpr int kMinShare = MEMRA_ATTN_MIN_SHARE;  // list entries that a CTA gets at least
-
-#ifndef MEMRA_ATTN_MAX_PARTS
-#define MEMRA_ATTN_MAX_PARTS 64
+static_assert(kWarps * kStrip == kTile, "a CTA's step is an entry of the list");
+constexpr int kUnitCost = 3;   // entries of the list for a unit's fixed time (1: 37 us, 3: 34, 6: 35
+                               // for 16 sequences of 37 to 16000 tokens)
+#ifndef MEMRA_ATTN_WIDE
+#define MEMRA_ATTN_WIDE 16
 #endif
-constexpr int kMaxParts = MEMRA_ATTN_MAX_PARTS;  // CTAs to a unit, on average
-
-// A weight enters the product as p * (vd / ref) * 2^8 in fp16, ref a running maximum of vd
-// kept within a factor 4, p = 2^(s - m) with m within 5 of the running maximum: at most
-// 2^(5 + 2 + 8) = 2^15, and down to 2^-33 of the largest before it rounds to zero.
-constexpr float kMaxSlack = 5.0f;
-constexpr float kRefSlack = 4.0f;
-constexpr float kWeightScale = 256.0f;
-
-struct AttnArgs {
-  const void* q;
-  int64_t T, stride_t, stride_h;
-  const int8_t *kq, *vq;
-  const float *kd, *vd;
-  const int32_t *table, *kv_lens, *cu_q;
-  int64_t B, max_pages, window;
-  int32_t n_pages;
-  int Hq, Hkv, G, page, block;
-  uint32_t block_magic;  // ceil(2^22 / block): off / block = off * magic >> 22, off < 1024
-  uint32_t page_bytes, page_scales;  // of one page in a plane, all heads
-  int step_pages, step_off;          // kTile = step_pages * page + step_off
-  float scale;
-  void* out;
-  float* lse;
-  int* arrived;   // [kMaxCtas], zero between calls
-  float* parts;   // [2][CTAs][rows * (D + 2)]
-  int32_t* status;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+constexpr int kWideRows = MEMRA_ATTN_WIDE;  // average rows to a unit above which the wide kernel takes them
+constexpr int kMaxParts = 64;  // CTAs to a unit, on average
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -163,19 +115,6 @@ template <>
 struct Row<float> {
   static constexpr bool kPair = true;   // fp32: two fp16, 22 bits
 };
-__device__ __forceinline__ float value(const float* p) { return *p; }
-__device__ __forceinline__ float value(const uint16_t* p) {
-  return __uint_as_float((uint32_t)*p << 16);
-}
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(uint16_t* p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  uint2 u;
-  u.x = *reinterpret_cast<const uint32_t*>(&a);
-  u.y = *reinterpret_cast<const uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(p) = u;
-}
-
 template <typename T, int kD, int kNT>
 struct Shape {
   static constexpr int kRows = 8 * kNT;
@@ -192,76 +131,13 @@ struct Shape {
   static constexpr int kSmem = kBig + kQ + kStats;
 };
 
-// Where a request's part of the list lies, from its lengths.
-struct Request {
-  int len, n;        // tokens in the cache, queries
-  int row;           // the first query's row of q
-  int lo;            // first key tile's start
-  int tiles, groups;
-  bool over;         // longer than its row of the block table
-};
-
-template <int kRows>
-__device__ __forceinline__ Request request_of(const AttnArgs& a, int64_t b) {
-  Request r;
-  const int64_t cap = a.max_pages * a.page;
-  int64_t len = a.kv_lens[b];
-  const int row = a.cu_q[b];
-  r.over = len > cap;
-  len = len < 0 ? 0 : (len > cap ? cap : len);
-  int64_t n = (int64_t)a.cu_q[b + 1] - row;
-  n = n < 0 ? 0 : (n > a.T ? a.T : n);
-  r.len = (int)len;
-  r.n = (int)n;
-  r.row = row;
-  int64_t lo = a.window > 0 ? len - n + 1 - a.window : 0;
-  lo = lo < 0 ? 0 : lo / kStrip * kStrip;
-  r.lo = (int)lo;
-  r.tiles = n > 0 && len > lo ? (int)((len - lo + kTile - 1) / kTile) : 0;
-  r.groups = (int)((n * a.G + kRows - 1) / kRows);
-  return r;
-}
-
-// total entries in ctas equal parts (the first ones one longer): where part c begins, and
-// which part holds entry x.
-struct Cut {
-  int64_t total, q, r;
-  static __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-  }
-  __device__ __forceinline__ Cut(int64_t t, int ctas) : total(t), q(divide(t, ctas)), r(t - q * ctas) {}
-  __device__ __forceinline__ int64_t begin(int c) const { return c * q + min((int64_t)c, r); }
-  __device__ __forceinline__ int part_of(int64_t x) const {
-    const int64_t longer = r * (q + 1);
-    return (int)(x < longer ? divide(x, q + 1) : r + divide(x - longer, q));
-  }
-};
-
 // What a CTA keeps in shared memory while its strips want the registers: where it stands in
 // the list, and the unit at hand.
-struct Walk {
-  int64_t x, at, stop;
-  int b;
-  Request req;
-};
 struct Unit {
   int h, row0, rows, token0;
   int first_cta, parts;  // CTAs that hold a part of it
   int begins, whole;
 };
-
-template <typename T, int kD>
-__device__ __forceinline__ void write_nothing(const AttnArgs& a, int64_t row0, int64_t row1,
-                                              int thread, int threads) {
-  T* out = static_cast<T*>(a.out);
-  row0 = row0 < 0 ? 0 : row0;
-  row1 = row1 > a.T ? a.T : row1;
-  for (int64_t i = row0 * a.Hq * kD / 4 + thread; i < row1 * a.Hq * kD / 4; i += threads)
-    store4(out + i * 4, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
-  if (a.lse != nullptr)
-    for (int64_t i = row0 * a.Hq + thread; i < row1 * a.Hq; i += threads)
-      a.lse[i] = __int_as_float(0xff800000);
-}
 
 template <typename T, int kD, int kNT>
 __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attention_kernel(AttnArgs a) {
@@ -281,9 +157,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
   float* row_scale = row_l + kRows;
   float* row_raise = row_scale + kRows;
   int* row_limit = reinterpret_cast<int*>(row_raise + kRows);
-  __shared__ int64_t scan[kWarps], found_at;
-  __shared__ int found_b, last_part;
-  __shared__ Request found;
+  __shared__ int last_part;
   __shared__ Walk walk;
   __shared__ Unit unit_at_hand;
 
@@ -293,116 +167,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
   const int g = lane >> 2, t4 = lane & 3;
   const int cta = blockIdx.x;
 
-  // ---- the list: every CTA sums the requests' entries and finds its own part ----
-  // A unit takes kUnitCost entries and one for each tile.
-  auto entries_of = [&](const Request& r) {
-    return r.tiles > 0 ? (int64_t)(r.tiles + kUnitCost) * r.groups * a.Hkv : (int64_t)0;
-  };
-  int64_t total = 0, first = 0, w = 0, sum = 0;
-  int ctas = 0;
-  Request r{};
-  int64_t no_row = a.B > 0 ? a.cu_q[a.B] : 0;  // first row that no request owns
-  int b;
-  int64_t at;  // list index of request b's first entry
-  Request req;
-  if (a.B <= 32) {
-    // a lane to a request, every warp for itself: no barrier
-    if (lane < a.B) {
-      r = request_of<kRows>(a, lane);
-      w = entries_of(r);
-      if (cta == 0 && warp == 0 && r.over && a.status != nullptr) atomicOr(a.status, 1);
-    }
-    sum = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(kFullMask, sum, o);
-      if (lane >= o) sum += u;
-    }
-    total = __shfl_sync(kFullMask, sum, 31);
-    const uint32_t empty = __ballot_sync(kFullMask, w == 0 && r.n > 0);
-    for (uint32_t todo = empty; todo != 0; todo &= todo - 1) {
-      const int e = __ffs(todo) - 1;
-      if (e % gridDim.x == cta) write_nothing<T, kD>(a, a.cu_q[e], a.cu_q[e + 1], tid, kThreads);
-    }
-    ctas = (int)min((int64_t)gridDim.x, (total + kMinShare - 1) / kMinShare);
-    for (no_row += cta; no_row < a.T; no_row += gridDim.x)
-      write_nothing<T, kD>(a, no_row, no_row + 1, tid, kThreads);
-    if (cta >= ctas) return;
-    first = Cut(total, ctas).begin(cta);
-    b = __ffs(__ballot_sync(kFullMask, w > 0 && sum - w <= first && first < sum)) - 1;
-    at = __shfl_sync(kFullMask, sum - w, b);
-    req.len = __shfl_sync(kFullMask, r.len, b);
-    req.n = __shfl_sync(kFullMask, r.n, b);
-    req.row = __shfl_sync(kFullMask, r.row, b);
-    req.lo = __shfl_sync(kFullMask, r.lo, b);
-    req.tiles = __shfl_sync(kFullMask, r.tiles, b);
-    req.groups = __shfl_sync(kFullMask, r.groups, b);
-  } else {
-    for (int pass = 0; pass < 2; ++pass) {
-      int64_t before = 0;
-      for (int64_t base = 0; base < a.B; base += kThreads) {
-        const int64_t b = base + tid;
-        if (pass == 0 || a.B > kThreads) {  // one chunk's sums stay in registers
-          w = 0;
-          bool empty = false;
-          if (b < a.B) {
-            r = request_of<kRows>(a, b);
-            w = entries_of(r);
-            empty = w == 0 && r.n > 0;
-            if (pass == 0 && cta == 0 && r.over && a.status != nullptr) atomicOr(a.status, 1);
-          }
-          if (pass == 0) {  // rows of requests without keys, each request by one CTA
-            uint32_t todo = __ballot_sync(kFullMask, empty && b % gridDim.x == cta);
-            while (todo != 0) {
-              const int64_t e = base + warp * 32 + (__ffs(todo) - 1);
-              todo &= todo - 1;
-              write_nothing<T, kD>(a, a.cu_q[e], a.cu_q[e + 1], lane, 32);
-            }
-          }
-          sum = w;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(kFullMask, sum, o);
-            if (lane >= o) sum += u;
-          }
-          if (lane == 31) scan[warp] = sum;
-          __syncthreads();
-          int64_t chunk = 0;
-          for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) sum += scan[i];
-            chunk += scan[i];
-          }
-          sum += before;
-          before += chunk;
-        }
-        if (pass == 1 && w > 0 && sum - w <= first && first < sum) {
-          found_b = (int)b;
-          found_at = sum - w;
-          found = r;
-        }
-        __syncthreads();
-      }
-      if (pass == 0) {
-        total = before;
-        ctas = (int)min((int64_t)gridDim.x, (total + kMinShare - 1) / kMinShare);
-        // rows that no request owns
-        for (no_row += cta; no_row < a.T; no_row += gridDim.x)
-          write_nothing<T, kD>(a, no_row, no_row + 1, tid, kThreads);
-        if (cta >= ctas) return;
-        first = Cut(total, ctas).begin(cta);
-      }
-    }
-    b = found_b;
-    at = found_at;
-    req = found;
-  }
-  if (tid == 0) {
-    walk.x = first;
-    walk.at = at;
-    walk.stop = Cut(total, ctas).begin(cta + 1);
-    walk.b = b;
-    walk.req = req;
-  }
+  int ctas;
+  int64_t total;
+  if (!locate<T, kD, kRows, kUnitCost, kThreads>(a, &walk, &ctas, &total)) return;
 
   const uint32_t my_ring = smem_addr(ring) + warp * Sh::kStages * Sh::kStage;
   // Lane constants of the ring: where this lane's 16 bytes of a copy go (row i * 512 bytes
@@ -421,14 +188,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
     __syncthreads();  // the ring, the queries and the statistics are free again
     const int64_t x = walk.x, stop = walk.stop;
     if (x >= stop) break;
-    at = walk.at;
-    b = walk.b;
-    req = walk.req;
-    w = entries_of(req);
+    int64_t at = walk.at;
+    int b = walk.b;
+    Request req = walk.req;
+    int64_t w = entries_of<kUnitCost>(a, req);
     while (x >= at + w) {
       at += w;
       req = request_of<kRows>(a, ++b);
-      w = entries_of(req);
+      w = entries_of<kUnitCost>(a, req);
     }
     // ---- this unit: cached head h, rows [row0, row0 + kRows) of the request's n * G ----
     const int unit_size = req.tiles + kUnitCost;
@@ -473,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
     uint32_t hidden = 0;  // bit i: stage i's strip has no page
     // The page of a strip is looked up one strip before its copies are issued (those of the
     // first strips at once).
-    int look = 0, look_at = key / a.page, look_off = key % a.page;
+    int look = 0, look_at = (int)a.by_page((uint32_t)key), look_off = key - look_at * a.page;
     int issued = 0, write_slot = 0;
     uint32_t write_at = my_ring;
 
@@ -506,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
           }
           cp4(write_at + 2 * kStrip * kD + lane * 4,
               scale_head + (uint64_t)(uint32_t)page * a.page_scales +
-                  (((uint32_t)(off + (lane & 15)) * a.block_magic) >> 22));
+                  a.by_block((uint32_t)(off + (lane & 15))));
         } else {
           hidden |= 1u << write_slot;
           if (lane == 0 && a.status != nullptr) atomicOr(a.status, 1);
@@ -987,6 +754,7 @@ template <typename T>
 cudaError_t launch_attention(const AttnArgs& a, int D, const DeviceInfo& info, cudaStream_t stream) {
   const int64_t rows = a.B > 0 ? (a.T * a.G + a.B - 1) / a.B : 1;
   const int64_t max_tiles = a.max_pages * a.page / kTile + 1 + kUnitCost;
+  if (sizeof(T) == 2 && D <= 128 && rows > kWideRows) return launch_wide_attention(a, D, rows, info, max_tiles, stream);
   if (D == 64) {
     if (rows <= 8) return launch_shape<T, 64, 1>(a, info, max_tiles, stream);
     if (rows <= 16) return launch_shape<T, 64, 2>(a, info, max_tiles, stream);
@@ -1058,7 +826,8 @@ extern "C" memra_status memra_kv_attention_q8(
   a.G = (int)(Hq / Hkv);
   a.page = (int)page_size;
   a.block = (int)block;
-  a.block_magic = (uint32_t)(((1u << 22) + block - 1) / block);
+  a.by_page = Divider((uint32_t)page_size);
+  a.by_block = Divider((uint32_t)block);
   a.page_bytes = (uint32_t)(Hkv * page_size * D);
   a.page_scales = (uint32_t)(Hkv * (page_size / block));
   a.step_pages = kTile / (int)page_size;

@@ -1,0 +1,795 @@
+// Attention over the paged 8-bit KV cache for many query rows: speculative verify, chunks
+// of a prompt, wide groups of heads.  bf16 queries, D 64 or 128; kv_attention.cu has the
+// rest.
+//
+// With tens of rows to a cached head, the work is two matrix products and goes to the
+// tcgen05 tensor cores: S [128 rows x 128 keys] = Q K^T and O [128 rows x D] += P V, both in
+// fp16 with fp32 accumulators in tensor memory.  Warps of one CTA an SM have three tasks:
+//   7 warps bring a tile of codes from the cache (a tile ahead, in registers), turn them
+//     into fp16 exactly and lay K and V out in shared memory as the products read them
+//     (rows of 64 dims, 128-byte swizzle; two stages);
+//   1 thread issues the products: S of the next tile before O of this one;
+//   8 warps turn scores into weights, four to every other tile, each group with its own
+//     statistics and its own accumulators, so that neither waits for the other; a thread
+//     has a row and its keys, and the weights go back to tensor memory, over the scores,
+//     as the second product's operand.
+// Units of up to 64 rows put every row into the product twice: each copy's thread takes
+// half of the keys (and gives weight 0 to the others), which spreads the exponentials, 16
+// a cycle on an SM, over all of its quarters.
+// Accumulators stay in tensor memory for a unit's whole range of keys; they are rescaled
+// only when a maximum moves by more than the slack, and the two groups' (and copies') are
+// joined at the end.  Scales never meet the codes: kd multiplies a score, vd a weight.
+#include <atomic>
+
+#include "kv_attention.cuh"
+
+namespace memra {
+namespace {
+
+constexpr int kLanes = 128;  // rows of a product
+constexpr int kSoftWarps = 8, kFeedWarps = 7;  // and one: 16 warps may have 128 registers
+constexpr int kSoftThreads = kSoftWarps * 32, kFeedThreads = kFeedWarps * 32;
+constexpr int kThreads = kSoftThreads + kFeedThreads + 32;
+constexpr float kLeastRef = 1e-25f;  // keeps 2^8 / ref times a row's sum in range; scales below are next to nothing
+constexpr int kCost = 3;  // entries of the list for a unit's fixed time
+
+// Tensor memory columns: scores of two tiles (the weights, two fp16 a column, over the last
+// half of them), then each group's accumulators.
+constexpr uint32_t kTmemColumns = 512, kTmemO = 256, kTmemGroup = 128, kTmemWeights = kTile / 2;
+
+// kRows: a unit's rows, 64 (two lanes to a row) or 128.
+template <int kD, int kRows>
+struct Shape {
+  static constexpr int kOperand = kTile * kD * 2;       // K or V of a tile in fp16
+  static constexpr int kQ = kLanes * kD * 2;
+  static constexpr int kQAt = 4 * kOperand;             // after two stages of K, V
+  static constexpr int kScalesAt = kQAt + kQ;           // kd [2][128], vd [2][128]
+  static constexpr int kUnitAt = kScalesAt + 4 * kTile * 4;  // amax [group][lane], [2 units][m, l][group][lane]
+  static constexpr int kMiscAt = kUnitAt + 10 * kLanes * 4;      // vd maxima [2][4], hidden [2][8]
+  static constexpr int kBarsAt = kMiscAt + 64;
+  static constexpr int kSmem = kBarsAt + 16 * 8 + 1024;          // and room to align to 1024
+  static constexpr int kPart = 2 * kRows + kRows * kD;           // m, l, values: floats
+};
+
+// ---- tcgen05 ----
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// D [128 x N] (+)= A [128 x 16] B [N x 16]^T, A from shared or tensor memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(what),
+      "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(what),
+      "r"((uint32_t)add)
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// Waits for this thread's loads; r: what they loaded, which nothing may use before.
+template <int kN>
+__device__ __forceinline__ void tmem_wait_loads(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Plain shared-memory writes become visible to the products.
+__device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Shared-memory operand: rows of 64 fp16 under the 128-byte swizzle, eight rows (1024
+// bytes) after one another; `lead` parts neighbouring blocks of 64 columns where those are
+// the product's rows.
+__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead) {
+  return (uint64_t)((at >> 4) & 0x3fff) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         1ull << 46 | 2ull << 61;
+}
+// kind::f16 with fp16 operands and fp32 sums, 128 rows, N columns; b_rows: B's rows (the
+// keys) are contiguous along N.
+template <int N, bool b_rows>
+constexpr uint32_t kProduct = 1u << 4 | (b_rows ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
+                              (uint32_t)(kLanes >> 4) << 24;
+
+// One CTA's range of one unit.
+struct Segment {
+  int b, h, row0, rows, token0;
+  int key0, key_stop, tiles;             // its keys, in tiles of kTile
+  int limit_min, limit_max, low_max;     // what the first and the last row see
+  int len, n;
+  bool begins, whole;
+  int64_t unit_at, unit_stop;
+};
+
+template <int kRows>
+struct Walker {
+  Walk w;
+  __device__ __forceinline__ bool next(const AttnArgs& a, Segment* s) {
+    if (w.x >= w.stop) return false;
+    int64_t entries = entries_of<kCost>(a, w.req);
+    while (w.x >= w.at + entries) {
+      w.at += entries;
+      w.req = request_of<kRows>(a, ++w.b);
+      entries = entries_of<kCost>(a, w.req);
+    }
+    const Request& req = w.req;
+    const int size = req.tiles + kCost;
+    const int unit = (int)Cut::divide(w.x - w.at, size);
+    s->unit_at = w.at + (int64_t)unit * size;
+    s->unit_stop = s->unit_at + size;
+    const int64_t x_stop = s->unit_stop < w.stop ? s->unit_stop : w.stop;
+    const int tile0 = max((int)(w.x - s->unit_at) - kCost, 0);
+    const int tile1 = (int)(x_stop - s->unit_at) - kCost;
+    w.x = x_stop;
+    if (tile1 <= 0) return false;  // the part ends within the unit's fixed entries
+    s->begins = tile0 == 0;
+    s->whole = s->begins && x_stop == s->unit_stop;
+    s->b = w.b;
+    s->h = unit / req.groups;
+    s->row0 = unit % req.groups * kRows;
+    s->rows = min(kRows, req.n * a.G - s->row0);
+    s->token0 = req.row;
+    s->len = req.len;
+    s->n = req.n;
+    s->limit_min = min(req.len, req.len - req.n + s->row0 / a.G + 1);
+    s->limit_max = min(req.len, req.len - req.n + (s->row0 + s->rows - 1) / a.G + 1);
+    s->low_max = a.window > 0 ? (int)max((int64_t)0, s->limit_max - a.window) : 0;
+    s->key0 = req.lo + tile0 * kTile;
+    s->key_stop = min(req.lo + tile1 * kTile, s->limit_max);
+    s->tiles = s->key0 < s->key_stop ? (s->key_stop - s->key0 + kTile - 1) / kTile : 0;
+    return true;
+  }
+};
+
+// A whole warp's bounded wait, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(kFullMask, mbar_wait(bar, parity, abort));
+}
+
+struct Bars {  // shared-memory addresses
+  uint32_t full[2], empty[2], scores[2], weights[2], q, pair[4], soft, done;
+};
+
+// ---- 7 warps: codes from the cache to fp16 operands ----
+template <int kD, int kRows>
+__device__ __forceinline__ void feed(const AttnArgs& a, Walker<kRows> walker, uint8_t* smem, const Bars& bars,
+                                     volatile int* abort) {
+  using Sh = Shape<kD, kRows>;
+  constexpr int kChunks = kD / 16;  // 16-code pieces of a row
+  constexpr int kLoads = (kTile * kChunks + kFeedThreads - 1) / kFeedThreads;  // of K, and of V, a thread
+  constexpr int kStep = kFeedThreads / kChunks;  // rows from one of a thread's pieces to the next
+  static_assert(kFeedThreads % kChunks == 0 && 2 * kTile - kFeedThreads == 32, "pieces and scales");
+  const int tid = threadIdx.x - kSoftThreads, lane = tid & 31, warp = tid >> 5;
+  // Eight neighbouring lanes write pieces of two rows' same block of 64 dims: the rows'
+  // swizzles differ in the lowest bit, so they meet in no bank.
+  const int row = kD == 64 ? tid >> 2 : (tid >> 4) * 2 + ((tid >> 2) & 1);
+  const int chunk = kD == 64 ? tid & 3 : (tid & 3) + ((tid >> 3) & 1) * 4;
+  // Scales: kd of key tid (tid < 128), else vd of key tid - 128; the last 32 vd go to warp 0
+  // as a second one.
+  const bool scale_v = tid >= kTile;
+  const int scale_key = tid & (kTile - 1), scale_key2 = kTile - 32 + lane;
+  float* scales = reinterpret_cast<float*>(smem + Sh::kScalesAt);  // [kd, vd][stage][key]
+  float* v_most = reinterpret_cast<float*>(smem + Sh::kMiscAt);    // [stage][4]
+  uint8_t* hidden = smem + Sh::kMiscAt + 32;                       // [stage][8]
+  const int blocks = (int)a.by_block((uint32_t)a.page);
+
+  Segment seg;
+  int tile = 0;
+  bool more = true;
+  seg.tiles = 0;
+  struct Ref {
+    int key, stop, h;      // first key; keys from stop on are not there
+    int32_t page[kLoads], off[kLoads], scale_page, scale_page2;
+  };
+  // The next tile of the CTA's range and its pages (-1: keys that are not there).
+  auto next_ref = [&](Ref& r) {
+    while (more && tile >= seg.tiles) {
+      more = walker.next(a, &seg);
+      tile = 0;
+    }
+    if (!more) return false;
+    r.key = seg.key0 + tile * kTile;
+    r.stop = seg.key_stop;
+    r.h = seg.h;
+    ++tile;
+    const int32_t* pages = a.table + (int64_t)seg.b * a.max_pages;
+    const int there = (r.stop + kStrip - 1) / kStrip * kStrip;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int k = r.key + j * kStep + row;
+      const int in = (int)a.by_page((uint32_t)k);
+      r.page[j] = j * kStep + row < kTile && k < there ? pages[in] : -1;
+      r.off[j] = k - in * a.page;
+    }
+    const int k = r.key + scale_key, k2 = r.key + scale_key2;
+    r.scale_page = k < there ? pages[a.by_page((uint32_t)k)] : -1;
+    r.scale_page2 = warp == 0 && k2 < there ? pages[a.by_page((uint32_t)k2)] : -1;
+    return true;
+  };
+  uint4 k_data[kLoads], v_data[kLoads];
+  float scale = 0.0f, scale2 = 0.0f;
+  bool gone = false;  // the strip of scale_key has no page
+  const int64_t v_minus_k = a.vq - a.kq;
+  auto load_piece = [&](const Ref& r, int j) {
+    k_data[j] = v_data[j] = make_uint4(0, 0, 0, 0);
+    if ((uint32_t)r.page[j] < (uint32_t)a.n_pages) {
+      const int8_t* at = a.kq + (uint64_t)(uint32_t)r.page[j] * a.page_bytes +
+                         (uint32_t)((r.h * a.page + r.off[j]) * kD + chunk * 16);
+      k_data[j] = ld_cg_16B(at);
+      v_data[j] = ld_cg_16B(at + v_minus_k);
+    }
+  };
+  auto scale_of = [&](const float* plane, const Ref& r, int key, int32_t page) {
+    const int k = r.key + key;
+    const int off = k - (int)a.by_page((uint32_t)k) * a.page;
+    if ((uint32_t)page >= (uint32_t)a.n_pages || k >= r.stop) return 0.0f;
+    return __ldcg(plane + (int64_t)(uint32_t)page * a.page_scales + (int64_t)r.h * blocks + a.by_block((uint32_t)off));
+  };
+  auto load_scales = [&](const Ref& r) {
+    gone = (uint32_t)r.scale_page >= (uint32_t)a.n_pages && r.key + scale_key < r.stop;
+    scale = scale_of(scale_v ? a.vd : a.kd, r, scale_key, r.scale_page);
+    if (warp == 0) scale2 = scale_of(a.vd, r, scale_key2, r.scale_page2);
+  };
+  // 16 codes as fp16 (the byte under the exponent of 1024 is 1024 + 128 + code) to two
+  // neighbouring 16-byte units of their row.
+  auto put = [&](uint8_t* base, int key, const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t y = w[i] ^ 0x80808080u;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint32_t z = __byte_perm(y, 0x64646464u, p ? 0x4342u : 0x4140u);
+        const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&z), __half2half2(__ushort_as_half(0x6480)));
+        h[2 * i + p] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+    uint8_t* line = base + (chunk >> 2) * (kTile * 128) + key * 128;
+    const int at = ((2 * (chunk & 3)) ^ (key & 7)) << 4;
+    *reinterpret_cast<uint4*>(line + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(line + (at ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+  };
+
+  // Each piece's register takes the next tile's as soon as it is written.
+  Ref next, after;
+  bool have = next_ref(next);
+  if (have) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) load_piece(next, j);
+    load_scales(next);
+  }
+  bool ahead = have && next_ref(next);
+  for (uint32_t g = 0; have; ++g) {
+    const bool beyond = ahead && next_ref(after);  // its pages are there a tile later
+    const int stage = g & 1;
+    if (g >= 2 && !warp_wait(bars.empty[stage], ((g >> 1) & 1) ^ 1, abort)) return;
+    uint8_t* k_at = smem + stage * 2 * Sh::kOperand;
+    float* kd = scales + stage * kTile;
+    float* vd = scales + (2 + stage) * kTile;
+    (scale_v ? vd : kd)[scale_key] = scale;
+    if (warp == 0) vd[scale_key2] = scale2;
+    if (scale_v || warp == 0) {
+      const uint32_t most = __reduce_max_sync(kFullMask, __float_as_uint(scale_v ? scale : scale2));
+      if (lane == 0) v_most[stage * 4 + (warp + 3) % 7] = __uint_as_float(most);
+    }
+    if (!scale_v && (lane & 15) == 0) {
+      hidden[stage * 8 + scale_key / kStrip] = gone ? 1 : 0;
+      if (gone && a.status != nullptr) atomicOr(a.status, 1);
+    }
+    if (ahead) load_scales(next);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int key = j * kStep + row;
+      if (key < kTile) {
+        put(k_at, key, k_data[j]);
+        put(k_at + Sh::kOperand, key, v_data[j]);
+      }
+      if (ahead) load_piece(next, j);
+    }
+    async_proxy_fence();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars.full[stage]);
+    have = ahead;
+    ahead = beyond;
+    next = after;
+  }
+}
+
+// ---- one thread: the products ----
+template <int kD, int kRows>
+__device__ __forceinline__ void multiply(const AttnArgs& a, Walker<kRows> walker, uint32_t smem, uint32_t tmem,
+                                         const Bars& bars, volatile int* abort) {
+  using Sh = Shape<kD, kRows>;
+  constexpr uint32_t kScores = kProduct<kTile, false>, kValues = kProduct<kD, true>;
+  Segment seg;
+  uint32_t g = 0, unit = 0;
+  auto scores = [&](uint32_t t) {
+    const uint32_t k = smem + (t & 1) * 2 * Sh::kOperand, q = smem + Sh::kQAt;
+#pragma unroll
+    for (int s = 0; s < kD / 16; ++s)
+      tc_mma_ss(tmem + (t & 1) * kTile, operand(q + (s >> 2) * (kLanes * 128) + (s & 3) * 32, 16),
+                operand(k + (s >> 2) * (kTile * 128) + (s & 3) * 32, 16), kScores, s > 0);
+    tc_commit(bars.scores[t & 1]);
+  };
+  while (walker.next(a, &seg)) {
+    if (seg.tiles == 0) continue;
+    if (!mbar_wait(bars.q, unit & 1, abort)) return;
+    ++unit;
+    if (!mbar_wait(bars.full[g & 1], (g >> 1) & 1, abort)) return;
+    tc_after();
+    scores(g);
+    for (int t = 0; t < seg.tiles; ++t, ++g) {
+      if (t + 1 < seg.tiles) {
+        if (!mbar_wait(bars.full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort)) return;
+        tc_after();
+        scores(g + 1);
+      }
+      if (!mbar_wait(bars.weights[g & 1], (g >> 1) & 1, abort)) return;
+      tc_after();
+      const uint32_t v = smem + (g & 1) * 2 * Sh::kOperand + Sh::kOperand;
+#pragma unroll
+      for (int s = 0; s < kTile / 16; ++s)  // 16 keys are two groups of eight rows
+        tc_mma_ts(tmem + kTmemO + (g & 1) * kTmemGroup, tmem + (g & 1) * kTile + kTmemWeights + s * 8,
+                  operand(v + s * 2048, kTile * 128), kValues, t > 1 || s > 0);
+      tc_commit(bars.empty[g & 1]);
+    }
+  }
+}
+
+// ---- 8 warps: scores to weights, results ----
+template <int kD, int kRows>
+__device__ __forceinline__ void soften(const AttnArgs& a, Walker<kRows> walker, uint8_t* smem, uint32_t tmem,
+                                       const Bars& bars, volatile int* abort, int64_t total, int ctas,
+                                       int* last_part) {
+  using Sh = Shape<kD, kRows>;
+  constexpr int kCopies = kLanes / kRows;
+  constexpr int kKeys = kTile / kCopies;  // of a tile, a thread
+  constexpr int kStepKeys = 64;           // of these, at a time in registers
+  constexpr int kDims = kD / 2;           // of a row, a thread, at a unit's two ends
+  const float kInf = __int_as_float(0x7f800000);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int quarter = warp & 3, group = warp >> 2, at_lane = quarter * 32 + lane;
+  const int row = quarter * (kRows / 4) + lane % (kRows / 4), copy = lane / (kRows / 4);
+  const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+  const uint32_t s_at = lanes + group * kTile, o_at = lanes + kTmemO + group * kTmemGroup;
+  const float4* kd = reinterpret_cast<const float4*>(smem + Sh::kScalesAt) + (group * kTile + copy * kKeys) / 4;
+  const float4* vd = kd + 2 * kTile / 4;
+  const float4* v_most = reinterpret_cast<const float4*>(smem + Sh::kMiscAt) + group;
+  const uint2* hidden = reinterpret_cast<const uint2*>(smem + Sh::kMiscAt + 32) + group;
+  float* unit_x = reinterpret_cast<float*>(smem + Sh::kUnitAt);
+  uint32_t pair_phase = 0, soft_phase = 0, units = 0, g0 = 0;  // g0: the CTA's tiles before this unit
+  // With the other group's warp of the same lanes; false when a wait ran out somewhere.
+  auto pair_sync = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars.pair[quarter]);
+    const bool ok = warp_wait(bars.pair[quarter], pair_phase, abort);
+    pair_phase ^= 1;
+    return ok;
+  };
+  auto soft_sync = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars.soft);
+    const bool ok = warp_wait(bars.soft, soft_phase, abort);
+    soft_phase ^= 1;
+    return ok;
+  };
+
+  Segment seg;
+  for (; walker.next(a, &seg); g0 += seg.tiles) {
+    const bool active = quarter * (kRows / 4) < seg.rows;  // the warp has rows
+    const int i = (seg.row0 + row) / a.G, hq = seg.h * a.G + (seg.row0 + row) % a.G;
+    const int64_t token = (int64_t)seg.token0 + i;
+    const bool real = row < seg.rows && token >= 0 && token < a.T;
+    const int limit = min(seg.len, seg.len - seg.n + i + 1);
+    float qs = 1.0f;
+    if (seg.tiles > 0) {
+      // This thread's half of its query, scaled by a power of two that brings the row's
+      // largest value to [2^13, 2^14) (bf16's eight bits fit fp16 then), |scale| kept apart.
+      uint4 raw[kDims / 8];
+      float amax = 0.0f;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (real ? token * a.stride_t + hq * a.stride_h : 0) + group * kDims;
+#pragma unroll
+      for (int k = 0; k < kDims / 8; ++k) {
+        raw[k] = real && active ? *reinterpret_cast<const uint4*>(src + 8 * k) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+      }
+      unit_x[group * kLanes + at_lane] = amax;
+      if (!pair_sync()) return;
+      amax = fmaxf(amax, unit_x[(group ^ 1) * kLanes + at_lane]);
+      int e = (int)(__float_as_uint(amax) >> 23) - 127;
+      e = e < -100 ? -100 : e;
+      float up = __int_as_float((13 - e + 127) << 23);
+      if (amax > 0.0f && a.scale != 0.0f) qs = fabsf(a.scale) * 1.44269504088896341f * __int_as_float((e - 13 + 127) << 23);
+      up = a.scale == 0.0f ? 0.0f : copysignf(up, a.scale);
+      uint8_t* q_at = smem + Sh::kQAt + at_lane * 128;
+#pragma unroll
+      for (int k = 0; k < kDims / 8; ++k) {
+        const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __half2 v = __floats2half2_rn(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
+          h[j] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        const int unit = group * (kDims / 8) + k;  // of the row's units of eight dims
+        *reinterpret_cast<uint4*>(q_at + (unit >> 3) * (kLanes * 128) + (((unit & 7) ^ (lane & 7)) << 4)) =
+            make_uint4(h[0], h[1], h[2], h[3]);
+      }
+    }
+    if (seg.tiles > 0) {
+      async_proxy_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars.q);
+    }
+
+    // Weights are taken as 2^(x - m) with the scales' reference in m = most - log2(2^8 / ref),
+    // most the reference of the row's maximum (bar: most + kMaxSlack, -inf until there is
+    // one), so that l and O are in the same units.
+    float most = 0.0f, bar = -kInf, m = 0.0f, l = 0.0f, ref = 0.0f, shift = 0.0f;
+    const int t0 = (int)((g0 ^ group) & 1);  // the group's first tile
+    for (int t = t0; t < seg.tiles; t += 2) {
+      const uint32_t phase = ((g0 + t) >> 1) & 1;
+      if (!warp_wait(bars.full[group], phase, abort)) return;  // the scales
+      if (!warp_wait(bars.scores[group], phase, abort)) return;
+      if (active) {
+        tc_after();
+        const int key = seg.key0 + t * kTile + copy * kKeys;
+        const uint2 gone = *hidden;  // a byte to a strip
+        const bool plain = seg.key0 + (t + 1) * kTile <= seg.limit_min && seg.key0 + t * kTile >= seg.low_max &&
+                           (gone.x | gone.y) == 0;
+        float s[kStepKeys];
+        // Scores of kStepKeys keys from `first` on (of this thread's), without the row's scale.
+        auto fetch = [&](int first) {
+          uint32_t bits[kStepKeys];
+          if (kCopies == 1) {
+            tmem_load32(s_at + first, bits);
+            tmem_load32(s_at + first + 32, bits + 32);
+            tmem_wait_loads<kStepKeys>(bits);
+          } else {  // a lane reads its copy's keys: all lanes of a load read the same columns
+            uint32_t other[32];
+#pragma unroll
+            for (int c = 0; c < kStepKeys; c += 32) {
+              tmem_load32(s_at + c, bits + c);
+              tmem_load32(s_at + kKeys + c, other);
+              tmem_wait_loads<32>(bits + c);
+              tmem_wait_loads<32>(other);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) bits[c + j] = copy ? other[j] : bits[c + j];
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kStepKeys; j += 4) {
+            const float4 d = kd[(first + j) / 4];
+            s[j] = __uint_as_float(bits[j]) * d.x;
+            s[j + 1] = __uint_as_float(bits[j + 1]) * d.y;
+            s[j + 2] = __uint_as_float(bits[j + 2]) * d.z;
+            s[j + 3] = __uint_as_float(bits[j + 3]) * d.w;
+          }
+          if (!plain) {
+#pragma unroll
+            for (int j = 0; j < kStepKeys; ++j) {
+              const int k = key + first + j, strip = (copy * kKeys + first + j) / kStrip;
+              const bool seen = k < limit && (a.window == 0 || k >= limit - a.window) &&
+                                (((strip & 4 ? gone.y : gone.x) >> (8 * (strip & 3))) & 1u) == 0;
+              s[j] = seen ? s[j] : -kInf;
+            }
+          }
+        };
+        float top = -kInf;
+        for (int first = 0; first < kKeys; first += kStepKeys) {
+          fetch(first);
+          float y[4] = {-kInf, -kInf, -kInf, -kInf};
+#pragma unroll
+          for (int j = 0; j < kStepKeys; ++j) y[j & 3] = fmaxf(y[j & 3], s[j]);
+          top = fmaxf(top, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+        }
+        if (kCopies == 2) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 16));
+        top *= qs;
+        const float4 vm = *v_most;
+        const float v_top = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
+        if (__any_sync(kFullMask, top > bar) || v_top > kRefSlack * ref) {
+          float f = 1.0f;
+          if (v_top > ref) {
+            ref = v_top;
+            const float new_shift = 8.0f - log2f(fmaxf(ref, kLeastRef));
+            f = ex2(new_shift - shift);
+            shift = new_shift;
+          }
+          if (bar == -kInf ? top > bar : top > most) {  // a new maximum
+            f = bar == -kInf ? 0.0f : f * ex2(most - top);
+            most = top;
+            bar = most + kMaxSlack;
+          }
+          m = most - shift;
+          l *= f;
+          if (t > 1) {  // the accumulators, once the group's last product is done
+            if (!warp_wait(bars.empty[group], phase ^ 1, abort)) return;
+            tc_after();
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 32) {
+              uint32_t o[32];
+              tmem_load32(o_at + c, o);
+              tmem_wait_loads<32>(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_store32(o_at + c, o);
+            }
+          }
+        }
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        // Weights over the last half of the scores, where they come in two steps those of the
+        // last keys first: they take columns whose scores are read.
+#pragma unroll
+        for (int first = kKeys - kStepKeys; first >= 0; first -= kStepKeys) {
+          if (kKeys > kStepKeys && first == 0) fetch(first);
+          uint32_t p[kStepKeys / 2];
+#pragma unroll
+          for (int j = 0; j < kStepKeys; j += 4) {
+            const float4 d = vd[(first + j) / 4];
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[k] = ex2(fmaf(s[j + k], qs, -m));
+              sum[k] += x[k];
+            }
+            const __half2 lo = __floats2half2_rn(x[0] * d.x, x[1] * d.y), hi = __floats2half2_rn(x[2] * d.z, x[3] * d.w);
+            p[j / 2] = *reinterpret_cast<const uint32_t*>(&lo);
+            p[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+          }
+          if (kCopies == 1) {
+            tmem_store32(s_at + kTmemWeights + first / 2, p);
+          } else {  // this copy's keys, and 0 for the other's
+            uint32_t z[kStepKeys / 2];
+#pragma unroll
+            for (int j = 0; j < kStepKeys / 2; ++j) z[j] = copy ? 0u : p[j];
+            tmem_store32(s_at + kTmemWeights, z);
+#pragma unroll
+            for (int j = 0; j < kStepKeys / 2; ++j) z[j] = copy ? p[j] : 0u;
+            tmem_store32(s_at + kTmemWeights + kKeys / 2, z);
+          }
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_stores();
+        tc_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars.weights[group]);
+    }
+
+    // ---- the unit's end: both groups' sums, and the copies' ----
+    const bool has[2] = {seg.tiles > (int)(g0 & 1), seg.tiles > (int)((g0 ^ 1) & 1)};  // group 0's, 1's tiles
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t last = g0 + seg.tiles - 1;  // the last tile of stage k is this or the one before
+      if (has[k] && !warp_wait(bars.empty[k], ((last - ((last ^ k) & 1)) >> 1) & 1, abort)) return;
+    }
+    tc_after();
+    float* mine = a.parts + (int64_t)((seg.begins ? gridDim.x : 0) + blockIdx.x) * Sh::kPart;
+    if (kCopies == 2) l += __shfl_xor_sync(kFullMask, l, 16);
+    float* ends = unit_x + (2 + 4 * (units++ & 1)) * kLanes + at_lane;
+    ends[group * kLanes] = bar == -kInf ? -kInf : m;
+    ends[(2 + group) * kLanes] = l;
+    if (!pair_sync()) return;
+    if (active) {
+      const float m0 = ends[0], m1 = ends[kLanes];
+      m = fmaxf(m0, m1);
+      float f0 = m0 > -kInf ? ex2(m0 - m) : 0.0f, f1 = m1 > -kInf ? ex2(m1 - m) : 0.0f;
+      l = f0 * ends[2 * kLanes] + f1 * ends[3 * kLanes];
+      if (seg.whole) {
+        const float f = l > 0.0f ? 1.0f / l : 0.0f;
+        f0 *= f;
+        f1 *= f;
+      }
+      uint16_t* out = static_cast<uint16_t*>(a.out) + (token * a.Hq + hq) * kD + group * kDims;
+#pragma unroll 1
+      for (int c = 0; c < kDims; c += 32) {
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+        for (int k = 0; k < 2; ++k) {
+          if (!has[k]) continue;
+          uint32_t o[32];
+          tmem_load32(lanes + kTmemO + k * kTmemGroup + group * kDims + c, o);
+          tmem_wait_loads<32>(o);
+          const float f = k ? f1 : f0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] += f != 0.0f ? __uint_as_float(o[j]) * f : 0.0f;
+        }
+        if (kCopies == 2)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] += __shfl_xor_sync(kFullMask, v[j], 16);
+        if (real && copy == 0)
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 x = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            if (seg.whole) store4(out + c + j, x);
+            else __stcg(reinterpret_cast<float4*>(mine + 2 * kRows + row * kD + group * kDims + c + j), x);
+          }
+      }
+      if (group == 0 && copy == 0) {
+        if (!seg.whole) {
+          __stcg(mine + row, m);
+          __stcg(mine + kRows + row, l);
+        } else if (real && a.lse != nullptr) {
+          a.lse[token * a.Hq + hq] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945309f : -kInf;
+        }
+      }
+    }
+    tc_before();
+    if (!seg.whole) {
+      const Cut cut(total, ctas);
+      const int c0 = cut.part_of(seg.unit_at + kCost), parts = cut.part_of(seg.unit_stop - 1) - c0 + 1;
+      if (!soft_sync()) return;
+      if (tid == 0) {
+        // releases the CTA's part (ordered before by the barrier), acquires the others'
+        int n;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(n) : "l"(a.arrived + c0) : "memory");
+        *last_part = n == parts - 1;
+        if (n == parts - 1) a.arrived[c0] = 0;
+      }
+      if (!soft_sync()) return;
+      if (*last_part) {  // joins the unit's parts, in the order of the keys
+        const float* part0 = a.parts + (int64_t)(gridDim.x + c0) * Sh::kPart;
+        const float* part1 = a.parts + (int64_t)c0 * Sh::kPart;
+        for (int item = tid; item < seg.rows * (kD / 4); item += kSoftThreads) {
+          const int r = item / (kD / 4), d = item % (kD / 4) * 4;
+          const int64_t tok = (int64_t)seg.token0 + (seg.row0 + r) / a.G;
+          if (tok < 0 || tok >= a.T) continue;
+          float high = -kInf, sum = 0.0f;
+          for (int k = 0; k < parts; ++k)
+            high = fmaxf(high, __ldcg((k == 0 ? part0 : part1 + (int64_t)k * Sh::kPart) + r));
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int k = 0; k < parts; ++k) {
+            const float* p = k == 0 ? part0 : part1 + (int64_t)k * Sh::kPart;
+            const float pm = __ldcg(p + r);
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(p + 2 * kRows + r * kD + d));
+            const float f = pm > -kInf ? ex2(pm - high) : 0.0f;
+            sum += f * __ldcg(p + kRows + r);
+            v.x += y.x * f; v.y += y.y * f; v.z += y.z * f; v.w += y.w * f;
+          }
+          const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
+          const int64_t at = tok * a.Hq + seg.h * a.G + (seg.row0 + r) % a.G;
+          store4(static_cast<uint16_t*>(a.out) + at * kD + d, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+          if (d == 0 && a.lse != nullptr)
+            a.lse[at] = sum > 0.0f ? (high + log2f(sum)) * 0.693147180559945309f : -kInf;
+        }
+        if (!soft_sync()) return;  // before *last_part is written again
+      }
+    }
+  }
+}
+
+template <int kD, int kRows>
+__global__ void __launch_bounds__(kThreads, 1) wide_attention_kernel(AttnArgs a) {
+  using Sh = Shape<kD, kRows>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+  __shared__ Walk walk;
+  __shared__ uint32_t tmem_at;
+  __shared__ int last_part, abort;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const uint32_t base = smem_addr(smem) + Sh::kBarsAt;
+  Bars bars;
+  for (int i = 0; i < 2; ++i) {
+    bars.full[i] = base + 8 * i;
+    bars.empty[i] = base + 16 + 8 * i;
+    bars.scores[i] = base + 32 + 8 * i;
+    bars.weights[i] = base + 48 + 8 * i;
+  }
+  bars.q = base + 64;
+  for (int i = 0; i < 4; ++i) bars.pair[i] = base + 72 + 8 * i;
+  bars.soft = base + 104;
+  bars.done = base + 112;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars.full[i], kFeedWarps);
+      mbar_init(bars.empty[i], 1);
+      mbar_init(bars.scores[i], 1);
+      mbar_init(bars.weights[i], kSoftWarps / 2);
+    }
+    mbar_init(bars.q, kSoftWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(bars.pair[i], 2);
+    mbar_init(bars.soft, kSoftWarps);
+    mbar_init(bars.done, 1);
+    mbar_init_fence();
+    abort = 0;
+  }
+  int ctas;
+  int64_t total;
+  if (!locate<uint16_t, kD, kRows, kCost, kThreads>(a, &walk, &ctas, &total)) return;
+  if (warp == kThreads / 32 - 1) tmem_alloc(smem_addr(&tmem_at), kTmemColumns);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = tmem_at;
+  Walker<kRows> walker{walk};
+  if (warp < kSoftWarps) {
+    soften<kD, kRows>(a, walker, smem, tmem, bars, &abort, total, ctas, &last_part);
+  } else if (warp < kSoftWarps + kFeedWarps) {
+    feed<kD, kRows>(a, walker, smem, bars, &abort);
+  } else if ((tid & 31) == 0) {
+    multiply<kD, kRows>(a, walker, smem_addr(smem), tmem, bars, &abort);
+    tc_commit(bars.done);  // nothing is in flight when the memory is given back
+    mbar_wait(bars.done, 0, &abort);
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  __syncwarp();
+  if (warp == kThreads / 32 - 1) tmem_free(tmem, kTmemColumns);
+  if (tid == 0 && abort != 0 && a.status != nullptr) atomicOr(a.status, 2);
+}
+
+template <int kD, int kRows>
+cudaError_t launch(const AttnArgs& a, const DeviceInfo& info, int64_t max_tiles, cudaStream_t stream) {
+  using Sh = Shape<kD, kRows>;
+  static std::atomic<uint64_t> ready{0};  // devices whose attribute is set (it stays with the function)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !((ready.load() >> dev) & 1u)) {
+    e = cudaFuncSetAttribute(wide_attention_kernel<kD, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev);
+  }
+  int64_t ctas = info.sms;
+  const int64_t fit = (MEMRA_KV_ATTENTION_WORKSPACE_BYTES - kMaxCtas * 4) / (2 * Sh::kPart * (int64_t)sizeof(float));
+  if (ctas > fit) ctas = fit;
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  const int64_t groups = (a.T * a.G + kRows - 1) / kRows + a.B;
+  const int64_t entries = (max_tiles + kCost) * groups * a.Hkv;  // what the list can hold at most
+  if (ctas > entries) ctas = entries;
+  if (ctas < 1) ctas = 1;
+  return launch_kernel(wide_attention_kernel<kD, kRows>, dim3((unsigned)ctas), dim3(kThreads), (size_t)Sh::kSmem, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_wide_attention(const AttnArgs& a, int D, int64_t rows, const DeviceInfo& info,
+                                  int64_t max_tiles, cudaStream_t stream) {
+  if (rows <= 64)
+    return D == 64 ? launch<64, 64>(a, info, max_tiles, stream) : launch<128, 64>(a, info, max_tiles, stream);
+  return D == 64 ? launch<64, 128>(a, info, max_tiles, stream) : launch<128, 128>(a, info, max_tiles, stream);
+}
+
+}  // namespace memra
