@@ -29,23 +29,13 @@ constexpr int kThreads = kWarps * 32;
 static_assert(kWarps * kStrip == kTile, "a CTA's step is an entry of the list");
 constexpr int kUnitCost = 3;   // entries of the list for a unit's fixed time (1: 37 us, 3: 34, 6: 35
                                // for 16 sequences of 37 to 16000 tokens)
-#ifndef MEMRA_ATTN_WIDE
-#define MEMRA_ATTN_WIDE 16
-#endif
-constexpr int kWideRows = MEMRA_ATTN_WIDE;  // average rows to a unit above which the wide kernel takes them
+// Above this many rows to a unit, and with at least so many in all (rows times heads), the
+// tcgen05 kernel takes bf16 queries: below, its larger parts and ends of units cost more than
+// its products save.  Contexts of 500 to 8000, us here / there: 32 rows, 16 requests 64 / 77;
+// 64 rows, 16 requests of 32 heads (4096 in all) 63 / 57; 128 rows, 16 requests 194 / 101; 64
+// rows, 8 requests (4096) 101 / 93, 4 (2048) 65 / 65, 1 (512) 44 / 73; 512 tokens of one prompt 408 / 178.
+constexpr int kWideRows = 32, kWideAll = 4096;
 constexpr int kMaxParts = 64;  // CTAs to a unit, on average
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kN>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
-}
 
 __device__ __forceinline__ void mma_16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -754,7 +744,8 @@ template <typename T>
 cudaError_t launch_attention(const AttnArgs& a, int D, const DeviceInfo& info, cudaStream_t stream) {
   const int64_t rows = a.B > 0 ? (a.T * a.G + a.B - 1) / a.B : 1;
   const int64_t max_tiles = a.max_pages * a.page / kTile + 1 + kUnitCost;
-  if (sizeof(T) == 2 && D <= 128 && rows > kWideRows) return launch_wide_attention(a, D, rows, info, max_tiles, stream);
+  if (sizeof(T) == 2 && D <= 128 && rows > kWideRows && a.T * a.Hq >= kWideAll)
+    return launch_wide_attention(a, D, rows, info, max_tiles, stream);
   if (D == 64) {
     if (rows <= 8) return launch_shape<T, 64, 1>(a, info, max_tiles, stream);
     if (rows <= 16) return launch_shape<T, 64, 2>(a, info, max_tiles, stream);

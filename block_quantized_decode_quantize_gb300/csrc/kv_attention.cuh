@@ -51,6 +51,23 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Copies to shared memory that this thread waits for by groups.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes, or zeros where `there` is false.
+__device__ __forceinline__ void cp16_or_zeros(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kN>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
+
 __device__ __forceinline__ float value(const float* p) { return *p; }
 __device__ __forceinline__ float value(const uint16_t* p) {
   return __uint_as_float((uint32_t)*p << 16);

@@ -4,8 +4,10 @@
 //
 // With tens of rows to a cached head, the work is two matrix products and goes to the
 // tcgen05 tensor cores: S [128 rows x 128 keys] = Q K^T and O [128 rows x D] += P V, both in
-// fp16 with fp32 accumulators in tensor memory.  Warps of one CTA an SM have three tasks:
-//   7 warps bring a tile of codes from the cache (a tile ahead, in registers), turn them
+// fp16 (exact for bf16 queries and 8-bit codes) with fp32 accumulators in tensor memory.
+// Weights as bf16 would need no scaling against the scales of V, but round at 2^-8, which
+// doubles the result's own rounding.  Warps of one CTA an SM have three tasks:
+//   11 warps bring a tile of codes from the cache (a tile ahead, each thread its own), turn them
 //     into fp16 exactly and lay K and V out in shared memory as the products read them
 //     (rows of 64 dims, 128-byte swizzle; two stages);
 //   1 thread issues the products: S of the next tile before O of this one;
@@ -13,9 +15,9 @@
 //     statistics and its own accumulators, so that neither waits for the other; a thread
 //     has a row and its keys, and the weights go back to tensor memory, over the scores,
 //     as the second product's operand.
-// Units of up to 64 rows put every row into the product twice: each copy's thread takes
-// half of the keys (and gives weight 0 to the others), which spreads the exponentials, 16
-// a cycle on an SM, over all of its quarters.
+// Units of up to 64 rows put every row into the product twice, and each copy's lane takes
+// half of the keys (the products write the lanes of one copy at a time): that spreads the
+// exponentials, 16 a cycle on an SM, over all of its quarters.
 // Accumulators stay in tensor memory for a unit's whole range of keys; they are rescaled
 // only when a maximum moves by more than the slack, and the two groups' (and copies') are
 // joined at the end.  Scales never meet the codes: kd multiplies a score, vd a weight.
@@ -27,10 +29,11 @@ namespace memra {
 namespace {
 
 constexpr int kLanes = 128;  // rows of a product
-constexpr int kSoftWarps = 8, kFeedWarps = 7;  // and one: 16 warps may have 128 registers
+constexpr int kSoftWarps = 8, kFeedWarps = 11;  // and one: 20 warps may have 96 registers
 constexpr int kSoftThreads = kSoftWarps * 32, kFeedThreads = kFeedWarps * 32;
 constexpr int kThreads = kSoftThreads + kFeedThreads + 32;
-constexpr float kLeastRef = 1e-25f;  // keeps 2^8 / ref times a row's sum in range; scales below are next to nothing
+// Keeps 2^8 / ref times a row's sum in range; blocks of smaller scales are next to nothing.
+constexpr float kLeastRef = 1e-25f;
 constexpr int kCost = 3;  // entries of the list for a unit's fixed time
 
 // Tensor memory columns: scores of two tiles (the weights, two fp16 a column, over the last
@@ -43,11 +46,13 @@ struct Shape {
   static constexpr int kOperand = kTile * kD * 2;       // K or V of a tile in fp16
   static constexpr int kQ = kLanes * kD * 2;
   static constexpr int kQAt = 4 * kOperand;             // after two stages of K, V
-  static constexpr int kScalesAt = kQAt + kQ;           // kd [2][128], vd [2][128]
-  static constexpr int kUnitAt = kScalesAt + 4 * kTile * 4;  // amax [group][lane], [2 units][m, l][group][lane]
-  static constexpr int kMiscAt = kUnitAt + 10 * kLanes * 4;      // vd maxima [2][4], hidden [2][8]
-  static constexpr int kBarsAt = kMiscAt + 64;
-  static constexpr int kSmem = kBarsAt + 16 * 8 + 1024;          // and room to align to 1024
+  static constexpr int kScalesAt = kQAt + kQ;           // kd [4][128], vd [4][128]
+  static constexpr int kUnitAt = kScalesAt + 8 * kTile * 4;  // amax [group][lane], [2 units][m, l][group][lane]
+  static constexpr int kMiscAt = kUnitAt + 10 * kLanes * 4;      // vd maxima [4][4], hidden strips [4][8]
+  static constexpr int kRawAt = kMiscAt + 128;  // the feeding threads' pieces of the next tile
+  static constexpr int kRaw = 2 * ((kTile * kD / 16 + kFeedThreads - 1) / kFeedThreads) * kFeedThreads * 16;
+  static constexpr int kBarsAt = kRawAt + kRaw;
+  static constexpr int kSmem = kBarsAt + 17 * 8 + 1024;          // and room to align to 1024
   static constexpr int kPart = 2 * kRows + kRows * kD;           // m, l, values: floats
 };
 
@@ -65,19 +70,20 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-// D [128 x N] (+)= A [128 x 16] B [N x 16]^T, A from shared or tensor memory.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t what, bool add) {
+// D [128 x N] (+)= A [128 x 16] B [N x 16]^T, A from shared or tensor memory; lanes whose bit
+// of `skip` (of each 32) is set keep their D.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t what, uint32_t skip, bool add) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(what),
-      "r"((uint32_t)add)
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n}" ::"r"(d), "l"(a), "l"(b),
+      "r"(what), "r"((uint32_t)add), "r"(skip)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t what, bool add) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t what, uint32_t skip, bool add) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(what),
-      "r"((uint32_t)add)
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n}" ::"r"(d), "r"(a), "l"(b),
+      "r"(what), "r"((uint32_t)add), "r"(skip)
       : "memory");
 }
 // 32 columns of this warp's 32 lanes.
@@ -102,6 +108,14 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t* r) {
       "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 // Waits for this thread's loads; r: what they loaded, which nothing may use before.
 template <int kN>
 __device__ __forceinline__ void tmem_wait_loads(uint32_t* r) {
@@ -110,7 +124,9 @@ __device__ __forceinline__ void tmem_wait_loads(uint32_t* r) {
   for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(r[i]));
 }
 __device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// Plain shared-memory writes become visible to the products.
+// Plain shared-memory writes that happened before become visible to the products.  The
+// thread that issues those makes this fence, after its waits: in the feeding warps it
+// would also wait for their loads of the next tile (a tile took 4500 cycles then).
 __device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Shared-memory operand: rows of 64 fp16 under the 128-byte swizzle, eight rows (1024
@@ -120,11 +136,55 @@ __device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead) {
   return (uint64_t)((at >> 4) & 0x3fff) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
          1ull << 46 | 2ull << 61;
 }
-// kind::f16 with fp16 operands and fp32 sums, 128 rows, N columns; b_rows: B's rows (the
-// keys) are contiguous along N.
-template <int N, bool b_rows>
-constexpr uint32_t kProduct = 1u << 4 | (b_rows ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
+// kind::f16 with fp16 operands and fp32 sums, 128 rows, N columns; values: B's rows (the
+// keys) lie one after another, contiguous along N.
+template <int N, bool values>
+constexpr uint32_t kProduct = 1u << 4 | (values ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
                               (uint32_t)(kLanes >> 4) << 24;
+
+// A value cached in L2 only, or 0: one piece of code without a branch, so that nothing waits
+// for the load here.
+__device__ __forceinline__ float load_or_zero(const float* p, bool there) {
+  float r;
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n mov.b32 %0, 0;\n @p ld.global.cg.f32 %0, [%1];\n}"
+               : "=&f"(r) : "l"(p), "r"((uint32_t)there));
+  return r;
+}
+__device__ __forceinline__ int32_t load_or_none(const int32_t* p, bool there) {  // -1
+  int32_t r;
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n mov.b32 %0, -1;\n @p ld.global.cg.s32 %0, [%1];\n}"
+               : "=&r"(r) : "l"(p), "r"((uint32_t)there));
+  return r;
+}
+
+// Pairs of fp32 in one instruction.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(uint32_t lo, uint32_t hi) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(lo), "r"(hi));
+  return p;
+}
+__device__ __forceinline__ Pair pair_of(float lo, float hi) { return pair_of(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float2 parts_of(Pair p) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(p));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 
 // One CTA's range of one unit.
 struct Segment {
@@ -176,97 +236,122 @@ struct Walker {
   }
 };
 
+// Each warp goes over the CTA's part of the list by itself; where it stands lies in shared
+// memory (registers hold the tile on its way).
+template <int kRows>
+struct Way {
+  Walker<kRows> walker;
+  Segment seg;
+};
+// The next unit, for a whole warp.
+template <int kRows>
+__device__ __forceinline__ bool next_unit(const AttnArgs& a, Way<kRows>* way) {
+  __syncwarp();
+  bool more = false;
+  if ((threadIdx.x & 31) == 0) more = way->walker.next(a, &way->seg);
+  return __shfl_sync(kFullMask, (int)more, 0) != 0;  // and what lane 0 wrote is there
+}
+
 // A whole warp's bounded wait, with one answer for all its lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   return __all_sync(kFullMask, mbar_wait(bar, parity, abort));
 }
 
 struct Bars {  // shared-memory addresses
-  uint32_t full[2], empty[2], scores[2], weights[2], q, pair[4], soft, done;
+  uint32_t k_full[2], v_full[2], empty[2], scores[2], weights[2], q, pair[4], soft, done;
 };
 
-// ---- 7 warps: codes from the cache to fp16 operands ----
+// ---- 11 warps: codes from the cache to fp16 operands ----
 template <int kD, int kRows>
-__device__ __forceinline__ void feed(const AttnArgs& a, Walker<kRows> walker, uint8_t* smem, const Bars& bars,
+__device__ __forceinline__ void feed(const AttnArgs& a, Way<kRows>* way, uint8_t* smem, const Bars& bars,
                                      volatile int* abort) {
   using Sh = Shape<kD, kRows>;
   constexpr int kChunks = kD / 16;  // 16-code pieces of a row
   constexpr int kLoads = (kTile * kChunks + kFeedThreads - 1) / kFeedThreads;  // of K, and of V, a thread
   constexpr int kStep = kFeedThreads / kChunks;  // rows from one of a thread's pieces to the next
-  static_assert(kFeedThreads % kChunks == 0 && 2 * kTile - kFeedThreads == 32, "pieces and scales");
+  static_assert(kFeedThreads % kChunks == 0 && kFeedThreads >= 2 * kTile, "pieces and scales");
   const int tid = threadIdx.x - kSoftThreads, lane = tid & 31, warp = tid >> 5;
   // Eight neighbouring lanes write pieces of two rows' same block of 64 dims: the rows'
   // swizzles differ in the lowest bit, so they meet in no bank.
   const int row = kD == 64 ? tid >> 2 : (tid >> 4) * 2 + ((tid >> 2) & 1);
   const int chunk = kD == 64 ? tid & 3 : (tid & 3) + ((tid >> 3) & 1) * 4;
-  // Scales: kd of key tid (tid < 128), else vd of key tid - 128; the last 32 vd go to warp 0
-  // as a second one.
-  const bool scale_v = tid >= kTile;
-  const int scale_key = tid & (kTile - 1), scale_key2 = kTile - 32 + lane;
-  float* scales = reinterpret_cast<float*>(smem + Sh::kScalesAt);  // [kd, vd][stage][key]
-  float* v_most = reinterpret_cast<float*>(smem + Sh::kMiscAt);    // [stage][4]
-  uint8_t* hidden = smem + Sh::kMiscAt + 32;                       // [stage][8]
+  // Scales: kd of key tid (warps 0 .. 3), vd of key tid - 128 (4 .. 7).
+  const bool scale_v = tid >= kTile, has_scale = tid < 2 * kTile;
+  const int scale_key = tid & (kTile - 1);
+  // A tile's scales stay until its weights are made, two tiles longer than its codes.
+  float* scales = reinterpret_cast<float*>(smem + Sh::kScalesAt);  // [kd, vd][tile & 3][key]
+  float* v_most = reinterpret_cast<float*>(smem + Sh::kMiscAt);    // [tile & 3][4]
+  uint8_t* hidden = smem + Sh::kMiscAt + 64;                       // [tile & 3][8]
   const int blocks = (int)a.by_block((uint32_t)a.page);
 
-  Segment seg;
-  int tile = 0;
+  int tile = 0, tiles = 0;
   bool more = true;
-  seg.tiles = 0;
+  // A tile: its first key, the end of the keys that are there, its head; the pages of strip
+  // lane & 7 and of this thread's scales (-1: not there).
   struct Ref {
-    int key, stop, h;      // first key; keys from stop on are not there
-    int32_t page[kLoads], off[kLoads], scale_page, scale_page2;
+    int key, stop, h;
+    int32_t page, scale_page;
   };
-  // The next tile of the CTA's range and its pages (-1: keys that are not there).
   auto next_ref = [&](Ref& r) {
-    while (more && tile >= seg.tiles) {
-      more = walker.next(a, &seg);
+    r.page = r.scale_page = -1;
+    while (more && tile >= tiles) {
+      more = next_unit(a, way);
+      tiles = way->seg.tiles;
       tile = 0;
     }
     if (!more) return false;
+    const Segment& seg = way->seg;
     r.key = seg.key0 + tile * kTile;
     r.stop = seg.key_stop;
     r.h = seg.h;
     ++tile;
     const int32_t* pages = a.table + (int64_t)seg.b * a.max_pages;
     const int there = (r.stop + kStrip - 1) / kStrip * kStrip;
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int k = r.key + j * kStep + row;
-      const int in = (int)a.by_page((uint32_t)k);
-      r.page[j] = j * kStep + row < kTile && k < there ? pages[in] : -1;
-      r.off[j] = k - in * a.page;
-    }
-    const int k = r.key + scale_key, k2 = r.key + scale_key2;
-    r.scale_page = k < there ? pages[a.by_page((uint32_t)k)] : -1;
-    r.scale_page2 = warp == 0 && k2 < there ? pages[a.by_page((uint32_t)k2)] : -1;
+    const int k0 = r.key + (lane & 7) * kStrip, k = r.key + scale_key;
+    r.page = load_or_none(pages + a.by_page((uint32_t)k0), k0 < there);
+    r.scale_page = load_or_none(pages + a.by_page((uint32_t)k), has_scale && k < there);
     return true;
   };
-  uint4 k_data[kLoads], v_data[kLoads];
-  float scale = 0.0f, scale2 = 0.0f;
+  // Where strip lane & 7 of the tile lies in a plane (-1: nowhere).
+  auto strip_of = [&](const Ref& r) {
+    const int k0 = r.key + (lane & 7) * kStrip, off = k0 - (int)a.by_page((uint32_t)k0) * a.page;
+    return (uint32_t)r.page < (uint32_t)a.n_pages
+               ? (int64_t)((uint64_t)(uint32_t)r.page * a.page_bytes + (uint32_t)((r.h * a.page + off) * kD))
+               : (int64_t)-1;
+  };
+  float scale = 0.0f;
   bool gone = false;  // the strip of scale_key has no page
-  const int64_t v_minus_k = a.vq - a.kq;
-  auto load_piece = [&](const Ref& r, int j) {
-    k_data[j] = v_data[j] = make_uint4(0, 0, 0, 0);
-    if ((uint32_t)r.page[j] < (uint32_t)a.n_pages) {
-      const int8_t* at = a.kq + (uint64_t)(uint32_t)r.page[j] * a.page_bytes +
-                         (uint32_t)((r.h * a.page + r.off[j]) * kD + chunk * 16);
-      k_data[j] = ld_cg_16B(at);
-      v_data[j] = ld_cg_16B(at + v_minus_k);
+  const int8_t* k_lane = a.kq + chunk * 16;
+  const int8_t* v_lane = a.vq + chunk * 16;
+  // This thread's own places for its pieces: the j-th of K, then of V.
+  const uint32_t raw = smem_addr(smem + Sh::kRawAt) + tid * 16;
+  constexpr uint32_t kPlace = kFeedThreads * 16;
+  auto load_pieces = [&](const int8_t* plane, int64_t strip, int v) {
+    const int8_t* from[kLoads];
+    bool there[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {  // a warp's rows of a piece lie in one strip
+      const int64_t at = __shfl_sync(kFullMask, strip, ((j * kStep + row) / kStrip) & 7);
+      there[j] = at >= 0 && j * kStep + row < kTile;
+      from[j] = there[j] ? plane + at + (j * kStep + row) % kStrip * kD : plane;
     }
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) cp16_or_zeros(raw + (v * kLoads + j) * kPlace, from[j], there[j]);
+    cp_commit();
   };
   auto scale_of = [&](const float* plane, const Ref& r, int key, int32_t page) {
     const int k = r.key + key;
     const int off = k - (int)a.by_page((uint32_t)k) * a.page;
-    if ((uint32_t)page >= (uint32_t)a.n_pages || k >= r.stop) return 0.0f;
-    return __ldcg(plane + (int64_t)(uint32_t)page * a.page_scales + (int64_t)r.h * blocks + a.by_block((uint32_t)off));
+    const bool there = (uint32_t)page < (uint32_t)a.n_pages && k < r.stop;
+    return load_or_zero(plane + (there ? (int64_t)(uint32_t)page * a.page_scales + (int64_t)r.h * blocks +
+                                             a.by_block((uint32_t)off) : 0), there);
   };
-  auto load_scales = [&](const Ref& r) {
-    gone = (uint32_t)r.scale_page >= (uint32_t)a.n_pages && r.key + scale_key < r.stop;
+  auto load_scales = [&](const Ref& r, bool ahead) {
+    gone = ahead && (uint32_t)r.scale_page >= (uint32_t)a.n_pages && r.key + scale_key < r.stop;
     scale = scale_of(scale_v ? a.vd : a.kd, r, scale_key, r.scale_page);
-    if (warp == 0) scale2 = scale_of(a.vd, r, scale_key2, r.scale_page2);
   };
-  // 16 codes as fp16 (the byte under the exponent of 1024 is 1024 + 128 + code) to two
-  // neighbouring 16-byte units of their row.
+  // 16 codes as fp16 (the byte code + 128 under the exponent of 1024 is 1024 + 128 + code) to
+  // two neighbouring 16-byte units of their row.
   auto put = [&](uint8_t* base, int key, const uint4& x) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t h[8];
@@ -286,87 +371,113 @@ __device__ __forceinline__ void feed(const AttnArgs& a, Walker<kRows> walker, ui
     *reinterpret_cast<uint4*>(line + (at ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
   };
 
-  // Each piece's register takes the next tile's as soon as it is written.
-  Ref next, after;
+  auto convert = [&](uint8_t* base, int v) {
+    uint4 x[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) x[j] = lds_v4(raw + (v * kLoads + j) * kPlace);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      if (j * kStep + row < kTile) put(base, j * kStep + row, x[j]);
+  };
+
+  // Each piece's place takes the next tile's as soon as it is read.
+  Ref next{}, after{};
   bool have = next_ref(next);
   if (have) {
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) load_piece(next, j);
-    load_scales(next);
+    const int64_t strip = strip_of(next);
+    load_pieces(k_lane, strip, 0);
+    load_pieces(v_lane, strip, 1);
+    load_scales(next, true);
   }
   bool ahead = have && next_ref(next);
   for (uint32_t g = 0; have; ++g) {
+    const int64_t strip = strip_of(next);
     const bool beyond = ahead && next_ref(after);  // its pages are there a tile later
-    const int stage = g & 1;
-    if (g >= 2 && !warp_wait(bars.empty[stage], ((g >> 1) & 1) ^ 1, abort)) return;
+    if (!ahead) after.page = after.scale_page = -1;
+    const int stage = g & 1, turn = g & 3;
+    const uint32_t free_phase = ((g >> 1) & 1) ^ 1;
     uint8_t* k_at = smem + stage * 2 * Sh::kOperand;
-    float* kd = scales + stage * kTile;
-    float* vd = scales + (2 + stage) * kTile;
-    (scale_v ? vd : kd)[scale_key] = scale;
-    if (warp == 0) vd[scale_key2] = scale2;
-    if (scale_v || warp == 0) {
-      const uint32_t most = __reduce_max_sync(kFullMask, __float_as_uint(scale_v ? scale : scale2));
-      if (lane == 0) v_most[stage * 4 + (warp + 3) % 7] = __uint_as_float(most);
-    }
-    if (!scale_v && (lane & 15) == 0) {
-      hidden[stage * 8 + scale_key / kStrip] = gone ? 1 : 0;
-      if (gone && a.status != nullptr) atomicOr(a.status, 1);
-    }
-    if (ahead) load_scales(next);
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int key = j * kStep + row;
-      if (key < kTile) {
-        put(k_at, key, k_data[j]);
-        put(k_at + Sh::kOperand, key, v_data[j]);
+    // K, once the scores two tiles back are made
+    if (g >= 2 && !warp_wait(bars.scores[stage], free_phase, abort)) break;
+    float* kd = scales + turn * kTile;
+    float* vd = scales + (4 + turn) * kTile;
+    if (has_scale) {
+      (scale_v ? vd : kd)[scale_key] = scale;
+      if (scale_v) {
+        const uint32_t most = __reduce_max_sync(kFullMask, __float_as_uint(scale));
+        if (lane == 0) v_most[turn * 4 + (warp & 3)] = __uint_as_float(most);
+      } else if ((lane & 15) == 0) {
+        hidden[turn * 8 + scale_key / kStrip] = gone ? 1 : 0;
+        if (gone && a.status != nullptr) atomicOr(a.status, 1);
       }
-      if (ahead) load_piece(next, j);
     }
-    async_proxy_fence();
+    load_scales(next, ahead);
+    cp_wait<1>();  // K's pieces are there, V's may be under way
+    convert(k_at, 0);
     __syncwarp();
-    if (lane == 0) mbar_arrive(bars.full[stage]);
+    if (lane == 0) mbar_arrive(bars.k_full[stage]);
+    load_pieces(k_lane, strip, 0);
+    // V, once the values two tiles back are summed
+    if (g >= 2 && !warp_wait(bars.empty[stage], free_phase, abort)) break;
+    cp_wait<1>();
+    convert(k_at + Sh::kOperand, 1);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars.v_full[stage]);
+    load_pieces(v_lane, strip, 1);
     have = ahead;
     ahead = beyond;
     next = after;
   }
+  cp_wait<0>();
 }
 
 // ---- one thread: the products ----
 template <int kD, int kRows>
-__device__ __forceinline__ void multiply(const AttnArgs& a, Walker<kRows> walker, uint32_t smem, uint32_t tmem,
+__device__ __forceinline__ void multiply(const AttnArgs& a, Walker<kRows>* walker, uint32_t smem, uint32_t tmem,
                                          const Bars& bars, volatile int* abort) {
   using Sh = Shape<kD, kRows>;
-  constexpr uint32_t kScores = kProduct<kTile, false>, kValues = kProduct<kD, true>;
+  constexpr int kCopies = kLanes / kRows, kKeys = kTile / kCopies;  // of a tile, a lane
+  constexpr uint32_t kScores = kProduct<kKeys, false>, kValues = kProduct<kD, true>;
   Segment seg;
   uint32_t g = 0, unit = 0;
+  auto skip = [](int copy) { return kCopies == 1 ? 0u : copy ? 0x0000ffffu : 0xffff0000u; };
   auto scores = [&](uint32_t t) {
     const uint32_t k = smem + (t & 1) * 2 * Sh::kOperand, q = smem + Sh::kQAt;
 #pragma unroll
-    for (int s = 0; s < kD / 16; ++s)
-      tc_mma_ss(tmem + (t & 1) * kTile, operand(q + (s >> 2) * (kLanes * 128) + (s & 3) * 32, 16),
-                operand(k + (s >> 2) * (kTile * 128) + (s & 3) * 32, 16), kScores, s > 0);
+    for (int c = 0; c < kCopies; ++c)
+#pragma unroll
+      for (int s = 0; s < kD / 16; ++s)
+        tc_mma_ss(tmem + (t & 1) * kTile, operand(q + (s >> 2) * (kLanes * 128) + (s & 3) * 32, 16),
+                  operand(k + c * (kKeys * 128) + (s >> 2) * (kTile * 128) + (s & 3) * 32, 16), kScores, skip(c), s > 0);
+    mbar_arrive(bars.scores[t & 1]);  // passes on what the feeding warps wrote (the scales)
     tc_commit(bars.scores[t & 1]);
   };
-  while (walker.next(a, &seg)) {
+  while (walker->next(a, &seg)) {
     if (seg.tiles == 0) continue;
     if (!mbar_wait(bars.q, unit & 1, abort)) return;
     ++unit;
-    if (!mbar_wait(bars.full[g & 1], (g >> 1) & 1, abort)) return;
+    if (!mbar_wait(bars.k_full[g & 1], (g >> 1) & 1, abort)) return;
+    async_proxy_fence();
     tc_after();
     scores(g);
     for (int t = 0; t < seg.tiles; ++t, ++g) {
       if (t + 1 < seg.tiles) {
-        if (!mbar_wait(bars.full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort)) return;
+        if (!mbar_wait(bars.k_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort)) return;
+        async_proxy_fence();
         tc_after();
         scores(g + 1);
       }
+      if (!mbar_wait(bars.v_full[g & 1], (g >> 1) & 1, abort)) return;
       if (!mbar_wait(bars.weights[g & 1], (g >> 1) & 1, abort)) return;
+      async_proxy_fence();
       tc_after();
       const uint32_t v = smem + (g & 1) * 2 * Sh::kOperand + Sh::kOperand;
 #pragma unroll
-      for (int s = 0; s < kTile / 16; ++s)  // 16 keys are two groups of eight rows
-        tc_mma_ts(tmem + kTmemO + (g & 1) * kTmemGroup, tmem + (g & 1) * kTile + kTmemWeights + s * 8,
-                  operand(v + s * 2048, kTile * 128), kValues, t > 1 || s > 0);
+      for (int c = 0; c < kCopies; ++c)
+#pragma unroll
+        for (int s = 0; s < kKeys / 16; ++s)  // 16 keys are two groups of eight rows
+          tc_mma_ts(tmem + kTmemO + (g & 1) * kTmemGroup, tmem + (g & 1) * kTile + kTmemWeights + s * 8,
+                    operand(v + c * (kKeys * 128) + s * 2048, kTile * 128), kValues, skip(c), t > 1 || s > 0);
       tc_commit(bars.empty[g & 1]);
     }
   }
@@ -374,13 +485,13 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Walker<kRows> walker
 
 // ---- 8 warps: scores to weights, results ----
 template <int kD, int kRows>
-__device__ __forceinline__ void soften(const AttnArgs& a, Walker<kRows> walker, uint8_t* smem, uint32_t tmem,
+__device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8_t* smem, uint32_t tmem,
                                        const Bars& bars, volatile int* abort, int64_t total, int ctas,
                                        int* last_part) {
   using Sh = Shape<kD, kRows>;
   constexpr int kCopies = kLanes / kRows;
   constexpr int kKeys = kTile / kCopies;  // of a tile, a thread
-  constexpr int kStepKeys = 64;           // of these, at a time in registers
+  constexpr int kStepKeys = 32;           // of these, at a time in registers
   constexpr int kDims = kD / 2;           // of a row, a thread, at a unit's two ends
   const float kInf = __int_as_float(0x7f800000);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -388,10 +499,9 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Walker<kRows> walker, 
   const int row = quarter * (kRows / 4) + lane % (kRows / 4), copy = lane / (kRows / 4);
   const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
   const uint32_t s_at = lanes + group * kTile, o_at = lanes + kTmemO + group * kTmemGroup;
-  const float4* kd = reinterpret_cast<const float4*>(smem + Sh::kScalesAt) + (group * kTile + copy * kKeys) / 4;
-  const float4* vd = kd + 2 * kTile / 4;
-  const float4* v_most = reinterpret_cast<const float4*>(smem + Sh::kMiscAt) + group;
-  const uint2* hidden = reinterpret_cast<const uint2*>(smem + Sh::kMiscAt + 32) + group;
+  const ulonglong2* scales = reinterpret_cast<const ulonglong2*>(smem + Sh::kScalesAt) + copy * kKeys / 4;
+  const float4* v_most = reinterpret_cast<const float4*>(smem + Sh::kMiscAt);
+  const uint2* hidden = reinterpret_cast<const uint2*>(smem + Sh::kMiscAt + 64);
   float* unit_x = reinterpret_cast<float*>(smem + Sh::kUnitAt);
   uint32_t pair_phase = 0, soft_phase = 0, units = 0, g0 = 0;  // g0: the CTA's tiles before this unit
   // With the other group's warp of the same lanes; false when a wait ran out somewhere.
@@ -410,8 +520,8 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Walker<kRows> walker, 
     return ok;
   };
 
-  Segment seg;
-  for (; walker.next(a, &seg); g0 += seg.tiles) {
+  const Segment& seg = way->seg;
+  for (; next_unit(a, way); g0 += seg.tiles) {
     const bool active = quarter * (kRows / 4) < seg.rows;  // the warp has rows
     const int i = (seg.row0 + row) / a.G, hq = seg.h * a.G + (seg.row0 + row) % a.G;
     const int64_t token = (int64_t)seg.token0 + i;
@@ -456,7 +566,6 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Walker<kRows> walker, 
       }
     }
     if (seg.tiles > 0) {
-      async_proxy_fence();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars.q);
     }
@@ -467,64 +576,56 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Walker<kRows> walker, 
     float most = 0.0f, bar = -kInf, m = 0.0f, l = 0.0f, ref = 0.0f, shift = 0.0f;
     const int t0 = (int)((g0 ^ group) & 1);  // the group's first tile
     for (int t = t0; t < seg.tiles; t += 2) {
-      const uint32_t phase = ((g0 + t) >> 1) & 1;
-      if (!warp_wait(bars.full[group], phase, abort)) return;  // the scales
+      const uint32_t phase = ((g0 + t) >> 1) & 1, turn = (g0 + t) & 3;
+      const ulonglong2* kd = scales + turn * (kTile / 4);
+      const ulonglong2* vd = kd + kTile;
       if (!warp_wait(bars.scores[group], phase, abort)) return;
       if (active) {
         tc_after();
         const int key = seg.key0 + t * kTile + copy * kKeys;
-        const uint2 gone = *hidden;  // a byte to a strip
+        const uint2 gone = hidden[turn];  // a byte to a strip
         const bool plain = seg.key0 + (t + 1) * kTile <= seg.limit_min && seg.key0 + t * kTile >= seg.low_max &&
                            (gone.x | gone.y) == 0;
-        float s[kStepKeys];
+        Pair s[kStepKeys / 2];
         // Scores of kStepKeys keys from `first` on (of this thread's), without the row's scale.
         auto fetch = [&](int first) {
           uint32_t bits[kStepKeys];
-          if (kCopies == 1) {
-            tmem_load32(s_at + first, bits);
-            tmem_load32(s_at + first + 32, bits + 32);
-            tmem_wait_loads<kStepKeys>(bits);
-          } else {  // a lane reads its copy's keys: all lanes of a load read the same columns
-            uint32_t other[32];
-#pragma unroll
-            for (int c = 0; c < kStepKeys; c += 32) {
-              tmem_load32(s_at + c, bits + c);
-              tmem_load32(s_at + kKeys + c, other);
-              tmem_wait_loads<32>(bits + c);
-              tmem_wait_loads<32>(other);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) bits[c + j] = copy ? other[j] : bits[c + j];
-            }
-          }
+          tmem_load32(s_at + first, bits);
+          tmem_wait_loads<kStepKeys>(bits);
 #pragma unroll
           for (int j = 0; j < kStepKeys; j += 4) {
-            const float4 d = kd[(first + j) / 4];
-            s[j] = __uint_as_float(bits[j]) * d.x;
-            s[j + 1] = __uint_as_float(bits[j + 1]) * d.y;
-            s[j + 2] = __uint_as_float(bits[j + 2]) * d.z;
-            s[j + 3] = __uint_as_float(bits[j + 3]) * d.w;
+            const ulonglong2 d = kd[(first + j) / 4];
+            s[j / 2] = mul2(pair_of(bits[j], bits[j + 1]), d.x);
+            s[j / 2 + 1] = mul2(pair_of(bits[j + 2], bits[j + 3]), d.y);
           }
           if (!plain) {
 #pragma unroll
-            for (int j = 0; j < kStepKeys; ++j) {
+            for (int j = 0; j < kStepKeys; j += 2) {
+              const float2 x = parts_of(s[j / 2]);
               const int k = key + first + j, strip = (copy * kKeys + first + j) / kStrip;
-              const bool seen = k < limit && (a.window == 0 || k >= limit - a.window) &&
-                                (((strip & 4 ? gone.y : gone.x) >> (8 * (strip & 3))) & 1u) == 0;
-              s[j] = seen ? s[j] : -kInf;
+              const bool there = (((strip & 4 ? gone.y : gone.x) >> (8 * (strip & 3))) & 1u) == 0;
+              const bool s0 = k < limit && (a.window == 0 || k >= limit - a.window) && there;
+              const bool s1 = k + 1 < limit && (a.window == 0 || k + 1 >= limit - a.window) && there;
+              s[j / 2] = pair_of(s0 ? x.x : -kInf, s1 ? x.y : -kInf);
             }
           }
         };
         float top = -kInf;
+#pragma unroll 1
         for (int first = 0; first < kKeys; first += kStepKeys) {
           fetch(first);
-          float y[4] = {-kInf, -kInf, -kInf, -kInf};
+          float y0 = -kInf, y1 = -kInf;
 #pragma unroll
-          for (int j = 0; j < kStepKeys; ++j) y[j & 3] = fmaxf(y[j & 3], s[j]);
-          top = fmaxf(top, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+          for (int j = 0; j < kStepKeys / 2; j += 2) {
+            const float2 u = parts_of(s[j]), w = parts_of(s[j + 1]);
+            y0 = fmaxf(fmaxf(y0, u.x), u.y);
+            y1 = fmaxf(fmaxf(y1, w.x), w.y);
+          }
+          top = fmaxf(top, fmaxf(y0, y1));
         }
         if (kCopies == 2) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 16));
         top *= qs;
-        const float4 vm = *v_most;
+        const float4 vm = v_most[turn];
         const float v_top = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
         if (__any_sync(kFullMask, top > bar) || v_top > kRefSlack * ref) {
           float f = 1.0f;
@@ -555,39 +656,30 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Walker<kRows> walker, 
             }
           }
         }
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        // Weights over the last half of the scores, where they come in two steps those of the
-        // last keys first: they take columns whose scores are read.
-#pragma unroll
+        // Weights: where a lane has all keys they lie over the last half of the scores, so the
+        // last keys come first, whose scores are read by then.
+        Pair sum0 = pair_of(0.0f, 0.0f), sum1 = sum0;
+        const Pair qs2 = pair_of(qs, qs), m2 = pair_of(-m, -m);
+#pragma unroll 1
         for (int first = kKeys - kStepKeys; first >= 0; first -= kStepKeys) {
-          if (kKeys > kStepKeys && first == 0) fetch(first);
+          fetch(first);
           uint32_t p[kStepKeys / 2];
 #pragma unroll
           for (int j = 0; j < kStepKeys; j += 4) {
-            const float4 d = vd[(first + j) / 4];
-            float x[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              x[k] = ex2(fmaf(s[j + k], qs, -m));
-              sum[k] += x[k];
-            }
-            const __half2 lo = __floats2half2_rn(x[0] * d.x, x[1] * d.y), hi = __floats2half2_rn(x[2] * d.z, x[3] * d.w);
+            const ulonglong2 d = vd[(first + j) / 4];
+            const float2 x0 = parts_of(fma2(s[j / 2], qs2, m2)), x1 = parts_of(fma2(s[j / 2 + 1], qs2, m2));
+            const Pair p0 = pair_of(ex2(x0.x), ex2(x0.y)), p1 = pair_of(ex2(x1.x), ex2(x1.y));
+            sum0 = add2(sum0, p0);
+            sum1 = add2(sum1, p1);
+            const float2 w0 = parts_of(mul2(p0, d.x)), w1 = parts_of(mul2(p1, d.y));
+            const __half2 lo = __floats2half2_rn(w0.x, w0.y), hi = __floats2half2_rn(w1.x, w1.y);
             p[j / 2] = *reinterpret_cast<const uint32_t*>(&lo);
             p[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&hi);
           }
-          if (kCopies == 1) {
-            tmem_store32(s_at + kTmemWeights + first / 2, p);
-          } else {  // this copy's keys, and 0 for the other's
-            uint32_t z[kStepKeys / 2];
-#pragma unroll
-            for (int j = 0; j < kStepKeys / 2; ++j) z[j] = copy ? 0u : p[j];
-            tmem_store32(s_at + kTmemWeights, z);
-#pragma unroll
-            for (int j = 0; j < kStepKeys / 2; ++j) z[j] = copy ? p[j] : 0u;
-            tmem_store32(s_at + kTmemWeights + kKeys / 2, z);
-          }
+          tmem_store16(s_at + kTmemWeights + first / 2, p);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float2 sums = parts_of(add2(sum0, sum1));
+        l += sums.x + sums.y;
         tmem_wait_stores();
         tc_before();
       }
@@ -636,12 +728,16 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Walker<kRows> walker, 
         if (kCopies == 2)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] += __shfl_xor_sync(kFullMask, v[j], 16);
-        if (real && copy == 0)
+        if (real)  // each copy its share
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 x = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-            if (seg.whole) store4(out + c + j, x);
-            else __stcg(reinterpret_cast<float4*>(mine + 2 * kRows + row * kD + group * kDims + c + j), x);
+          for (int j = 0; j < 32 / kCopies; j += 4) {
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = kCopies == 2 && copy ? v[(j + k + 16) & 31] : v[j + k];
+            const int d = c + j + copy * (32 / kCopies);
+            const float4 y = make_float4(x[0], x[1], x[2], x[3]);
+            if (seg.whole) store4(out + d, y);
+            else __stcg(reinterpret_cast<float4*>(mine + 2 * kRows + row * kD + group * kDims + d), y);
           }
       }
       if (group == 0 && copy == 0) {
@@ -669,27 +765,52 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Walker<kRows> walker, 
       if (*last_part) {  // joins the unit's parts, in the order of the keys
         const float* part0 = a.parts + (int64_t)(gridDim.x + c0) * Sh::kPart;
         const float* part1 = a.parts + (int64_t)c0 * Sh::kPart;
-        for (int item = tid; item < seg.rows * (kD / 4); item += kSoftThreads) {
-          const int r = item / (kD / 4), d = item % (kD / 4) * 4;
-          const int64_t tok = (int64_t)seg.token0 + (seg.row0 + r) / a.G;
-          if (tok < 0 || tok >= a.T) continue;
-          float high = -kInf, sum = 0.0f;
-          for (int k = 0; k < parts; ++k)
-            high = fmaxf(high, __ldcg((k == 0 ? part0 : part1 + (int64_t)k * Sh::kPart) + r));
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        constexpr int kItems = 8;  // four values each that a thread joins at a time
+        for (int item0 = tid; item0 < seg.rows * (kD / 4); item0 += kItems * kSoftThreads) {
+          float4 v[kItems];
+          float high[kItems], sum[kItems];
+#pragma unroll
+          for (int j = 0; j < kItems; ++j) {
+            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            high[j] = -kInf;
+            sum[j] = 0.0f;
+          }
           for (int k = 0; k < parts; ++k) {
             const float* p = k == 0 ? part0 : part1 + (int64_t)k * Sh::kPart;
-            const float pm = __ldcg(p + r);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(p + 2 * kRows + r * kD + d));
-            const float f = pm > -kInf ? ex2(pm - high) : 0.0f;
-            sum += f * __ldcg(p + kRows + r);
-            v.x += y.x * f; v.y += y.y * f; v.z += y.z * f; v.w += y.w * f;
+            float4 y[kItems];
+            float pm[kItems], pl[kItems];
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) {
+              const int item = min(item0 + j * kSoftThreads, kRows * (kD / 4) - 1), r = item / (kD / 4);
+              pm[j] = __ldcg(p + r);
+              pl[j] = __ldcg(p + kRows + r);
+              y[j] = __ldcg(reinterpret_cast<const float4*>(p + 2 * kRows) + item);
+            }
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) {
+              if (pm[j] == -kInf) continue;
+              const float to = fmaxf(high[j], pm[j]);
+              const float f0 = high[j] > -kInf ? ex2(high[j] - to) : 0.0f, f1 = ex2(pm[j] - to);
+              high[j] = to;
+              sum[j] = sum[j] * f0 + pl[j] * f1;
+              v[j].x = v[j].x * f0 + y[j].x * f1;
+              v[j].y = v[j].y * f0 + y[j].y * f1;
+              v[j].z = v[j].z * f0 + y[j].z * f1;
+              v[j].w = v[j].w * f0 + y[j].w * f1;
+            }
           }
-          const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
-          const int64_t at = tok * a.Hq + seg.h * a.G + (seg.row0 + r) % a.G;
-          store4(static_cast<uint16_t*>(a.out) + at * kD + d, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-          if (d == 0 && a.lse != nullptr)
-            a.lse[at] = sum > 0.0f ? (high + log2f(sum)) * 0.693147180559945309f : -kInf;
+#pragma unroll
+          for (int j = 0; j < kItems; ++j) {
+            const int item = item0 + j * kSoftThreads, r = item / (kD / 4), d = item % (kD / 4) * 4;
+            const int64_t tok = (int64_t)seg.token0 + (seg.row0 + r) / a.G;
+            if (item >= seg.rows * (kD / 4) || tok < 0 || tok >= a.T) continue;
+            const float f = sum[j] > 0.0f ? 1.0f / sum[j] : 0.0f;
+            const int64_t at = tok * a.Hq + seg.h * a.G + (seg.row0 + r) % a.G;
+            store4(static_cast<uint16_t*>(a.out) + at * kD + d,
+                   make_float4(v[j].x * f, v[j].y * f, v[j].z * f, v[j].w * f));
+            if (d == 0 && a.lse != nullptr)
+              a.lse[at] = sum[j] > 0.0f ? (high[j] + log2f(sum[j])) * 0.693147180559945309f : -kInf;
+          }
         }
         if (!soft_sync()) return;  // before *last_part is written again
       }
@@ -703,6 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_attention_kernel(AttnArgs a)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   __shared__ Walk walk;
+  __shared__ Way<kRows> ways[kThreads / 32];
   __shared__ uint32_t tmem_at;
   __shared__ int last_part, abort;
   pdl_launch_dependents();
@@ -711,20 +833,22 @@ __global__ void __launch_bounds__(kThreads, 1) wide_attention_kernel(AttnArgs a)
   const uint32_t base = smem_addr(smem) + Sh::kBarsAt;
   Bars bars;
   for (int i = 0; i < 2; ++i) {
-    bars.full[i] = base + 8 * i;
-    bars.empty[i] = base + 16 + 8 * i;
-    bars.scores[i] = base + 32 + 8 * i;
-    bars.weights[i] = base + 48 + 8 * i;
+    bars.k_full[i] = base + 8 * i;
+    bars.v_full[i] = base + 16 + 8 * i;
+    bars.empty[i] = base + 32 + 8 * i;
+    bars.scores[i] = base + 48 + 8 * i;
+    bars.weights[i] = base + 64 + 8 * i;
   }
-  bars.q = base + 64;
-  for (int i = 0; i < 4; ++i) bars.pair[i] = base + 72 + 8 * i;
-  bars.soft = base + 104;
-  bars.done = base + 112;
+  bars.q = base + 80;
+  for (int i = 0; i < 4; ++i) bars.pair[i] = base + 88 + 8 * i;
+  bars.soft = base + 120;
+  bars.done = base + 128;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bars.full[i], kFeedWarps);
+      mbar_init(bars.k_full[i], kFeedWarps);
+      mbar_init(bars.v_full[i], kFeedWarps);
       mbar_init(bars.empty[i], 1);
-      mbar_init(bars.scores[i], 1);
+      mbar_init(bars.scores[i], 2);
       mbar_init(bars.weights[i], kSoftWarps / 2);
     }
     mbar_init(bars.q, kSoftWarps);
@@ -742,13 +866,14 @@ __global__ void __launch_bounds__(kThreads, 1) wide_attention_kernel(AttnArgs a)
   __syncthreads();
   tc_after();
   const uint32_t tmem = tmem_at;
-  Walker<kRows> walker{walk};
+  Way<kRows>* way = ways + warp;
+  if ((tid & 31) == 0) way->walker.w = walk;
   if (warp < kSoftWarps) {
-    soften<kD, kRows>(a, walker, smem, tmem, bars, &abort, total, ctas, &last_part);
+    soften<kD, kRows>(a, way, smem, tmem, bars, &abort, total, ctas, &last_part);
   } else if (warp < kSoftWarps + kFeedWarps) {
-    feed<kD, kRows>(a, walker, smem, bars, &abort);
+    feed<kD, kRows>(a, way, smem, bars, &abort);
   } else if ((tid & 31) == 0) {
-    multiply<kD, kRows>(a, walker, smem_addr(smem), tmem, bars, &abort);
+    multiply<kD, kRows>(a, &way->walker, smem_addr(smem), tmem, bars, &abort);
     tc_commit(bars.done);  // nothing is in flight when the memory is given back
     mbar_wait(bars.done, 0, &abort);
   }

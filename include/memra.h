@@ -585,7 +585,9 @@ memra_status memra_kv_read_q8(const int32_t* slots, int64_t N, const int8_t* kq,
  * lse = -inf.  Cache entries at and beyond kv_lens[b], and page entries that hold no
  * visible key, are not used, whatever they hold.  A page number outside [0, n_pages) hides
  * its tokens and kv_lens beyond max_pages * P are cut to it (status 1).
- * Statistics and sums are fp32.
+ * Statistics and sums are fp32.  exp(s_j) and the scale of v_j are held to 11 bits (bf16
+ * queries) or 22 (fp32) for the sum over v, on a grid that ends at 2^-33 of the largest
+ * exp(s_j) times the largest scale of V that the row meets: what is smaller counts as 0.
  *   workspace: MEMRA_KV_ATTENTION_WORKSPACE_BYTES, 16-byte aligned, zeroed once by the
  *   caller before its first use; every call leaves it fit for the next.  Calls that may
  *   overlap on the GPU need one each.

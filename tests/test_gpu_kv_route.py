@@ -326,7 +326,7 @@ def ref_attention(q, kq, kd, vq, vd, table, lens, cu, scale, window):
                 out[t, h] = (p / l) @ vv
                 size[t, h] = (p / l) @ np.abs(vv)
                 lse[t, h] = m + np.log(l)
-                reach[t, h] = (scale * np.abs(kk) @ np.abs(q[t, h])).max()
+                reach[t, h] = (abs(scale) * np.abs(kk) @ np.abs(q[t, h])).max()
     return out, lse, size, reach
 
 
@@ -355,7 +355,7 @@ def attention_case(rs, lens, new, Hq, Hkv, D, P, S, dtype, peak=1.5):
 
 
 def check_attention(mem, q, kq, kd, vq, vd, table, lens, cu, scale=None, window=0, status=0, workspace=None,
-                    rows=None):
+                    rows=None, wide_scales=False):
     D = q.shape[2]
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     i32 = torch.int32
@@ -375,7 +375,15 @@ def check_attention(mem, q, kq, kd, vq, vd, table, lens, cu, scale=None, window=
     # 2^-11 for bf16 results (next to their own rounding, 2^-9), 2^-19 for fp32 ones.
     ds = 2.0 ** -18 * reach + 1e-6
     e = (2.0 ** -8 + 2.0 ** -10 if q.dtype == torch.bfloat16 else 2.0 ** -18) + 2 * ds
-    assert (np.abs(got - want) <= e[..., None] * size + 1e-7).all()
+    # ... and on a grid that ends at 2^-33 of the largest weight and scale (a half of it a key)
+    floor = np.zeros(got.shape[:2])
+    if wide_scales:
+        for b in range(len(lens)):
+            live = table[b, :-(-min(int(lens[b]), table.shape[1] * kq.shape[2]) // kq.shape[2])]
+            live = live[(live >= 0) & (live < len(vd))]
+            most = np.nanmax(np.where(np.isfinite(vd[live]), vd[live], 0), axis=(0, 2)) if len(live) else np.zeros(vd.shape[1])
+            floor[int(cu[b]):int(cu[b + 1])] = (2.0 ** -33 * 127 * lens[b] * np.repeat(most, q.shape[1] // len(most)))[None, :]
+    assert (np.abs(got - want) <= e[..., None] * size + floor[..., None] + 1e-7).all()
     fine = ~none
     assert (np.abs(glse - np.where(fine, wlse, 0))[fine] <= (ds + 2e-6 + 4e-7 * np.abs(np.where(fine, wlse, 0)))[fine]).all()
     return out, lse
@@ -405,6 +413,71 @@ def test_attention(mem, case):
     lens, new, Hq, Hkv, D, P, S, dtype, window = ATTEND[case]
     c = attention_case(np.random.RandomState(case), lens, new, Hq, Hkv, D, P, S, dtype)
     check_attention(mem, *c, window=window)
+
+
+WIDE = [
+    # bf16, more than 32 rows to a cached head, 4096 rows in all: the kernel on tcgen05
+    # lens, new, Hq, Hkv, D, P, S, window
+    ([500, 130, 17, 0, 300], [40, 30, 30, 20, 30], 32, 8, 128, 64, 16, 0),
+    ([2000], [16], 256, 4, 128, 128, 64, 0),
+    ([700, 40, 333], [22, 22, 20], 64, 16, 64, 16, 4, 0),
+    ([260, 900], [33, 5], 128, 1, 128, 48, 16, 100),
+    ([400], [130], 32, 2, 64, 1024, 1024, 33),
+    ([60, 300, 1, 2], [100, 9, 8, 8], 48, 6, 128, 32, 1, 0),
+    ([3000, 128, 256, 129], [8, 8, 8, 8], 128, 16, 128, 64, 16, 1),
+    ([2500, 5, 77], [10, 60, 10], 64, 2, 64, 96, 24, 0),
+]
+
+
+@pytest.mark.parametrize("case", range(len(WIDE)))
+def test_attention_wide(mem, case):
+    lens, new, Hq, Hkv, D, P, S, window = WIDE[case]
+    c = attention_case(np.random.RandomState(50 + case), lens, new, Hq, Hkv, D, P, S, "bf16")
+    ws = torch.zeros(mem.KV_ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    o, l = check_attention(mem, *c, window=window, workspace=ws)
+    o2, l2 = check_attention(mem, *c, window=window, workspace=ws)
+    assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 0.3])
+def test_attention_wide_extremes(mem, scale):
+    """Scales of either sign, peaked scores, zero blocks, scales of V far apart, pages out of
+    range."""
+    q, kq, kd, vq, vd, table, lens, cu = attention_case(np.random.RandomState(77), [900, 450], [40, 40], 64, 8, 128, 32,
+                                                        16, "bf16", 4.0)
+    rs = np.random.RandomState(78)
+    vd *= np.where(rs.rand(*vd.shape) < 0.2, np.float32(1e6), np.float32(1.0)).astype(np.float32)
+    vd[table[0, :4]] = 0.0
+    kd[table[1, 1], 1, 0] = 0.0
+    check_attention(mem, q, kq, kd, vq, vd, table, lens, cu, scale=scale, wide_scales=True)
+    bad = table.copy()
+    bad[0, 3], bad[0, 9], bad[1, 0] = -1, 10 ** 6, -5
+    check_attention(mem, q, kq, kd, vq, vd, bad, lens, cu, scale=scale, status=1, wide_scales=True)
+
+
+def test_attention_wide_strides_and_unowned_rows(mem):
+    q, kq, kd, vq, vd, table, lens, cu = attention_case(np.random.RandomState(79), [400, 200], [60, 60], 40, 8, 128, 64,
+                                                        16, "bf16")
+    o, l = check_attention(mem, q, kq, kd, vq, vd, table, lens, cu)
+    wide = torch.full((125, 44, 128), float("nan"), dtype=q.dtype, device="cuda")
+    wide[:120, 3:43] = q
+    i32 = torch.int32
+    o2, l2 = mem.memra_kv_attention_q8(wide[:, 3:43], dev(kq), dev(kd), dev(vq), dev(vd), dev(table, i32),
+                                       dev(lens, i32), dev(cu, i32))
+    assert torch.equal(o2[:120], o) and torch.equal(l2[:120], l)
+    assert bool((o2[120:] == 0).all()) and bool(torch.isneginf(l2[120:]).all())
+
+
+def test_attention_many_requests(mem):
+    """More requests than a CTA has threads, most of them without a token or a query."""
+    rs = np.random.RandomState(81)
+    lens = np.where(rs.rand(1300) < 0.9, 0, rs.randint(1, 60, 1300))
+    new = np.where(rs.rand(1300) < 0.7, 0, 1)
+    c = attention_case(rs, lens, new, 4, 2, 64, 16, 16, "fp32")
+    check_attention(mem, *c)
+    new = np.where(rs.rand(1300) < 0.9, 0, 40)
+    c = attention_case(rs, lens, new, 4, 2, 64, 16, 16, "bf16")
+    check_attention(mem, *c)
 
 
 def test_attention_is_the_same_every_time_and_leaves_its_workspace_fit(mem):
