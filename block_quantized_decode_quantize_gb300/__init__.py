@@ -891,6 +891,13 @@ def _rows(t, name, dev, ndim):
     return dt
 
 
+def _strides(t):
+    """Strides of rows and heads of [rows, heads, D]; those of a single row or head, which
+    reach nothing and may be any number, as if dense."""
+    rows, heads, D = t.shape
+    return (t.stride(0) if rows > 1 else heads * D), (t.stride(1) if heads > 1 else D)
+
+
 # The current stream's handle without a Stream object around it (1 us less).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -1007,12 +1014,12 @@ def memra_kv_append_q8(k, v, slots, kq, kd, vq, vd, dev_status=None):
     T = k.shape[0]
     if k.shape[1] != Hkv or k.shape[2] != D:
         raise ValueError("k has shape %s, expected %s" % (tuple(k.shape), (T, Hkv, D)))
-    if _rows(v, "v", dev, 3) != dt or v.shape != k.shape or v.stride() != k.stride():
+    if _rows(v, "v", dev, 3) != dt or v.shape != k.shape or _strides(v) != _strides(k):
         raise ValueError("v must have k's dtype, shape and strides")
     _ok(slots, "slots", torch.int32, dev, (T,))
     if dev_status is not None:
         _ok(dev_status, "dev_status", torch.int32, dev, (1,))
-    stride_t, stride_h, _ = k.stride()
+    stride_t, stride_h = _strides(k)
     _launch("memra_kv_append_q8", dev, k.data_ptr(), v.data_ptr(), dt, T, stride_t, stride_h,
             slots.data_ptr(), kq.data_ptr(), kd.data_ptr(), vq.data_ptr(), vd.data_ptr(), n_pages,
             Hkv, page, D, block, _addr(dev_status))
@@ -1096,7 +1103,7 @@ def memra_kv_attention_q8(q, kq, kd, vq, vd, block_table, kv_lens, cu_q, scale=N
         _ok(workspace, "workspace", torch.uint8, dev, workspace.shape)
     if dev_status is not None:
         _ok(dev_status, "dev_status", i32, dev, (1,))
-    stride_t, stride_h, _ = q.stride()
+    stride_t, stride_h = _strides(q)
     _launch("memra_kv_attention_q8", dev, q.data_ptr(), dt, T, Hq, stride_t, stride_h,
             kq.data_ptr(), kd.data_ptr(), vq.data_ptr(), vd.data_ptr(), n_pages, Hkv, page, D,
             block, block_table.data_ptr(), B, max_pages, kv_lens.data_ptr(), cu_q.data_ptr(),

@@ -45,6 +45,16 @@ inline bool rows(const Tensor* t, int64_t dims, int32_t* code) {
   return t->size(dims - 1) <= 1 || t->stride(dims - 1) == 1;
 }
 
+// Strides of rows and heads of [rows][heads][D]; those of a single row or head, which reach
+// nothing and may be any number, as if dense.
+struct Strides {
+  int64_t t, h;
+  explicit Strides(const Tensor* x)
+      : t(x->size(0) > 1 ? x->stride(0) : x->size(1) * x->size(2)),
+        h(x->size(1) > 1 ? x->stride(1) : x->size(2)) {}
+  bool operator==(const Strides& o) const { return t == o.t && h == o.h; }
+};
+
 template <typename V>
 inline V* data(const Tensor* t) {
   return t != nullptr ? static_cast<V*>(t->data_ptr()) : nullptr;
@@ -167,10 +177,11 @@ PyObject* append(PyObject*, PyObject* const* o, Py_ssize_t n) {
   const Tensor *k = tensor(o[0], &dev), *v = tensor(o[1], &dev), *slots = tensor(o[2], &dev);
   int32_t code, code_v, *status;
   if (!rows(k, 3, &code) || !rows(v, 3, &code_v) || code != code_v || k->size(1) != c.heads ||
-      k->size(2) != c.D || v->sizes() != k->sizes() || v->strides() != k->strides() ||
+      k->size(2) != c.D || v->sizes() != k->sizes() || !(Strides(v) == Strides(k)) ||
       !dense(slots, at::kInt, {k->size(0)}) || !word(o[7], dev, &status) || !current(dev))
     Py_RETURN_NONE;
-  if (memra_kv_append_q8(data<void>(k), data<void>(v), code, k->size(0), k->stride(0), k->stride(1),
+  const Strides step(k);
+  if (memra_kv_append_q8(data<void>(k), data<void>(v), code, k->size(0), step.t, step.h,
                          data<int32_t>(slots), c.kq, c.kd, c.vq, c.vd, c.n_pages, c.heads, c.page,
                          c.D, c.block, status, stream(dev)) != MEMRA_OK)
     Py_RETURN_NONE;
@@ -229,7 +240,8 @@ PyObject* attention(PyObject*, PyObject* const* o, Py_ssize_t n) {
   at::AutoDispatchBelowADInplaceOrView guard;
   const Tensor out = at::empty({T, Hq, c.D}, on(dev, q->scalar_type()));
   const Tensor lse = at::empty({T, Hq}, on(dev, at::kFloat));
-  if (memra_kv_attention_q8(data<void>(q), code, T, Hq, q->stride(0), q->stride(1), c.kq, c.kd,
+  const Strides step(q);
+  if (memra_kv_attention_q8(data<void>(q), code, T, Hq, step.t, step.h, c.kq, c.kd,
                             c.vq, c.vd, c.n_pages, c.heads, c.page, c.D, c.block,
                             data<int32_t>(table), B, max_pages, data<int32_t>(lens),
                             data<int32_t>(cu), scale, window, out.data_ptr(),

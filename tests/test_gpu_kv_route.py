@@ -258,6 +258,28 @@ def test_append_and_read(mem, Hkv, D, P, S, T, dtype, strided):
             assert torch.equal(got.cpu(), val)
 
 
+@pytest.mark.parametrize("quick", [True, False])
+def test_a_single_row_may_have_any_strides(mem, quick, monkeypatch):
+    """A view of one row or one head keeps whatever strides it was cut with."""
+    if not quick:
+        class Slow:
+            append = attention = staticmethod(lambda *a: None)
+        monkeypatch.setattr(mem, "_fast", Slow)
+    rs = np.random.RandomState(3)
+    x = torch.randn(1, 3, 64, generator=torch.Generator().manual_seed(3)).cuda()
+    odd = torch.as_strided(x[:, 1:], (1, 1, 64), (197, 333, 1))
+    c = [dev(t) for t in pool(rs, 2, 1, 16, 64, 16) + pool(rs, 2, 1, 16, 64, 16)]
+    want = [t.clone() for t in c]
+    slots = dev([16], torch.int32)
+    mem.memra_kv_append_q8(x[:, 1:2].clone(), x[:, 1:2].clone(), slots, *want)
+    mem.memra_kv_append_q8(odd, x[:, 1:2].clone(), slots, *c)
+    assert all(torch.equal(a, b) for a, b in zip(c, want))
+    table, lens, cu = dev([[1]], torch.int32), dev([1], torch.int32), dev([0, 1], torch.int32)
+    ws = torch.zeros(mem.KV_ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    got = [mem.memra_kv_attention_q8(q, *c, table, lens, cu, scale=0.125, workspace=ws) for q in (odd, odd.clone())]
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_append_refuses_slots_beyond_the_pool(mem):
     rs = np.random.RandomState(0)
     kq, kd = pool(rs, 2, 1, 16, 64, 16)
