@@ -132,6 +132,10 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity,
 // The default limit of a bounded wait: about a second of SM cycles.
 constexpr long long kWaitLimitCycles = 1ll << 31;
 
+// The limit of a launch's waits (SM cycles) and the stages after which its producers stop
+// (-1: none do), as memra_debug_set_wait_test left them.
+void wait_settings(long long* limit, int* stall_after);
+
 // Bounded wait for barrier phase `parity`.  Gives up when `*abort` is set by
 // another thread or after `limit` SM cycles, setting `*abort`; returns whether the
 // phase completed.

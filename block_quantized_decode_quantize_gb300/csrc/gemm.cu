@@ -1443,9 +1443,7 @@ memra_status run_product(Params p, cudaStream_t stream) {
   p.prefill_stages = MODE != kDense ? tma_tuning().routed_prefill
                      : (FMT != kQ8 && M == 1 ? tma_tuning().prefill_4bit
                                              : tma_tuning().prefill_stages);
-  const long long wl = g_test_wait_limit.load(std::memory_order_relaxed);
-  p.wait_limit = wl > 0 ? wl : kWaitLimitCycles;
-  p.stall_after = (int)g_test_stall_after.load(std::memory_order_relaxed);
+  wait_settings(&p.wait_limit, &p.stall_after);
   p.qrow = FMT == kQ8 ? p.K : p.K / 2;
   p.nb = (int)(p.K / 32);
   p.cpr = (p.nb + 31) / 32;
@@ -1545,6 +1543,13 @@ memra_status in_passes(int64_t M, Pass&& pass) {
 }
 
 }  // namespace
+
+void wait_settings(long long* limit, int* stall_after) {
+  const long long wl = g_test_wait_limit.load(std::memory_order_relaxed);
+  *limit = wl > 0 ? wl : kWaitLimitCycles;
+  *stall_after = (int)g_test_stall_after.load(std::memory_order_relaxed);
+}
+
 }  // namespace memra
 
 using namespace memra;

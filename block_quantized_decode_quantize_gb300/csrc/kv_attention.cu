@@ -829,6 +829,7 @@ extern "C" memra_status memra_kv_attention_q8(
   a.arrived = static_cast<int*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + kMaxCtas * 4);
   a.status = dev_status;
+  wait_settings(&a.wait_limit, &a.stall_after);
   const cudaError_t e = dtype == MEMRA_BF16 ? launch_attention<uint16_t>(a, (int)D, info, stream)
                                             : launch_attention<float>(a, (int)D, info, stream);
   if (e != cudaSuccess) return cuda_fail(e);

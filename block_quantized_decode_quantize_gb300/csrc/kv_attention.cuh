@@ -43,6 +43,8 @@ struct AttnArgs {
   int* arrived;   // [kMaxCtas], zero between calls
   float* parts;   // [2][CTAs][rows * (D + 2)]
   int32_t* status;
+  long long wait_limit;  // of the wide kernel's waits (cycles), and the test hook's stall
+  int stall_after;
 };
 
 __device__ __forceinline__ float ex2(float x) {

@@ -18,6 +18,8 @@
 // Units of up to 64 rows put every row into the product twice, and each copy's lane takes
 // half of the keys (the products write the lanes of one copy at a time): that spreads the
 // exponentials, 16 a cycle on an SM, over all of its quarters.
+// Every wait is bounded: when one runs out the CTA's other warps are released too, its rows
+// become NaN and status bit 2 is set.
 // Accumulators stay in tensor memory for a unit's whole range of keys; they are rescaled
 // only when a maximum moves by more than the slack, and the two groups' (and copies') are
 // joined at the end.  Scales never meet the codes: kd multiplies a score, vd a weight.
@@ -253,8 +255,8 @@ __device__ __forceinline__ bool next_unit(const AttnArgs& a, Way<kRows>* way) {
 }
 
 // A whole warp's bounded wait, with one answer for all its lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(kFullMask, mbar_wait(bar, parity, abort));
+__device__ __forceinline__ bool warp_wait(const AttnArgs& a, uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(kFullMask, mbar_wait(bar, parity, abort, a.wait_limit));
 }
 
 struct Bars {  // shared-memory addresses
@@ -390,7 +392,7 @@ __device__ __forceinline__ void feed(const AttnArgs& a, Way<kRows>* way, uint8_t
     load_scales(next, true);
   }
   bool ahead = have && next_ref(next);
-  for (uint32_t g = 0; have; ++g) {
+  for (uint32_t g = 0; have && (int)g != a.stall_after; ++g) {
     const int64_t strip = strip_of(next);
     const bool beyond = ahead && next_ref(after);  // its pages are there a tile later
     if (!ahead) after.page = after.scale_page = -1;
@@ -398,7 +400,7 @@ __device__ __forceinline__ void feed(const AttnArgs& a, Way<kRows>* way, uint8_t
     const uint32_t free_phase = ((g >> 1) & 1) ^ 1;
     uint8_t* k_at = smem + stage * 2 * Sh::kOperand;
     // K, once the scores two tiles back are made
-    if (g >= 2 && !warp_wait(bars.scores[stage], free_phase, abort)) break;
+    if (g >= 2 && !warp_wait(a, bars.scores[stage], free_phase, abort)) break;
     float* kd = scales + turn * kTile;
     float* vd = scales + (4 + turn) * kTile;
     if (has_scale) {
@@ -418,7 +420,7 @@ __device__ __forceinline__ void feed(const AttnArgs& a, Way<kRows>* way, uint8_t
     if (lane == 0) mbar_arrive(bars.k_full[stage]);
     load_pieces(k_lane, strip, 0);
     // V, once the values two tiles back are summed
-    if (g >= 2 && !warp_wait(bars.empty[stage], free_phase, abort)) break;
+    if (g >= 2 && !warp_wait(a, bars.empty[stage], free_phase, abort)) break;
     cp_wait<1>();
     convert(k_at + Sh::kOperand, 1);
     __syncwarp();
@@ -454,21 +456,21 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Walker<kRows>* walke
   };
   while (walker->next(a, &seg)) {
     if (seg.tiles == 0) continue;
-    if (!mbar_wait(bars.q, unit & 1, abort)) return;
+    if (!mbar_wait(bars.q, unit & 1, abort, a.wait_limit)) return;
     ++unit;
-    if (!mbar_wait(bars.k_full[g & 1], (g >> 1) & 1, abort)) return;
+    if (!mbar_wait(bars.k_full[g & 1], (g >> 1) & 1, abort, a.wait_limit)) return;
     async_proxy_fence();
     tc_after();
     scores(g);
     for (int t = 0; t < seg.tiles; ++t, ++g) {
       if (t + 1 < seg.tiles) {
-        if (!mbar_wait(bars.k_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort)) return;
+        if (!mbar_wait(bars.k_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort, a.wait_limit)) return;
         async_proxy_fence();
         tc_after();
         scores(g + 1);
       }
-      if (!mbar_wait(bars.v_full[g & 1], (g >> 1) & 1, abort)) return;
-      if (!mbar_wait(bars.weights[g & 1], (g >> 1) & 1, abort)) return;
+      if (!mbar_wait(bars.v_full[g & 1], (g >> 1) & 1, abort, a.wait_limit)) return;
+      if (!mbar_wait(bars.weights[g & 1], (g >> 1) & 1, abort, a.wait_limit)) return;
       async_proxy_fence();
       tc_after();
       const uint32_t v = smem + (g & 1) * 2 * Sh::kOperand + Sh::kOperand;
@@ -508,14 +510,14 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
   auto pair_sync = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(bars.pair[quarter]);
-    const bool ok = warp_wait(bars.pair[quarter], pair_phase, abort);
+    const bool ok = warp_wait(a, bars.pair[quarter], pair_phase, abort);
     pair_phase ^= 1;
     return ok;
   };
   auto soft_sync = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(bars.soft);
-    const bool ok = warp_wait(bars.soft, soft_phase, abort);
+    const bool ok = warp_wait(a, bars.soft, soft_phase, abort);
     soft_phase ^= 1;
     return ok;
   };
@@ -579,7 +581,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
       const uint32_t phase = ((g0 + t) >> 1) & 1, turn = (g0 + t) & 3;
       const ulonglong2* kd = scales + turn * (kTile / 4);
       const ulonglong2* vd = kd + kTile;
-      if (!warp_wait(bars.scores[group], phase, abort)) return;
+      if (!warp_wait(a, bars.scores[group], phase, abort)) return;
       if (active) {
         tc_after();
         const int key = seg.key0 + t * kTile + copy * kKeys;
@@ -643,7 +645,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
           m = most - shift;
           l *= f;
           if (t > 1) {  // the accumulators, once the group's last product is done
-            if (!warp_wait(bars.empty[group], phase ^ 1, abort)) return;
+            if (!warp_wait(a, bars.empty[group], phase ^ 1, abort)) return;
             tc_after();
 #pragma unroll 1
             for (int c = 0; c < kD; c += 32) {
@@ -691,7 +693,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
     const bool has[2] = {seg.tiles > (int)(g0 & 1), seg.tiles > (int)((g0 ^ 1) & 1)};  // group 0's, 1's tiles
     for (int k = 0; k < 2; ++k) {
       const uint32_t last = g0 + seg.tiles - 1;  // the last tile of stage k is this or the one before
-      if (has[k] && !warp_wait(bars.empty[k], ((last - ((last ^ k) & 1)) >> 1) & 1, abort)) return;
+      if (has[k] && !warp_wait(a, bars.empty[k], ((last - ((last ^ k) & 1)) >> 1) & 1, abort)) return;
     }
     tc_after();
     float* mine = a.parts + (int64_t)((seg.begins ? gridDim.x : 0) + blockIdx.x) * Sh::kPart;
@@ -826,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_attention_kernel(AttnArgs a)
   __shared__ Walk walk;
   __shared__ Way<kRows> ways[kThreads / 32];
   __shared__ uint32_t tmem_at;
-  __shared__ int last_part, abort;
+  __shared__ int last_part, abort, late;
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -856,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_attention_kernel(AttnArgs a)
     mbar_init(bars.soft, kSoftWarps);
     mbar_init(bars.done, 1);
     mbar_init_fence();
-    abort = 0;
+    abort = late = 0;
   }
   int ctas;
   int64_t total;
@@ -875,14 +877,27 @@ __global__ void __launch_bounds__(kThreads, 1) wide_attention_kernel(AttnArgs a)
   } else if ((tid & 31) == 0) {
     multiply<kD, kRows>(a, &way->walker, smem_addr(smem), tmem, bars, &abort);
     tc_commit(bars.done);  // nothing is in flight when the memory is given back
-    mbar_wait(bars.done, 0, &abort);
+    mbar_wait(bars.done, 0, &late);
   }
   tc_before();
   __syncthreads();
   tc_after();
   __syncwarp();
   if (warp == kThreads / 32 - 1) tmem_free(tmem, kTmemColumns);
-  if (tid == 0 && abort != 0 && a.status != nullptr) atomicOr(a.status, 2);
+  if (abort != 0) {  // a wait ran out: the CTA's rows are not to be taken for results
+    if (tid == 0 && a.status != nullptr) atomicOr(a.status, 2);
+    const float nan = __int_as_float(0x7fffffff);
+    Walker<kRows> walker{walk};
+    Segment seg;
+    while (walker.next(a, &seg))
+      for (int i = tid; i < seg.rows * (kD / 4); i += kThreads) {
+        const int r = seg.row0 + i / (kD / 4), d = i % (kD / 4) * 4;
+        const int64_t token = (int64_t)seg.token0 + r / a.G, at = token * a.Hq + seg.h * a.G + r % a.G;
+        if (token < 0 || token >= a.T) continue;
+        store4(static_cast<uint16_t*>(a.out) + at * kD + d, make_float4(nan, nan, nan, nan));
+        if (d == 0 && a.lse != nullptr) a.lse[at] = nan;
+      }
+  }
 }
 
 template <int kD, int kRows>

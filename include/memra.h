@@ -591,6 +591,9 @@ memra_status memra_kv_read_q8(const int32_t* slots, int64_t N, const int8_t* kq,
  *   workspace: MEMRA_KV_ATTENTION_WORKSPACE_BYTES, 16-byte aligned, zeroed once by the
  *   caller before its first use; every call leaves it fit for the next.  Calls that may
  *   overlap on the GPU need one each.
+ * With many rows a call waits on its own barriers, for about a second at most; when a wait
+ * runs out, the rows that it was for become NaN (lse too), *dev_status is OR-ed with 2, and
+ * the workspace has to be zeroed before it is used again.
  */
 memra_status memra_kv_attention_q8(const void* q, int32_t dtype, int64_t T, int64_t Hq,
                                    int64_t stride_t, int64_t stride_h, const int8_t* kq,
@@ -649,8 +652,9 @@ memra_status memra_read_stream(const void* buf, int64_t bytes, uint32_t* sink,
                                int32_t ctas_per_sm, cudaStream_t stream);
 
 /*
- * Test hook for the device-side failure handling; the pages have no counterpart.  The
- * bulk-copy product kernel bounds every wait on its shared-memory barriers (about a
+ * Test hook for the device-side failure handling; the pages have no counterpart.  (The
+ * many-row kernel of memra_kv_attention_q8 takes it too, a stage being a tile of 128 keys.)
+ * The bulk-copy product kernel bounds every wait on its shared-memory barriers (about a
  * second of SM cycles by default): when a wait runs out, the CTA raises an abort flag
  * that releases its other warps, lets the copies it issued land, writes NaN into the
  * outputs it owns, ORs 2 into *dev_status (routed entry points, when given) and

@@ -490,6 +490,32 @@ def test_attention_wide_strides_and_unowned_rows(mem):
     assert bool((o2[120:] == 0).all()) and bool(torch.isneginf(l2[120:]).all())
 
 
+def test_attention_wide_gives_up_and_recovers(mem):
+    """Every wait of the many-row kernel is bounded: when one runs out the rows become NaN and
+    status bit 2 is set, and with a zeroed workspace the next call is as before."""
+    rs = np.random.RandomState(80)
+    c = attention_case(rs, [900, 700, 64], [60, 60, 60], 32, 4, 128, 64, 16, "bf16")
+    t = [c[0]] + [dev(x) for x in c[1:5]] + [dev(x, torch.int32) for x in c[5:]]
+    ws = torch.zeros(mem.KV_ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = mem.memra_kv_attention_q8(*t, scale=0.1, workspace=ws, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    try:
+        mem.memra_debug_set_wait_test(1 << 16, 0)
+        out, lse = mem.memra_kv_attention_q8(*t, scale=0.1, workspace=ws, dev_status=st)
+        torch.cuda.synchronize()                      # the kernel returned
+    finally:
+        mem.memra_debug_set_wait_test()
+    assert int(st) == 2
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+    ws.zero_()
+    st.zero_()
+    again = mem.memra_kv_attention_q8(*t, scale=0.1, workspace=ws, dev_status=st)
+    assert int(st) == 0
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
 def test_attention_many_requests(mem):
     """More requests than a CTA has threads, most of them without a token or a query."""
     rs = np.random.RandomState(81)
