@@ -38,9 +38,10 @@ constexpr int kThreads = kSoftThreads + kFeedThreads + 32;
 constexpr float kLeastRef = 1e-25f;
 constexpr int kCost = 3;  // entries of the list for a unit's fixed time
 
-// Tensor memory columns: scores of two tiles (the weights, two fp16 a column, over the last
-// half of them), then each group's accumulators.
-constexpr uint32_t kTmemColumns = 512, kTmemO = 256, kTmemGroup = 128, kTmemWeights = kTile / 2;
+// Tensor memory columns: scores of two or three tiles and each group's weights (two fp16 a
+// column), then each group's accumulators.
+constexpr uint32_t kTmemColumns = 512, kTmemO = 256, kTmemGroup = 128;
+constexpr int kTurns = 8;  // tiles whose scales of K and V are kept
 
 // kRows: a unit's rows, 64 (two lanes to a row) or 128.
 template <int kD, int kRows>
@@ -48,14 +49,26 @@ struct Shape {
   static constexpr int kOperand = kTile * kD * 2;       // K or V of a tile in fp16
   static constexpr int kQ = kLanes * kD * 2;
   static constexpr int kQAt = 4 * kOperand;             // after two stages of K, V
-  static constexpr int kScalesAt = kQAt + kQ;           // kd [4][128], vd [4][128]
-  static constexpr int kUnitAt = kScalesAt + 8 * kTile * 4;  // amax [group][lane], [2 units][m, l][group][lane]
-  static constexpr int kMiscAt = kUnitAt + 10 * kLanes * 4;      // vd maxima [4][4], hidden strips [4][8]
-  static constexpr int kRawAt = kMiscAt + 128;  // the feeding threads' pieces of the next tile
+  static constexpr int kScalesAt = kQAt + kQ;           // kd, then vd: [kTurns][128]
+  static constexpr int kUnitAt = kScalesAt + 2 * kTurns * kTile * 4;  // amax [group][lane], [2 units][m, l][group][lane]
+  static constexpr int kMiscAt = kUnitAt + 10 * kLanes * 4;      // vd maxima [kTurns][4], hidden strips [kTurns][8]
+  static constexpr int kHiddenAt = kMiscAt + kTurns * 16;
+  static constexpr int kRawAt = kHiddenAt + kTurns * 8;  // the feeding threads' pieces of the next tile
   static constexpr int kRaw = 2 * ((kTile * kD / 16 + kFeedThreads - 1) / kFeedThreads) * kFeedThreads * 16;
   static constexpr int kBarsAt = kRawAt + kRaw;
-  static constexpr int kSmem = kBarsAt + 17 * 8 + 1024;          // and room to align to 1024
+  static constexpr int kSmem = kBarsAt + 18 * 8 + 1024;          // and room to align to 1024
   static constexpr int kPart = 2 * kRows + kRows * kD;           // m, l, values: floats
+  // Scores run kStages - 1 tiles ahead of the values: two where a lane has half of the keys,
+  // so that a group finds its next scores when it has made its weights (a tile took 3500
+  // cycles with one tile); with all keys the columns are full, and the weights lie over the
+  // last half of the scores.
+  static constexpr int kCopies = kLanes / kRows, kKeys = kTile / kCopies;  // of a tile, a lane
+  static constexpr int kStages = kCopies == 2 ? 3 : 2;
+  static __device__ __forceinline__ uint32_t scores_at(uint32_t tile) { return tile % kStages * kKeys; }
+  static __device__ __forceinline__ uint32_t scores_phase(uint32_t tile) { return tile / kStages & 1; }
+  static __device__ __forceinline__ uint32_t weights_at(uint32_t group) {
+    return kCopies == 2 ? kStages * kKeys + group * (kKeys / 2) : group * kTile + kTile / 2;
+  }
 };
 
 // ---- tcgen05 ----
@@ -260,7 +273,7 @@ __device__ __forceinline__ bool warp_wait(const AttnArgs& a, uint32_t bar, uint3
 }
 
 struct Bars {  // shared-memory addresses
-  uint32_t k_full[2], v_full[2], empty[2], scores[2], weights[2], q, pair[4], soft, done;
+  uint32_t k_full[2], v_full[2], empty[2], scores[3], weights[2], q, pair[4], soft, done;
 };
 
 // ---- 11 warps: codes from the cache to fp16 operands ----
@@ -280,10 +293,11 @@ __device__ __forceinline__ void feed(const AttnArgs& a, Way<kRows>* way, uint8_t
   // Scales: kd of key tid (warps 0 .. 3), vd of key tid - 128 (4 .. 7).
   const bool scale_v = tid >= kTile, has_scale = tid < 2 * kTile;
   const int scale_key = tid & (kTile - 1);
-  // A tile's scales stay until its weights are made, two tiles longer than its codes.
-  float* scales = reinterpret_cast<float*>(smem + Sh::kScalesAt);  // [kd, vd][tile & 3][key]
-  float* v_most = reinterpret_cast<float*>(smem + Sh::kMiscAt);    // [tile & 3][4]
-  uint8_t* hidden = smem + Sh::kMiscAt + 64;                       // [tile & 3][8]
+  // A tile's scales stay until its weights are made.  They are written after the scores two
+  // tiles back, which follow the weights of three more tiles back at least.
+  float* scales = reinterpret_cast<float*>(smem + Sh::kScalesAt);  // [kd, vd][turn][key]
+  float* v_most = reinterpret_cast<float*>(smem + Sh::kMiscAt);    // [turn][4]
+  uint8_t* hidden = smem + Sh::kHiddenAt;                          // [turn][8]
   const int blocks = (int)a.by_block((uint32_t)a.page);
 
   int tile = 0, tiles = 0;
@@ -382,29 +396,14 @@ __device__ __forceinline__ void feed(const AttnArgs& a, Way<kRows>* way, uint8_t
       if (j * kStep + row < kTile) put(base, j * kStep + row, x[j]);
   };
 
-  // Each piece's place takes the next tile's as soon as it is read.
-  Ref next{}, after{};
-  bool have = next_ref(next);
-  if (have) {
-    const int64_t strip = strip_of(next);
-    load_pieces(k_lane, strip, 0);
-    load_pieces(v_lane, strip, 1);
-    load_scales(next, true);
-  }
-  bool ahead = have && next_ref(next);
-  for (uint32_t g = 0; have && (int)g != a.stall_after; ++g) {
-    const int64_t strip = strip_of(next);
-    const bool beyond = ahead && next_ref(after);  // its pages are there a tile later
-    if (!ahead) after.page = after.scale_page = -1;
-    const int stage = g & 1, turn = g & 3;
-    const uint32_t free_phase = ((g >> 1) & 1) ^ 1;
-    uint8_t* k_at = smem + stage * 2 * Sh::kOperand;
-    // K, once the scores two tiles back are made
-    if (g >= 2 && !warp_wait(a, bars.scores[stage], free_phase, abort)) break;
-    float* kd = scales + turn * kTile;
-    float* vd = scales + (4 + turn) * kTile;
+  // Each piece's place takes the next tile's as soon as it is read; K goes a tile ahead of V,
+  // so that no scores wait for the values of a tile before.
+  Ref next{};
+  auto put_k = [&](uint32_t g, int wait_for) {  // tile g: scales and K, once the scores two tiles back are made
+    const int stage = g & 1, turn = g & (kTurns - 1);
+    if (g >= 2 && !warp_wait(a, bars.scores[(g - 2) % Sh::kStages], Sh::scores_phase(g - 2), abort)) return false;
     if (has_scale) {
-      (scale_v ? vd : kd)[scale_key] = scale;
+      scales[(scale_v ? kTurns + turn : turn) * kTile + scale_key] = scale;
       if (scale_v) {
         const uint32_t most = __reduce_max_sync(kFullMask, __float_as_uint(scale));
         if (lane == 0) v_most[turn * 4 + (warp & 3)] = __uint_as_float(most);
@@ -413,22 +412,47 @@ __device__ __forceinline__ void feed(const AttnArgs& a, Way<kRows>* way, uint8_t
         if (gone && a.status != nullptr) atomicOr(a.status, 1);
       }
     }
-    load_scales(next, ahead);
-    cp_wait<1>();  // K's pieces are there, V's may be under way
-    convert(k_at, 0);
+    if (wait_for == 0) cp_wait<0>();
+    else cp_wait<1>();  // V's pieces may be under way
+    convert(smem + stage * 2 * Sh::kOperand, 0);
     __syncwarp();
     if (lane == 0) mbar_arrive(bars.k_full[stage]);
+    return true;
+  };
+  bool have = a.stall_after != 0 && next_ref(next);  // tile g, then g + 1 and g + 2
+  int64_t strip = -1;
+  if (have) {
+    strip = strip_of(next);
     load_pieces(k_lane, strip, 0);
+    load_pieces(v_lane, strip, 1);
+    load_scales(next, true);
+  }
+  bool ahead = have && next_ref(next);
+  if (have) {
+    put_k(0, 1);
+    strip = strip_of(next);
+    load_pieces(k_lane, strip, 0);
+    load_scales(next, ahead);
+  }
+  for (uint32_t g = 0; have && (int)g != a.stall_after; ++g) {
+    // at this point: V of tile g and K of g + 1 are under way, strip is tile g + 1's
+    const bool beyond = ahead && next_ref(next);  // tile g + 2: its pages are there when K of g + 1 is done
+    if (!beyond) next.page = next.scale_page = -1;
+    if (ahead && !put_k(g + 1, g == 0 ? 0 : 1)) break;
+    const int64_t strip2 = strip_of(next);
+    load_pieces(k_lane, strip2, 0);
+    load_scales(next, beyond);
     // V, once the values two tiles back are summed
-    if (g >= 2 && !warp_wait(a, bars.empty[stage], free_phase, abort)) break;
+    const int stage = g & 1;
+    if (g >= 2 && !warp_wait(a, bars.empty[stage], ((g >> 1) & 1) ^ 1, abort)) break;
     cp_wait<1>();
-    convert(k_at + Sh::kOperand, 1);
+    convert(smem + stage * 2 * Sh::kOperand + Sh::kOperand, 1);
     __syncwarp();
     if (lane == 0) mbar_arrive(bars.v_full[stage]);
     load_pieces(v_lane, strip, 1);
+    strip = strip2;
     have = ahead;
     ahead = beyond;
-    next = after;
   }
   cp_wait<0>();
 }
@@ -438,7 +462,7 @@ template <int kD, int kRows>
 __device__ __forceinline__ void multiply(const AttnArgs& a, Walker<kRows>* walker, uint32_t smem, uint32_t tmem,
                                          const Bars& bars, volatile int* abort) {
   using Sh = Shape<kD, kRows>;
-  constexpr int kCopies = kLanes / kRows, kKeys = kTile / kCopies;  // of a tile, a lane
+  constexpr int kCopies = Sh::kCopies, kKeys = Sh::kKeys;
   constexpr uint32_t kScores = kProduct<kKeys, false>, kValues = kProduct<kD, true>;
   Segment seg;
   uint32_t g = 0, unit = 0;
@@ -449,26 +473,26 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Walker<kRows>* walke
     for (int c = 0; c < kCopies; ++c)
 #pragma unroll
       for (int s = 0; s < kD / 16; ++s)
-        tc_mma_ss(tmem + (t & 1) * kTile, operand(q + (s >> 2) * (kLanes * 128) + (s & 3) * 32, 16),
+        tc_mma_ss(tmem + Sh::scores_at(t), operand(q + (s >> 2) * (kLanes * 128) + (s & 3) * 32, 16),
                   operand(k + c * (kKeys * 128) + (s >> 2) * (kTile * 128) + (s & 3) * 32, 16), kScores, skip(c), s > 0);
-    mbar_arrive(bars.scores[t & 1]);  // passes on what the feeding warps wrote (the scales)
-    tc_commit(bars.scores[t & 1]);
+    mbar_arrive(bars.scores[t % Sh::kStages]);  // passes on what the feeding warps wrote (the scales)
+    tc_commit(bars.scores[t % Sh::kStages]);
+  };
+  auto scores_when_there = [&](uint32_t t) {
+    if (!mbar_wait(bars.k_full[t & 1], (t >> 1) & 1, abort, a.wait_limit)) return false;
+    async_proxy_fence();
+    tc_after();
+    scores(t);
+    return true;
   };
   while (walker->next(a, &seg)) {
     if (seg.tiles == 0) continue;
     if (!mbar_wait(bars.q, unit & 1, abort, a.wait_limit)) return;
     ++unit;
-    if (!mbar_wait(bars.k_full[g & 1], (g >> 1) & 1, abort, a.wait_limit)) return;
-    async_proxy_fence();
-    tc_after();
-    scores(g);
+    for (int t = 0; t < Sh::kStages - 1 && t < seg.tiles; ++t)
+      if (!scores_when_there(g + t)) return;
     for (int t = 0; t < seg.tiles; ++t, ++g) {
-      if (t + 1 < seg.tiles) {
-        if (!mbar_wait(bars.k_full[(g + 1) & 1], ((g + 1) >> 1) & 1, abort, a.wait_limit)) return;
-        async_proxy_fence();
-        tc_after();
-        scores(g + 1);
-      }
+      if (t + Sh::kStages - 1 < seg.tiles && !scores_when_there(g + Sh::kStages - 1)) return;
       if (!mbar_wait(bars.v_full[g & 1], (g >> 1) & 1, abort, a.wait_limit)) return;
       if (!mbar_wait(bars.weights[g & 1], (g >> 1) & 1, abort, a.wait_limit)) return;
       async_proxy_fence();
@@ -478,7 +502,7 @@ __device__ __forceinline__ void multiply(const AttnArgs& a, Walker<kRows>* walke
       for (int c = 0; c < kCopies; ++c)
 #pragma unroll
         for (int s = 0; s < kKeys / 16; ++s)  // 16 keys are two groups of eight rows
-          tc_mma_ts(tmem + kTmemO + (g & 1) * kTmemGroup, tmem + (g & 1) * kTile + kTmemWeights + s * 8,
+          tc_mma_ts(tmem + kTmemO + (g & 1) * kTmemGroup, tmem + Sh::weights_at(g & 1) + s * 8,
                     operand(v + c * (kKeys * 128) + s * 2048, kTile * 128), kValues, skip(c), t > 1 || s > 0);
       tc_commit(bars.empty[g & 1]);
     }
@@ -491,8 +515,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
                                        const Bars& bars, volatile int* abort, int64_t total, int ctas,
                                        int* last_part) {
   using Sh = Shape<kD, kRows>;
-  constexpr int kCopies = kLanes / kRows;
-  constexpr int kKeys = kTile / kCopies;  // of a tile, a thread
+  constexpr int kCopies = Sh::kCopies, kKeys = Sh::kKeys;
   constexpr int kStepKeys = 32;           // of these, at a time in registers
   constexpr int kDims = kD / 2;           // of a row, a thread, at a unit's two ends
   const float kInf = __int_as_float(0x7f800000);
@@ -500,10 +523,10 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
   const int quarter = warp & 3, group = warp >> 2, at_lane = quarter * 32 + lane;
   const int row = quarter * (kRows / 4) + lane % (kRows / 4), copy = lane / (kRows / 4);
   const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-  const uint32_t s_at = lanes + group * kTile, o_at = lanes + kTmemO + group * kTmemGroup;
+  const uint32_t w_at = lanes + Sh::weights_at(group), o_at = lanes + kTmemO + group * kTmemGroup;
   const ulonglong2* scales = reinterpret_cast<const ulonglong2*>(smem + Sh::kScalesAt) + copy * kKeys / 4;
   const float4* v_most = reinterpret_cast<const float4*>(smem + Sh::kMiscAt);
-  const uint2* hidden = reinterpret_cast<const uint2*>(smem + Sh::kMiscAt + 64);
+  const uint2* hidden = reinterpret_cast<const uint2*>(smem + Sh::kHiddenAt);
   float* unit_x = reinterpret_cast<float*>(smem + Sh::kUnitAt);
   uint32_t pair_phase = 0, soft_phase = 0, units = 0, g0 = 0;  // g0: the CTA's tiles before this unit
   // With the other group's warp of the same lanes; false when a wait ran out somewhere.
@@ -578,10 +601,11 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
     float most = 0.0f, bar = -kInf, m = 0.0f, l = 0.0f, ref = 0.0f, shift = 0.0f;
     const int t0 = (int)((g0 ^ group) & 1);  // the group's first tile
     for (int t = t0; t < seg.tiles; t += 2) {
-      const uint32_t phase = ((g0 + t) >> 1) & 1, turn = (g0 + t) & 3;
+      const uint32_t phase = ((g0 + t) >> 1) & 1, turn = (g0 + t) & (kTurns - 1);
+      const uint32_t s_at = lanes + Sh::scores_at(g0 + t);
       const ulonglong2* kd = scales + turn * (kTile / 4);
-      const ulonglong2* vd = kd + kTile;
-      if (!warp_wait(a, bars.scores[group], phase, abort)) return;
+      const ulonglong2* vd = kd + kTurns * (kTile / 4);
+      if (!warp_wait(a, bars.scores[(g0 + t) % Sh::kStages], Sh::scores_phase(g0 + t), abort)) return;
       if (active) {
         tc_after();
         const int key = seg.key0 + t * kTile + copy * kKeys;
@@ -658,6 +682,9 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
             }
           }
         }
+        // The group's last weights are read when its last product is done; with two stages that
+        // came before these scores.
+        if (Sh::kStages == 3 && t > 1 && !warp_wait(a, bars.empty[group], phase ^ 1, abort)) return;
         // Weights: where a lane has all keys they lie over the last half of the scores, so the
         // last keys come first, whose scores are read by then.
         Pair sum0 = pair_of(0.0f, 0.0f), sum1 = sum0;
@@ -678,7 +705,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
             p[j / 2] = *reinterpret_cast<const uint32_t*>(&lo);
             p[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&hi);
           }
-          tmem_store16(s_at + kTmemWeights + first / 2, p);
+          tmem_store16(w_at + first / 2, p);
         }
         const float2 sums = parts_of(add2(sum0, sum1));
         l += sums.x + sums.y;
@@ -767,52 +794,61 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
       if (*last_part) {  // joins the unit's parts, in the order of the keys
         const float* part0 = a.parts + (int64_t)(gridDim.x + c0) * Sh::kPart;
         const float* part1 = a.parts + (int64_t)c0 * Sh::kPart;
-        constexpr int kItems = 8;  // four values each that a thread joins at a time
-        for (int item0 = tid; item0 < seg.rows * (kD / 4); item0 += kItems * kSoftThreads) {
+        // Four threads to a row.  Every other part comes through the queries' place in shared
+        // memory, so that a thread has two parts on the way.
+        constexpr int kItems = kD / 16;  // four values each
+        const int sub = tid & 3;
+        uint4* held = reinterpret_cast<uint4*>(smem + Sh::kQAt) + tid;
+        for (int r = tid >> 2; r < seg.rows; r += kSoftThreads / 4) {
           float4 v[kItems];
-          float high[kItems], sum[kItems];
+          float high = -kInf, sum = 0.0f;
 #pragma unroll
-          for (int j = 0; j < kItems; ++j) {
-            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            high[j] = -kInf;
-            sum[j] = 0.0f;
-          }
-          for (int k = 0; k < parts; ++k) {
-            const float* p = k == 0 ? part0 : part1 + (int64_t)k * Sh::kPart;
-            float4 y[kItems];
-            float pm[kItems], pl[kItems];
-#pragma unroll
-            for (int j = 0; j < kItems; ++j) {
-              const int item = min(item0 + j * kSoftThreads, kRows * (kD / 4) - 1), r = item / (kD / 4);
-              pm[j] = __ldcg(p + r);
-              pl[j] = __ldcg(p + kRows + r);
-              y[j] = __ldcg(reinterpret_cast<const float4*>(p + 2 * kRows) + item);
-            }
+          for (int j = 0; j < kItems; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          auto values_of = [&](int k) { return (k == 0 ? part0 : part1 + (int64_t)k * Sh::kPart) + 2 * kRows + r * kD + sub * 4; };
+          auto fold = [&](float pm, float pl, const float4* y) {
+            if (pm == -kInf) return;
+            const float to = fmaxf(high, pm);
+            const float f0 = high > -kInf ? ex2(high - to) : 0.0f, f1 = ex2(pm - to);
+            high = to;
+            sum = sum * f0 + pl * f1;
 #pragma unroll
             for (int j = 0; j < kItems; ++j) {
-              if (pm[j] == -kInf) continue;
-              const float to = fmaxf(high[j], pm[j]);
-              const float f0 = high[j] > -kInf ? ex2(high[j] - to) : 0.0f, f1 = ex2(pm[j] - to);
-              high[j] = to;
-              sum[j] = sum[j] * f0 + pl[j] * f1;
               v[j].x = v[j].x * f0 + y[j].x * f1;
               v[j].y = v[j].y * f0 + y[j].y * f1;
               v[j].z = v[j].z * f0 + y[j].z * f1;
               v[j].w = v[j].w * f0 + y[j].w * f1;
             }
-          }
+          };
+          for (int k = 0; k < parts; k += 2) {
+            const float* p = values_of(k);
+            const float* p2 = values_of(min(k + 1, parts - 1));
+            float4 y[kItems];
 #pragma unroll
-          for (int j = 0; j < kItems; ++j) {
-            const int item = item0 + j * kSoftThreads, r = item / (kD / 4), d = item % (kD / 4) * 4;
-            const int64_t tok = (int64_t)seg.token0 + (seg.row0 + r) / a.G;
-            if (item >= seg.rows * (kD / 4) || tok < 0 || tok >= a.T) continue;
-            const float f = sum[j] > 0.0f ? 1.0f / sum[j] : 0.0f;
-            const int64_t at = tok * a.Hq + seg.h * a.G + (seg.row0 + r) % a.G;
-            store4(static_cast<uint16_t*>(a.out) + at * kD + d,
-                   make_float4(v[j].x * f, v[j].y * f, v[j].z * f, v[j].w * f));
-            if (d == 0 && a.lse != nullptr)
-              a.lse[at] = sum[j] > 0.0f ? (high[j] + log2f(sum[j])) * 0.693147180559945309f : -kInf;
+            for (int j = 0; j < kItems; ++j) cp16(smem_addr(held + j * kSoftThreads), p2 + j * 16);
+            cp_commit();
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) y[j] = __ldcg(reinterpret_cast<const float4*>(p + j * 16));
+            const int back = -2 * kRows - r * kD - sub * 4 + r;  // from a row's values to its m
+            const float pm = __ldcg(p + back), pl = __ldcg(p + back + kRows);
+            const float pm2 = __ldcg(p2 + back), pl2 = __ldcg(p2 + back + kRows);
+            fold(pm, pl, y);
+            cp_wait<0>();
+            if (k + 1 < parts) {
+#pragma unroll
+              for (int j = 0; j < kItems; ++j) y[j] = *reinterpret_cast<const float4*>(held + j * kSoftThreads);
+              fold(pm2, pl2, y);
+            }
           }
+          const int64_t tok = (int64_t)seg.token0 + (seg.row0 + r) / a.G;
+          if (tok < 0 || tok >= a.T) continue;
+          const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
+          const int64_t at = tok * a.Hq + seg.h * a.G + (seg.row0 + r) % a.G;
+#pragma unroll
+          for (int j = 0; j < kItems; ++j)
+            store4(static_cast<uint16_t*>(a.out) + at * kD + j * 16 + sub * 4,
+                   make_float4(v[j].x * f, v[j].y * f, v[j].z * f, v[j].w * f));
+          if (sub == 0 && a.lse != nullptr)
+            a.lse[at] = sum > 0.0f ? (high + log2f(sum)) * 0.693147180559945309f : -kInf;
         }
         if (!soft_sync()) return;  // before *last_part is written again
       }
@@ -830,17 +866,18 @@ __global__ void __launch_bounds__(kThreads, 1) wide_attention_kernel(AttnArgs a)
   __shared__ uint32_t tmem_at;
   __shared__ int last_part, abort, late;
   pdl_launch_dependents();
-  pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5;
+  if (warp == kThreads / 32 - 1) tmem_alloc(smem_addr(&tmem_at), kTmemColumns);
   const uint32_t base = smem_addr(smem) + Sh::kBarsAt;
   Bars bars;
   for (int i = 0; i < 2; ++i) {
     bars.k_full[i] = base + 8 * i;
     bars.v_full[i] = base + 16 + 8 * i;
     bars.empty[i] = base + 32 + 8 * i;
-    bars.scores[i] = base + 48 + 8 * i;
     bars.weights[i] = base + 64 + 8 * i;
   }
+  for (int i = 0; i < 2; ++i) bars.scores[i] = base + 48 + 8 * i;
+  bars.scores[2] = base + 136;
   bars.q = base + 80;
   for (int i = 0; i < 4; ++i) bars.pair[i] = base + 88 + 8 * i;
   bars.soft = base + 120;
@@ -850,9 +887,9 @@ __global__ void __launch_bounds__(kThreads, 1) wide_attention_kernel(AttnArgs a)
       mbar_init(bars.k_full[i], kFeedWarps);
       mbar_init(bars.v_full[i], kFeedWarps);
       mbar_init(bars.empty[i], 1);
-      mbar_init(bars.scores[i], 2);
       mbar_init(bars.weights[i], kSoftWarps / 2);
     }
+    for (int i = 0; i < 3; ++i) mbar_init(bars.scores[i], 2);
     mbar_init(bars.q, kSoftWarps);
     for (int i = 0; i < 4; ++i) mbar_init(bars.pair[i], 2);
     mbar_init(bars.soft, kSoftWarps);
@@ -860,17 +897,18 @@ __global__ void __launch_bounds__(kThreads, 1) wide_attention_kernel(AttnArgs a)
     mbar_init_fence();
     abort = late = 0;
   }
+  pdl_wait();
   int ctas;
   int64_t total;
-  if (!locate<uint16_t, kD, kRows, kCost, kThreads>(a, &walk, &ctas, &total)) return;
-  if (warp == kThreads / 32 - 1) tmem_alloc(smem_addr(&tmem_at), kTmemColumns);
+  const bool busy = locate<uint16_t, kD, kRows, kCost, kThreads>(a, &walk, &ctas, &total);
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = tmem_at;
   Way<kRows>* way = ways + warp;
   if ((tid & 31) == 0) way->walker.w = walk;
-  if (warp < kSoftWarps) {
+  if (!busy) {
+  } else if (warp < kSoftWarps) {
     soften<kD, kRows>(a, way, smem, tmem, bars, &abort, total, ctas, &last_part);
   } else if (warp < kSoftWarps + kFeedWarps) {
     feed<kD, kRows>(a, way, smem, bars, &abort);
