@@ -31,10 +31,11 @@ constexpr int kUnitCost = 3;   // entries of the list for a unit's fixed time (1
                                // for 16 sequences of 37 to 16000 tokens)
 // Above this many rows to a unit, and with at least so many in all (rows times heads), the
 // tcgen05 kernel takes bf16 queries: below, its larger parts and ends of units cost more than
-// its products save.  Contexts of 500 to 8000, us here / there: 32 rows, 16 requests 64 / 77;
-// 64 rows, 16 requests of 32 heads (4096 in all) 63 / 57; 128 rows, 16 requests 194 / 101; 64
-// rows, 8 requests (4096) 101 / 93, 4 (2048) 65 / 65, 1 (512) 44 / 73; 512 tokens of one prompt 408 / 178.
-constexpr int kWideRows = 32, kWideAll = 4096;
+// its products save.  8 cached heads, us here / there: 32 rows, 16 requests of 500 to 8000
+// tokens 64 / 69; 48 rows 104 / 71; 64 rows, 8 requests (4096 in all) 64 / 46, 4 (2048) 41 / 37,
+// 2 (1024) 32.1 / 31.5, one of 8000 (512) 30.2 / 31.7; 128 rows, one of 16000 (1024) 64 / 60;
+// 256 rows, one of 8000 (2048) 61 / 49; 64 rows, 32 requests of 100 to 500 56 / 41.
+constexpr int kWideRows = 32, kWideAll = 1024;
 constexpr int kMaxParts = 64;  // CTAs to a unit, on average
 
 __device__ __forceinline__ void mma_16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2,
