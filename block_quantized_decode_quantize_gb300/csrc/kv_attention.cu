@@ -14,9 +14,16 @@
 // tensor cores take at full rate.  The 128 leaves S through its initial value, -128 sum q,
 // and O, for 8-row units of bf16 queries, through a second product of a constant -128
 // matrix with the same weights, so the two parts cancel within a strip; elsewhere codes of
-// V are made as 1024 + 128 + c and an fp16 subtraction, which is exact and costs the
-// arithmetic pipe instead.  Scales never meet the codes: kd multiplies the score, vd the
-// weight.
+// V, and with fp32 queries of K too (the sums that cancel are thrice as large, and the
+// result was 1.1e-6 off instead of 5e-7), are made as 1024 + 128 + c and an fp16
+// subtraction, which is exact and costs the arithmetic pipe instead (29.1 us for 28.7 of
+// 16 sequences of 37 to 16000 tokens).  Scales never meet the codes: kd multiplies the
+// score, vd the weight.
+//
+// One token of one sequence of 130k (40 heads on 8, D 128) takes 52.0 us, 5.1 TB/s of codes
+// and scales: about 10 us are fixed (launch, the list, first copies, the join of a unit's
+// parts), and the strips' instructions fill the issue slots at 60 % of the copy rate.  16
+// sequences of 37 to 16000 tokens, fp32: 29.1 us, 3.4 TB/s (twice the products).
 #include <atomic>
 
 #include "kv_attention.cuh"
@@ -111,6 +118,7 @@ struct Shape {
   static constexpr int kRows = 8 * kNT;
   static constexpr bool kPair = Row<T>::kPair;
   static constexpr bool kRaisedV = !kPair && kNT == 1;
+  static constexpr bool kRaisedK = !kPair;
   static constexpr int kCtas = kD <= 128 && kNT * kD <= 256 ? 2 : 1;  // a SM
   static constexpr int kStage = 2 * kStrip * kD + 8 * kStrip;  // K, V, 16 kd, 16 vd
   static constexpr int kStages = kD == 64 ? 5 : (kCtas == 2 ? 3 : (kD == 128 ? 6 : 3));
@@ -302,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
       e = e < -100 ? -100 : e;
       const float up = __int_as_float((13 - e + 127) << 23);  // 2^(13 - e), e in [-100, 128]
       if (lane == 0) {  // the codes' 2^-24 goes back in here
-        row_scale[r] = amax > 0.0f ? a.scale * (0x1p24f * 1.44269504088896341f) *
+        row_scale[r] = amax > 0.0f ? a.scale * ((Sh::kRaisedK ? 0x1p24f : 1.0f) * 1.44269504088896341f) *
                                          __int_as_float((e - 13 + 127) << 23)
                                    : 0.0f;
         row_limit[r] = min(req.len, req.len - req.n + i + 1);
@@ -319,15 +327,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         const float s = v[j] * up;
         const __half hi = __float2half_rn(s);
         frag[idx] = hi;
-        sum_q += __half2float(hi);
-        if (kPair) {
-          const __half lo = __float2half_rn(s - __half2float(hi));
-          frag[idx + kSteps * kNT * 32 * 4] = lo;
-          sum_q += __half2float(lo);
-        }
+        if (Sh::kRaisedK) sum_q += __half2float(hi);
+        if (kPair) frag[idx + kSteps * kNT * 32 * 4] = __float2half_rn(s - __half2float(hi));
       }
+      if (Sh::kRaisedK) {
 #pragma unroll
-      for (int w2 = 16; w2 > 0; w2 >>= 1) sum_q += __shfl_xor_sync(kFullMask, sum_q, w2);
+        for (int w2 = 16; w2 > 0; w2 >>= 1) sum_q += __shfl_xor_sync(kFullMask, sum_q, w2);
+      }
       if (lane == 0) row_raise[r] = -128.0f * 0x1p-24f * sum_q;
     }
     __syncthreads();
@@ -392,8 +398,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int step = 4 * q + i;
-          const uint32_t a0 = even_raised(wa[i]), a1 = even_raised(wb[i]);
-          const uint32_t a2 = odd_raised(wa[i]), a3 = odd_raised(wb[i]);
+          const uint32_t a0 = Sh::kRaisedK ? even_raised(wa[i]) : even_bytes(wa[i]);
+          const uint32_t a1 = Sh::kRaisedK ? even_raised(wb[i]) : even_bytes(wb[i]);
+          const uint32_t a2 = Sh::kRaisedK ? odd_raised(wa[i]) : odd_bytes(wa[i]);
+          const uint32_t a3 = Sh::kRaisedK ? odd_raised(wb[i]) : odd_bytes(wb[i]);
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
             const uint2 f = q_frag[(step * kNT + n) * 32 + lane];
