@@ -13,7 +13,8 @@ namespace {
 // its own share of the chunk's table entries and rows: a thread finds the request of its
 // entry, or of its four rows, by bisection in shared memory.  Nothing passes between CTAs,
 // so one launch does for any size, and what bounds it is latency: launch, one read of the
-// lengths, two scans, one read of pages, one write.
+// lengths, two scans, one read of pages, one write.  4.4 us for 16 sequences of one token
+// (a kernel that does nothing: 2.2), 8.2 us for 512 prompts, 328,486 slots.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 
@@ -173,7 +174,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
 // ---------------------------------------------------------------------------
 // The write.  A warp takes one run of tokens (one scale block) of one head and plane: the
 // run's largest magnitude first, then the older tokens' codes if the scale grew, then the
-// run's own codes.  A lane holds 16 bytes of input at a time.
+// run's own codes.  A lane holds 16 bytes of input at a time, and a run of up to eight
+// such pieces a lane (16 tokens of 128 bf16) stays in registers between the two passes.  Latency bounds the small calls (one
+// token of 8 heads and its read-back: 3.9 us), instructions the large ones: 8191
+// bf16 tokens of 8 heads (34 MB in, 17 out) and their read-back take 20.3 us, 5.0 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
 
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 8) append_kernel(AppendArgs
 }
 
 // ---------------------------------------------------------------------------
-// The read-back: a thread takes 16 bytes of output.
+// The read-back: a lane takes 16 bytes of output at a time.  A stream: its bytes bound it.
 // ---------------------------------------------------------------------------
 struct ReadArgs {
   CacheArgs c;
