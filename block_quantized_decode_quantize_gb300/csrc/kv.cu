@@ -417,89 +417,72 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 
 constexpr int kReadWarps = 8;
 constexpr int kReadPieces = 4;  // 16-byte pieces of output a lane
-constexpr int kReadTokens = 4;  // tokens a warp, where there are many (with 2: 23.7 us for 20.3)
 
-// A warp takes 128 pieces of the K or V rows of kTokens tokens (all heads lie one after
-// another in the output); a slot is looked up and divided once for all of them, and the
-// tokens' codes are on their way together.
-template <typename T, int kTokens>
+// A warp takes 128 pieces of the K or V rows of one token (all heads lie one after another in
+// the output).  Several tokens to a warp are slower at every size (4 x 8000 tokens of 8
+// heads, with their write: 70.6 us, with two a warp 79.7, with four 89.8).
+template <typename T>
 __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(ReadArgs a, int head_bits) {
   constexpr int kN = Vec<T>::kN;
   pdl_launch_dependents();
   pdl_wait();
   // grid: x tokens, y K or V, z 128 pieces
-  const int64_t n0 = ((int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5)) * kTokens;
+  const int64_t n = (int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5);
+  if (n >= a.N) return;
   const bool is_v = blockIdx.y;
   const int lane = threadIdx.x & 31;
   const int total = a.c.Hkv << head_bits;  // pieces of a row, 2^head_bits of a head
   const int blocks = (int)a.c.by_block((uint32_t)a.c.page);
-  const int8_t* codes = is_v ? a.c.vq : a.c.kq;
-  const float* scales = is_v ? a.c.vd : a.c.kd;
-  int32_t slot[kTokens];
+  const int32_t slot = a.slots[n];
+  const bool have = slot >= 0 && slot < a.c.slots_in_pool;
+  if (slot >= a.c.slots_in_pool && a.status != nullptr && lane == 0) atomicOr(a.status, 1);
+  const uint32_t page = have ? a.c.by_page((uint32_t)slot) : 0;
+  const uint32_t off = have ? (uint32_t)slot - page * (uint32_t)a.c.page : 0;
+  const int64_t head0 = (int64_t)page * a.c.Hkv;
+  const int8_t* q0 = (is_v ? a.c.vq : a.c.kq) + (head0 * a.c.page + off) * a.c.D;
+  const float* d0 = (is_v ? a.c.vd : a.c.kd) + head0 * blocks + a.c.by_block(off);
+  float d[kReadPieces];
+  uint2 w[kReadPieces];
 #pragma unroll
-  for (int k = 0; k < kTokens; ++k) slot[k] = n0 + k < a.N ? a.slots[n0 + k] : -1;
-  float d[kTokens][kReadPieces];
-  uint2 w[kTokens][kReadPieces];
-#pragma unroll
-  for (int k = 0; k < kTokens; ++k) {
-    const bool have = slot[k] >= 0 && slot[k] < a.c.slots_in_pool;
-    if (slot[k] >= a.c.slots_in_pool && a.status != nullptr && lane == 0) atomicOr(a.status, 1);
-    const uint32_t page = have ? a.c.by_page((uint32_t)slot[k]) : 0;
-    const uint32_t off = have ? (uint32_t)slot[k] - page * (uint32_t)a.c.page : 0;
-    const int64_t head0 = (int64_t)page * a.c.Hkv;
-    const int8_t* q0 = codes + (head0 * a.c.page + off) * a.c.D;
-    const float* d0 = scales + head0 * blocks + a.c.by_block(off);
-#pragma unroll
-    for (int i = 0; i < kReadPieces; ++i) {
-      const int piece = (int)blockIdx.z * (32 * kReadPieces) + i * 32 + lane;
-      d[k][i] = 0.0f;
-      w[k][i] = make_uint2(0, 0);
-      if (have && piece < total) {
-        const int h = piece >> head_bits, e = (piece & ((1 << head_bits) - 1)) * kN;
-        const int8_t* q = q0 + (int64_t)h * a.c.page * a.c.D + e;
-        d[k][i] = d0[h * blocks];
-        if (kN == 8) w[k][i] = *reinterpret_cast<const uint2*>(q);
-        else w[k][i].x = *reinterpret_cast<const uint32_t*>(q);
-      }
+  for (int i = 0; i < kReadPieces; ++i) {
+    const int piece = (int)blockIdx.z * (32 * kReadPieces) + i * 32 + lane;
+    d[i] = 0.0f;
+    w[i] = make_uint2(0, 0);
+    if (have && piece < total) {
+      const int h = piece >> head_bits, e = (piece & ((1 << head_bits) - 1)) * kN;
+      const int8_t* q = q0 + (int64_t)h * a.c.page * a.c.D + e;
+      d[i] = d0[h * blocks];
+      if (kN == 8) w[i] = *reinterpret_cast<const uint2*>(q);
+      else w[i].x = *reinterpret_cast<const uint32_t*>(q);
     }
   }
   T* out = static_cast<T*>(is_v ? a.v : a.k);
 #pragma unroll
-  for (int k = 0; k < kTokens; ++k) {
-    if (n0 + k >= a.N) break;
+  for (int i = 0; i < kReadPieces; ++i) {
+    const int piece = (int)blockIdx.z * (32 * kReadPieces) + i * 32 + lane;
+    if (piece >= total) continue;
+    // a code q as the float 2^23 + 128 + q (its byte under that exponent), less 2^23 + 128
+    const uint32_t raised[2] = {w[i].x ^ 0x80808080u, w[i].y ^ 0x80808080u};
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < kReadPieces; ++i) {
-      const int piece = (int)blockIdx.z * (32 * kReadPieces) + i * 32 + lane;
-      if (piece >= total) continue;
-      // a code q as the float 2^23 + 128 + q (its byte under that exponent), less 2^23 + 128
-      const uint32_t raised[2] = {w[k][i].x ^ 0x80808080u, w[k][i].y ^ 0x80808080u};
-      float v[8];
-#pragma unroll
-      for (int x = 0; x < kN; ++x)
-        v[x] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(raised[x / 4], 0x4b000000u, 0x7440 | (x % 4))),
-                                   8388736.0f), d[k][i]);
-      uint4 o;
-      if (kN == 4)
-        o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                       __float_as_uint(v[3]));
-      else
-        o = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
-                       bf16_pair(v[6], v[7]));
-      *reinterpret_cast<uint4*>(out + ((n0 + k) * total + piece) * kN) = o;
-    }
+    for (int x = 0; x < kN; ++x)
+      v[x] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(raised[x / 4], 0x4b000000u, 0x7440 | (x % 4))),
+                                 8388736.0f), d[i]);
+    uint4 o;
+    if (kN == 4)
+      o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                     __float_as_uint(v[3]));
+    else
+      o = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
+                     bf16_pair(v[6], v[7]));
+    *reinterpret_cast<uint4*>(out + (n * total + piece) * kN) = o;
   }
 }
 
 template <typename T>
-cudaError_t launch_read(const ReadArgs& a, int head_bits, unsigned groups, const DeviceInfo& info,
-                        cudaStream_t stream) {
-  // Several tokens a warp where that leaves 32 warps to an SM.
-  const int tokens = 2 * a.N * groups >= (int64_t)info.sms * 32 * kReadTokens ? kReadTokens : 1;
-  const dim3 grid((unsigned)((a.N + kReadWarps * tokens - 1) / (kReadWarps * tokens)), 2, groups);
-  const dim3 block(kReadWarps * 32);
-  if (tokens > 1)
-    return launch_kernel(read_kernel<T, kReadTokens>, grid, block, 0, stream, a, head_bits);
-  return launch_kernel(read_kernel<T, 1>, grid, block, 0, stream, a, head_bits);
+cudaError_t launch_read(const ReadArgs& a, int head_bits, unsigned groups, cudaStream_t stream) {
+  const dim3 grid((unsigned)((a.N + kReadWarps - 1) / kReadWarps), 2, groups);
+  return launch_kernel(read_kernel<T>, grid, dim3(kReadWarps * 32), 0, stream, a, head_bits);
 }
 
 template <typename T>
@@ -654,8 +637,6 @@ extern "C" memra_status memra_kv_read_q8(const int32_t* slots, int64_t N, const 
   if (!slots || !k || !v) return MEMRA_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) || !aligned(dev_status, 4))
     return MEMRA_ERR_ALIGNMENT;
-  DeviceInfo info;
-  if (!device_info(&info)) return MEMRA_ERR_CUDA;
   a.slots = slots;
   a.N = N;
   a.k = k;
@@ -667,8 +648,8 @@ extern "C" memra_status memra_kv_read_q8(const int32_t* slots, int64_t N, const 
   const int64_t groups = (pieces + 32 * kReadPieces - 1) / (32 * kReadPieces);
   if (groups > 65535) return MEMRA_ERR_UNSUPPORTED;
   const cudaError_t e = dtype == MEMRA_BF16
-                            ? launch_read<uint16_t>(a, head_bits, (unsigned)groups, info, stream)
-                            : launch_read<float>(a, head_bits, (unsigned)groups, info, stream);
+                            ? launch_read<uint16_t>(a, head_bits, (unsigned)groups, stream)
+                            : launch_read<float>(a, head_bits, (unsigned)groups, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }
