@@ -447,14 +447,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
       }
 
       // The references move only when a score (a scale) passes them by more than the slack.
-      bool move = fmaxf(vda, vdb) > kRefSlack * ref;
+      const float v_top = fmaxf(fabsf(vda), fabsf(vdb));
+      bool move = v_top > kRefSlack * ref;
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         move |= fmaxf(c[n][0], c[n][2]) > bar[n][0];
         move |= fmaxf(c[n][1], c[n][3]) > bar[n][1];
       }
       if (__any_sync(kFullMask, move)) {
-        const float top = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(fmaxf(vda, vdb))));
+        const float top = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(v_top)));
         const float new_ref = fmaxf(ref, top);
         const float rescale = new_ref > 0.0f ? ref / new_ref : 1.0f;
         ref = new_ref;

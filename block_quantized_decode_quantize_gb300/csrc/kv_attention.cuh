@@ -170,9 +170,11 @@ __device__ __forceinline__ bool locate(const AttnArgs& a, Walk* walk, int* ctas,
   auto entries = [&](const Request& r) { return entries_of<kCost>(a, r); };
   int64_t w = 0, sum = 0;
   Request r{};
-  int64_t no_row = a.B > 0 ? a.cu_q[a.B] : 0;  // first row that no request owns
-  auto rest = [&]() {
+  int64_t no_row = a.B > 0 ? a.cu_q[a.B] : 0;
+  // Rows that no request owns: below the first one's, and from the last one's end on.
+  auto rest = [&](int64_t owned) {
     *ctas = (int)min((int64_t)gridDim.x, *total);
+    for (int64_t i = cta; i < owned && i < a.T; i += gridDim.x) write_nothing<T, kD>(a, i, i + 1, tid, kThreads);
     for (no_row += cta; no_row < a.T; no_row += gridDim.x)
       write_nothing<T, kD>(a, no_row, no_row + 1, tid, kThreads);
   };
@@ -194,7 +196,7 @@ __device__ __forceinline__ bool locate(const AttnArgs& a, Walk* walk, int* ctas,
       const int e = __ffs(todo) - 1;
       if (e % gridDim.x == cta) write_nothing<T, kD>(a, a.cu_q[e], a.cu_q[e + 1], tid, kThreads);
     }
-    rest();
+    rest(__shfl_sync(kFullMask, r.row, 0));
     if (cta >= *ctas) return false;
     const Cut cut(*total, *ctas);
     const int64_t first = cut.begin(cta);
@@ -246,7 +248,7 @@ __device__ __forceinline__ bool locate(const AttnArgs& a, Walk* walk, int* ctas,
     }
     if (pass == 0) {
       *total = before;
-      rest();
+      rest(a.cu_q[0]);
       if (cta >= *ctas) return false;
       first = Cut(*total, *ctas).begin(cta);
     }

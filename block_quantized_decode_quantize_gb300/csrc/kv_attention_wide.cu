@@ -25,7 +25,7 @@
 // joined at the end.  Scales never meet the codes: kd multiplies a score, vd a weight.
 //
 // A verify step of 16 sequences (8 tokens each, contexts of 500 to 8000, 32 heads on 4, D 128)
-// takes 44.9 us; bytes and operations alone need 7.1.  A CTA has some ten tiles.  About half
+// takes 45.5 us; bytes and operations alone need 7.1.  A CTA has some ten tiles.  About half
 // of the time is a unit's two ends (list, queries, first tile: 8 us; last products, parts,
 // arrival, join: 10), the rest the tiles, 3000 cycles each: the operands' way through shared
 // memory (codes in and out, fp16 in, read by the products: some 2000 cycles of it) and the
@@ -413,7 +413,7 @@ __device__ __forceinline__ void feed(const AttnArgs& a, Way<kRows>* way, uint8_t
     if (has_scale) {
       scales[(scale_v ? kTurns + turn : turn) * kTile + scale_key] = scale;
       if (scale_v) {
-        const uint32_t most = __reduce_max_sync(kFullMask, __float_as_uint(scale));
+        const uint32_t most = __reduce_max_sync(kFullMask, __float_as_uint(fabsf(scale)));
         if (lane == 0) v_most[turn * 4 + (warp & 3)] = __uint_as_float(most);
       } else if ((lane & 15) == 0) {
         hidden[turn * 8 + scale_key / kStrip] = gone ? 1 : 0;

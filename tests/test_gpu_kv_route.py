@@ -377,7 +377,7 @@ def attention_case(rs, lens, new, Hq, Hkv, D, P, S, dtype, peak=1.5):
 
 
 def check_attention(mem, q, kq, kd, vq, vd, table, lens, cu, scale=None, window=0, status=0, workspace=None,
-                    rows=None, wide_scales=False):
+                    rows=None, wide_scales=False, code_unit=False):
     D = q.shape[2]
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     i32 = torch.int32
@@ -405,6 +405,11 @@ def check_attention(mem, q, kq, kd, vq, vd, table, lens, cu, scale=None, window=
             live = live[(live >= 0) & (live < len(vd))]
             most = np.nanmax(np.where(np.isfinite(vd[live]), vd[live], 0), axis=(0, 2)) if len(live) else np.zeros(vd.shape[1])
             floor[int(cu[b]):int(cu[b + 1])] = (2.0 ** -33 * 127 * lens[b] * np.repeat(most, q.shape[1] // len(most)))[None, :]
+    if code_unit:
+        # Codes enter the sum over v as c + 128, and 128 leaves it 16 keys at a time: two fp32 sums
+        # (2^-23 each, cut off) of up to 128 of each weight times its scale, 2^-15 of theirs in all.
+        ones = ref_attention(q.double().cpu().numpy(), kq, kd, np.ones_like(vq), np.abs(vd), table, lens, cu, sc, window)[0]
+        floor = floor + 2.0 ** -15 * ones[..., 0]
     assert (np.abs(got - want) <= e[..., None] * size + floor[..., None] + 1e-7).all()
     fine = ~none
     assert (np.abs(glse - np.where(fine, wlse, 0))[fine] <= (ds + 2e-6 + 4e-7 * np.abs(np.where(fine, wlse, 0)))[fine]).all()
@@ -514,6 +519,23 @@ def test_attention_wide_gives_up_and_recovers(mem):
     again = mem.memra_kv_attention_q8(*t, scale=0.1, workspace=ws, dev_status=st)
     assert int(st) == 0
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+@pytest.mark.parametrize("n,dtype", [(1, "bf16"), (1, "fp32"), (40, "bf16")])
+def test_attention_negative_scales(mem, n, dtype):
+    """A cache from elsewhere may have scales of either sign, or none above zero."""
+    c = list(attention_case(np.random.RandomState(97), [300, 170], [n, n], 32, 4, 64, 32, 8, dtype))
+    for change in (lambda d: -d, lambda d: np.where(np.arange(d.shape[2]) % 2, d, -d).astype(np.float32)):
+        check_attention(mem, c[0], c[1], change(c[2]), c[3], change(c[4]), *c[5:], code_unit=dtype == "bf16")
+
+
+@pytest.mark.parametrize("n", [2, 60])
+def test_attention_rows_before_the_first_request(mem, n):
+    c = attention_case(np.random.RandomState(98), [300, 170], [n, n], 32, 4, 64, 32, 8, "bf16")
+    q = torch.cat([c[0][:5], c[0], c[0][:3]] if n > 2 else [c[0], c[0][:1], c[0], c[0][:3]])
+    out, lse = check_attention(mem, q, *c[1:7], c[7] + 5, scale=0.1, code_unit=True)
+    for part in (slice(0, 5), slice(2 * n + 5, None)):
+        assert bool((out[part] == 0).all()) and bool(torch.isneginf(lse[part]).all())
 
 
 def test_attention_many_requests(mem):
