@@ -34,8 +34,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 static_assert(kWarps * kStrip == kTile, "a CTA's step is an entry of the list");
-constexpr int kUnitCost = 3;   // entries of the list for a unit's fixed time (1: 37 us, 3: 34, 6: 35
-                               // for 16 sequences of 37 to 16000 tokens)
+constexpr int kUnitCost = 3;   // entries of the list for a unit's fixed time (1: 34.4 us, 3: 29.1, 6:
+                               // 30.8 for 16 sequences of 37 to 16000 tokens, fp32)
 // Above this many rows to a unit, and with at least so many in all (rows times heads), the
 // tcgen05 kernel takes bf16 queries: below, its larger parts and ends of units cost more than
 // its products save.  8 cached heads, us here / there: 32 rows, 16 requests of 500 to 8000
@@ -43,7 +43,8 @@ constexpr int kUnitCost = 3;   // entries of the list for a unit's fixed time (1
 // 2 (1024) 32.1 / 31.5, one of 8000 (512) 30.2 / 31.7; 128 rows, one of 16000 (1024) 64 / 60;
 // 256 rows, one of 8000 (2048) 61 / 49; 64 rows, 32 requests of 100 to 500 56 / 41.
 constexpr int kWideRows = 32, kWideAll = 1024;
-constexpr int kMaxParts = 64;  // CTAs to a unit, on average
+constexpr int kMaxParts = 64;  // CTAs to a unit, on average (32: 57.5 us, 64 and 128: 52.2 for one
+                               // sequence of 130k)
 
 __device__ __forceinline__ void mma_16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {

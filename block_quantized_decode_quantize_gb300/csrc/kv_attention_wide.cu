@@ -25,7 +25,7 @@
 // joined at the end.  Scales never meet the codes: kd multiplies a score, vd a weight.
 //
 // A verify step of 16 sequences (8 tokens each, contexts of 500 to 8000, 32 heads on 4, D 128)
-// takes 45.5 us; bytes and operations alone need 7.1.  A CTA has some ten tiles.  About half
+// takes 43.6 us; bytes and operations alone need 7.1.  A CTA has some ten tiles.  About half
 // of the time is a unit's two ends (list, queries, first tile: 8 us; last products, parts,
 // arrival, join: 10), the rest the tiles, 3000 cycles each: the operands' way through shared
 // memory (codes in and out, fp16 in, read by the products: some 2000 cycles of it) and the
@@ -44,7 +44,8 @@ constexpr int kSoftThreads = kSoftWarps * 32, kFeedThreads = kFeedWarps * 32;
 constexpr int kThreads = kSoftThreads + kFeedThreads + 32;
 // Keeps 2^8 / ref times a row's sum in range; blocks of smaller scales are next to nothing.
 constexpr float kLeastRef = 1e-25f;
-constexpr int kCost = 3;  // entries of the list for a unit's fixed time
+constexpr int kCost = 5;  // entries of the list for a unit's fixed time (3: 45.9 us, 4: 45.8, 5: 43.6, 6:
+                          // 44.1 for the verify step above; 32 requests of 100 to 500: 41.7, 36.5, 36.1, 35.5)
 
 // Tensor memory columns: scores of two or three tiles and each group's weights (two fp16 a
 // column), then each group's accumulators.
