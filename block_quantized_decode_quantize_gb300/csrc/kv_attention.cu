@@ -39,9 +39,10 @@ constexpr int kUnitCost = 3;   // entries of the list for a unit's fixed time (1
 // Above this many rows to a unit, and with at least so many in all (rows times heads), the
 // tcgen05 kernel takes bf16 queries: below, its larger parts and ends of units cost more than
 // its products save.  8 cached heads, us here / there: 32 rows, 16 requests of 500 to 8000
-// tokens 64 / 69; 48 rows 104 / 71; 64 rows, 8 requests (4096 in all) 64 / 46, 4 (2048) 41 / 37,
-// 2 (1024) 32.1 / 31.5, one of 8000 (512) 30.2 / 31.7; 128 rows, one of 16000 (1024) 64 / 60;
-// 256 rows, one of 8000 (2048) 61 / 49; 64 rows, 32 requests of 100 to 500 56 / 41.
+// tokens 64 / 68, 64 of 500 to 3000 124 / 139; 48 rows, 16 requests 104 / 70; 64 rows, 8
+// requests (4096 in all) 64 / 44, 4 (2048) 41 / 35, 2 (1024) 32 / 31, one of 8000 (512) 30 / 32;
+// 128 rows, one of 16000 (1024) 64 / 56; 256 rows, one of 8000 (2048) 61 / 45; 64 rows, 32
+// requests of 100 to 500 56 / 36.
 constexpr int kWideRows = 32, kWideAll = 1024;
 constexpr int kMaxParts = 64;  // CTAs to a unit, on average (32: 57.5 us, 64 and 128: 52.2 for one
                                // sequence of 130k)
