@@ -273,7 +273,8 @@ __device__ __forceinline__ bool next_unit(const AttnArgs& a, Way<kRows>* way) {
   __syncwarp();
   bool more = false;
   if ((threadIdx.x & 31) == 0) more = way->walker.next(a, &way->seg);
-  return __shfl_sync(kFullMask, (int)more, 0) != 0;  // and what lane 0 wrote is there
+  __syncwarp();  // orders lane 0's writes before the other lanes' reads (an exchange does not)
+  return __shfl_sync(kFullMask, (int)more, 0) != 0;
 }
 
 // A whole warp's bounded wait, with one answer for all its lanes.
