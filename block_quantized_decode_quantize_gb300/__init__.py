@@ -947,7 +947,8 @@ def memra_kv_plan(ctx_lens, new_lens, page_size, free_pages, block_table, num_to
     of this step), free_pages int32 [F], block_table int32 [B, max_pages] (its new entries
     are written in place), free_head int32 [1] or None (start of the unused free pages).
     Returns kv_lens [B], cu_q [B+1], slots [num_tokens], positions [num_tokens] and
-    free_head_out [1], all int32.  free_head_out may be free_head, to advance it in place."""
+    free_head_out [1], all int32.  free_head_out may be free_head, and kv_lens ctx_lens or
+    new_lens, to advance them in place."""
     if kv_lens is None and cu_q is None and slots is None and positions is None:
         done = (_fast or _binding()).plan(ctx_lens, new_lens, page_size, free_pages, block_table,
                                           num_tokens, free_head, free_head_out, dev_status)

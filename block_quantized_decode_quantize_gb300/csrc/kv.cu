@@ -59,9 +59,10 @@ __device__ __forceinline__ int last_at_most(const int64_t* a, int n, int64_t x) 
   return lo;
 }
 
-// kHeadOnly: *free_head_out alone, for a plan that advances its own free_head (no CTA of
-// the plan itself may write what another still reads).
-template <bool kHeadOnly>
+// kLater: *free_head_out and kv_lens alone, where they are the plan's own inputs and it has
+// several CTAs (none of which may write what another still reads).  One CTA: a thread
+// reads a request's lengths before it writes its new one.
+template <bool kLater>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   __shared__ int64_t sum_a[32], sum_b[32];
   __shared__ int64_t first_row[kPlanThreads], first_page[kPlanThreads];
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   if (head < 0) head = 0;
   int64_t row0 = 0, last_end = head;
   int bits = 0;
-  if (!kHeadOnly && cta == 0 && tid == 0) a.cu_q[0] = 0;
+  if (!kLater && cta == 0 && tid == 0) a.cu_q[0] = 0;
   const bool wide = (((uintptr_t)a.slots | (uintptr_t)a.positions) & 15) == 0;
   for (int64_t base = 0; base < a.B; base += threads) {
     const int64_t b = base + tid;
@@ -96,17 +97,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     if (ok && need > 0) last_end = end;  // those that take pages come before those refused them
     if (mine && !fits) bits |= 1;
     if (fits && !ok) bits |= 4;
-    if (!kHeadOnly) {
+    if (mine && cta == 0 && a.kv_lens != nullptr) a.kv_lens[b] = ok ? (int32_t)(ctx + add) : 0;
+    if (!kLater) {
       first_row[tid] = min(upto - add, a.T);
       first_page[tid] = end - need;
       have_of[tid] = have;
       ctx_of[tid] = (int32_t)ctx;
       const uint32_t no = __ballot_sync(kFullMask, !ok);
       if ((tid & 31) == 0) refused[tid >> 5] = no;
-      if (mine && cta == 0) {
-        a.kv_lens[b] = ok ? (int32_t)(ctx + add) : 0;
-        a.cu_q[b + 1] = (int32_t)min(upto, a.T);
-      }
+      if (mine && cta == 0) a.cu_q[b + 1] = (int32_t)min(upto, a.T);
       __syncthreads();
       // new table entries: pages head .. of the chunk that the free list holds
       const int64_t last = min(head + pages, a.n_free);
@@ -153,12 +152,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     row0 += rows;
     __syncthreads();
   }
-  if (!kHeadOnly)
+  if (!kLater)
     for (int64_t t = min(row0, a.T) + (int64_t)cta * threads + tid; t < a.T; t += (int64_t)ctas * threads) {
       a.slots[t] = -1;
       a.positions[t] = -1;
     }
-  if (cta == 0 && (kHeadOnly || a.free_head_out != nullptr)) {
+  if (cta == 0 && a.free_head_out != nullptr) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) last_end = max(last_end, (int64_t)__shfl_xor_sync(kFullMask, last_end, o));
     if ((tid & 31) == 0) sum_a[tid >> 5] = last_end;
@@ -168,7 +167,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
       *a.free_head_out = (int32_t)last_end;
     }
   }
-  if (!kHeadOnly && cta == 0 && bits != 0 && a.status != nullptr) atomicOr(a.status, bits);
+  if (!kLater && cta == 0 && bits != 0 && a.status != nullptr) atomicOr(a.status, bits);
 }
 
 // ---------------------------------------------------------------------------
@@ -518,6 +517,30 @@ extern "C" memra_status memra_kv_plan(const int32_t* ctx_lens, const int32_t* ne
                        slots, positions, free_head_out, dev_status};
   for (const void* p : all)
     if (!aligned(p, 4)) return MEMRA_ERR_ALIGNMENT;
+  // What is written lies apart from all else, but for lengths and the free list's position
+  // that advance in place.
+  struct Span {
+    const int32_t* at;
+    int64_t words;
+    bool meets(const Span& o) const {
+      const uintptr_t a = (uintptr_t)at, b = (uintptr_t)o.at;
+      return words > 0 && o.words > 0 && a < b + 4 * (uint64_t)o.words && b < a + 4 * (uint64_t)words;
+    }
+  };
+  const int64_t row = max_pages < INT32_MAX ? max_pages : INT32_MAX;
+  const Span in[] = {{ctx_lens, B}, {new_lens, B}, {free_head, free_head != nullptr}, {free_pages, n_free}};
+  const Span out[] = {{kv_lens, B}, {free_head_out, 1}, {cu_q, B + 1}, {slots, T}, {positions, T},
+                      {block_table, B * row}, {dev_status, dev_status != nullptr}};
+  const bool lens_in_place = B > 0 && (kv_lens == ctx_lens || kv_lens == new_lens);
+  const bool head_in_place = free_head == free_head_out;
+  for (int i = 0; i < 7; ++i) {
+    for (int j = 0; j < 4; ++j) {
+      const bool in_place = out[i].at == in[j].at && ((i == 0 && j < 2) || (i == 1 && j == 2));
+      if (!in_place && out[i].meets(in[j])) return MEMRA_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < i; ++j)
+      if (out[i].meets(out[j])) return MEMRA_ERR_INVALID_ARG;
+  }
   PlanArgs a;
   a.ctx = ctx_lens;
   a.add = new_lens;
@@ -542,12 +565,14 @@ extern "C" memra_status memra_kv_plan(const int32_t* ctx_lens, const int32_t* ne
   const bool small = B <= 256 && T <= 1024;
   int64_t ctas = (T + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
   ctas = ctas < 1 ? 1 : (ctas > info.sms ? info.sms : ctas);
-  const bool in_place = ctas > 1 && free_head == free_head_out;
-  if (in_place) a.free_head_out = nullptr;
+  const bool later = ctas > 1 && (lens_in_place || head_in_place);
+  if (later && lens_in_place) a.kv_lens = nullptr;
+  if (later && head_in_place) a.free_head_out = nullptr;
   cudaError_t e = launch_kernel(plan_kernel<false>, dim3((unsigned)ctas),
                                 dim3(small ? 256 : kPlanThreads), 0, stream, a);
-  if (e == cudaSuccess && in_place) {
-    a.free_head_out = free_head_out;
+  if (e == cudaSuccess && later) {
+    a.kv_lens = lens_in_place ? kv_lens : nullptr;
+    a.free_head_out = head_in_place ? free_head_out : nullptr;
     e = launch_kernel(plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, stream, a);
   }
   if (e != cudaSuccess) return cuda_fail(e);

@@ -523,7 +523,8 @@ memra_status memra_q8_0_moe_ffn_noalloc(const int8_t* gu_q, const uint16_t* gu_d
  *   T                   rows of slots and positions; the step's tokens fill the first ones,
  *                       request after request.
  * Out:
- *   kv_lens   int32 [B]    ctx + new (0 for a refused request);
+ *   kv_lens   int32 [B]    ctx + new (0 for a refused request); may be ctx_lens or new_lens
+ *                          itself;
  *   cu_q      int32 [B+1]  first row of each request, min(sum of new before it, T);
  *   slots     int32 [T]    slot of each row's token (-1: a refused request's, or no token);
  *   positions int32 [T]    its position in the sequence (-1: no token);
@@ -533,7 +534,8 @@ memra_status memra_q8_0_moe_ffn_noalloc(const int8_t* gu_q, const uint16_t* gu_d
  * negative, its pages do not fit max_pages or its rows do not fit T (status 1), and, when
  * it needs a page, if the pages of the requests up to it run past n_free (status 4): once
  * one does not fit, none after it takes a page.
- * B == 0 fills slots and positions with -1.
+ * B == 0 fills slots and positions with -1.  What is written must not overlap anything else
+ * but as said (MEMRA_ERR_INVALID_ARG).
  */
 memra_status memra_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t B,
                            int64_t page_size, const int32_t* free_pages, int64_t n_free,

@@ -38,3 +38,58 @@ def test_attention_wide_many_units_to_a_cta(mem, rows):
     for _ in range(5):
         o2, l2 = mem.memra_kv_attention_q8(c[0], *[dev(x) for x in c[1:5]], *[dev(x, i32) for x in c[5:]])
         assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
+# ---------------------------------------------------------------------------
+# The plan: lengths in place, arrays that overlap.
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("B,max_new", [(5, 40), (40, 900), (1500, 9), (700, 60)])
+@pytest.mark.parametrize("which", ["ctx", "new"])
+@pytest.mark.parametrize("head_too", [False, True])
+def test_plan_lengths_in_place(mem, B, max_new, which, head_too):
+    """kv_lens may be the lengths themselves, with one CTA and with several (above 4096 rows)."""
+    rs = np.random.RandomState(B + max_new)
+    P, ctx, new = 16, rs.randint(0, 60, B), rs.randint(0, max_new + 1, B)
+    have, after = -(-ctx // P), -(-(ctx + new) // P)
+    ids = rs.permutation(int(after.sum()) + 9)
+    table = np.full((B, int(after.max())), -1, np.int64)
+    at = 0
+    for b in range(B):
+        table[b, :have[b]] = ids[at:at + have[b]]
+        at += int(have[b])
+    free = ids[at:at + int(0.9 * (after - have).sum()) + 2]   # the last requests go without
+    T = int(new.sum()) + 3
+    want = ref_plan(ctx, new, P, free, table, T, 1)
+    c, n, t, h = dev(ctx, i32), dev(new, i32), dev(table, i32), dev([1], i32)
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    kv, cu, slots, pos, head = mem.memra_kv_plan(c, n, P, dev(free, i32), t, T, free_head=h, kv_lens=c if which == "ctx" else n,
+                                                 free_head_out=h if head_too else None, dev_status=st)
+    assert kv.data_ptr() == (c if which == "ctx" else n).data_ptr()
+    for got, ref in ((kv, want[0]), (cu, want[1]), (slots, want[2]), (pos, want[3]), (t, want[4])):
+        assert np.array_equal(got.cpu().numpy(), ref)
+    assert int(head) == want[5] and int(st) == want[6] and int(h) == (want[5] if head_too else 1)
+
+
+def test_plan_refuses_overlaps(mem):
+    """Anything written that overlaps something else by a part, or by all where that is not
+    allowed, is refused before a launch."""
+    def call(**at):
+        buf = torch.zeros(64, dtype=i32, device="cuda")
+        v = dict(ctx_lens=buf[:3], new_lens=buf[4:7], free_pages=buf[8:16], block_table=buf[16:22].view(3, 2), free_head=buf[24:25],
+                 kv_lens=buf[28:31], cu_q=buf[32:36], slots=buf[36:42], positions=buf[42:48], free_head_out=buf[50:51],
+                 dev_status=buf[52:53])
+        for name, i in at.items():
+            v[name] = buf[i:i + v[name].numel()].view(v[name].shape)
+        return mem.memra_kv_plan(v.pop("ctx_lens"), v.pop("new_lens"), 16, v.pop("free_pages"), v.pop("block_table"), 6, **v)
+
+    call()
+    call(kv_lens=0)
+    call(kv_lens=4)
+    call(free_head_out=24)
+    for at in (dict(kv_lens=1), dict(kv_lens=2), dict(kv_lens=5), dict(kv_lens=14), dict(cu_q=28), dict(cu_q=0), dict(slots=42),
+               dict(slots=3), dict(positions=20), dict(free_head_out=28), dict(free_head_out=2), dict(dev_status=24),
+               dict(dev_status=50), dict(block_table=14), dict(block_table=20, free_head=25)):
+        with pytest.raises(mem.MemraError) as e:
+            call(**at)
+        assert e.value.status == 1, at
