@@ -22,6 +22,7 @@ struct PlanArgs {
   const int32_t *ctx, *add;
   int64_t B, n_free, max_pages, T;
   int page;
+  uint32_t pages_named;  // pages whose every slot is an int32
   const int32_t *free_pages, *free_head;
   int32_t *table, *kv_lens, *cu_q, *slots, *positions, *free_head_out, *status;
 };
@@ -76,6 +77,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   if (head < 0) head = 0;
   int64_t row0 = 0, last_end = head;
   int bits = 0;
+  bool no_page = false;
   if (!kLater && cta == 0 && tid == 0) a.cu_q[0] = 0;
   const bool wide = (((uintptr_t)a.slots | (uintptr_t)a.positions) & 15) == 0;
   for (int64_t base = 0; base < a.B; base += threads) {
@@ -131,9 +133,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
           pos[i] = (int32_t)at;
           if ((refused[r >> 5] >> (r & 31)) & 1u) continue;
           const int p = (int)(at / (uint32_t)a.page);
-          const int64_t page = p < have_of[r] ? a.table[(base + r) * a.max_pages + p]
+          const uint32_t page = p < have_of[r] ? a.table[(base + r) * a.max_pages + p]
                                               : a.free_pages[first_page[r] + (p - have_of[r])];
-          slot[i] = (int32_t)(page * a.page + (at - (uint32_t)p * (uint32_t)a.page));
+          const bool named = page < a.pages_named;
+          no_page |= !named;
+          slot[i] = named ? (int32_t)(page * (uint32_t)a.page + (at - (uint32_t)p * (uint32_t)a.page)) : -1;
         }
         if (wide && hi - lo == 4) {
           *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
@@ -167,7 +171,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
       *a.free_head_out = (int32_t)last_end;
     }
   }
-  if (!kLater && cta == 0 && bits != 0 && a.status != nullptr) atomicOr(a.status, bits);
+  if (cta != 0) bits = 0;
+  if (no_page) bits |= 1;
+  if (!kLater && bits != 0 && a.status != nullptr) atomicOr(a.status, bits);
 }
 
 // ---------------------------------------------------------------------------
@@ -549,6 +555,7 @@ extern "C" memra_status memra_kv_plan(const int32_t* ctx_lens, const int32_t* ne
   a.max_pages = max_pages;
   a.T = T;
   a.page = (int)page_size;
+  a.pages_named = (uint32_t)(INT32_MAX / page_size);
   a.free_pages = free_pages;
   a.free_head = free_head;
   a.table = block_table;

@@ -526,14 +526,16 @@ memra_status memra_q8_0_moe_ffn_noalloc(const int8_t* gu_q, const uint16_t* gu_d
  *   kv_lens   int32 [B]    ctx + new (0 for a refused request); may be ctx_lens or new_lens
  *                          itself;
  *   cu_q      int32 [B+1]  first row of each request, min(sum of new before it, T);
- *   slots     int32 [T]    slot of each row's token (-1: a refused request's, or no token);
+ *   slots     int32 [T]    slot of each row's token (-1: a refused request's, or no token, or
+ *                          no page's);
  *   positions int32 [T]    its position in the sequence (-1: no token);
  *   free_head_out int32 [1]  *free_head + pages taken; may be free_head itself.
  * With need_b = ceil((ctx+new)/P) - ceil(ctx/P), request b takes the pages after those of
  * all requests before it.  A request is refused, and takes no page, when a length is
  * negative, its pages do not fit max_pages or its rows do not fit T (status 1), and, when
  * it needs a page, if the pages of the requests up to it run past n_free (status 4): once
- * one does not fit, none after it takes a page.
+ * one does not fit, none after it takes a page.  A page number (of the free list or the
+ * table) below 0, or from (2^31 - 1) / P on, gives the tokens in it slot -1 (status 1).
  * B == 0 fills slots and positions with -1.  What is written must not overlap anything else
  * but as said (MEMRA_ERR_INVALID_ARG).
  */

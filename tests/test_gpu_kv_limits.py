@@ -93,3 +93,25 @@ def test_plan_refuses_overlaps(mem):
         with pytest.raises(mem.MemraError) as e:
             call(**at)
         assert e.value.status == 1, at
+
+
+def test_plan_page_numbers_out_of_range(mem):
+    """A page number that no slot can name gives no slot: not a valid one of another page, as its
+    low 32 bits would."""
+    P = 16
+    ctx, new = np.array([5, 0, 3, 0]), np.array([20, 33, 2, 16])
+    table = np.full((4, 4), -1)
+    table[0, 0], table[2, 0] = 7, -4                    # the third request's own page is none
+    free = np.array([2 ** 28, 3, 2 ** 27, -1, 2 ** 27 - 2])
+    t, st = dev(table, i32), torch.zeros(1, dtype=i32, device="cuda")
+    kv, cu, slots, pos, head = mem.memra_kv_plan(dev(ctx, i32), dev(new, i32), P, dev(free, i32), t, 75, dev_status=st)
+    want = ref_plan(ctx, new, P, free, table, 75)
+    page = np.full(75, -1)
+    for b in range(4):
+        for i in range(new[b]):
+            page[sum(new[:b]) + i] = want[4][b, (ctx[b] + i) // P]
+    named = (page >= 0) & (page < (2 ** 31 - 1) // P)
+    assert np.array_equal(slots.cpu().numpy(), np.where(named, page * P + want[3] % P, -1))
+    assert int(st) == 1 and int(head) == 5
+    for got, ref in ((kv, want[0]), (cu, want[1]), (pos, want[3]), (t, want[4])):
+        assert np.array_equal(got.cpu().numpy(), ref)
