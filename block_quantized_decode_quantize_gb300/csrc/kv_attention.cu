@@ -16,14 +16,19 @@
 // matrix with the same weights, so the two parts cancel within a strip; elsewhere codes of
 // V, and with fp32 queries of K too (the sums that cancel are thrice as large, and the
 // result was 1.1e-6 off instead of 5e-7), are made as 1024 + 128 + c and an fp16
-// subtraction, which is exact and costs the arithmetic pipe instead (29.1 us for 28.7 of
-// 16 sequences of 37 to 16000 tokens).  Scales never meet the codes: kd multiplies the
-// score, vd the weight.
+// subtraction, which is exact (1.4 % of the time of 16 sequences of 37 to 16000 tokens).
+// Scales never meet the codes: kd multiplies the score, vd the weight.
+//
+// The tensor cores cut their fp32 sums off, so a sum over V that stayed in them would lose
+// up to 2^-23 of itself with each product, always to the same side (7e-5 after the 1024
+// strips that a warp has of 131072 keys).  A strip's products therefore start from zero,
+// and its sums are added to the running ones in registers, rounded to nearest: no loss
+// for 8 bf16 rows (51.8 us for 52.0 at 130k), 31.2 us for 29.1 of the 16 fp32 sequences.
 //
 // One token of one sequence of 130k (40 heads on 8, D 128) takes 52.0 us, 5.1 TB/s of codes
 // and scales: about 10 us are fixed (launch, the list, first copies, the join of a unit's
 // parts), and the strips keep the arithmetic pipe 55 % busy beside memory's 60 %.  16
-// sequences of 37 to 16000 tokens, fp32: 29.1 us, 3.4 TB/s (twice the products).
+// sequences of 37 to 16000 tokens, fp32: 31.2 us, 3.2 TB/s (twice the products).
 #include <atomic>
 
 #include "kv_attention.cuh"
@@ -54,6 +59,21 @@ __device__ __forceinline__ void mma_16816(float c[4], uint32_t a0, uint32_t a1, 
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from zero: c is written only.
+__device__ __forceinline__ void mma_16816_zero(float c[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+__device__ __forceinline__ void add4(float c[4], const float a[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] += a[i];
 }
 
 // Codes 0 and 2 (1 and 3) of w plus 128, times 2^-24, as two fp16.
@@ -121,7 +141,10 @@ struct Shape {
   static constexpr bool kPair = Row<T>::kPair;
   static constexpr bool kRaisedV = !kPair && kNT == 1;
   static constexpr bool kRaisedK = !kPair;
-  static constexpr int kCtas = kD <= 128 && kNT * kD <= 256 ? 2 : 1;  // a SM
+  // CTAs of an SM: two where 128 registers hold the rows' sums, else one with 255 (16
+  // sequences of 500 to 8000 tokens, two CTAs / one: 16 bf16 rows of 128 32.8 / 26.4 us, fp32
+  // 37.7 / 28.4; 32 bf16 rows of 64 40.1 / 28.0; but 8 fp32 rows of 128 31.2 / 33.4).
+  static constexpr int kCtas = kNT * kD <= 128 ? 2 : 1;
   static constexpr int kStage = 2 * kStrip * kD + 8 * kStrip;  // K, V, 16 kd, 16 vd
   static constexpr int kStages = kD == 64 ? 5 : (kCtas == 2 ? 3 : (kD == 128 ? 6 : 3));
   static constexpr int kRing = kWarps * kStages * kStage;
@@ -528,16 +551,20 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
             const int tile = (q * kWords + w2) * 2 + half;
             if (Sh::kRaisedV) {
               constexpr uint32_t kLower = 0x80808080u;  // -128 * 2^-24, twice
-              mma_16816(o[tile][0], kLower, kLower, kLower, kLower, p0[0], p1[0]);
-              mma_16816(o[tile][0], even_raised(z0), odd_raised(z0), even_raised(z1), odd_raised(z1),
+              float strip[4];
+              mma_16816_zero(strip, kLower, kLower, kLower, kLower, p0[0], p1[0]);
+              mma_16816(strip, even_raised(z0), odd_raised(z0), even_raised(z1), odd_raised(z1),
                         p0[0], p1[0]);
+              add4(o[tile][0], strip);
             } else {
               const uint32_t a0 = even_bytes(z0), a1 = odd_bytes(z0);
               const uint32_t a2 = even_bytes(z1), a3 = odd_bytes(z1);
 #pragma unroll
               for (int n = 0; n < kNT; ++n) {
-                mma_16816(o[tile][n], a0, a1, a2, a3, p0[n], p1[n]);
-                if (kPair) mma_16816(o[tile][n], a0, a1, a2, a3, e0[n], e1[n]);
+                float strip[4];
+                mma_16816_zero(strip, a0, a1, a2, a3, p0[n], p1[n]);
+                if (kPair) mma_16816(strip, a0, a1, a2, a3, e0[n], e1[n]);
+                add4(o[tile][n], strip);
               }
             }
           }

@@ -40,6 +40,64 @@ def test_attention_wide_many_units_to_a_cta(mem, rows):
         assert torch.equal(o, o2) and torch.equal(l, l2)
 
 
+LONG = [
+    # dtype, G, n, D
+    ("bf16", 5, 1, 128), ("bf16", 8, 1, 64), ("bf16", 8, 1, 256), ("bf16", 8, 2, 128), ("bf16", 8, 4, 64),
+    ("fp32", 5, 1, 128), ("fp32", 8, 1, 64), ("fp32", 8, 1, 256), ("fp32", 8, 2, 128), ("fp32", 8, 4, 64),
+]
+
+
+def long_unit(mem, dtype, G, n, D, L, seed=0):
+    """B requests of L tokens whose tables name one page of 1024 tokens over and over, so that
+    the 64-bit result needs that page's keys alone; V of one sign.  Units are as many as the
+    GPU has CTAs, so a CTA takes most of one by itself. Returns out, what it should be, lse and what
+    that should be."""
+    B, Hkv, P = 40, 8, 1024
+    Hq = G * Hkv
+    g = torch.Generator(device="cuda").manual_seed(100 * D + 10 * G + n + seed)
+    kq = torch.randint(-127, 128, (1, Hkv, P, D), generator=g, device="cuda", dtype=torch.int8)
+    vq = torch.randint(64, 128, (1, Hkv, P, D), generator=g, device="cuda", dtype=torch.int8)
+    kd = 0.01 * (1 + torch.rand(1, Hkv, P // 16, generator=g, device="cuda"))
+    vd = 0.01 * (1 + torch.rand(1, Hkv, P // 16, generator=g, device="cuda"))
+    # scores of a few tenths: sum |q| |k| scale below 1/2, so that 2^-18 of it is 2^-19
+    q = (torch.rand(B * n, Hq, D, generator=g, device="cuda") - 0.5).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    scale = 2.0 / D
+    table = torch.zeros(B, L // P, dtype=i32, device="cuda")
+    lens = torch.full((B,), L, dtype=i32, device="cuda")
+    cu = torch.arange(B + 1, dtype=i32, device="cuda") * n
+    ws = torch.zeros(mem.KV_ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    out, lse = mem.memra_kv_attention_q8(q, kq, kd, vq, vd, table, lens, cu, scale=scale, workspace=ws)
+    k = kq[0].double() * kd[0].double().repeat_interleave(16, 1)[..., None]
+    v = vq[0].double() * vd[0].double().repeat_interleave(16, 1)[..., None]
+    x = torch.einsum("bihgd,hjd->bihgj", q.double().view(B, n, Hkv, G, D), k) * scale
+    seen = L - n + 1 + torch.arange(n, device="cuda")                    # keys that query i sees
+    j = torch.arange(P, device="cuda")
+    count = (seen // P)[:, None] + (j[None, :] < (seen % P)[:, None])    # how often each of the page's
+    p = torch.exp(x) * count[None, :, None, None, :]
+    l = p.sum(-1)
+    want = torch.einsum("bihgj,hjd->bihgd", p, v) / l[..., None]
+    return out.double(), want.reshape(B * n, Hq, D), lse.double(), torch.log(l).reshape(B * n, Hq)
+
+
+@pytest.mark.parametrize("dtype,G,n,D", LONG)
+def test_attention_sums_do_not_drift(mem, dtype, G, n, D):
+    """A sum over 131072 keys of V of one sign.  Scores are off by at most 2^-18 of their terms'
+    sum (below 1/2), weights by 2^-22 (fp32) or 2^-12 (bf16, and the output by 2^-9 more), all
+    to either side.  The running sums of a warp take 1024 steps, each rounded to nearest: a walk
+    of steps of at most 2^-24, 2^-23 / sqrt(12) * sqrt(1024 / 3) = 6.4e-7 after the last, and six
+    times that are 3.8e-6; the strip's own products, cut off, add 2 * 2^-23 at most.  So fp32
+    elements are within 2^-17.  A sum that cuts off at every step loses 2 * 1024 half steps on
+    average: 3e-5 and more.  In bf16 that hides below the rounding of the output; but the last
+    query sees the same page 128 times or once, so that the same number is rounded in both
+    cases, and the mean of the difference is that of the sums."""
+    out, want, lse, wlse = long_unit(mem, dtype, G, n, D, 131072)
+    err = (out - want) / want
+    assert float(err.abs().max()) < (2.0 ** -17 if dtype == "fp32" else 2.0 ** -8 + 2.0 ** -10)
+    assert float((lse - wlse).abs().max()) < 2.0 ** -17 + 4e-7 * float(wlse.abs().max())
+    once = long_unit(mem, dtype, G, n, D, 1024)[0]
+    assert abs(float(((out - once) / want)[n - 1::n].mean())) < 2.0 ** -17
+
+
 # ---------------------------------------------------------------------------
 # The plan: lengths in place, arrays that overlap.
 # ---------------------------------------------------------------------------
