@@ -47,6 +47,13 @@ constexpr float kLeastRef = 1e-25f;
 constexpr int kCost = 5;  // entries of the list for a unit's fixed time (3: 45.9 us, 4: 45.8, 5: 43.6, 6:
                           // 44.1 for the verify step above; 32 requests of 100 to 500: 41.7, 36.5, 36.1, 35.5)
 
+// Tiles after which a range's sums leave tensor memory: the tensor cores cut their fp32 sums
+// off at every product, to one side (of V of one sign 1.7e-4 over 131072 keys with units of 64
+// rows, 3.6e-4 with 128, and so on with the length).  With 512 tiles it is 1e-4 and 2.2e-4 at
+// any length.  An end and a new beginning cost about 22 us (512 queries on 130k keys: 1629 us
+// without, 1666 so, 1783 with 128 tiles).
+constexpr int kRun = 512;
+
 // Tensor memory columns: scores of two or three tiles and each group's weights (two fp16 a
 // column), then each group's accumulators.
 constexpr uint32_t kTmemColumns = 512, kTmemO = 256, kTmemGroup = 128;
@@ -64,7 +71,8 @@ struct Shape {
   static constexpr int kHiddenAt = kMiscAt + kTurns * 16;
   static constexpr int kRawAt = kHiddenAt + kTurns * 8;  // the feeding threads' pieces of the next tile
   static constexpr int kRaw = 2 * ((kTile * kD / 16 + kFeedThreads - 1) / kFeedThreads) * kFeedThreads * 16;
-  static constexpr int kBarsAt = kRawAt + kRaw;
+  static constexpr int kHeldAt = kRawAt + kRaw;         // m and l of a range so far, a soft thread's own
+  static constexpr int kBarsAt = kHeldAt + kSoftThreads * 8;
   static constexpr int kSmem = kBarsAt + 18 * 8 + 1024;          // and room to align to 1024
   static constexpr int kPart = 2 * kRows + kRows * kD;           // m, l, values: floats
   // Scores run kStages - 1 tiles ahead of the values: two where a lane has half of the keys,
@@ -210,19 +218,21 @@ __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
   return d;
 }
 
-// One CTA's range of one unit.
+// One CTA's range of one unit, or kRun tiles of it.
 struct Segment {
   int b, h, row0, rows, token0;
   int key0, key_stop, tiles;             // its keys, in tiles of kTile
   int limit_min, limit_max, low_max;     // what the first and the last row see
   int len, n;
-  bool begins, whole;
+  bool begins, whole;                    // the CTA has the unit's first keys, all of them
+  bool continues, ends;                  // not the range's first keys; its last ones
   int64_t unit_at, unit_stop;
 };
 
 template <int kRows>
 struct Walker {
   Walk w;
+  bool begins, inside;  // of the range that w.x is inside of
   __device__ __forceinline__ bool next(const AttnArgs& a, Segment* s) {
     if (w.x >= w.stop) return false;
     int64_t entries = entries_of<kCost>(a, w.req);
@@ -241,8 +251,10 @@ struct Walker {
     const int tile1 = (int)(x_stop - s->unit_at) - kCost;
     w.x = x_stop;
     if (tile1 <= 0) return false;  // the part ends within the unit's fixed entries
-    s->begins = tile0 == 0;
-    s->whole = s->begins && x_stop == s->unit_stop;
+    s->continues = inside;
+    if (!inside) begins = tile0 == 0;
+    s->begins = begins;
+    s->whole = begins && x_stop == s->unit_stop;
     s->b = w.b;
     s->h = unit / req.groups;
     s->row0 = unit % req.groups * kRows;
@@ -256,6 +268,13 @@ struct Walker {
     s->key0 = req.lo + tile0 * kTile;
     s->key_stop = min(req.lo + tile1 * kTile, s->limit_max);
     s->tiles = s->key0 < s->key_stop ? (s->key_stop - s->key0 + kTile - 1) / kTile : 0;
+    inside = s->tiles > kRun;
+    s->ends = !inside;
+    if (inside) {
+      s->tiles = kRun;
+      s->key_stop = s->key0 + kRun * kTile;
+      w.x = s->unit_at + kCost + tile0 + kRun;
+    }
     return true;
   }
 };
@@ -538,6 +557,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
   const float4* v_most = reinterpret_cast<const float4*>(smem + Sh::kMiscAt);
   const uint2* hidden = reinterpret_cast<const uint2*>(smem + Sh::kHiddenAt);
   float* unit_x = reinterpret_cast<float*>(smem + Sh::kUnitAt);
+  float2* held = reinterpret_cast<float2*>(smem + Sh::kHeldAt) + tid;
   uint32_t pair_phase = 0, soft_phase = 0, units = 0, g0 = 0;  // g0: the CTA's tiles before this unit
   // With the other group's warp of the same lanes; false when a wait ran out somewhere.
   auto pair_sync = [&]() {
@@ -726,7 +746,9 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
       if (lane == 0) mbar_arrive(bars.weights[group]);
     }
 
-    // ---- the unit's end: both groups' sums, and the copies' ----
+    // ---- the unit's end, or the run's: both groups' sums, and the copies', and those of the
+    // range's runs before (each thread's own part of them lies where it will put the sum) ----
+    const bool finished = seg.whole && seg.ends;
     const bool has[2] = {seg.tiles > (int)(g0 & 1), seg.tiles > (int)((g0 ^ 1) & 1)};  // group 0's, 1's tiles
     for (int k = 0; k < 2; ++k) {
       const uint32_t last = g0 + seg.tiles - 1;  // the last tile of stage k is this or the one before
@@ -744,10 +766,22 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
       m = fmaxf(m0, m1);
       float f0 = m0 > -kInf ? ex2(m0 - m) : 0.0f, f1 = m1 > -kInf ? ex2(m1 - m) : 0.0f;
       l = f0 * ends[2 * kLanes] + f1 * ends[3 * kLanes];
-      if (seg.whole) {
+      float before = 0.0f;
+      if (seg.continues) {
+        const float2 h = *held;
+        const float to = fmaxf(m, h.x), f = m > -kInf ? ex2(m - to) : 0.0f;
+        before = h.x > -kInf ? ex2(h.x - to) : 0.0f;
+        f0 *= f;
+        f1 *= f;
+        l = l * f + h.y * before;
+        m = to;
+      }
+      *held = make_float2(m, l);
+      if (finished) {
         const float f = l > 0.0f ? 1.0f / l : 0.0f;
         f0 *= f;
         f1 *= f;
+        before *= f;
       }
       uint16_t* out = static_cast<uint16_t*>(a.out) + (token * a.Hq + hq) * kD + group * kDims;
 #pragma unroll 1
@@ -774,13 +808,18 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[k] = kCopies == 2 && copy ? v[(j + k + 16) & 31] : v[j + k];
             const int d = c + j + copy * (32 / kCopies);
-            const float4 y = make_float4(x[0], x[1], x[2], x[3]);
-            if (seg.whole) store4(out + d, y);
-            else __stcg(reinterpret_cast<float4*>(mine + 2 * kRows + row * kD + group * kDims + d), y);
+            float4 y = make_float4(x[0], x[1], x[2], x[3]);
+            float4* part = reinterpret_cast<float4*>(mine + 2 * kRows + row * kD + group * kDims + d);
+            if (before != 0.0f) {
+              const float4 z = __ldcg(part);
+              y = make_float4(y.x + z.x * before, y.y + z.y * before, y.z + z.z * before, y.w + z.w * before);
+            }
+            if (finished) store4(out + d, y);
+            else __stcg(part, y);
           }
       }
       if (group == 0 && copy == 0) {
-        if (!seg.whole) {
+        if (!finished) {
           __stcg(mine + row, m);
           __stcg(mine + kRows + row, l);
         } else if (real && a.lse != nullptr) {
@@ -789,7 +828,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
       }
     }
     tc_before();
-    if (!seg.whole) {
+    if (seg.ends && !seg.whole) {
       const Cut cut(total, ctas);
       const int c0 = cut.part_of(seg.unit_at + kCost), parts = cut.part_of(seg.unit_stop - 1) - c0 + 1;
       if (!soft_sync()) return;
@@ -808,7 +847,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
         // memory, so that a thread has two parts on the way.
         constexpr int kItems = kD / 16;  // four values each
         const int sub = tid & 3;
-        uint4* held = reinterpret_cast<uint4*>(smem + Sh::kQAt) + tid;
+        uint4* second = reinterpret_cast<uint4*>(smem + Sh::kQAt) + tid;
         for (int r = tid >> 2; r < seg.rows; r += kSoftThreads / 4) {
           float4 v[kItems];
           float high = -kInf, sum = 0.0f;
@@ -834,7 +873,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
             const float* p2 = values_of(min(k + 1, parts - 1));
             float4 y[kItems];
 #pragma unroll
-            for (int j = 0; j < kItems; ++j) cp16(smem_addr(held + j * kSoftThreads), p2 + j * 16);
+            for (int j = 0; j < kItems; ++j) cp16(smem_addr(second + j * kSoftThreads), p2 + j * 16);
             cp_commit();
 #pragma unroll
             for (int j = 0; j < kItems; ++j) y[j] = __ldcg(reinterpret_cast<const float4*>(p + j * 16));
@@ -845,7 +884,7 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
             cp_wait<0>();
             if (k + 1 < parts) {
 #pragma unroll
-              for (int j = 0; j < kItems; ++j) y[j] = *reinterpret_cast<const float4*>(held + j * kSoftThreads);
+              for (int j = 0; j < kItems; ++j) y[j] = *reinterpret_cast<const float4*>(second + j * kSoftThreads);
               fold(pm2, pl2, y);
             }
           }
@@ -916,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_attention_kernel(AttnArgs a)
   tc_after();
   const uint32_t tmem = tmem_at;
   Way<kRows>* way = ways + warp;
-  if ((tid & 31) == 0) way->walker.w = walk;
+  if ((tid & 31) == 0) way->walker = {walk, false, false};
   if (!busy) {
   } else if (warp < kSoftWarps) {
     soften<kD, kRows>(a, way, smem, tmem, bars, &abort, total, ctas, &last_part);
@@ -935,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_attention_kernel(AttnArgs a)
   if (abort != 0) {  // a wait ran out: the CTA's rows are not to be taken for results
     if (tid == 0 && a.status != nullptr) atomicOr(a.status, 2);
     const float nan = __int_as_float(0x7fffffff);
-    Walker<kRows> walker{walk};
+    Walker<kRows> walker{walk, false, false};
     Segment seg;
     while (walker.next(a, &seg))
       for (int i = tid; i < seg.rows * (kD / 4); i += kThreads) {

@@ -82,7 +82,7 @@ def long_unit(mem, dtype, G, n, D, L, seed=0):
 @pytest.mark.parametrize("dtype,G,n,D", LONG)
 def test_attention_sums_do_not_drift(mem, dtype, G, n, D):
     """A sum over 131072 keys of V of one sign.  Scores are off by at most 2^-18 of their terms'
-    sum (below 1/2), weights by 2^-22 (fp32) or 2^-12 (bf16, and the output by 2^-9 more), all
+    sum (below 1/2), weights by 2^-22 (fp32) or 2^-12 (bf16, and the output by 2^-8 more), all
     to either side.  The running sums of a warp take 1024 steps, each rounded to nearest: a walk
     of steps of at most 2^-24, 2^-23 / sqrt(12) * sqrt(1024 / 3) = 6.4e-7 after the last, and six
     times that are 3.8e-6; the strip's own products, cut off, add 2 * 2^-23 at most.  So fp32
@@ -96,6 +96,59 @@ def test_attention_sums_do_not_drift(mem, dtype, G, n, D):
     assert float((lse - wlse).abs().max()) < 2.0 ** -17 + 4e-7 * float(wlse.abs().max())
     once = long_unit(mem, dtype, G, n, D, 1024)[0]
     assert abs(float(((out - once) / want)[n - 1::n].mean())) < 2.0 ** -17
+
+
+@pytest.mark.parametrize("G,D", [(8, 128), (16, 128), (8, 64), (16, 64)])
+def test_attention_wide_sums_do_not_drift(mem, G, D):
+    """The many-row kernel's sums leave the tensor cores every 65536 keys: 256 tiles of a group,
+    8 products each (4 where a lane has half of the keys), of which each may cut 2^-22 off a sum
+    that is half of its last value on average: 2048 * 2^-23 = 2^-12 at most, and 2^-11 with the
+    estimate's own scatter (about a hundred of its results round elsewhere, a tenth of that).
+    Over 2^20 keys without an end they would lose 1.4e-3 (64 rows) and 2.9e-3 (128)."""
+    out, want, lse, wlse = long_unit(mem, "bf16", G, 8, D, 1 << 20)
+    err = (out - want) / want
+    assert float(err.abs().max()) < 2.0 ** -8 + 2.0 ** -10
+    assert float((lse - wlse).abs().max()) < 2.0 ** -17 + 4e-7 * float(wlse.abs().max())
+    once = long_unit(mem, "bf16", G, 8, D, 1024)[0]
+    assert abs(float(((out - once) / want)[7::8].mean())) < 2.0 ** -11
+
+
+@pytest.mark.parametrize("window", [0, 100000])
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 16, 2), (128, 16, 1)])
+def test_attention_wide_ranges_of_several_runs(mem, window, D, Hq, Hkv):
+    """Ranges that are cut into runs, whole units and parts of them, some of which see nothing in
+    their first or last run: requests of up to 150000 keys, as the 8-row kernel has them one query
+    at a time."""
+    rs = np.random.RandomState(71)
+    lens, new = [150000, 70000, 16500, 140000, 5, 90000], [40, 9, 16, 8, 8, 25]
+    P = 1024
+    n_pages = 80
+    table = np.array([[rs.randint(0, n_pages) for _ in range(147)] for _ in lens])
+    kq, vq = (torch.randint(-127, 128, (n_pages, Hkv, P, D), generator=torch.Generator().manual_seed(i), dtype=torch.int8).cuda() for i in (1, 2))
+    kd, vd = (0.01 * torch.rand(n_pages, Hkv, P // 32, generator=torch.Generator().manual_seed(i)).cuda() for i in (3, 4))
+    q = torch.randn(sum(new), Hq, D, generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+    ws = torch.zeros(mem.KV_ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    cu = np.concatenate([[0], np.cumsum(new)])
+    reps = 3                                               # enough units for each CTA to have whole ones too
+    many = [np.concatenate([np.asarray(x)] * reps) for x in (table, lens)]
+    cus = np.concatenate([[0], np.cumsum(new * reps)])
+    out, lse = mem.memra_kv_attention_q8(q.repeat(reps, 1, 1), kq, kd, vq, vd, dev(many[0], i32), dev(many[1], i32), dev(cus, i32),
+                                         scale=D ** -0.5, window=window, workspace=ws)
+    # one query at a time: the lengths up to it, of rows of their own
+    one = dev(np.concatenate([np.arange(L - n + 1, L + 1) for L, n in zip(lens, new)]), i32)
+    rows = dev(np.repeat(table, new, axis=0), i32)
+    want, wlse = mem.memra_kv_attention_q8(q.float(), kq, kd, vq, vd, rows, one, dev(np.arange(len(q) + 1), i32), scale=D ** -0.5,
+                                           window=window, workspace=ws)
+    assert q.shape[0] == cu[-1]
+    for r in range(reps):
+        o, l = out[r * len(q):(r + 1) * len(q)].double(), lse[r * len(q):(r + 1) * len(q)]
+        assert torch.equal(torch.isneginf(l), torch.isneginf(wlse))
+        live = ~torch.isneginf(wlse)
+        # scores: 2^-18 of sum |q| |k| scale, below 127 * 0.01 * 128 * 0.8 * 128 ** -0.5 = 12 here: 4.4e-5 either
+        # side; values of at most 1.27, off by 2^-12, by twice the scores' error and by what sums lose in
+        # a run (2^-12), rounded at 2^-8
+        assert float((l - wlse)[live].abs().max()) < 2 * 4.4e-5 + 1e-5
+        assert float((o - want.double()).abs().max()) < 1.27 * (2.0 ** -11 + 4 * 4.4e-5) + 2.0 ** -8 * float(want.abs().max())
 
 
 # ---------------------------------------------------------------------------
