@@ -49,6 +49,9 @@ constexpr int kUnitCost = 3;   // entries of the list for a unit's fixed time (1
 // 128 rows, one of 16000 (1024) 64 / 56; 256 rows, one of 8000 (2048) 61 / 45; 64 rows, 32
 // requests of 100 to 500 56 / 36.
 constexpr int kWideRows = 32, kWideAll = 1024;
+// Where the reference for scales of V starts: 2^8 over it is an fp32 number, which 2^8 over
+// a scale below 7.6e-37 is not.  Smaller scales are next to nothing.
+constexpr float kLeastRef = 0x1p-115f;
 constexpr int kMaxParts = 64;  // CTAs to a unit, on average (32: 57.5 us, 64 and 128: 52.2 for one
                                // sequence of 130k)
 
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
     // m: the reference that weights are taken against (0 while a row has seen no key);
     // bar: m + kMaxSlack (-inf then).
     float o[kSteps][kNT][4];
-    float m[kNT][2], bar[kNT][2], l[kNT][2], ref = 0.0f, inv_ref = 0.0f;
+    float m[kNT][2], bar[kNT][2], l[kNT][2], ref = kLeastRef, inv_ref = kWeightScale / kLeastRef;
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
 #pragma unroll
@@ -482,9 +485,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
       if (__any_sync(kFullMask, move)) {
         const float top = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(v_top)));
         const float new_ref = fmaxf(ref, top);
-        const float rescale = new_ref > 0.0f ? ref / new_ref : 1.0f;
+        const float rescale = ref / new_ref;
         ref = new_ref;
-        inv_ref = ref > 0.0f ? kWeightScale / ref : 0.0f;
+        inv_ref = kWeightScale / ref;
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll

@@ -591,7 +591,8 @@ memra_status memra_kv_read_q8(const int32_t* slots, int64_t N, const int8_t* kq,
  * its tokens and kv_lens beyond max_pages * P are cut to it (status 1).
  * Statistics and sums are fp32.  exp(s_j) and the scale of v_j are held to 11 bits (bf16
  * queries) or 22 (fp32) for the sum over v, on a grid that ends at 2^-33 of the largest
- * exp(s_j) times the largest scale of V that the row meets: what is smaller counts as 0.
+ * exp(s_j) times the largest scale of V that the row meets, or times 2^-83 where all are
+ * smaller: what is smaller counts as 0.  Queries and scales are of magnitude 2^90 at most.
  * With bf16 queries a sum over v is off by up to 2^-15 of sum_j softmax(s)_j |vd_j| besides:
  * 2^-22 of the largest values that its blocks' codes can stand for.  Scales may have either
  * sign.  Rows below cu_q[0] and from cu_q[B] on are no request's.

@@ -151,6 +151,34 @@ def test_attention_wide_ranges_of_several_runs(mem, window, D, Hq, Hkv):
         assert float((o - want.double()).abs().max()) < 1.27 * (2.0 ** -11 + 4 * 4.4e-5) + 2.0 ** -8 * float(want.abs().max())
 
 
+@pytest.mark.parametrize("n,dtype,D", [(1, "bf16", 128), (1, "fp32", 64), (2, "fp32", 128), (1, "fp32", 256), (60, "bf16", 64)])
+@pytest.mark.parametrize("size", [1e-33, 1e-37, 1e-39, 1e-44])
+def test_attention_next_to_no_values(mem, n, dtype, D, size):
+    """Scales of V so small that 2^8 over them is no fp32 number, alone and before blocks of
+    usual ones: nothing infinite, and no trace in the rows of usual ones."""
+    q, kq, kd, vq, vd, table, lens, cu = attention_case(np.random.RandomState(31), [700, 90], [n, n], 16, 4, D, 32, 16, dtype)
+    least = np.where(np.isfinite(vd), vd * np.float32(size), vd).astype(np.float32)
+    mixed = vd.copy()
+    mixed[table[0, :9]] = least[table[0, :9]]
+    for plane in (least, mixed):
+        check_attention(mem, q, kq, kd, vq, plane, table, lens, cu, wide_scales=True, code_unit=n == 1 and dtype == "bf16")
+
+
+@pytest.mark.parametrize("n,dtype,D", [(1, "bf16", 128), (1, "fp32", 64), (2, "fp32", 128), (1, "bf16", 256)])
+@pytest.mark.parametrize("power", [-100, 80])
+def test_attention_of_values_scaled_by_a_power_of_two(mem, n, dtype, D, power):
+    """Scales of V times a power of two: the result times it.  Factors of parts far below a row's
+    largest may be subnormal then (2^-149 of rounding, of up to 2^15 times as much, next to results
+    of 2^-100), which can turn a last bit: to one part in 2^23 of the row's largest."""
+    c = attention_case(np.random.RandomState(33), [700, 90], [n, n], 16, 4, D, 32, 16, dtype)
+    t = [c[0]] + [dev(x) for x in c[1:5]] + [dev(x, i32) for x in c[5:]]
+    o, l = mem.memra_kv_attention_q8(*t)
+    t[4] = t[4] * 2.0 ** power
+    o2, l2 = mem.memra_kv_attention_q8(*t)
+    most = o.double().abs().amax(-1, keepdim=True)
+    assert bool(((o2.double() * 2.0 ** -power - o.double()).abs() <= 2.0 ** -23 * most).all()) and torch.equal(l, l2)
+
+
 # ---------------------------------------------------------------------------
 # The plan: lengths in place, arrays that overlap.
 # ---------------------------------------------------------------------------
