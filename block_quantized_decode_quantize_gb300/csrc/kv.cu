@@ -344,9 +344,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 8) append_kernel(AppendArgs
         largest.take(*reinterpret_cast<const uint4*>(rows + r * a.stride_t + p * 32 * kN));
     float amax = largest.value();
     amax = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(amax)));
-    const float d = fmaxf(d_old, amax / 127.0f);
+    // a scale of either sign stays until its magnitude has to grow (one that is no number is
+    // replaced)
+    const float least = amax / 127.0f;
+    const bool grows = !(least <= fabsf(d_old));
+    const float d = grows ? least : d_old;
 
-    if (first > 0 && d > d_old) {
+    if (first > 0 && grows) {
       const float ratio = d_old / d;
       for (int i = lane * 4; i < first * kD; i += 128) {
         const char4 q = *reinterpret_cast<const char4*>(block_codes + i);
@@ -366,7 +370,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 8) append_kernel(AppendArgs
     };
     float v[kN];
     uint32_t w[kN / 4];
-    if (d > 1e-30f) {
+    if (fabsf(d) > 1e-30f) {
       const float inv = 1.0f / d;
 #pragma unroll
       for (int s = 0; s < kHeld; ++s) {

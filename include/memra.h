@@ -553,9 +553,9 @@ memra_status memra_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int
  * Consecutive rows whose slots lie in one scale block are one run; within a run the slots
  * rise by one (as memra_kv_plan gives them), and the tokens at smaller offsets of the
  * block are its older tokens.  For each run, head and plane:
- *   d = max(d_old, amax / 127) over the run's values, d_old = 0 for a run that begins at
- *   the block's first token; if d > d_old the older tokens' codes become
- *   rha(q * (d_old / d)); the run's codes are clamp(rha(x / d), -127, 127).
+ *   with d' = amax / 127 over the run's values and d_old = 0 for a run that begins at the
+ *   block's first token, d = d' if d' > |d_old|, and the older tokens' codes become
+ *   rha(q * (d_old / d)), else d = d_old; the run's codes are clamp(rha(x / d), -127, 127).
  * (IEEE fp32 division and product, rha: to nearest, halves away from zero; d = 0 gives
  * codes 0.)  A repeated call with the same tokens changes nothing.  A slot beyond the pool
  * is left out (status 1).  Inputs must be finite; no two runs may share a block.

@@ -180,6 +180,32 @@ def test_attention_of_values_scaled_by_a_power_of_two(mem, n, dtype, D, power):
 
 
 # ---------------------------------------------------------------------------
+# The write: a block whose scale is negative.
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("size", [1e-4, 1.0, 50.0])
+def test_append_to_a_block_of_negative_scale(mem, dtype, size):
+    """Attention takes scales of either sign; a token written after such a block's own must
+    leave the older ones what they stand for: to within half a step of the scale."""
+    rs = np.random.RandomState(41)
+    P, S, Hkv, D = 32, 16, 2, 64
+    kq = rs.randint(-127, 128, (2, Hkv, P, D)).astype(np.int8)
+    kd = (-0.01 * (1 + rs.rand(2, Hkv, P // S))).astype(np.float32)
+    c = [dev(kq), dev(kd), dev(kq), dev(-kd)]
+    x = (size * torch.randn(3, Hkv, D, generator=torch.Generator().manual_seed(2))).to(torch.bfloat16 if dtype == "bf16" else torch.float32).cuda()
+    mem.memra_kv_append_q8(x, x, dev(np.arange(37, 40), i32), *c)
+    k, v = mem.memra_kv_read_q8(dev(np.arange(32, 40), i32), *c, dtype=torch.float32)
+    step = np.maximum(-kd[1, :, 0], x.float().abs().amax(dim=(0, 2)).cpu().numpy() / 127)
+    older = kq[1, :, :5].astype(np.float64) * kd[1, :, :1, None]          # [Hkv, 5, D]
+    for got, sign in ((k, 1.0), (v, -1.0)):
+        got = got.double().cpu().numpy()
+        tol = (0.5 + 1e-4) * step[None, :, None]
+        assert (np.abs(got[:5] - sign * older.transpose(1, 0, 2)) <= tol).all()
+        assert (np.abs(got[5:] - x.double().cpu().numpy()) <= tol).all()
+
+
+# ---------------------------------------------------------------------------
 # The plan: lengths in place, arrays that overlap.
 # ---------------------------------------------------------------------------
 
