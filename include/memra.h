@@ -559,6 +559,12 @@ memra_status memra_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int
  * (IEEE fp32 division and product, rha: to nearest, halves away from zero; d = 0 gives
  * codes 0.)  A repeated call with the same tokens changes nothing.  A slot beyond the pool
  * is left out (status 1).  Inputs must be finite; no two runs may share a block.
+ * A block's scale falls only when its first token is written again.  So tokens that are
+ * written and then given up (rejected drafts: the next call writes over them) leave their
+ * mark on the block's tokens before them: the scale may stay larger than these need, and
+ * each growth has rounded their codes once more, by half a step of the new scale at most.
+ * What a block stands for therefore also depends on how its tokens came in calls.  With S = 1
+ * none of this happens, and no call reads or changes an older token.
  */
 memra_status memra_kv_append_q8(const void* k, const void* v, int32_t dtype, int64_t T,
                                 int64_t stride_t, int64_t stride_h, const int32_t* slots,

@@ -205,6 +205,47 @@ def test_append_to_a_block_of_negative_scale(mem, dtype, size):
         assert (np.abs(got[5:] - x.double().cpu().numpy()) <= tol).all()
 
 
+@pytest.mark.parametrize("S", [1, 4, 16])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_append_over_rejected_drafts(mem, S, dtype):
+    """Verify steps that write five drafts and keep one to five of them: the stated rule call by
+    call; kept tokens within half a step for each growth of their block's scale; and with S = 1
+    what is kept is as if the drafts had never been."""
+    rs = np.random.RandomState(43)
+    P, Hkv, D, L = 16, 2, 64, 60
+    g = torch.Generator().manual_seed(44)
+    tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    kept = torch.randn(L, Hkv, D, generator=g).to(tdt)
+    order = rs.permutation(6)
+    slot = lambda p: order[p // P] * P + p % P
+    zero = np.zeros((6, Hkv, P, D), np.int8), np.zeros((6, Hkv, P // S), np.float32)
+    c = [dev(x) for x in zero + zero]
+    want, step, at = zero, np.zeros((L, Hkv)), 0
+    scale = np.zeros((6, Hkv, P // S), np.float32)
+    while at < L - 5:
+        n = int(rs.randint(1, 6))
+        rows = torch.cat([kept[at:at + n], (3.0 * torch.randn(5 - n, Hkv, D, generator=g)).to(tdt)])
+        slots = np.array([slot(p) for p in range(at, at + 5)])
+        mem.memra_kv_append_q8(rows.cuda(), rows.cuda(), dev(slots, i32), *c)
+        want = ref_append(rows.float().numpy(), slots, *want)
+        assert all(np.array_equal(c[i].cpu().numpy(), want[i % 2]) for i in range(4))
+        for p in range(at + n):                          # what this call may have moved a kept token by
+            i = slot(p)
+            d = want[1][i // P, :, i % P // S]
+            grown = d > scale[i // P, :, i % P // S]
+            step[p] = np.where(p >= at, d, step[p] + np.where(grown, d, 0))
+        scale = want[1].copy()
+        at += n
+    k, v = mem.memra_kv_read_q8(dev([slot(p) for p in range(at)], i32), *c, dtype=torch.float32)
+    off = (k.double().cpu() - kept[:at].double()).abs().numpy()
+    assert torch.equal(k, v) and (off <= (0.5 + 1e-4) * step[:at, :, None]).all()
+    if S == 1:
+        clean = [dev(x) for x in zero + zero]
+        mem.memra_kv_append_q8(kept[:at].cuda(), kept[:at].cuda(), dev([slot(p) for p in range(at)], i32), *clean)
+        k2, _ = mem.memra_kv_read_q8(dev([slot(p) for p in range(at)], i32), *clean, dtype=torch.float32)
+        assert torch.equal(k, k2)
+
+
 # ---------------------------------------------------------------------------
 # The plan: lengths in place, arrays that overlap.
 # ---------------------------------------------------------------------------
