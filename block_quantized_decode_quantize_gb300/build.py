@@ -3,8 +3,10 @@
 Each .cu file under csrc/ is compiled by nvcc in parallel and linked into one shared
 library next to this file.  No fast-math: the quantisers rely on IEEE division and
 rounding.  csrc/binding.cpp, the Python extension with the quick paths of the small
-calls, is compiled against torch's headers at the same time and linked to that library.
-Rebuilds only when a source or the public header is newer than the libraries.
+calls, is compiled against torch's headers at the same time and linked to that library;
+where it cannot be built, a warning says why, and the library, which needs no torch, is
+there all the same (the Python functions then take their long way to it).
+Rebuilds only what has a source or the public header newer than itself.
 """
 import glob
 import importlib.util
@@ -12,6 +14,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -36,16 +39,23 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _inputs():
-    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [BINDING_SRC] +
-            glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+def _newer_than(path, inputs):
+    """Whether `path` is there and no input is newer."""
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path)
+                                        for f in inputs + [os.path.abspath(__file__)])
+
+
+def library_up_to_date():
+    return _newer_than(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
+                       glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def binding_up_to_date():
+    return _newer_than(BINDING, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date():
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return library_up_to_date() and binding_up_to_date()
 
 
 def _binding_cmds():
@@ -65,46 +75,71 @@ def _binding_cmds():
     return compile_, link
 
 
-def build(force=False, verbose=False, extra_flags=()):
-    """Compile and link libmemra.so if needed; return its path."""
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    procs = []
-    objs = []
-    for src in sources():
-        obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
-        cmd = [nvcc()] + NVCC_FLAGS + list(extra_flags) + ["-c", src, "-o", obj]
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE,
-                                            stderr=subprocess.STDOUT)))
-        objs.append(obj)
-    compile_binding, link_binding = _binding_cmds()
-    if verbose:
-        print(" ".join(compile_binding), file=sys.stderr)
-    procs.append((BINDING_SRC, subprocess.Popen(compile_binding, stdout=subprocess.PIPE,
-                                                stderr=subprocess.STDOUT)))
-    failed = []
-    for src, p in procs:
-        out, _ = p.communicate()
-        if p.returncode != 0:
-            failed.append((src, out.decode(errors="replace")))
-        elif verbose and out:
-            sys.stderr.write(out.decode(errors="replace"))
-    if failed:
-        msg = "\n".join("%s:\n%s" % f for f in failed)
-        raise RuntimeError("nvcc failed:\n" + msg)
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [nvcc()] + ARCH + ["-shared", "-Xlinker", "-soname=libmemra.so", "-o", tmp] + objs
+def _start(cmd, verbose):
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
-    if verbose:
-        print(" ".join(link_binding), file=sys.stderr)
-    subprocess.run(link_binding, check=True)
-    os.replace(BINDING + ".tmp.%d" % os.getpid(), BINDING)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish(p, verbose):
+    """What a failed command printed, None if it succeeded."""
+    out = p.communicate()[0].decode(errors="replace")
+    if p.returncode != 0:
+        return out or "status %d" % p.returncode
+    if verbose and out:
+        sys.stderr.write(out)
+    return None
+
+
+def _start_binding(verbose):
+    """(started compiler or None, link command, what kept it from starting)."""
+    try:
+        compile_, link = _binding_cmds()
+        return _start(compile_, verbose), link, None
+    except Exception as e:  # no torch, no compiler
+        return None, None, "%s: %s" % (type(e).__name__, e)
+
+
+def _finish_binding(p, link, why, verbose):
+    if p is not None:
+        why = _finish(p, verbose) or _finish(_start(link, verbose), verbose)
+    if why is None:
+        os.replace(link[link.index("-o") + 1], BINDING)
+        return
+    if os.path.exists(BINDING):
+        os.remove(BINDING)  # of other sources
+    warnings.warn("%s is not built; the calls of the cache, attention and routing take their long "
+                  "way (14 to 40 us on the host).  The C++ compiler (%s) said:\n%s"
+                  % (os.path.basename(BINDING), os.environ.get("CXX", "g++"), why), RuntimeWarning, stacklevel=3)
+
+
+def build(force=False, verbose=False, extra_flags=()):
+    """Compile and link libmemra.so and the Python extension if needed; return the library's path."""
+    library = force or not library_up_to_date()
+    binding = force or not binding_up_to_date()
+    if not library and not binding:
+        return LIB
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    extension = _start_binding(verbose) if binding else None
+    if library:
+        procs, objs = [], []
+        for src in sources():
+            obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
+            procs.append((src, _start([nvcc()] + NVCC_FLAGS + list(extra_flags) + ["-c", src, "-o", obj], verbose)))
+            objs.append(obj)
+        failed = [(src, why) for src, why in [(src, _finish(p, verbose)) for src, p in procs] if why is not None]
+        if failed:
+            if extension and extension[0] is not None:
+                extension[0].communicate()
+            raise RuntimeError("nvcc failed:\n" + "\n".join("%s:\n%s" % f for f in failed))
+        tmp = LIB + ".tmp.%d" % os.getpid()
+        why = _finish(_start([nvcc()] + ARCH + ["-shared", "-Xlinker", "-soname=libmemra.so", "-o", tmp] + objs, verbose),
+                      verbose)
+        if why is not None:
+            raise RuntimeError("linking %s failed:\n%s" % (LIB, why))
+        os.replace(tmp, LIB)
+    if binding:
+        _finish_binding(*extension, verbose)
     return LIB
 
 
