@@ -9,14 +9,11 @@
 // A strip is two products on the tensor cores with the keys (dims) in the 16-row operand,
 // so that 8 query rows waste nothing:
 //   S^T [16 keys x 8 rows]  = K [16 x D] * Q^T,   O^T [D x 8 rows] += V^T [D x 16] * P^T.
-// An int8 code c becomes an fp16 operand exactly and without arithmetic: the byte c + 128
-// (one xor) alone in an fp16's mantissa is the subnormal (c + 128) * 2^-24, which the
-// tensor cores take at full rate.  The 128 leaves S through its initial value, -128 sum q,
-// and O, for 8-row units of bf16 queries, through a second product of a constant -128
-// matrix with the same weights, so the two parts cancel within a strip; elsewhere codes of
-// V, and with fp32 queries of K too (the sums that cancel are thrice as large, and the
-// result was 1.1e-6 off instead of 5e-7), are made as 1024 + 128 + c and an fp16
-// subtraction, which is exact (1.4 % of the time of 16 sequences of 37 to 16000 tokens).
+// An int8 code c becomes an fp16 operand exactly: the byte c + 128 (one xor) under the
+// exponent of 1024 is 1024 + 128 + c, and an fp16 subtraction leaves c.  (Taking the byte
+// as it is, for the subnormal (c + 128) * 2^-24, and the 128 out of the sums saves the
+// subtraction but no time (130k keys 52.1 us so, 52.1 with it), and leaves an error of the
+// 128's own size: ten times as much in the log-sum, 2^-14 of the scale in the result.)
 // Scales never meet the codes: kd multiplies the score, vd the weight.
 //
 // The tensor cores cut their fp32 sums off, so a sum over V that stayed in them would lose
@@ -79,12 +76,7 @@ __device__ __forceinline__ void add4(float c[4], const float a[4]) {
   for (int i = 0; i < 4; ++i) c[i] += a[i];
 }
 
-// Codes 0 and 2 (1 and 3) of w plus 128, times 2^-24, as two fp16.
-__device__ __forceinline__ uint32_t even_raised(uint32_t w) { return (w & 0x00ff00ffu) ^ 0x00800080u; }
-__device__ __forceinline__ uint32_t odd_raised(uint32_t w) {
-  return ((w >> 8) & 0x00ff00ffu) ^ 0x00800080u;
-}
-// The codes themselves: the byte under the exponent of 1024 is 1024 + 128 + code.
+// Codes 0 and 2 (1 and 3) of w as two fp16: the byte under the exponent of 1024 is 1024 + 128 + code.
 __device__ __forceinline__ uint32_t minus_1152(uint32_t h) {
   const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x6480)));
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -142,8 +134,6 @@ template <typename T, int kD, int kNT>
 struct Shape {
   static constexpr int kRows = 8 * kNT;
   static constexpr bool kPair = Row<T>::kPair;
-  static constexpr bool kRaisedV = !kPair && kNT == 1;
-  static constexpr bool kRaisedK = !kPair;
   // CTAs of an SM: two where 128 registers hold the rows' sums, else one with 255 (16
   // sequences of 500 to 8000 tokens, two CTAs / one: 16 bf16 rows of 128 32.8 / 26.4 us, fp32
   // 37.7 / 28.4; 32 bf16 rows of 64 40.1 / 28.0; but 8 fp32 rows of 128 31.2 / 33.4).
@@ -154,7 +144,7 @@ struct Shape {
   static constexpr int kJoin = kWarps * kRows * kD * 4;  // reuses the ring
   static constexpr int kBig = kRing > kJoin ? kRing : kJoin;
   static constexpr int kQ = (kPair ? 2 : 1) * (kD / 16) * kNT * 32 * 8;
-  static constexpr int kStats = (2 * kWarps + 5) * kRows * 4;
+  static constexpr int kStats = (2 * kWarps + 4) * kRows * 4;
   static constexpr int kSmem = kBig + kQ + kStats;
 };
 
@@ -182,8 +172,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
   float* row_m = warp_l + kWarps * kRows;      // [kRows]
   float* row_l = row_m + kRows;
   float* row_scale = row_l + kRows;
-  float* row_raise = row_scale + kRows;
-  int* row_limit = reinterpret_cast<int*>(row_raise + kRows);
+  int* row_limit = reinterpret_cast<int*>(row_scale + kRows);
   __shared__ int last_part;
   __shared__ Walk walk;
   __shared__ Unit unit_at_hand;
@@ -337,14 +326,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
       int e = (int)(__float_as_uint(amax) >> 23) - 127;
       e = e < -100 ? -100 : e;
       const float up = __int_as_float((13 - e + 127) << 23);  // 2^(13 - e), e in [-100, 128]
-      if (lane == 0) {  // the codes' 2^-24 goes back in here
-        row_scale[r] = amax > 0.0f ? a.scale * ((Sh::kRaisedK ? 0x1p24f : 1.0f) * 1.44269504088896341f) *
-                                         __int_as_float((e - 13 + 127) << 23)
-                                   : 0.0f;
+      if (lane == 0) {
+        row_scale[r] = amax > 0.0f ? a.scale * 1.44269504088896341f * __int_as_float((e - 13 + 127) << 23) : 0.0f;
         row_limit[r] = min(req.len, req.len - req.n + i + 1);
       }
       __half* frag = reinterpret_cast<__half*>(q_frag);
-      float sum_q = 0.0f;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int d = j * 32 + lane;
@@ -355,14 +341,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         const float s = v[j] * up;
         const __half hi = __float2half_rn(s);
         frag[idx] = hi;
-        if (Sh::kRaisedK) sum_q += __half2float(hi);
         if (kPair) frag[idx + kSteps * kNT * 32 * 4] = __float2half_rn(s - __half2float(hi));
       }
-      if (Sh::kRaisedK) {
-#pragma unroll
-        for (int w2 = 16; w2 > 0; w2 >>= 1) sum_q += __shfl_xor_sync(kFullMask, sum_q, w2);
-      }
-      if (lane == 0) row_raise[r] = -128.0f * 0x1p-24f * sum_q;
     }
     __syncthreads();
     if (tid == 0) {
@@ -376,14 +356,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
       walk.b = b;
       walk.req = req;
     }
-    float qs[kNT][2], raise[kNT][2];
+    float qs[kNT][2];
     int limit[kNT][2];
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         qs[n][c] = row_scale[8 * n + 2 * t4 + c];
-        raise[n][c] = row_raise[8 * n + 2 * t4 + c];
         limit[n][c] = row_limit[8 * n + 2 * t4 + c];
       }
 
@@ -412,10 +391,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
       __syncwarp();
       float c[kNT][4];
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        c[n][0] = c[n][2] = raise[n][0];
-        c[n][1] = c[n][3] = raise[n][1];
-      }
+      for (int n = 0; n < kNT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
       // with one tile of rows, odd steps sum apart: two chains of products instead of one
       float c2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -426,10 +402,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int step = 4 * q + i;
-          const uint32_t a0 = Sh::kRaisedK ? even_raised(wa[i]) : even_bytes(wa[i]);
-          const uint32_t a1 = Sh::kRaisedK ? even_raised(wb[i]) : even_bytes(wb[i]);
-          const uint32_t a2 = Sh::kRaisedK ? odd_raised(wa[i]) : odd_bytes(wa[i]);
-          const uint32_t a3 = Sh::kRaisedK ? odd_raised(wb[i]) : odd_bytes(wb[i]);
+          const uint32_t a0 = even_bytes(wa[i]), a1 = even_bytes(wb[i]);
+          const uint32_t a2 = odd_bytes(wa[i]), a3 = odd_bytes(wb[i]);
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
             const uint2 f = q_frag[(step * kNT + n) * 32 + lane];
@@ -552,23 +526,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
             const uint32_t z0 = __byte_perm(v[0][w2], v[1][w2], sel);
             const uint32_t z1 = __byte_perm(v[2][w2], v[3][w2], sel);
             const int tile = (q * kWords + w2) * 2 + half;
-            if (Sh::kRaisedV) {
-              constexpr uint32_t kLower = 0x80808080u;  // -128 * 2^-24, twice
-              float strip[4];
-              mma_16816_zero(strip, kLower, kLower, kLower, kLower, p0[0], p1[0]);
-              mma_16816(strip, even_raised(z0), odd_raised(z0), even_raised(z1), odd_raised(z1),
-                        p0[0], p1[0]);
-              add4(o[tile][0], strip);
-            } else {
-              const uint32_t a0 = even_bytes(z0), a1 = odd_bytes(z0);
-              const uint32_t a2 = even_bytes(z1), a3 = odd_bytes(z1);
+            const uint32_t a0 = even_bytes(z0), a1 = odd_bytes(z0);
+            const uint32_t a2 = even_bytes(z1), a3 = odd_bytes(z1);
 #pragma unroll
-              for (int n = 0; n < kNT; ++n) {
-                float strip[4];
-                mma_16816_zero(strip, a0, a1, a2, a3, p0[n], p1[n]);
-                if (kPair) mma_16816(strip, a0, a1, a2, a3, e0[n], e1[n]);
-                add4(o[tile][n], strip);
-              }
+            for (int n = 0; n < kNT; ++n) {
+              float strip[4];
+              mma_16816_zero(strip, a0, a1, a2, a3, p0[n], p1[n]);
+              if (kPair) mma_16816(strip, a0, a1, a2, a3, e0[n], e1[n]);
+              add4(o[tile][n], strip);
             }
           }
         }
@@ -615,8 +580,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<T, kD, kNT>::kCtas)) attentio
         float top = -kInf;
         for (int k = 0; k < kWarps; ++k) top = fmaxf(top, warp_m[k * kRows + r]);
         const float f = bar[n][i] == -kInf ? 0.0f
-                                            : ex2(m[n][i] - top) * ref *
-                                                  ((Sh::kRaisedV ? 0x1p24f : 1.0f) / kWeightScale);
+                                            : ex2(m[n][i] - top) * ref * (1.0f / kWeightScale);
         constexpr int kRun = kD == 64 ? 8 : 16;  // consecutive dims of a lane
 #pragma unroll
         for (int j = 0; j < kSteps / 2; ++j) {

@@ -599,9 +599,7 @@ memra_status memra_kv_read_q8(const int32_t* slots, int64_t N, const int8_t* kq,
  * queries) or 22 (fp32) for the sum over v, on a grid that ends at 2^-33 of the largest
  * exp(s_j) times the largest scale of V that the row meets, or times 2^-83 where all are
  * smaller: what is smaller counts as 0.  Queries and scales are of magnitude 2^90 at most.
- * With bf16 queries a sum over v is off by up to 2^-15 of sum_j softmax(s)_j |vd_j| besides:
- * 2^-22 of the largest values that its blocks' codes can stand for.  Scales may have either
- * sign.  Rows below cu_q[0] and from cu_q[B] on are no request's.
+ * Scales may have either sign.  Rows below cu_q[0] and from cu_q[B] on are no request's.
  *   workspace: MEMRA_KV_ATTENTION_WORKSPACE_BYTES, 16-byte aligned, zeroed once by the
  *   caller before its first use; every call leaves it fit for the next.  Calls that may
  *   overlap on the GPU need one each.

@@ -151,6 +151,22 @@ def test_attention_wide_ranges_of_several_runs(mem, window, D, Hq, Hkv):
         assert float((o - want.double()).abs().max()) < 1.27 * (2.0 ** -11 + 4 * 4.4e-5) + 2.0 ** -8 * float(want.abs().max())
 
 
+@pytest.mark.parametrize("dtype,G,n,D", [("bf16", 1, 1, 64), ("bf16", 5, 1, 128), ("bf16", 8, 1, 256), ("bf16", 8, 2, 128),
+                                         ("bf16", 8, 4, 64), ("bf16", 16, 16, 128), ("fp32", 8, 1, 128)])
+def test_attention_beside_a_heavy_key_of_code_zero(mem, dtype, G, n, D):
+    """One key takes nearly all of the weight and has code 0 in every dim of V: the result is what
+    the others leave, to their own accuracy.  (The tolerance is that of check_attention with the
+    grid's end and without anything for the heavy key's scale.)"""
+    q, kq, kd, vq, vd, table, lens, cu = attention_case(np.random.RandomState(35), [300, 90], [n, n], 4 * G, 4, D, 32, 16, dtype)
+    for b in range(2):
+        page, off = int(table[b, 0]), 7
+        vq[page, :, off] = 0
+        k = kq[page, :, off].astype(np.float64) * kd[page, :, off // 16, None]
+        heavy = 16.0 * D ** 0.5 * k / np.square(k).sum(1, keepdims=True)     # its score: 16
+        q[n * b:n * b + n] = torch.from_numpy(np.repeat(heavy, G, axis=0)).to(q.dtype).cuda()
+    check_attention(mem, q, kq, kd, vq, vd, table, lens, cu, wide_scales=True)
+
+
 @pytest.mark.parametrize("n,dtype,D", [(1, "bf16", 128), (1, "fp32", 64), (2, "fp32", 128), (1, "fp32", 256), (60, "bf16", 64)])
 @pytest.mark.parametrize("size", [1e-33, 1e-37, 1e-39, 1e-44])
 def test_attention_next_to_no_values(mem, n, dtype, D, size):
