@@ -741,6 +741,11 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
         l += sums.x + sums.y;
         tmem_wait_stores();
         tc_before();
+      } else if (Sh::kStages == 3 && t > 1 && !warp_wait(a, bars.empty[group], phase ^ 1, abort)) {
+        // A warp without rows waits for the group's last product too: with scores two tiles ahead
+        // it would else arrive for this tile before the others have for that one, and stand in
+        // for one of them.
+        return;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bars.weights[group]);

@@ -40,6 +40,25 @@ def test_attention_wide_many_units_to_a_cta(mem, rows):
         assert torch.equal(o, o2) and torch.equal(l, l2)
 
 
+@pytest.mark.parametrize("new,G,Hkv", [([8, 0, 0, 5, 2], 16, 8), ([5, 6, 5, 6], 8, 8), ([1, 1, 1, 1, 1], 40, 8), ([1] * 4, 48, 6),
+                                       ([9, 1, 1, 1, 30], 8, 16)])
+def test_attention_wide_units_of_few_rows(mem, new, G, Hkv):
+    """Units whose rows leave some of the softmax warps without any: those must not arrive for a
+    tile while the others still make the weights of the one before.  Repeated with a cold cache."""
+    rs = np.random.RandomState(62)
+    lens = [1540, 2438, 2064, 998, 1637][:len(new)]
+    c = attention_case(rs, lens, new, G * Hkv, Hkv, 64, 16, 16, "bf16")
+    o, l = check_attention(mem, *c)
+    t = [dev(x) for x in c[1:5]] + [dev(x, i32) for x in c[5:]]
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(mem.KV_ATTENTION_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    for i in range(60):
+        if i % 2:
+            flush.fill_(i)
+        o2, l2 = mem.memra_kv_attention_q8(c[0], *t, workspace=ws)
+        assert torch.equal(o, o2) and torch.equal(l, l2), i
+
+
 LONG = [
     # dtype, G, n, D
     ("bf16", 5, 1, 128), ("bf16", 8, 1, 64), ("bf16", 8, 1, 256), ("bf16", 8, 2, 128), ("bf16", 8, 4, 64),
