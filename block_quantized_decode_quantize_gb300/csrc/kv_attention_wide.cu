@@ -714,7 +714,10 @@ __device__ __forceinline__ void soften(const AttnArgs& a, Way<kRows>* way, uint8
         }
         // The group's last weights are read when its last product is done; with two stages that
         // came before these scores.
-        if (Sh::kStages == 3 && t > 1 && !warp_wait(a, bars.empty[group], phase ^ 1, abort)) return;
+        if (Sh::kStages == 3 && t > 1) {
+          if (!warp_wait(a, bars.empty[group], phase ^ 1, abort)) return;
+          tc_after();
+        }
         // Weights: where a lane has all keys they lie over the last half of the scores, so the
         // last keys come first, whose scores are read by then.
         Pair sum0 = pair_of(0.0f, 0.0f), sum1 = sum0;
