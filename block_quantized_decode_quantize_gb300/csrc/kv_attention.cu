@@ -786,8 +786,9 @@ extern "C" memra_status memra_kv_attention_q8(
     return MEMRA_ERR_INVALID_ARG;
   if (D != 64 && D != 128 && D != 256) return MEMRA_ERR_UNSUPPORTED;
   if (page_size > MEMRA_MAX_KV_PAGE || Hkv > 65535 || n_pages > INT32_MAX / page_size ||
-      max_pages > INT32_MAX / page_size || T > INT32_MAX / Hq || B > (1 << 24))
+      max_pages > (INT32_MAX - kTile) / page_size || T > INT32_MAX / Hq || B > (1 << 24))
     return MEMRA_ERR_UNSUPPORTED;
+  // (a sequence's last tile of keys ends below 2^31)
   if (Hkv * page_size * D > (int64_t)UINT32_MAX) return MEMRA_ERR_UNSUPPORTED;
   if (T == 0) return MEMRA_OK;
   if (!q || !out || !workspace || !cu_q) return MEMRA_ERR_INVALID_ARG;

@@ -600,6 +600,7 @@ memra_status memra_kv_read_q8(const int32_t* slots, int64_t N, const int8_t* kq,
  * exp(s_j) times the largest scale of V that the row meets, or times 2^-83 where all are
  * smaller: what is smaller counts as 0.  Queries and scales are of magnitude 2^90 at most.
  * Scales may have either sign.  Rows below cu_q[0] and from cu_q[B] on are no request's.
+ * max_pages * P is 2^31 - 129 at most.
  *   workspace: MEMRA_KV_ATTENTION_WORKSPACE_BYTES, 16-byte aligned, zeroed once by the
  *   caller before its first use; every call leaves it fit for the next.  Calls that may
  *   overlap on the GPU need one each.
