@@ -13,8 +13,9 @@ namespace {
 // its own share of the chunk's table entries and rows: a thread finds the request of its
 // entry, or of its four rows, by bisection in shared memory.  Nothing passes between CTAs,
 // so one launch does for any size, and what bounds it is latency: launch, one read of the
-// lengths, two scans, one read of pages, one write.  4.4 us for 16 sequences of one token
-// (a kernel that does nothing: 2.2), 8.2 us for 512 prompts, 328,486 slots.
+// lengths, two scans, one read of pages, one write.  4.3 us for 16 sequences of one token
+// (a kernel that does nothing: 2.2), 8.2 us for 512 prompts, 328,486 slots (81 CTAs, the
+// arithmetic pipe 56 % busy).
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 
@@ -180,9 +181,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
 // The write.  A warp takes one run of tokens (one scale block) of one head and plane: the
 // run's largest magnitude first, then the older tokens' codes if the scale grew, then the
 // run's own codes.  A lane holds 16 bytes of input at a time, and a run of up to eight
-// such pieces a lane (16 tokens of 128 bf16) stays in registers between the two passes.  Latency bounds the small calls (one
-// token of 8 heads and its read-back: 3.9 us), instructions the large ones: 8191
-// bf16 tokens of 8 heads (34 MB in, 17 out) and their read-back take 20.3 us, 5.0 TB/s.
+// such pieces a lane (16 tokens of 128 bf16) stays in registers between the two passes.
+// Latency bounds the small calls (one token of 8 heads and its read-back: 3.8 us).  8191 bf16
+// tokens of 8 heads (34 MB in, 17 out) take 12.2 us, where their bytes need 7.4 and their
+// instructions 6.2: neither is at its rate in so short a call.  32000 take 34.3, 85 % of the
+// copy rate; in fp32 19.7 us (12.4) and 62.1 (48.3).
 // ---------------------------------------------------------------------------
 constexpr int kAppendWarps = 4;
 
@@ -409,7 +412,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 8) append_kernel(AppendArgs
 }
 
 // ---------------------------------------------------------------------------
-// The read-back: a lane takes 16 bytes of output at a time.  A stream: its bytes bound it.
+// The read-back: a lane takes 16 bytes of output at a time.  Its bytes bound it, or the wait for
+// them: 8191 bf16 tokens of 8 heads take 8.8 us (bytes alone 7.4), 32000 37.9 (29.0), in fp32
+// 16.7 (12.4) and 63.4 (48.3).
 // ---------------------------------------------------------------------------
 struct ReadArgs {
   CacheArgs c;

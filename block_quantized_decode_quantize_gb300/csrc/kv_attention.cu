@@ -20,12 +20,14 @@
 // up to 2^-23 of itself with each product, always to the same side (7e-5 after the 1024
 // strips that a warp has of 131072 keys).  A strip's products therefore start from zero,
 // and its sums are added to the running ones in registers, rounded to nearest: no loss
-// for 8 bf16 rows (51.8 us for 52.0 at 130k), 31.2 us for 29.1 of the 16 fp32 sequences.
+// for 8 bf16 rows (52.1 us for 52.2 at 130k), 31.4 us for 29.2 of the 16 fp32 sequences.
 //
 // One token of one sequence of 130k (40 heads on 8, D 128) takes 52.0 us, 5.1 TB/s of codes
 // and scales: about 10 us are fixed (launch, the list, first copies, the join of a unit's
-// parts), and the strips keep the arithmetic pipe 55 % busy beside memory's 60 %.  16
-// sequences of 37 to 16000 tokens, fp32: 31.2 us, 3.2 TB/s (twice the products).
+// parts), and the strips keep the arithmetic pipe 50 % busy beside memory's 55 %.  16
+// sequences of 37 to 16000 tokens, fp32: 31.4 us, 3.2 TB/s (twice the products); nothing is
+// near its rate there (memory 35 %, arithmetic pipe 36 %, tensor pipe 17 %), and the first
+// reason why a warp waits is that its next instruction has not been fetched.
 #include <atomic>
 
 #include "kv_attention.cuh"
@@ -36,20 +38,21 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 static_assert(kWarps * kStrip == kTile, "a CTA's step is an entry of the list");
-constexpr int kUnitCost = 3;   // entries of the list for a unit's fixed time (1: 34.4 us, 3: 29.1, 6:
-                               // 30.8 for 16 sequences of 37 to 16000 tokens, fp32)
+constexpr int kUnitCost = 3;   // entries of the list for a unit's fixed time (1: 36.8 us, 3: 31.5, 6:
+                               // 33.1 for 16 sequences of 37 to 16000 tokens, fp32)
 // Above this many rows to a unit, and with at least so many in all (rows times heads), the
 // tcgen05 kernel takes bf16 queries: below, its larger parts and ends of units cost more than
-// its products save.  8 cached heads, us here / there: 32 rows, 16 requests of 500 to 8000
-// tokens 64 / 68, 64 of 500 to 3000 124 / 139; 48 rows, 16 requests 104 / 70; 64 rows, 8
-// requests (4096 in all) 64 / 44, 4 (2048) 41 / 35, 2 (1024) 32 / 31, one of 8000 (512) 30 / 32;
-// 128 rows, one of 16000 (1024) 64 / 56; 256 rows, one of 8000 (2048) 61 / 45; 64 rows, 32
-// requests of 100 to 500 56 / 36.
+// its products save.  8 cached heads of 128, us here / there: 32 rows, 16 requests of 500 to
+// 8000 tokens 64 / 69, 64 of 500 to 3000 121 / 141; 48 rows, 16 requests 104 / 70; 64 rows, 8
+// requests (4096 in all) 64 / 44, 4 (2048) 41 / 35, 2 (1024) 32 / 31, one of 8000 (512) 31 / 33;
+// 128 rows, one of 16000 (1024) 64 / 55; 256 rows, one of 8000 (2048) 62 / 45; 64 rows, 32
+// requests of 100 to 500 56 / 36.  Heads of 64, in the same order: 46 / 49, 88 / 101, 74 / 50,
+// 46 / 32, 30 / 26, 24 / 24, 23 / 25, 44 / 41, 44 / 34, 40 / 28.
 constexpr int kWideRows = 32, kWideAll = 1024;
 // Where the reference for scales of V starts: 2^8 over it is an fp32 number, which 2^8 over
 // a scale below 7.6e-37 is not.  Smaller scales are next to nothing.
 constexpr float kLeastRef = 0x1p-115f;
-constexpr int kMaxParts = 64;  // CTAs to a unit, on average (32: 57.5 us, 64 and 128: 52.2 for one
+constexpr int kMaxParts = 64;  // CTAs to a unit, on average (32: 57.0 us, 64 and 128: 52.0 for one
                                // sequence of 130k)
 
 __device__ __forceinline__ void mma_16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2,

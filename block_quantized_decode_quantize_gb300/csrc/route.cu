@@ -5,10 +5,12 @@
 // ranks and choice never leave the warp.  A rank is kept as an order-preserving uint32 of
 // its fp32 value.  The choice: the top_k-th largest of the 32 lanes' own maxima is a bound
 // that top_k experts reach, so only the few at or above it are sorted, by counting for
-// each how many come before it.  Large batches are bound by instructions (about a third of
-// them the exponentials), small ones by the chain of exchanges between lanes: 8191 tokens of
-// 256 experts in 8 groups, bf16, take 13.5 us (0.35 TB/s; 7 us of instruction issue alone),
-// 16 tokens 4.0 us, one of 128 experts 2.4 us, where a kernel that does nothing takes 2.2.
+// each how many come before it.  8191 tokens of 256 experts in 8 groups, bf16, take 13.5 us
+// (0.35 TB/s): 7 us are instruction issue (1181 a token, about a third of them the
+// exponentials), the rest dependent latency at 43 % of the warps and a second, partly empty
+// round of tokens (1216 CTAs of 4 warps).  Small batches are bound by the chain of exchanges
+// between lanes: 16 tokens 4.0 us, one of 128 experts 2.4 us, where a kernel that does
+// nothing takes 2.2.
 #include "common.cuh"
 
 namespace memra {

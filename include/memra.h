@@ -595,12 +595,13 @@ memra_status memra_kv_read_q8(const int32_t* slots, int64_t N, const int8_t* kq,
  * lse = -inf.  Cache entries at and beyond kv_lens[b], and page entries that hold no
  * visible key, are not used, whatever they hold.  A page number outside [0, n_pages) hides
  * its tokens and kv_lens beyond max_pages * P are cut to it (status 1).
- * Statistics and sums are fp32.  exp(s_j) and the scale of v_j are held to 11 bits (bf16
- * queries) or 22 (fp32) for the sum over v, on a grid that ends at 2^-33 of the largest
- * exp(s_j) times the largest scale of V that the row meets, or times 2^-83 where all are
- * smaller: what is smaller counts as 0.  Queries and scales are of magnitude 2^90 at most.
- * Scales may have either sign.  Rows below cu_q[0] and from cu_q[B] on are no request's.
- * max_pages * P is 2^31 - 129 at most.
+ * Statistics and sums are fp32; with many bf16 rows a sum over v stays in the tensor cores,
+ * which cut off, for up to 65536 keys: 2^-12 of sum_j softmax(s)_j |v_j| at most.
+ * exp(s_j) and the scale of v_j are held to 11 bits (bf16 queries) or 22 (fp32) for the sum
+ * over v, on a grid that ends at 2^-33 of the largest exp(s_j) times the largest scale of V
+ * that the row meets, or times 2^-83 where all are smaller: what is smaller counts as 0.
+ * Queries and scales are of magnitude 2^90 at most.  Scales may have either sign.  Rows
+ * below cu_q[0] and from cu_q[B] on are no request's.  max_pages * P is 2^31 - 129 at most.
  *   workspace: MEMRA_KV_ATTENTION_WORKSPACE_BYTES, 16-byte aligned, zeroed once by the
  *   caller before its first use; every call leaves it fit for the next.  Calls that may
  *   overlap on the GPU need one each.
@@ -623,10 +624,11 @@ memra_status memra_kv_attention_q8(const void* q, int32_t dtype, int64_t T, int6
  * products take them, from logits [T][E] of `dtype` (row t at t * stride_t elements).
  *   score (MEMRA_SCORE_SOFTMAX)  s_e = exp(l_e - max l) / sum exp(l - max l)
  *         (MEMRA_SCORE_SIGMOID)  s_e = 1 / (1 + exp(-l_e))
- *   v_e = s_e + bias[e] (bias fp32 [E] or NULL) ranks the experts.  With n_groups > 1, E /
- *   n_groups neighbouring experts make a group, its rank is the largest v in it (group_top
- *   1) or the sum of the two largest (2), and only experts of the topk_groups first groups
- *   stay.  ids: the top_k largest v, descending, ties to the lowest index (of groups too).
+ *   v_e = s_e + bias[e] (bias fp32 [E], finite or -inf, or NULL) ranks the experts.  With
+ *   n_groups > 1, E / n_groups neighbouring experts make a group, its rank is the largest v
+ *   in it (group_top 1) or the sum of the two largest (2), and only experts of the
+ *   topk_groups first groups stay.  ids: the top_k largest v, descending, ties to the lowest
+ *   index (of groups too).
  *   gate_w = s of the chosen, divided by their sum if renormalize (0 where that is 0), times
  *   route_scale.
  * Every fp32 operation is rounded once; exp is the one of memra_swiglu_quantize_q8_1, and
