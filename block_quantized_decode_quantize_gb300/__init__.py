@@ -9,7 +9,10 @@ library's sm_103a kernels; there is no fallback.  If the library has not been bu
 
 The decode step's other half is here too: the page plan of a step (memra_kv_plan), a paged
 KV cache in 8 bits (memra_kv_append_q8, memra_kv_read_q8), attention over it
-(memra_kv_attention_q8) and the routing to experts (memra_moe_route).
+(memra_kv_attention_q8) and the routing to experts (memra_moe_route); the norm and rotation of
+queries and keys before the write (memra_qk_norm_rope), pages that sequences share, give back or
+move (memra_kv_fork, memra_kv_unshare, memra_kv_copy_pages, memra_kv_release, memra_kv_compact)
+and the log probabilities of tokens behind the LM head (memra_token_logprobs).
 
 Tensor conventions (all on one CUDA device, contiguous):
   wq  int8 [N, K]          Q8_0 quants            wd  float16 [N, K/32]  Q8_0 scales
@@ -32,6 +35,8 @@ MAX_M = 16
 MAX_TOP_K = 64
 MOE_NOALLOC_SCRATCH_FLOATS = 65536
 KV_ATTENTION_WORKSPACE_BYTES = 33554432
+MAX_VOCAB = 1048576
+MAX_TOP_LOGPROBS = 32
 
 _STATUS = {0: "MEMRA_OK", 1: "MEMRA_ERR_INVALID_ARG", 2: "MEMRA_ERR_ALIGNMENT",
            3: "MEMRA_ERR_UNSUPPORTED", 4: "MEMRA_ERR_CUDA"}
@@ -105,6 +110,16 @@ _SIGS = {
     "memra_kv_attention_q8": [_p, _i32, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _i64, _i64, _i64,
                               _i64, _i64, _p, _i64, _i64, _p, _p, ctypes.c_float, _i64, _p, _p,
                               _p, _p, _p],
+    "memra_qk_norm_rope": [_p, _p, _i32, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _p, _p,
+                           ctypes.c_float, _p, _p, _i64, _i32, _p, _i32, _i64, _i64, _p, _i32, _i64,
+                           _i64, _p],
+    "memra_kv_fork": [_p, _p, _i64, _p, _p, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _p],
+    "memra_kv_unshare": [_p, _p, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _p, _p, _p, _p,
+                         _p, _p],
+    "memra_kv_copy_pages": [_p, _p, _p, _i64, _p, _i64, _i64, _i64, _i64, _i64, _i64, _p, _p],
+    "memra_kv_release": [_p, _p, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _p],
+    "memra_kv_compact": [_p, _p, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p, _p],
+    "memra_token_logprobs": [_p, _i32, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p, _p],
     "memra_moe_route": [_p, _i32, _i64, _i64, _i64, _p, _i32, _i64, _i64, _i64, _i64, _i32,
                         ctypes.c_float, _p, _p, _p],
 }
@@ -858,6 +873,7 @@ class _NoBinding:
         return None
 
     append = read = attention = route = plan
+    rope = fork = unshare = copy_pages = release = compact = logprobs = plan
 
 
 def _binding():
@@ -1161,6 +1177,276 @@ def memra_moe_route(logits, top_k, bias=None, score="softmax", n_groups=1, topk_
             _SCORES[score], n_groups, topk_groups, group_top, top_k, 1 if renormalize else 0,
             scale, ids.data_ptr(), gate_w.data_ptr())
     return ids, gate_w
+
+
+_LAYOUTS = {"halves": 0, "pairs": 1}
+_ROW_TYPES = {torch.bfloat16: MEMRA_BF16, torch.float32: MEMRA_F32, None: -1}
+
+
+def memra_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_weight=None, eps=None,
+                       layout="halves", q_dtype=None, k_dtype=None, q_out=None, k_out=None):
+    """Norm of each head and rotation by position, queries and keys in one pass.  q [T, Hq, D],
+    k [T, Hkv, D] (bf16 or fp32 alike, strided as for memra_kv_append_q8; k may be None), positions
+    int32 [T] (as memra_kv_plan gives them; below 0: zeros come out) and inv_freq float64 [R / 2]:
+    the first R values of a head are turned by positions * inv_freq, R 0 (both None) to D.  layout
+    "halves" turns value j with j + R / 2, "pairs" 2j with 2j + 1.  eps None: no norm; else every
+    head is divided by its root mean square and multiplied by q_weight or k_weight (float32 [D] or
+    None).  Returns q_out, k_out of q_dtype, k_dtype (default: the inputs').  The outputs may be the
+    inputs themselves: k_out=k leaves k beside v in the projection's rows, with the strides that
+    memra_kv_append_q8 wants alike."""
+    done = (_fast or _binding()).rope(q, k, positions, inv_freq, q_weight, k_weight, eps,
+                                      _LAYOUTS.get(layout, -1), _ROW_TYPES.get(q_dtype, -2),
+                                      _ROW_TYPES.get(k_dtype, -2), q_out, k_out)
+    if done is not None:
+        return done
+    dev = q.get_device() if isinstance(q, torch.Tensor) else -1
+    dt = _rows(q, "q", dev, 3)
+    T, Hq, D = q.shape
+    if k is None:
+        Hkv = 0
+        if k_out is not None or k_weight is not None:
+            raise ValueError("k_out and k_weight go with k")
+    else:
+        if _rows(k, "k", dev, 3) != dt or k.shape[0] != T or k.shape[2] != D:
+            raise ValueError("k must have q's dtype, rows and head size")
+        Hkv = k.shape[1]
+    if layout not in _LAYOUTS:
+        raise ValueError("layout must be halves or pairs, got %r" % (layout,))
+    R = 0
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a 1-D tensor")
+        R = 2 * inv_freq.shape[0]
+        _ok(inv_freq, "inv_freq", torch.float64, dev, (R // 2,))
+        if R and positions is None:
+            raise ValueError("a rotation needs positions")
+    if positions is not None:
+        _ok(positions, "positions", torch.int32, dev, (T,))
+    if eps is None:
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("weights go with a norm: eps must be given")
+    elif not eps >= 0:
+        raise ValueError("eps must be 0 or more")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _ok(w, name, torch.float32, dev, (D,))
+
+    def output(name, out, dtype, x):
+        if out is None:
+            dtype = x.dtype if dtype is None else dtype
+            if dtype is not torch.bfloat16 and dtype is not torch.float32:
+                raise TypeError("%s must be bfloat16 or float32" % name.replace("out", "dtype"))
+            return torch.empty(x.shape, dtype=dtype, device=x.device)
+        if dtype is not None and out.dtype is not dtype:
+            raise TypeError("%s is not of %s" % (name, dtype))
+        _rows(out, name, dev, 3)
+        if out.shape != x.shape:
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(out.shape), tuple(x.shape)))
+        return out
+
+    q_out = output("q_out", q_out, q_dtype, q)
+    none = (None, MEMRA_F32, 0, 0)
+    k_args, ko_args = (None, 0, 0), none
+    if k is not None:
+        k_out = output("k_out", k_out, k_dtype, k)
+        k_args = (k.data_ptr(),) + _strides(k)
+        ko_args = (k_out.data_ptr(), _ROW_TYPES[k_out.dtype]) + _strides(k_out)
+    _launch("memra_qk_norm_rope", dev, q.data_ptr(), k_args[0], dt, T, Hq, Hkv, D, *_strides(q),
+            *k_args[1:], _addr(q_weight), _addr(k_weight), -1.0 if eps is None else eps,
+            _addr(positions), _addr(inv_freq), R, _LAYOUTS[layout], q_out.data_ptr(),
+            _ROW_TYPES[q_out.dtype], *_strides(q_out), *ko_args)
+    return q_out, k_out
+
+
+def _ints(name, t, dev, shape, optional=False):
+    """An int32 argument: its address, None where it may be and is left out."""
+    if t is None and optional:
+        return None
+    _ok(t, name, torch.int32, dev, shape)
+    return t.data_ptr()
+
+
+def _table(lens, block_table):
+    """(device, B, max_pages) of sequences' lengths and block table."""
+    if not isinstance(lens, torch.Tensor) or not lens.is_cuda or lens.dim() != 1:
+        raise ValueError("lens must be a 1-D CUDA tensor")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a 2-D tensor")
+    dev, B = lens.get_device(), lens.shape[0]
+    max_pages = block_table.shape[1]
+    _ok(lens, "lens", torch.int32, dev, (B,))
+    _ok(block_table, "block_table", torch.int32, dev, (B, max_pages))
+    return dev, B, max_pages
+
+
+def _vector(name, t, dev):
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError("%s must be a 1-D tensor" % name)
+    _ok(t, name, torch.int32, dev, t.shape)
+    return t.shape[0]
+
+
+def _new(like, *shape):
+    return torch.empty(shape, dtype=torch.int32, device=like.device)
+
+
+def memra_kv_fork(parents, lens, block_table, page_size, refs, prefix_lens=None, lens_out=None,
+                  table_out=None, dev_status=None):
+    """New sequences that share the pages of old ones: parents int32 [C] names rows of lens [B] and
+    block_table [B, max_pages] (-1: an empty sequence), of which the first prefix_lens int32 [C]
+    tokens are taken (None: all).  refs int32 [n_pages], the holders of each page beyond the first,
+    grows in place.  Returns lens_out [C] and table_out [C, max_pages].  The last page is shared too:
+    call memra_kv_unshare before a step writes into it."""
+    if lens_out is None and table_out is None:
+        done = (_fast or _binding()).fork(parents, lens, block_table, page_size, refs, prefix_lens,
+                                          dev_status)
+        if done is not None:
+            return done
+    dev, B, max_pages = _table(lens, block_table)
+    C, n_pages = _vector("parents", parents, dev), _vector("refs", refs, dev)
+    lens_out = _new(lens, C) if lens_out is None else lens_out
+    table_out = _new(lens, C, max_pages) if table_out is None else table_out
+    _launch("memra_kv_fork", dev, parents.data_ptr(), _ints("prefix_lens", prefix_lens, dev, (C,), True),
+            C, lens.data_ptr(), block_table.data_ptr(), B, max_pages, page_size, refs.data_ptr(),
+            n_pages, _ints("lens_out", lens_out, dev, (C,)),
+            _ints("table_out", table_out, dev, (C, max_pages)),
+            _ints("dev_status", dev_status, dev, (1,), True))
+    return lens_out, table_out
+
+
+def memra_kv_unshare(lens, new_lens, page_size, refs, free_pages, block_table, free_head=None,
+                     new_lens_out=None, src=None, dst=None, tokens=None, free_head_out=None,
+                     dev_status=None):
+    """Copy on write before a step's plan: sequences with new tokens (new_lens int32 [B]) that stand
+    inside a page others hold too take a free page for it; block_table and refs change in place.
+    Returns new_lens_out [B] (0 for those the free list has no page for: give it to memra_kv_plan),
+    src, dst, tokens [B] for memra_kv_copy_pages (-1, -1, 0 where nothing is to be copied) and
+    free_head_out [1].  free_head_out may be free_head, and new_lens_out new_lens."""
+    if new_lens_out is None and src is None and dst is None and tokens is None:
+        done = (_fast or _binding()).unshare(lens, new_lens, page_size, refs, free_pages, block_table,
+                                             free_head, free_head_out, dev_status)
+        if done is not None:
+            return done
+    dev, B, max_pages = _table(lens, block_table)
+    n_pages, n_free = _vector("refs", refs, dev), _vector("free_pages", free_pages, dev)
+    new_lens_out = _new(lens, B) if new_lens_out is None else new_lens_out
+    src = _new(lens, B) if src is None else src
+    dst = _new(lens, B) if dst is None else dst
+    tokens = _new(lens, B) if tokens is None else tokens
+    free_head_out = _new(lens, 1) if free_head_out is None else free_head_out
+    _launch("memra_kv_unshare", dev, lens.data_ptr(), _ints("new_lens", new_lens, dev, (B,)), B,
+            page_size, refs.data_ptr(), n_pages, free_pages.data_ptr(), n_free,
+            _ints("free_head", free_head, dev, (1,), True), block_table.data_ptr(), max_pages,
+            _ints("new_lens_out", new_lens_out, dev, (B,)), _ints("src", src, dev, (B,)),
+            _ints("dst", dst, dev, (B,)), _ints("tokens", tokens, dev, (B,)),
+            _ints("free_head_out", free_head_out, dev, (1,)),
+            _ints("dev_status", dev_status, dev, (1,), True))
+    return new_lens_out, src, dst, tokens, free_head_out
+
+
+def memra_kv_copy_pages(src, dst, caches, tokens=None, dev_status=None):
+    """Copy pages src[i] to dst[i] (int32 [N]; -1: nothing) in every layer, their first tokens[i]
+    tokens (int32 [N], None: all).  caches: the layers' (kq, kd, vq, vd), a list of one or more
+    of the same sizes."""
+    if (_fast or _binding()).copy_pages(src, dst, caches, tokens, dev_status):
+        return
+    caches = list(caches)
+    if any(isinstance(c, torch.Tensor) or len(c) != 4 for c in caches):
+        raise ValueError("caches must be a list of (kq, kd, vq, vd)")
+    sizes = {_cache(*c) for c in caches}
+    if len(sizes) > 1:
+        raise ValueError("the caches differ in device or sizes")
+    if not caches:
+        return
+    dev, n_pages, Hkv, page, D, block = sizes.pop()
+    N = _vector("src", src, dev)
+    layers = (_p * (4 * len(caches)))(*[t.data_ptr() for c in caches for t in c])
+    _launch("memra_kv_copy_pages", dev, src.data_ptr(), _ints("dst", dst, dev, (N,)),
+            _ints("tokens", tokens, dev, (N,), True), N, ctypes.cast(layers, _p), len(caches),
+            n_pages, Hkv, page, D, block, _ints("dev_status", dev_status, dev, (1,), True))
+
+
+def memra_kv_release(lens, page_size, block_table, refs, free_pages, free_head, keep_lens=None,
+                     lens_out=None, free_head_out=None, dev_status=None):
+    """Cut sequences to their first keep_lens int32 [B] tokens (None: none) and give the pages behind
+    them up: refs falls, and pages that nobody holds any more go back to the free list, below
+    free_head, in place.  Returns lens_out [B] and free_head_out [1], which may be lens and
+    free_head."""
+    if lens_out is None:
+        done = (_fast or _binding()).release(lens, page_size, block_table, refs, free_pages, free_head,
+                                             keep_lens, free_head_out, dev_status)
+        if done is not None:
+            return done
+    dev, B, max_pages = _table(lens, block_table)
+    n_pages, n_free = _vector("refs", refs, dev), _vector("free_pages", free_pages, dev)
+    lens_out = _new(lens, B) if lens_out is None else lens_out
+    free_head_out = _new(lens, 1) if free_head_out is None else free_head_out
+    _launch("memra_kv_release", dev, lens.data_ptr(), _ints("keep_lens", keep_lens, dev, (B,), True), B,
+            page_size, block_table.data_ptr(), max_pages, refs.data_ptr(), n_pages,
+            free_pages.data_ptr(), n_free, _ints("free_head", free_head, dev, (1,)),
+            _ints("lens_out", lens_out, dev, (B,)), _ints("free_head_out", free_head_out, dev, (1,)),
+            _ints("dev_status", dev_status, dev, (1,), True))
+    return lens_out, free_head_out
+
+
+def memra_kv_compact(lens, block_table, page_size, n_pages, table_out=None, refs_out=None,
+                     free_out=None, dev_status=None):
+    """Renumber a pool's pages so that those in use come first.  Returns table_out [B, max_pages]
+    (which may be block_table), refs_out and free_out [n_pages], the moves src, dst [n_pages // 2]
+    for memra_kv_copy_pages (-1 behind them) and free_head_out [1], the number of pages in use."""
+    if table_out is None and refs_out is None and free_out is None:
+        done = (_fast or _binding()).compact(lens, block_table, page_size, n_pages, dev_status)
+        if done is not None:
+            return done
+    dev, B, max_pages = _table(lens, block_table)
+    if n_pages < 0:
+        raise ValueError("n_pages must not be negative")
+    table_out = _new(lens, B, max_pages) if table_out is None else table_out
+    refs_out = _new(lens, n_pages) if refs_out is None else refs_out
+    free_out = _new(lens, n_pages) if free_out is None else free_out
+    src, dst, head = _new(lens, n_pages // 2), _new(lens, n_pages // 2), _new(lens, 1)
+    _launch("memra_kv_compact", dev, lens.data_ptr(), block_table.data_ptr(), B, max_pages, page_size,
+            n_pages, _ints("table_out", table_out, dev, (B, max_pages)),
+            _ints("refs_out", refs_out, dev, (n_pages,)), _ints("free_out", free_out, dev, (n_pages,)),
+            src.data_ptr(), dst.data_ptr(), head.data_ptr(),
+            _ints("dev_status", dev_status, dev, (1,), True))
+    return table_out, refs_out, free_out, src, dst, head
+
+
+def memra_token_logprobs(logits, tokens=None, top_n=0, logprobs=None, entropy=None, top_ids=None,
+                         top_logprobs=None, dev_status=None):
+    """Log probabilities under logits [T, V] (bf16 or fp32, the last dimension dense): of tokens
+    int32 [T] (-1: none, 0), the entropy of each row, and the top_n (up to MAX_TOP_LOGPROBS) largest
+    entries, ties to the lowest index.  Logits of -inf or NaN mask tokens.  Returns logprobs [T]
+    (None without tokens), entropy [T], top_ids int32 and top_logprobs [T, top_n]."""
+    if logprobs is None and entropy is None and top_ids is None and top_logprobs is None:
+        done = (_fast or _binding()).logprobs(logits, tokens, top_n, dev_status)
+        if done is not None:
+            return done
+    dev = logits.get_device() if isinstance(logits, torch.Tensor) else -1
+    dt = _rows(logits, "logits", dev, 2)
+    T, V = logits.shape
+    if not 0 <= top_n <= V:
+        raise ValueError("top_n must be 0 to %d, got %r" % (V, top_n))
+
+    def output(name, out, dtype, shape):
+        if out is None:
+            return torch.empty(shape, dtype=dtype, device=logits.device)
+        _ok(out, name, dtype, dev, shape)
+        return out
+
+    if tokens is not None:
+        _ok(tokens, "tokens", torch.int32, dev, (T,))
+        logprobs = output("logprobs", logprobs, torch.float32, (T,))
+    elif logprobs is not None:
+        raise ValueError("logprobs go with tokens")
+    entropy = output("entropy", entropy, torch.float32, (T,))
+    top_ids = output("top_ids", top_ids, torch.int32, (T, top_n))
+    top_logprobs = output("top_logprobs", top_logprobs, torch.float32, (T, top_n))
+    _launch("memra_token_logprobs", dev, logits.data_ptr(), dt, T, V, logits.stride(0) if T > 1 else V,
+            _addr(tokens), top_n, _addr(logprobs), entropy.data_ptr(), top_ids.data_ptr(),
+            top_logprobs.data_ptr(), _ints("dev_status", dev_status, dev, (1,), True))
+    return logprobs, entropy, top_ids, top_logprobs
 
 
 def memra_debug_set_wait_test(wait_limit_cycles=0, stall_after_stages=-1):

@@ -282,8 +282,270 @@ PyObject* route(PyObject*, PyObject* const* o, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A dense int32 tensor of `dims` dimensions.
+inline bool ints(const Tensor* t, int64_t dims) {
+  return t != nullptr && t->dim() == dims && t->scalar_type() == at::kInt && t->is_contiguous();
+}
+
+// One that may be None (nullptr).  False: neither.
+inline bool optional(PyObject* o, int dev, at::ScalarType type, at::IntArrayRef shape, const Tensor** t) {
+  *t = nullptr;
+  if (o == Py_None) return true;
+  *t = tensor(o, &dev);
+  return dense(*t, type, shape);
+}
+
+// An int32 word that a call writes: the one given, or the last of `parts`.
+inline PyObject* pack_with(std::initializer_list<Tensor> ts, PyObject* given, const Tensor& own) {
+  std::vector<Tensor> all(ts);
+  all.push_back(given == Py_None ? own : THPVariable_Unpack(given));
+  PyObject* out = PyTuple_New((Py_ssize_t)all.size());
+  if (out == nullptr) return nullptr;
+  for (size_t i = 0; i < all.size(); ++i) {
+    PyObject* o = THPVariable_Wrap(all[i]);
+    if (o == nullptr) {
+      Py_DECREF(out);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(out, (Py_ssize_t)i, o);
+  }
+  return out;
+}
+
+// Rows that a call writes: those given, or new ones like x, of the C library's dtype code `want` (-1:
+// the input's).
+inline bool out_rows(PyObject* o, int* dev, const Tensor* x, int64_t want, int32_t code, Tensor* t, int32_t* type) {
+  if (want < 0 && o == Py_None) want = code;
+  if (o == Py_None) {
+    *t = at::empty(x->sizes(), x->options().dtype(want == MEMRA_BF16 ? at::kBFloat16 : at::kFloat));
+    *type = (int32_t)want;
+    return true;
+  }
+  const Tensor* given = tensor(o, dev);
+  if (!rows(given, 3, type) || given->sizes() != x->sizes() || (want >= 0 && want != *type)) return false;
+  *t = *given;
+  return true;
+}
+
+// rope(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, q_dtype, k_dtype, q_out, k_out)
+//   -> (q_out, k_out)
+PyObject* rope(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 12) Py_RETURN_NONE;
+  int dev = -1;
+  const Tensor *q = tensor(o[0], &dev), *k = tensor(o[1], &dev);
+  int32_t code, code_k, qo_type, ko_type;
+  int64_t layout, q_type, k_type;
+  float eps = -1.0f;
+  if (!rows(q, 3, &code) || !rows(k, 3, &code_k) || code != code_k || k->size(0) != q->size(0) ||
+      k->size(2) != q->size(2) || (o[6] != Py_None && (!real(o[6], &eps) || !(eps >= 0.0f))) ||
+      !whole(o[7], &layout) || !whole(o[8], &q_type) || !whole(o[9], &k_type) || q_type < -1 || k_type < -1 ||
+      !current(dev))
+    Py_RETURN_NONE;
+  const int64_t T = q->size(0), Hq = q->size(1), Hkv = k->size(1), D = q->size(2);
+  const Tensor *positions, *freq = nullptr, *qw, *kw;
+  if (!optional(o[2], dev, at::kInt, {T}, &positions) || !optional(o[4], dev, at::kFloat, {D}, &qw) ||
+      !optional(o[5], dev, at::kFloat, {D}, &kw))
+    Py_RETURN_NONE;
+  int64_t R = 0;
+  if (o[3] != Py_None) {
+    freq = tensor(o[3], &dev);
+    if (freq == nullptr || freq->dim() != 1 || !dense(freq, at::kDouble, freq->sizes())) Py_RETURN_NONE;
+    R = 2 * freq->size(0);
+  }
+  at::AutoDispatchBelowADInplaceOrView guard;
+  Tensor qo, ko;
+  if (!out_rows(o[10], &dev, q, q_type, code, &qo, &qo_type) || !out_rows(o[11], &dev, k, k_type, code, &ko, &ko_type))
+    Py_RETURN_NONE;
+  const Strides sq(q), sk(k), so(&qo), sko(&ko);
+  if (memra_qk_norm_rope(data<void>(q), data<void>(k), code, T, Hq, Hkv, D, sq.t, sq.h, sk.t, sk.h,
+                         data<float>(qw), data<float>(kw), eps, data<int32_t>(positions),
+                         data<double>(freq), R, (int32_t)layout, qo.data_ptr(), qo_type, so.t, so.h,
+                         ko.data_ptr(), ko_type, sko.t, sko.h, stream(dev)) != MEMRA_OK)
+    Py_RETURN_NONE;
+  return pack({qo, ko});
+  END_HANDLE_TH_ERRORS
+}
+
+// Sequences: lens [B] and block_table [B, max_pages].
+struct Sequences {
+  int32_t *lens, *table;
+  int64_t B, max_pages;
+};
+inline bool sequences(PyObject* lens, PyObject* table, int* dev, Sequences* s) {
+  const Tensor *l = tensor(lens, dev), *t = tensor(table, dev);
+  if (!ints(l, 1) || !ints(t, 2) || t->size(0) != l->size(0)) return false;
+  s->lens = data<int32_t>(l);
+  s->table = data<int32_t>(t);
+  s->B = l->size(0);
+  s->max_pages = t->size(1);
+  return true;
+}
+
+// fork(parents, lens, block_table, page_size, refs, prefix_lens, dev_status) -> (lens, table)
+PyObject* fork(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 7) Py_RETURN_NONE;
+  int dev = -1;
+  Sequences s;
+  int64_t page;
+  int32_t* status;
+  if (!sequences(o[1], o[2], &dev, &s) || !whole(o[3], &page) || !word(o[6], dev, &status) || !current(dev))
+    Py_RETURN_NONE;
+  const Tensor *parents = tensor(o[0], &dev), *refs = tensor(o[4], &dev), *prefix;
+  if (!ints(parents, 1) || !ints(refs, 1)) Py_RETURN_NONE;
+  const int64_t C = parents->size(0);
+  if (!optional(o[5], dev, at::kInt, {C}, &prefix)) Py_RETURN_NONE;
+  at::AutoDispatchBelowADInplaceOrView guard;
+  const Tensor lens = at::empty({C}, on(dev, at::kInt)), table = at::empty({C, s.max_pages}, on(dev, at::kInt));
+  if (memra_kv_fork(data<int32_t>(parents), data<int32_t>(prefix), C, s.lens, s.table, s.B, s.max_pages, page,
+                    data<int32_t>(refs), refs->size(0), data<int32_t>(&lens), data<int32_t>(&table), status,
+                    stream(dev)) != MEMRA_OK)
+    Py_RETURN_NONE;
+  return pack({lens, table});
+  END_HANDLE_TH_ERRORS
+}
+
+// unshare(lens, new_lens, page_size, refs, free_pages, block_table, free_head, free_head_out,
+//         dev_status) -> (new_lens, src, dst, tokens, free_head)
+PyObject* unshare(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 9) Py_RETURN_NONE;
+  int dev = -1;
+  Sequences s;
+  int64_t page;
+  int32_t *head, *head_out, *status;
+  if (!sequences(o[0], o[5], &dev, &s) || !whole(o[2], &page) || !word(o[6], dev, &head) ||
+      !word(o[7], dev, &head_out) || !word(o[8], dev, &status) || !current(dev))
+    Py_RETURN_NONE;
+  const Tensor *add = tensor(o[1], &dev), *refs = tensor(o[3], &dev), *free = tensor(o[4], &dev);
+  if (!dense(add, at::kInt, {s.B}) || !ints(refs, 1) || !ints(free, 1)) Py_RETURN_NONE;
+  at::AutoDispatchBelowADInplaceOrView guard;
+  const Tensor buf = at::empty({4 * s.B + 1}, on(dev, at::kInt));
+  const int64_t sizes[5] = {s.B, s.B, s.B, s.B, 1};
+  const std::vector<Tensor> part = buf.split_with_sizes(sizes);
+  if (head_out == nullptr) head_out = data<int32_t>(&part[4]);
+  if (memra_kv_unshare(s.lens, data<int32_t>(add), s.B, page, data<int32_t>(refs), refs->size(0),
+                       data<int32_t>(free), free->size(0), head, s.table, s.max_pages,
+                       data<int32_t>(&part[0]), data<int32_t>(&part[1]), data<int32_t>(&part[2]),
+                       data<int32_t>(&part[3]), head_out, status, stream(dev)) != MEMRA_OK)
+    Py_RETURN_NONE;
+  return pack_with({part[0], part[1], part[2], part[3]}, o[7], part[4]);
+  END_HANDLE_TH_ERRORS
+}
+
+// copy_pages(src, dst, caches, tokens, dev_status): True when done.  caches: a list or tuple of
+// tuples (kq, kd, vq, vd).
+PyObject* copy_pages(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 5 || (!PyList_CheckExact(o[2]) && !PyTuple_CheckExact(o[2]))) Py_RETURN_NONE;
+  const Py_ssize_t L = PySequence_Fast_GET_SIZE(o[2]);
+  if (L < 1) Py_RETURN_NONE;
+  int dev = -1;
+  Cache first{}, c;
+  std::vector<memra_kv_layer> layers((size_t)L);
+  for (Py_ssize_t l = 0; l < L; ++l) {
+    PyObject* one = PySequence_Fast_GET_ITEM(o[2], l);
+    if (!PyTuple_CheckExact(one) || PyTuple_GET_SIZE(one) != 4) Py_RETURN_NONE;
+    if (!cache(PySequence_Fast_ITEMS(one), &dev, &c)) Py_RETURN_NONE;
+    if (l == 0) first = c;
+    if (c.n_pages != first.n_pages || c.heads != first.heads || c.page != first.page || c.D != first.D ||
+        c.block != first.block)
+      Py_RETURN_NONE;
+    layers[(size_t)l] = {c.kq, c.kd, c.vq, c.vd};
+  }
+  const Tensor *src = tensor(o[0], &dev), *dst = tensor(o[1], &dev), *tokens;
+  int32_t* status;
+  if (!ints(src, 1) || !dense(dst, at::kInt, {src->size(0)}) ||
+      !optional(o[3], dev, at::kInt, {src->size(0)}, &tokens) || !word(o[4], dev, &status) || !current(dev))
+    Py_RETURN_NONE;
+  if (memra_kv_copy_pages(data<int32_t>(src), data<int32_t>(dst), data<int32_t>(tokens), src->size(0),
+                          layers.data(), L, first.n_pages, first.heads, first.page, first.D, first.block,
+                          status, stream(dev)) != MEMRA_OK)
+    Py_RETURN_NONE;
+  Py_RETURN_TRUE;
+  END_HANDLE_TH_ERRORS
+}
+
+// release(lens, page_size, block_table, refs, free_pages, free_head, keep_lens, free_head_out,
+//         dev_status) -> (lens, free_head)
+PyObject* release(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 9) Py_RETURN_NONE;
+  int dev = -1;
+  Sequences s;
+  int64_t page;
+  int32_t *head, *head_out, *status;
+  if (!sequences(o[0], o[2], &dev, &s) || !whole(o[1], &page) || !word(o[5], dev, &head) || head == nullptr ||
+      !word(o[7], dev, &head_out) || !word(o[8], dev, &status) || !current(dev))
+    Py_RETURN_NONE;
+  const Tensor *refs = tensor(o[3], &dev), *free = tensor(o[4], &dev), *keep;
+  if (!ints(refs, 1) || !ints(free, 1) || !optional(o[6], dev, at::kInt, {s.B}, &keep)) Py_RETURN_NONE;
+  at::AutoDispatchBelowADInplaceOrView guard;
+  const Tensor lens = at::empty({s.B}, on(dev, at::kInt)), own = at::empty({1}, on(dev, at::kInt));
+  if (head_out == nullptr) head_out = data<int32_t>(&own);
+  if (memra_kv_release(s.lens, data<int32_t>(keep), s.B, page, s.table, s.max_pages, data<int32_t>(refs),
+                       refs->size(0), data<int32_t>(free), free->size(0), head, data<int32_t>(&lens),
+                       head_out, status, stream(dev)) != MEMRA_OK)
+    Py_RETURN_NONE;
+  return pack_with({lens}, o[7], own);
+  END_HANDLE_TH_ERRORS
+}
+
+// compact(lens, block_table, page_size, n_pages, dev_status) -> (table, refs, free, src, dst, head)
+PyObject* compact(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 5) Py_RETURN_NONE;
+  int dev = -1;
+  Sequences s;
+  int64_t page, pages;
+  int32_t* status;
+  if (!sequences(o[0], o[1], &dev, &s) || !whole(o[2], &page) || !whole(o[3], &pages) || pages < 0 ||
+      pages > INT32_MAX || !word(o[4], dev, &status) || !current(dev))
+    Py_RETURN_NONE;
+  at::AutoDispatchBelowADInplaceOrView guard;
+  const Tensor table = at::empty({s.B, s.max_pages}, on(dev, at::kInt));
+  const Tensor buf = at::empty({2 * pages + 2 * (pages / 2) + 1}, on(dev, at::kInt));
+  const int64_t sizes[5] = {pages, pages, pages / 2, pages / 2, 1};
+  const std::vector<Tensor> part = buf.split_with_sizes(sizes);
+  if (memra_kv_compact(s.lens, s.table, s.B, s.max_pages, page, pages, data<int32_t>(&table),
+                       data<int32_t>(&part[0]), data<int32_t>(&part[1]), data<int32_t>(&part[2]),
+                       data<int32_t>(&part[3]), data<int32_t>(&part[4]), status, stream(dev)) != MEMRA_OK)
+    Py_RETURN_NONE;
+  return pack({table, part[0], part[1], part[2], part[3], part[4]});
+  END_HANDLE_TH_ERRORS
+}
+
+// logprobs(logits, tokens, top_n, dev_status) -> (logprobs or None, entropy, top_ids, top_logprobs)
+PyObject* logprobs(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 4) Py_RETURN_NONE;
+  int dev = -1;
+  const Tensor* x = tensor(o[0], &dev);
+  int32_t code, *status;
+  int64_t top;
+  if (!rows(x, 2, &code) || !whole(o[2], &top) || top < 0 || top > x->size(1) || !word(o[3], dev, &status) ||
+      !current(dev))
+    Py_RETURN_NONE;
+  const int64_t T = x->size(0), V = x->size(1);
+  const Tensor* tokens;
+  if (!optional(o[1], dev, at::kInt, {T}, &tokens)) Py_RETURN_NONE;
+  at::AutoDispatchBelowADInplaceOrView guard;
+  const Tensor two = at::empty({2, T}, on(dev, at::kFloat));
+  const std::vector<Tensor> part = two.unbind(0);
+  const Tensor ids = at::empty({T, top}, on(dev, at::kInt)), best = at::empty({T, top}, on(dev, at::kFloat));
+  if (memra_token_logprobs(data<void>(x), code, T, V, T > 1 ? x->stride(0) : V, data<int32_t>(tokens), top,
+                           tokens != nullptr ? data<float>(&part[0]) : nullptr, data<float>(&part[1]),
+                           data<int32_t>(&ids), data<float>(&best), status, stream(dev)) != MEMRA_OK)
+    Py_RETURN_NONE;
+  return pack({tokens != nullptr ? part[0] : Tensor(), part[1], ids, best});
+  END_HANDLE_TH_ERRORS
+}
+
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(plan), FAST(append), FAST(read), FAST(attention), FAST(route),
+                         FAST(rope), FAST(fork), FAST(unshare), FAST(copy_pages), FAST(release),
+                         FAST(compact), FAST(logprobs),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_memra_binding",
                           "Quick paths of the package's small calls.", -1, methods};

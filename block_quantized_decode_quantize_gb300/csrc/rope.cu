@@ -1,0 +1,322 @@
+// Norm of queries and keys for each head and their rotation by position, in one pass.
+//
+// n = x * w / sqrt(mean x^2 + eps), then (a, b) -> (a cos - b sin, b cos + a sin).  A head's
+// row of D values lies on D / 8 lanes, so the sum of squares takes 3 to 5 exchanges, and each
+// lane holds two pieces of four values that are each other's partners in the rotation:
+// nothing else passes between lanes, and a row is read and written once.  A CTA takes one
+// to four tokens and some or all of their heads; its threads compute the R / 2 angles of a
+// token once, for all heads, and leave cos and sin in shared memory while the first rows are
+// on their way.
+//
+// Angles: F = inv_freq / 2 pi as a fraction of a turn in 64-bit fixed point, and
+// position * F modulo 2^64 is the angle of any position, exact to the bits of F.
+//
+// Bytes bound it for many tokens, one launch and one read for few.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace memra {
+namespace {
+
+constexpr int kRopeWarps = 8;
+constexpr int kRopeTokens = 4;   // of a CTA, at most
+constexpr int kMaxPairs = 128;   // R / 2, at most
+
+struct Rows {
+  void* at;
+  int64_t stride_t, stride_h;
+  int bf16;
+};
+
+struct RopeArgs {
+  Rows q, k, q_out, k_out;
+  int64_t T;
+  int Hq, heads, R, pairs, tokens, groups;  // groups: warps' shares of heads that a CTA takes
+  const float *q_weight, *k_weight;
+  float eps;
+  const int32_t* positions;
+  const double* inv_freq;
+  Divider by_groups, by_pairs;
+};
+
+// Four values of a row.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<float> {
+  uint4 u;
+  __device__ __forceinline__ void load(const void* p) { u = __ldcg(static_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void unpack(float* v) const {
+    v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+  }
+};
+template <>
+struct Piece<uint16_t> {
+  uint2 u;
+  __device__ __forceinline__ void load(const void* p) { u = __ldcg(static_cast<const uint2*>(p)); }
+  __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
+  __device__ __forceinline__ void unpack(float* v) const {
+    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+};
+
+__device__ __forceinline__ void store4(const Rows& r, int64_t at, const float* v) {
+  if (r.bf16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(r.at) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(r.at) + at) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// The angle's sine and cosine of a position: F is the frequency in turns, 64 bits behind the point.
+__device__ __forceinline__ uint64_t turns_of(double inv_freq) {
+  double u = inv_freq * 0.15915494309189533577;  // 1 / 2 pi
+  u -= floor(u);
+  return __double2ull_rn(u * 18446744073709551616.0);
+}
+
+template <typename T, int kD>
+__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(RopeArgs a) {
+  constexpr int kLanes = kD / 8;         // of a head
+  constexpr int kHeads = 32 / kLanes;    // that a warp takes at once
+  __shared__ __align__(16) float cos_of[kRopeTokens][kMaxPairs], sin_of[kRopeTokens][kMaxPairs];
+  __shared__ int32_t pos_of[kRopeTokens];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+  const int tokens = (int)min((int64_t)a.tokens, a.T - t0);
+  const int group0 = blockIdx.y * a.groups;
+  const int all_groups = (a.heads + kHeads - 1) / kHeads;
+  const int groups = min(a.groups, all_groups - group0);
+  const int items = tokens * groups;
+
+  // The values that the lane takes of a head: two pieces of four, from off_a and off_b.
+  const int l = lane % kLanes;
+  const bool turned = l < a.R / 8, halves = turned && !a.pairs;
+  const int off_a = halves ? 4 * l : 8 * l, off_b = halves ? a.R / 2 + 4 * l : 8 * l + 4;
+
+  struct Item {
+    Piece<T> pa, pb;
+    int token, head;
+  };
+  auto fetch = [&](int i) {
+    Item it;
+    it.token = groups == a.groups ? (int)a.by_groups((uint32_t)i) : i / groups;
+    it.head = (group0 + i - it.token * groups) * kHeads + lane / kLanes;
+    it.pa.zero();
+    it.pb.zero();
+    if (i < items && it.head < a.heads) {
+      const bool is_q = it.head < a.Hq;
+      const Rows& r = is_q ? a.q : a.k;
+      const T* p = static_cast<const T*>(r.at) + (t0 + it.token) * r.stride_t +
+                   (is_q ? it.head : it.head - a.Hq) * r.stride_h;
+      it.pa.load(p + off_a);
+      it.pb.load(p + off_b);
+    }
+    return it;
+  };
+
+  Item next = fetch(warp);
+  const int half = a.R / 2;
+  for (int i = threadIdx.x; i < tokens * half; i += kRopeWarps * 32) {
+    const int t = (int)a.by_pairs((uint32_t)i), j = i - t * half;
+    const uint64_t turn = turns_of(a.inv_freq[j]) * (uint64_t)(uint32_t)a.positions[t0 + t];
+    // the upper 32 bits as half turns in [-1, 1)
+    sincospif((float)(int32_t)(uint32_t)(turn >> 32) * 4.6566128730773926e-10f, &sin_of[t][j], &cos_of[t][j]);
+  }
+  if (threadIdx.x < tokens) pos_of[threadIdx.x] = a.positions != nullptr ? a.positions[t0 + threadIdx.x] : 0;
+  float w[2][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int at = i < 4 ? off_a + i : off_b + i - 4;
+    w[0][i] = a.q_weight != nullptr ? a.q_weight[at] : 1.0f;
+    w[1][i] = a.k_weight != nullptr ? a.k_weight[at] : 1.0f;
+  }
+  __syncthreads();
+
+  for (int i = warp; i < items; i += kRopeWarps) {
+    const Item it = next;
+    next = fetch(i + kRopeWarps);
+    float v[8];
+    it.pa.unpack(v);
+    it.pb.unpack(v + 4);
+    const bool is_q = it.head < a.Hq, real = pos_of[it.token] >= 0;
+    if (a.eps >= 0.0f) {
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
+      s = fmaf(s, 1.0f / kD, a.eps);
+      const float r = s > 0.0f ? __frsqrt_rn(s) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = v[j] * r * (is_q ? w[0][j] : w[1][j]);
+    }
+    if (turned) {
+      const float4 c4 = *reinterpret_cast<const float4*>(&cos_of[it.token][4 * l]);
+      const float4 s4 = *reinterpret_cast<const float4*>(&sin_of[it.token][4 * l]);
+      const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // halves: values j and j + 4; pairs: 2j and 2j + 1
+        const float x = a.pairs ? v[2 * j] : v[j], y = a.pairs ? v[2 * j + 1] : v[j + 4];
+        const float xr = x * c[j] - y * s[j], yr = y * c[j] + x * s[j];
+        if (a.pairs) {
+          v[2 * j] = xr;
+          v[2 * j + 1] = yr;
+        } else {
+          v[j] = xr;
+          v[j + 4] = yr;
+        }
+      }
+    }
+    if (!real) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    }
+    if (it.head < a.heads) {
+      const Rows& r = is_q ? a.q_out : a.k_out;
+      const int64_t at = (t0 + it.token) * r.stride_t + (is_q ? it.head : it.head - a.Hq) * r.stride_h;
+      store4(r, at + off_a, v);
+      store4(r, at + off_b, v + 4);
+    }
+  }
+}
+
+template <typename T, int kD>
+cudaError_t launch_rope(RopeArgs a, int sms, cudaStream_t stream) {
+  constexpr int kHeads = 32 / (kD / 8);
+  const int groups = (a.heads + kHeads - 1) / kHeads;
+  // Few tokens: one to a CTA, and a CTA for every eight groups of heads.  More: all heads of a
+  // token in one CTA, so that its angles are computed once, and up to four tokens, whose angles
+  // keep all threads busy.
+  const int64_t spread = (int64_t)sms * 2;
+  a.tokens = (int)(a.T / spread < 1 ? 1 : (a.T / spread > kRopeTokens ? kRopeTokens : a.T / spread));
+  a.groups = a.T < spread ? kRopeWarps : groups;
+  if (a.groups > groups) a.groups = groups;
+  a.by_groups = Divider((uint32_t)a.groups);
+  a.by_pairs = Divider((uint32_t)(a.R > 0 ? a.R / 2 : 1));
+  const dim3 grid((unsigned)((a.T + a.tokens - 1) / a.tokens), (unsigned)((groups + a.groups - 1) / a.groups));
+  return launch_kernel(rope_kernel<T, kD>, grid, dim3(kRopeWarps * 32), 0, stream, a);
+}
+
+template <typename T>
+cudaError_t launch_rope(const RopeArgs& a, int64_t D, int sms, cudaStream_t stream) {
+  if (D == 64) return launch_rope<T, 64>(a, sms, stream);
+  if (D == 128) return launch_rope<T, 128>(a, sms, stream);
+  return launch_rope<T, 256>(a, sms, stream);
+}
+
+// Whether no two rows that are written share a value: heads side by side within a token's row,
+// or tokens side by side within a head's.
+bool apart(const Rows& r, int64_t T, int64_t H, int64_t D) {
+  if (T == 0 || H == 0) return true;
+  if (T == 1) return H == 1 || r.stride_h >= D;
+  if (H == 1) return r.stride_t >= D;
+  return (r.stride_h >= D && r.stride_t >= (H - 1) * r.stride_h + D) ||
+         (r.stride_t >= D && r.stride_h >= (T - 1) * r.stride_t + D);
+}
+
+// Bytes that rows of heads take: from `at`, T rows `row` bytes apart whose heads lie within `width`.
+struct Extent {
+  uintptr_t at;
+  uint64_t row, width, all;
+  Extent(const Rows& r, int64_t T, int64_t H, int64_t D) : at((uintptr_t)r.at), row(0), width(0), all(0) {
+    if (T == 0 || H == 0) return;
+    const uint64_t es = r.bf16 ? 2 : 4;
+    row = (uint64_t)r.stride_t * es;
+    width = ((uint64_t)(H - 1) * r.stride_h + D) * es;
+    all = (uint64_t)(T - 1) * row + width;
+  }
+  Extent(const void* p, uint64_t bytes) : at((uintptr_t)p), row(0), width(bytes), all(p != nullptr ? bytes : 0) {}
+  bool meets(const Extent& o) const {
+    if (all == 0 || o.all == 0 || at >= o.at + o.all || o.at >= at + all) return false;
+    if (row == 0 || row != o.row || width > row || o.width > row) return true;
+    // rows side by side: where the other's begin, seen from this one's, modulo a row
+    const uint64_t d = o.at >= at ? (o.at - at) % row : (row - (at - o.at) % row) % row;
+    return d < width || d + o.width > row;
+  }
+};
+
+}  // namespace
+}  // namespace memra
+
+using namespace memra;
+
+extern "C" memra_status memra_qk_norm_rope(
+    const void* q, const void* k, int32_t dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+    int64_t q_stride_t, int64_t q_stride_h, int64_t k_stride_t, int64_t k_stride_h,
+    const float* q_weight, const float* k_weight, float eps, const int32_t* positions,
+    const double* inv_freq, int64_t R, int32_t layout, void* q_out, int32_t q_out_dtype,
+    int64_t q_out_stride_t, int64_t q_out_stride_h, void* k_out, int32_t k_out_dtype,
+    int64_t k_out_stride_t, int64_t k_out_stride_h, cudaStream_t stream) {
+  if (T < 0 || Hq < 0 || Hkv < 0 || R < 0 || R % 8 != 0) return MEMRA_ERR_INVALID_ARG;
+  for (const int32_t t : {dtype, q_out_dtype, k_out_dtype})
+    if (t != MEMRA_BF16 && t != MEMRA_F32) return MEMRA_ERR_INVALID_ARG;
+  for (const int64_t s : {q_stride_t, q_stride_h, k_stride_t, k_stride_h, q_out_stride_t,
+                          q_out_stride_h, k_out_stride_t, k_out_stride_h})
+    if (s < 0) return MEMRA_ERR_INVALID_ARG;
+  if (layout != MEMRA_ROPE_HALVES && layout != MEMRA_ROPE_PAIRS) return MEMRA_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f || eps < 0.0f) || eps > 3e38f) return MEMRA_ERR_INVALID_ARG;
+  if (eps < 0.0f && (q_weight || k_weight)) return MEMRA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128 && D != 256) return MEMRA_ERR_UNSUPPORTED;
+  if (R > D) return MEMRA_ERR_INVALID_ARG;
+  if (T > INT32_MAX || Hq > 65535 || Hkv > 65535 || Hq + Hkv > 65535) return MEMRA_ERR_UNSUPPORTED;
+  // every offset in bytes stays far inside an int64
+  for (const int64_t s : {q_stride_t, k_stride_t, q_out_stride_t, k_out_stride_t})
+    if (s > ((int64_t)1 << 56) / (T + 1)) return MEMRA_ERR_UNSUPPORTED;
+  for (const int64_t s : {q_stride_h, k_stride_h, q_out_stride_h, k_out_stride_h})
+    if (s > ((int64_t)1 << 56) / 65536) return MEMRA_ERR_UNSUPPORTED;
+  if (T == 0 || Hq + Hkv == 0) return MEMRA_OK;
+  if ((Hq > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out))) return MEMRA_ERR_INVALID_ARG;
+  if (R > 0 && (!positions || !inv_freq)) return MEMRA_ERR_INVALID_ARG;
+  RopeArgs a;
+  a.q = {const_cast<void*>(q), q_stride_t, q_stride_h, dtype == MEMRA_BF16};
+  a.k = {const_cast<void*>(k), k_stride_t, k_stride_h, dtype == MEMRA_BF16};
+  a.q_out = {q_out, q_out_stride_t, q_out_stride_h, q_out_dtype == MEMRA_BF16};
+  a.k_out = {k_out, k_out_stride_t, k_out_stride_h, k_out_dtype == MEMRA_BF16};
+  const Rows* rows[] = {&a.q, &a.k, &a.q_out, &a.k_out};
+  const int64_t heads[] = {Hq, Hkv, Hq, Hkv};
+  for (int i = 0; i < 4; ++i) {
+    const int64_t per16 = rows[i]->bf16 ? 8 : 4;
+    if (heads[i] > 0 && (!aligned(rows[i]->at, 16) || rows[i]->stride_t % per16 != 0 || rows[i]->stride_h % per16 != 0))
+      return MEMRA_ERR_ALIGNMENT;
+  }
+  if (!aligned(q_weight, 4) || !aligned(k_weight, 4) || !aligned(positions, 4) || !aligned(inv_freq, 8))
+    return MEMRA_ERR_ALIGNMENT;
+  if (!apart(a.q_out, T, Hq, D) || !apart(a.k_out, T, Hkv, D)) return MEMRA_ERR_INVALID_ARG;
+  const Extent in[] = {Extent(a.q, T, Hq, D), Extent(a.k, T, Hkv, D), Extent(q_weight, 4 * D), Extent(k_weight, 4 * D),
+                       Extent(positions, 4 * T), Extent(inv_freq, 4 * R)};
+  const Extent out[] = {Extent(a.q_out, T, Hq, D), Extent(a.k_out, T, Hkv, D)};
+  for (int i = 0; i < 2; ++i) {
+    for (int j = 0; j < 6; ++j) {
+      const Rows &x = *rows[i], &y = *rows[2 + i];
+      const bool in_place = i == j && x.at == y.at && x.stride_t == y.stride_t && x.stride_h == y.stride_h && x.bf16 == y.bf16;
+      if (!in_place && out[i].meets(in[j])) return MEMRA_ERR_INVALID_ARG;
+    }
+  }
+  if (out[0].meets(out[1])) return MEMRA_ERR_INVALID_ARG;
+  DeviceInfo info;
+  if (!device_info(&info)) return MEMRA_ERR_CUDA;
+  a.T = T;
+  a.Hq = (int)Hq;
+  a.heads = (int)(Hq + Hkv);
+  a.R = (int)R;
+  a.pairs = layout == MEMRA_ROPE_PAIRS;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  const cudaError_t e = dtype == MEMRA_BF16 ? launch_rope<uint16_t>(a, D, info.sms, stream)
+                                            : launch_rope<float>(a, D, info.sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return MEMRA_OK;
+}

@@ -648,6 +648,168 @@ memra_status memra_moe_route(const void* logits, int32_t dtype, int64_t T, int64
                              float* gate_w, cudaStream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Around the cache and the LM head: norm and rotation of queries and keys before the
+ * write, pages after they are taken, and the log probabilities of tokens.  Conventions of
+ * the cache's calls hold (*dev_status, waiting for the preceding kernel).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Norm of each head's row and rotation by its position, queries and keys in one pass.
+ *   q [T][Hq][D], k [T][Hkv][D] of `dtype` (bf16 bits or fp32): row t, head h at
+ *   t * stride_t + h * stride_h elements, the D values consecutive; D 64, 128 or 256.  Hq or
+ *   Hkv may be 0 (its pointers NULL); Hq + Hkv <= 65535.
+ *   norm (eps >= 0): n_i = x_i * w_i / sqrt(sum_j x_j^2 / D + eps), w fp32 [D] (NULL: ones);
+ *   a row whose sum + eps is 0 gives zeros.  eps < 0: no norm (weights must be NULL).
+ *   rotation of the first R values (R a multiple of 8, 0 to D), inv_freq fp64 [R/2], by the
+ *   angle positions[t] * inv_freq[j]: (a, b) -> (a cos - b sin, b cos + a sin) with
+ *     MEMRA_ROPE_HALVES  a = n_j, b = n_(j + R/2);   MEMRA_ROPE_PAIRS  a = n_2j, b = n_(2j+1).
+ *   positions int32 [T]: below 0 a row is no token's, its outputs are zeros and its inputs
+ *   are not used.  NULL (with R == 0 only): every row is a token's.
+ *   q_out, k_out: each of its own dtype and strides.
+ * Arithmetic is fp32 with one rounding to the output type.  The angle is taken as a fraction
+ * of a turn in 64-bit fixed point (inv_freq / 2 pi to 2^-64, times the position modulo one
+ * turn), so far positions lose nothing: it is off by position * inv_freq * 2^-52 + 2^-22 at
+ * most.  |x| <= 2^60 with a norm; without eps, |x| below 2^-70 counts as 0.
+ * Alignment: q, k and outputs 16 bytes, strides keep them; inv_freq 8, else 4.
+ * Outputs may be their own inputs (same address, strides and dtype); apart from that they
+ * overlap nothing, their own other rows neither (MEMRA_ERR_INVALID_ARG), but rows may lie side by side with equal stride_t
+ * in bytes, as columns of the fused projection's rows do.
+ */
+typedef enum memra_rope { MEMRA_ROPE_HALVES = 0, MEMRA_ROPE_PAIRS = 1 } memra_rope;
+memra_status memra_qk_norm_rope(const void* q, const void* k, int32_t dtype, int64_t T, int64_t Hq,
+                                int64_t Hkv, int64_t D, int64_t q_stride_t, int64_t q_stride_h,
+                                int64_t k_stride_t, int64_t k_stride_h, const float* q_weight,
+                                const float* k_weight, float eps, const int32_t* positions,
+                                const double* inv_freq, int64_t R, int32_t layout, void* q_out,
+                                int32_t q_out_dtype, int64_t q_out_stride_t,
+                                int64_t q_out_stride_h, void* k_out, int32_t k_out_dtype,
+                                int64_t k_out_stride_t, int64_t k_out_stride_h,
+                                cudaStream_t stream);
+
+/*
+ * Pages that several sequences hold.  refs int32 [n_pages] counts for every page its holders
+ * beyond the first: 0 for a page that one sequence holds or none, so pages that memra_kv_plan
+ * takes need no change of it; zeroed once at first.  All calls that change it agree on it: a
+ * page is held once for each entry of a block table among the first ceil(len / P) of a
+ * sequence.  Lengths below 0 count as 0 and lengths above max_pages * P are cut to that;
+ * entries outside [0, n_pages) are no pages (each: status 1).  P as for the cache;
+ * B * max_pages <= 2^30.  What a call writes must not overlap anything else but as said
+ * (MEMRA_ERR_INVALID_ARG).
+ *
+ * memra_kv_fork: C new sequences that share the pages of old ones.  Row r of lens_out,
+ * table_out [C][max_pages] holds the first min(lens[parents[r]], prefix_lens[r]) tokens of
+ * sequence parents[r] (int32 [C]; prefix_lens int32 [C], NULL: all of them; below 0 counts as
+ * 0): its entries of their pages, whose refs grow by one each, and -1 behind them.  A parent of
+ * -1, or outside [0, B) (status 1), gives an empty sequence.  A parent may be named any
+ * number of times.  The last page is shared too, full or not: see memra_kv_unshare.
+ */
+memra_status memra_kv_fork(const int32_t* parents, const int32_t* prefix_lens, int64_t C,
+                           const int32_t* lens, const int32_t* block_table, int64_t B,
+                           int64_t max_pages, int64_t page_size, int32_t* refs, int64_t n_pages,
+                           int32_t* lens_out, int32_t* table_out, int32_t* dev_status,
+                           cudaStream_t stream);
+
+/*
+ * Copy on write, before a step's memra_kv_plan: sequences that are about to write into a page
+ * that others hold too (new_lens[b] > 0 and lens[b] no multiple of P) take a page of their own
+ * for it.  Request after request: where refs[p] of its last page p is above 0 at its turn, it
+ * takes the next free page f (from *free_head on, as in memra_kv_plan), refs[p] falls by one,
+ * its table entry becomes f, and src[b] = p, dst[b] = f, tokens[b] = lens[b] % P say what
+ * memra_kv_copy_pages has to copy in every layer; src = dst = -1, tokens = 0 for all others.
+ * The last of a page's holders keeps it.  When the free list ends, this and every later
+ * request that needs a page stays as it is (status 4) and its new_lens_out is 0; else
+ * new_lens_out[b] = new_lens[b] (below 0: 0, status 1).
+ * src, dst, tokens, new_lens_out int32 [B]; new_lens_out may be new_lens, free_head_out may be
+ * free_head.
+ */
+memra_status memra_kv_unshare(const int32_t* lens, const int32_t* new_lens, int64_t B,
+                              int64_t page_size, int32_t* refs, int64_t n_pages,
+                              const int32_t* free_pages, int64_t n_free,
+                              const int32_t* free_head, int32_t* block_table, int64_t max_pages,
+                              int32_t* new_lens_out, int32_t* src, int32_t* dst, int32_t* tokens,
+                              int32_t* free_head_out, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Copy the first tokens[i] tokens (NULL: the whole page) of page src[i] to page dst[i], i < N,
+ * in every layer: codes, and the scales of the blocks that they begin, bit for bit; what is
+ * behind them in dst stays.  layers: HOST array of n_layers caches of the same sizes.  An
+ * entry with a page of -1, or with src == dst, copies nothing; one with a page outside
+ * [0, n_pages), or tokens outside [0, P], neither (status 1).  No page may be the dst of two
+ * entries, or of one and the src of another.
+ */
+typedef struct memra_kv_layer {
+  int8_t* kq;
+  float* kd;
+  int8_t* vq;
+  float* vd;
+} memra_kv_layer;
+memra_status memra_kv_copy_pages(const int32_t* src, const int32_t* dst, const int32_t* tokens,
+                                 int64_t N, const memra_kv_layer* layers, int64_t n_layers,
+                                 int64_t n_pages, int64_t Hkv, int64_t page_size, int64_t D,
+                                 int64_t block, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Cut sequences to their first keep_lens[b] tokens (int32 [B], NULL: none; a sequence with no
+ * more than that stays as it is) and give up the pages behind them: each entry takes one
+ * from refs of its page, and a page whose last holder goes returns to the free list.  The
+ * entry that lets a page go is the last one of it in the order of (request, page of the
+ * request); in that order the n pages that go are written to free_pages[*free_head - n] up to
+ * free_pages[*free_head - 1], and *free_head_out = *free_head - n: what was taken last is
+ * taken first again, in the same order.  Pages that do not fit below *free_head are lost (the
+ * first ones; status 4); a page given up more often than it is held goes once (status 1).
+ * keep_lens below 0 counts as 0 (status 1).  lens_out may be lens, free_head_out free_head.
+ * block_table is only read: entries behind a sequence's pages are not used.
+ */
+memra_status memra_kv_release(const int32_t* lens, const int32_t* keep_lens, int64_t B,
+                              int64_t page_size, const int32_t* block_table, int64_t max_pages,
+                              int32_t* refs, int64_t n_pages, int32_t* free_pages,
+                              int64_t n_free, const int32_t* free_head, int32_t* lens_out,
+                              int32_t* free_head_out, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Renumber pages so that the U pages that sequences hold are pages 0 .. U - 1 (the pool can
+ * then be cut behind them): the highest page in use becomes the lowest one that is not, and
+ * so on until they meet; pages below U keep their numbers.
+ *   table_out [B][max_pages]: the renumbered entries, -1 behind a sequence's pages (and for
+ *   entries that are no pages); may be block_table.
+ *   src, dst int32 [n_pages / 2]: the moves for memra_kv_copy_pages, in that order, -1 behind
+ *   them.  refs_out, free_out int32 [n_pages]: holders - 1 of each page, counted from the
+ *   table (0 for the others), and a free list with free_out[i] = i and position
+ *   *free_head_out = U.
+ * Every sequence has to be in the table: what no sequence holds is free afterwards.
+ */
+memra_status memra_kv_compact(const int32_t* lens, const int32_t* block_table, int64_t B,
+                              int64_t max_pages, int64_t page_size, int64_t n_pages,
+                              int32_t* table_out, int32_t* refs_out, int32_t* free_out,
+                              int32_t* src, int32_t* dst, int32_t* free_head_out,
+                              int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Log probabilities from logits [T][V] of `dtype` (row t at t * stride_t elements), in one
+ * pass over them.  With m = max x and Z = sum_v exp(x_v - m):
+ *   logprobs[t]  = (x_token - m) - ln Z for token tokens[t] (int32 [T]); -1: no token, 0; any
+ *                  other number outside [0, V): -inf (status 1);
+ *   entropy[t]   = ln Z - sum_v exp(x_v - m) (x_v - m) / Z  (fp32 [T], NULL: not wanted);
+ *   top_ids, top_logprobs [T][top_n]: the top_n largest x, descending, ties to the lowest
+ *                  index (-0 equals 0), and their log probabilities.
+ * tokens and logprobs may be NULL together.  Sums are fp32 without the largest term (ln Z =
+ * log1p of the others), so log probabilities near 0 keep their digits.
+ * A logit of -inf or NaN masks a token (probability 0); +inf counts as the largest finite
+ * value.  Where fewer than top_n tokens are left, the remaining slots hold the lowest indexes
+ * not yet taken, with -inf.  A row with no token left has entropy 0 and -inf everywhere.
+ * V <= MEMRA_MAX_VOCAB, top_n <= min(MEMRA_MAX_TOP_LOGPROBS, V).  logits are aligned to
+ * their type only; rows that start on 16 bytes are no quicker than others.
+ */
+#define MEMRA_MAX_VOCAB 1048576
+#define MEMRA_MAX_TOP_LOGPROBS 32
+memra_status memra_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t V,
+                                  int64_t stride_t, const int32_t* tokens, int64_t top_n,
+                                  float* logprobs, float* entropy, int32_t* top_ids,
+                                  float* top_logprobs, int32_t* dev_status, cudaStream_t stream);
+
+/*
  * Exact int32 block sums s[m][n][b] = sum_{i<32} wq[n][32b+i] * xq[m][32b+i],
  * computed with the same dp4a block-dot routine as the product kernels.  For
  * verification of the integer stage.  s: int32 [M][N][K/32], 4-byte aligned.
