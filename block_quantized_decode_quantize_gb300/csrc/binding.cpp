@@ -104,6 +104,17 @@ PyObject* pack(std::initializer_list<Tensor> ts) {
   return out;
 }
 
+// A contiguous part of a buffer of 4-byte elements, from element `at` on, as a tensor that shares
+// its storage: what views of it would be, at a fraction of their cost.
+Tensor part(const Tensor& buf, int64_t at, at::IntArrayRef shape, at::ScalarType type) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()), buf.key_set(),
+                                                      c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(buf.storage_offset() + at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+Tensor part(const Tensor& buf, int64_t at, at::IntArrayRef shape) { return part(buf, at, shape, buf.scalar_type()); }
+
 struct Cache {
   int8_t *kq, *vq;
   float *kd, *vd;
@@ -295,23 +306,6 @@ inline bool optional(PyObject* o, int dev, at::ScalarType type, at::IntArrayRef 
   return dense(*t, type, shape);
 }
 
-// An int32 word that a call writes: the one given, or the last of `parts`.
-inline PyObject* pack_with(std::initializer_list<Tensor> ts, PyObject* given, const Tensor& own) {
-  std::vector<Tensor> all(ts);
-  all.push_back(given == Py_None ? own : THPVariable_Unpack(given));
-  PyObject* out = PyTuple_New((Py_ssize_t)all.size());
-  if (out == nullptr) return nullptr;
-  for (size_t i = 0; i < all.size(); ++i) {
-    PyObject* o = THPVariable_Wrap(all[i]);
-    if (o == nullptr) {
-      Py_DECREF(out);
-      return nullptr;
-    }
-    PyTuple_SET_ITEM(out, (Py_ssize_t)i, o);
-  }
-  return out;
-}
-
 // Rows that a call writes: those given, or new ones like x, of the C library's dtype code `want` (-1:
 // the input's).
 inline bool out_rows(PyObject* o, int* dev, const Tensor* x, int64_t want, int32_t code, Tensor* t, int32_t* type) {
@@ -397,12 +391,12 @@ PyObject* fork(PyObject*, PyObject* const* o, Py_ssize_t n) {
   const int64_t C = parents->size(0);
   if (!optional(o[5], dev, at::kInt, {C}, &prefix)) Py_RETURN_NONE;
   at::AutoDispatchBelowADInplaceOrView guard;
-  const Tensor lens = at::empty({C}, on(dev, at::kInt)), table = at::empty({C, s.max_pages}, on(dev, at::kInt));
+  const Tensor buf = at::empty({C + C * s.max_pages}, on(dev, at::kInt));
+  int32_t* at = data<int32_t>(&buf);
   if (memra_kv_fork(data<int32_t>(parents), data<int32_t>(prefix), C, s.lens, s.table, s.B, s.max_pages, page,
-                    data<int32_t>(refs), refs->size(0), data<int32_t>(&lens), data<int32_t>(&table), status,
-                    stream(dev)) != MEMRA_OK)
+                    data<int32_t>(refs), refs->size(0), at, at + C, status, stream(dev)) != MEMRA_OK)
     Py_RETURN_NONE;
-  return pack({lens, table});
+  return pack({part(buf, 0, {C}), part(buf, C, {C, s.max_pages})});
   END_HANDLE_TH_ERRORS
 }
 
@@ -422,15 +416,14 @@ PyObject* unshare(PyObject*, PyObject* const* o, Py_ssize_t n) {
   if (!dense(add, at::kInt, {s.B}) || !ints(refs, 1) || !ints(free, 1)) Py_RETURN_NONE;
   at::AutoDispatchBelowADInplaceOrView guard;
   const Tensor buf = at::empty({4 * s.B + 1}, on(dev, at::kInt));
-  const int64_t sizes[5] = {s.B, s.B, s.B, s.B, 1};
-  const std::vector<Tensor> part = buf.split_with_sizes(sizes);
-  if (head_out == nullptr) head_out = data<int32_t>(&part[4]);
+  int32_t* at = data<int32_t>(&buf);
   if (memra_kv_unshare(s.lens, data<int32_t>(add), s.B, page, data<int32_t>(refs), refs->size(0),
-                       data<int32_t>(free), free->size(0), head, s.table, s.max_pages,
-                       data<int32_t>(&part[0]), data<int32_t>(&part[1]), data<int32_t>(&part[2]),
-                       data<int32_t>(&part[3]), head_out, status, stream(dev)) != MEMRA_OK)
+                       data<int32_t>(free), free->size(0), head, s.table, s.max_pages, at, at + s.B,
+                       at + 2 * s.B, at + 3 * s.B, head_out != nullptr ? head_out : at + 4 * s.B, status,
+                       stream(dev)) != MEMRA_OK)
     Py_RETURN_NONE;
-  return pack_with({part[0], part[1], part[2], part[3]}, o[7], part[4]);
+  return pack({part(buf, 0, {s.B}), part(buf, s.B, {s.B}), part(buf, 2 * s.B, {s.B}), part(buf, 3 * s.B, {s.B}),
+               o[7] == Py_None ? part(buf, 4 * s.B, {1}) : THPVariable_Unpack(o[7])});
   END_HANDLE_TH_ERRORS
 }
 
@@ -482,13 +475,13 @@ PyObject* release(PyObject*, PyObject* const* o, Py_ssize_t n) {
   const Tensor *refs = tensor(o[3], &dev), *free = tensor(o[4], &dev), *keep;
   if (!ints(refs, 1) || !ints(free, 1) || !optional(o[6], dev, at::kInt, {s.B}, &keep)) Py_RETURN_NONE;
   at::AutoDispatchBelowADInplaceOrView guard;
-  const Tensor lens = at::empty({s.B}, on(dev, at::kInt)), own = at::empty({1}, on(dev, at::kInt));
-  if (head_out == nullptr) head_out = data<int32_t>(&own);
+  const Tensor buf = at::empty({s.B + 1}, on(dev, at::kInt));
+  int32_t* at = data<int32_t>(&buf);
   if (memra_kv_release(s.lens, data<int32_t>(keep), s.B, page, s.table, s.max_pages, data<int32_t>(refs),
-                       refs->size(0), data<int32_t>(free), free->size(0), head, data<int32_t>(&lens),
-                       head_out, status, stream(dev)) != MEMRA_OK)
+                       refs->size(0), data<int32_t>(free), free->size(0), head, at,
+                       head_out != nullptr ? head_out : at + s.B, status, stream(dev)) != MEMRA_OK)
     Py_RETURN_NONE;
-  return pack_with({lens}, o[7], own);
+  return pack({part(buf, 0, {s.B}), o[7] == Py_None ? part(buf, s.B, {1}) : THPVariable_Unpack(o[7])});
   END_HANDLE_TH_ERRORS
 }
 
@@ -504,15 +497,19 @@ PyObject* compact(PyObject*, PyObject* const* o, Py_ssize_t n) {
       pages > INT32_MAX || !word(o[4], dev, &status) || !current(dev))
     Py_RETURN_NONE;
   at::AutoDispatchBelowADInplaceOrView guard;
-  const Tensor table = at::empty({s.B, s.max_pages}, on(dev, at::kInt));
-  const Tensor buf = at::empty({2 * pages + 2 * (pages / 2) + 1}, on(dev, at::kInt));
-  const int64_t sizes[5] = {pages, pages, pages / 2, pages / 2, 1};
-  const std::vector<Tensor> part = buf.split_with_sizes(sizes);
-  if (memra_kv_compact(s.lens, s.table, s.B, s.max_pages, page, pages, data<int32_t>(&table),
-                       data<int32_t>(&part[0]), data<int32_t>(&part[1]), data<int32_t>(&part[2]),
-                       data<int32_t>(&part[3]), data<int32_t>(&part[4]), status, stream(dev)) != MEMRA_OK)
+  const int64_t cells = s.B * s.max_pages, moves = pages / 2;
+  const Tensor buf = at::empty({cells + 2 * pages + 2 * moves + 1}, on(dev, at::kInt));
+  int32_t *table = data<int32_t>(&buf), *refs = table + cells, *free = refs + pages, *src = free + pages;
+  if (memra_kv_compact(s.lens, s.table, s.B, s.max_pages, page, pages, table, refs, free, src, src + moves,
+                       src + 2 * moves, status, stream(dev)) != MEMRA_OK)
     Py_RETURN_NONE;
-  return pack({table, part[0], part[1], part[2], part[3], part[4]});
+  int64_t at = cells;
+  auto next = [&](int64_t n) {
+    at += n;
+    return part(buf, at - n, {n});
+  };
+  const Tensor r = next(pages), f = next(pages), from = next(moves), to = next(moves), head = next(1);
+  return pack({part(buf, 0, {s.B, s.max_pages}), r, f, from, to, head});
   END_HANDLE_TH_ERRORS
 }
 
@@ -531,14 +528,15 @@ PyObject* logprobs(PyObject*, PyObject* const* o, Py_ssize_t n) {
   const Tensor* tokens;
   if (!optional(o[1], dev, at::kInt, {T}, &tokens)) Py_RETURN_NONE;
   at::AutoDispatchBelowADInplaceOrView guard;
-  const Tensor two = at::empty({2, T}, on(dev, at::kFloat));
-  const std::vector<Tensor> part = two.unbind(0);
-  const Tensor ids = at::empty({T, top}, on(dev, at::kInt)), best = at::empty({T, top}, on(dev, at::kFloat));
+  const int64_t ids_at = 2 * T, best_at = ids_at + T * top;
+  const Tensor buf = at::empty({best_at + T * top}, on(dev, at::kFloat));
+  float* at = data<float>(&buf);
   if (memra_token_logprobs(data<void>(x), code, T, V, T > 1 ? x->stride(0) : V, data<int32_t>(tokens), top,
-                           tokens != nullptr ? data<float>(&part[0]) : nullptr, data<float>(&part[1]),
-                           data<int32_t>(&ids), data<float>(&best), status, stream(dev)) != MEMRA_OK)
+                           tokens != nullptr ? at : nullptr, at + T, reinterpret_cast<int32_t*>(at + ids_at),
+                           at + best_at, status, stream(dev)) != MEMRA_OK)
     Py_RETURN_NONE;
-  return pack({tokens != nullptr ? part[0] : Tensor(), part[1], ids, best});
+  return pack({tokens != nullptr ? part(buf, 0, {T}) : Tensor(), part(buf, T, {T}), part(buf, ids_at, {T, top}, at::kInt),
+               part(buf, best_at, {T, top})});
   END_HANDLE_TH_ERRORS
 }
 

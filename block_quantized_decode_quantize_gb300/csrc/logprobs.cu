@@ -1,16 +1,23 @@
 // Log probabilities of tokens from a row of logits, its entropy and its largest entries.
 //
-// One pass over the logits: each warp keeps a running maximum m, its lanes z = sum e^(x - m)
-// and s = sum e^(x - m) (x - m), and rescales them when m grows.  The largest element itself
-// stays outside the sums (its term is 1 and 0), so that ln Z = log1p(z) and log probabilities
-// near 0 keep their digits.  The vocabulary is cut into segments; a segment's maximum goes to
-// shared memory as the pass goes by.  The top_n-th largest of 32 groups of these maxima is a
-// bound that top_n elements reach, so only segments whose maximum reaches it are read once
-// more (from L2), and the few elements at or above it are ranked by counting.
+// One pass over the logits.  Each lane sums z = sum 2^u and s = sum 2^u u over its elements, with
+// u = x log2 e - M, M a whole number next to the maximum of its warp's first blocks, so that u is
+// one rounding and the sums of other warps differ by a power of two.  What exceeds that maximum
+// makes terms above 1, which fp32 holds up to 2^127; a warp whose sums are not finite takes its
+// blocks again, with care.  The row is cut into segments whose maxima go to shared memory as the
+// pass goes by.
 //
-// A row is taken by the CTAs of a cluster, which leave maxima and sums in the first one's
-// shared memory: with few rows many SMs share the read of one.
+// Then the row's sums are joined, and a number is found that the maxima of top_n groups of
+// segments reach, a bound that top_n elements reach: only segments whose maximum reaches it are
+// read again (from L2), and the few elements at or above it are ranked by counting.  Relative to
+// its largest term, Z is 1 + rest.  Where the rest is below a quarter, the elements of the lane
+// that met the largest are summed again without it, so that ln Z = log1p(rest) keeps the digits
+// of log probabilities near 0.
+//
+// A row is taken by one CTA, or, with few rows, by the CTAs of a cluster, which leave maxima and
+// sums in the first one's shared memory.
 #include <cooperative_groups.h>
+#include <cuda_bf16.h>
 
 #include "common.cuh"
 
@@ -21,16 +28,25 @@ namespace cg = cooperative_groups;
 
 constexpr int kBlock = 256;         // elements a warp looks at together: 8 a lane
 constexpr int kMost = 512;          // candidates that are ranked by counting
-constexpr int kFineVocab = 16384; // see memra_token_logprobs
-constexpr int kMaxWarps = 512;      // of a row: 16 CTAs of 32
-constexpr float kLog2e = 1.44269504088896341f;
+constexpr int kFineVocab = 8192;    // see logprob_kernel
+constexpr int kMaxWarps = 256;      // of a row: 16 CTAs of 16
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 constexpr float kLargest = 3.402823466e38f;
-constexpr float kFloor = -150.0f;   // e^x is 0 in fp32 below
+constexpr float kFloor = -160.0f;   // 2^u is 0 in fp32 below
+
+struct alignas(16) Part {  // of a warp
+  float m, of;        // its maximum, and what its sums refer to: Reference(of)
+  float z, s;         // of all lanes but one
+  float z_lane, s_lane;
+  int lane;           // that one, which has met m
+  int pad;
+};
 
 struct LogprobArgs {
   const void* logits;
   int64_t T, stride_t;
-  int V, top_n, fine, segments;     // fine: a segment is 16 bytes of the row, else a block; at most so many
+  int V, top_n;
+  int segments;             // of a row, at most
   const int32_t* tokens;
   float *logprobs, *entropy, *top_logprobs;
   int32_t *top_ids, *status;
@@ -69,6 +85,16 @@ __device__ __forceinline__ float element<float>(const float* p) { return *p; }
 template <>
 __device__ __forceinline__ float element<uint16_t>(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
+// An address in the shared memory of the cluster's first CTA, and a store there.
+__device__ __forceinline__ uint32_t mapped(const void* p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
+  return r;
+}
+__device__ __forceinline__ void put(uint32_t at, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+
 // A row seen from the 16-byte boundary at or before it: element i of the row is place
 // i + shift, and block b holds places 256 b ..  A lane's 8 of them: bf16 16 bytes, fp32 twice
 // 16 bytes, 512 apart.
@@ -84,208 +110,465 @@ struct Row {
     end = V + shift;
   }
   __device__ __forceinline__ int blocks() const { return (end + kBlock - 1) / kBlock; }
+  // blocks that lie within the row: first_whole .. end_whole - 1
+  __device__ __forceinline__ int first_whole() const { return shift > 0 ? 1 : 0; }
+  __device__ __forceinline__ int end_whole() const { return end / kBlock; }
   // place of the lane's value i of a block
   static __device__ __forceinline__ int place(int b, int lane, int i) {
     return b * kBlock + (kWide ? 4 * lane + (i & 3) + 32 * (i & 4) : 8 * lane + i);
   }
-  __device__ __forceinline__ bool whole(int b) const { return b * kBlock >= shift && (b + 1) * kBlock <= end; }
+  __device__ __forceinline__ const uint4* at(int b, int lane) const {
+    return reinterpret_cast<const uint4*>(base + (int64_t)b * kBlock) + lane;
+  }
   struct Raw {
-    uint4 u[kWide ? 2 : 1];
+    uint4 u[kPieces];
   };
-  __device__ __forceinline__ Raw fetch(int b, int lane) const {  // of a whole block
+  __device__ __forceinline__ Raw fetch_whole(int b, int lane) const {
     Raw r;
-    const uint4* p = reinterpret_cast<const uint4*>(base + (int64_t)b * kBlock) + lane;
-    r.u[0] = __ldcs(p);
-    if (kWide) r.u[kWide ? 1 : 0] = __ldcs(p + 32);
+#pragma unroll
+    for (int h = 0; h < kPieces; ++h) r.u[h] = __ldcg(at(b, lane) + 32 * h);
+    return r;
+  }
+  // any block's values, -inf for places outside the row
+  __device__ __forceinline__ Raw fetch(int b, int lane) const {
+    if (b >= first_whole() && b < end_whole()) return fetch_whole(b, lane);
+    Raw r;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = place(b, lane, i);
+      w[i] = __float_as_uint(p >= shift && p < end ? element<T>(base + p) : -inf());
+    }
+    if (kWide) {
+      r.u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      r.u[kPieces - 1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+      r.u[0] = make_uint4((w[0] >> 16) | w[1], (w[2] >> 16) | w[3], (w[4] >> 16) | w[5], (w[6] >> 16) | w[7]);
+    }
     return r;
   }
   static __device__ __forceinline__ void unpack(const Raw& r, float* v) {
-    if (kWide) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4& u = r.u[kWide ? h : 0];
-        v[4 * h] = __uint_as_float(u.x); v[4 * h + 1] = __uint_as_float(u.y);
-        v[4 * h + 2] = __uint_as_float(u.z); v[4 * h + 3] = __uint_as_float(u.w);
-      }
-    } else {
-      const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
+    for (int h = 0; h < kPieces; ++h) {
+      const uint32_t w[4] = {r.u[h].x, r.u[h].y, r.u[h].z, r.u[h].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        if (kWide) {
+          v[4 * h + i] = __uint_as_float(w[i]);
+        } else {
+          v[2 * i] = __uint_as_float(w[i] << 16);
+          v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
       }
     }
   }
-  // any block, -inf for places outside the row
-  __device__ __forceinline__ void load(int b, int lane, float* v) const {
-    if (whole(b)) {
-      unpack(fetch(b, lane), v);
+  // the largest of 16 bytes' values, exactly (NaN only where nothing else is there)
+  static __device__ __forceinline__ float largest_of(const uint4& u) {
+    if (kWide) return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+    const uint32_t m = most2(most2(u.x, u.y), most2(u.z, u.w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  static __device__ __forceinline__ float largest(const Raw& r) {
+    return kWide ? fmaxf(largest_of(r.u[0]), largest_of(r.u[kPieces - 1])) : largest_of(r.u[0]);
+  }
+  static __device__ __forceinline__ uint32_t most2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 x = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&x);
+  }
+};
+
+// What a maximum's sums refer to: 2^(m log2 e - delta), m log2 e - delta a whole number M, or
+// m log2 e itself (delta 0) where that is too large to have neighbours next to it.
+struct Reference {
+  float m, delta, M;
+  bool far;
+  __device__ __forceinline__ explicit Reference(float max) : m(max) {
+    far = !(fabsf(m) < 1048576.0f);
+    M = ceilf(m * kLog2e);
+    delta = far ? 0.0f : fmaf(m, kLog2e, -M);
+  }
+  // log2 of x's term; clamped where it is 0
+  __device__ __forceinline__ float term(float x) const {
+    return fmaxf(far ? (x - m) * kLog2e : fmaf(x, kLog2e, -M), kFloor);
+  }
+  // log2 of what relates sums of another reference to this one
+  __device__ __forceinline__ float from(const Reference& o) const {
+    return fmaxf(far || o.far ? (o.m - m) * kLog2e - o.delta + delta : o.M - M, kFloor);
+  }
+};
+
+// The lane's part of a warp's sums, in two halves.
+struct Sums {
+  float2 z = {0.0f, 0.0f}, s = {0.0f, 0.0f};
+  // 8 values, M as in Reference.  What is infinite, no number or too large to be a term makes s no
+  // finite number; with kClamp, only what is too large does.
+  template <bool kClamp>
+  __device__ __forceinline__ void add(const float* v, float M) {
+    const float2 minus = {-M, -M}, scale = {kLog2e, kLog2e};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      float2 u = __ffma2_rn(make_float2(v[i], v[i + 1]), scale, minus);
+      if (kClamp) u = make_float2(fmaxf(u.x, kFloor), fmaxf(u.y, kFloor));
+      const float2 e = {exp2_approx(u.x), exp2_approx(u.y)};
+      z = __fadd2_rn(z, e);
+      s = __ffma2_rn(e, u, s);
+    }
+  }
+  __device__ __forceinline__ void add_one(float u) {
+    const float e = exp2_approx(u);
+    z.x += e;
+    s.x = fmaf(e, u, s.x);
+  }
+  __device__ __forceinline__ bool sound() const { return fabsf(s.x + s.y) < inf(); }
+};
+
+// The bound: a number that the maxima of top_n segments reach, by bisection between the least
+// and the largest of the maxima of 128 groups of segments, until at most 1.25 top_n + 1 of
+// these reach it: of the values, a few steps for logits as they are, and of their bits, which
+// ends for any.  -inf: fewer than top_n groups have a token left.
+__device__ __forceinline__ float bound_of(const float* seg_max, int segments, int top_n, int lane) {
+  float g[4] = {-inf(), -inf(), -inf(), -inf()};
+  for (int i = lane; i < segments; i += 128) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + 32 * j < segments) g[j] = fmaxf(g[j], seg_max[i + 32 * j]);
+  }
+  float least = inf(), over = -inf();
+  int numbers = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (g[j] == -inf()) continue;
+    least = fminf(least, g[j]);
+    over = fmaxf(over, g[j]);
+    ++numbers;
+  }
+  if ((int)__reduce_add_sync(kFullMask, numbers) < top_n) return -inf();
+  float bound = -warp_max(-least);
+  over = warp_max(over);
+  for (int n = 0; n < 44; ++n) {
+    const uint32_t lo = order_of(bound), hi = order_of(over);
+    const float mid = n < 12 ? 0.5f * bound + 0.5f * over : value_of(lo + (hi - lo) / 2);
+    if (!(mid > bound && mid < over)) {
+      if (n < 12) continue;
+      break;
+    }
+    int reach = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) reach += g[j] >= mid ? 1 : 0;
+    reach = (int)__reduce_add_sync(kFullMask, reach);
+    if (reach < top_n) {
+      over = mid;
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int at = place(b, lane, i);
-        v[i] = at >= shift && at < end ? element<T>(base + at) : -inf();
-      }
+      bound = mid;
+      if (4 * reach <= 5 * top_n + 4) break;
     }
+  }
+  return bound;
+}
+
+// Which blocks a warp takes: the whole ones, kAhead neighbours (a batch) at a time, batch after
+// batch in turn with the other warps; those that are left at the ends one by one, the last warps
+// first.
+template <typename T>
+struct Share {
+  static constexpr int kAhead = sizeof(T) == 4 ? 2 : 4;  // 64 bytes a lane
+  int f, batches, mine, left, first_left, warp, warps;
+  __device__ __forceinline__ Share(const Row<T>& row, int w, int n) : warp(w), warps(n) {
+    f = row.first_whole();
+    batches = max(row.end_whole() - f, 0) / kAhead;
+    mine = batches > w ? (batches - w - 1) / n + 1 : 0;
+    const int all_left = row.blocks() - kAhead * batches;
+    first_left = n - 1 - w;
+    left = all_left > first_left ? (all_left - first_left - 1) / n + 1 : 0;
+  }
+  __device__ __forceinline__ int count() const { return mine * kAhead + left; }
+  __device__ __forceinline__ int block(int i) const {  // the warp's i-th
+    if (i < mine * kAhead) return f + kAhead * (warp + i / kAhead * warps) + i % kAhead;
+    const int e = first_left + (i - mine * kAhead) * warps;
+    return e < f ? 0 : kAhead * batches + e;
   }
 };
 
-struct Part {  // of a warp: the row's terms but its largest one, relative to m
-  float m, z, s;
-};
-
-struct Shared {
-  Part part[kMaxWarps];
-  unsigned long long candidate[kMost];
-  int count, listed;
-  float bound, m, log_z;
-  uint32_t taken[MEMRA_MAX_TOP_LOGPROBS];
-};
-
-// The warp's sums take in the 8 values of each lane.  m: the warp's maximum so far, over these too.
-__device__ __forceinline__ void add8(const float* v, float m, float& z, float& s) {
+// The batches of a warp's share.  Two are under way: one arrives while the other is summed.
+template <typename T, bool kClamp>
+__device__ __forceinline__ void sum_batches(const LogprobArgs& a, const Row<T>& row, const Share<T>& share, int lane, bool fine, float* seg_max,
+                                            Sums& sums, float& of, float& lane_top) {
+  using R = Row<T>;
+  constexpr int kAhead = Share<T>::kAhead;
+  typename R::Raw raw[kAhead], next[kAhead];
+  const uint4* p = row.at(share.f + kAhead * share.warp, lane);
+  const int64_t step = share.warps * (kAhead * R::kPieces * 32);
+  float M = 0.0f;
+  auto fetch = [&](typename R::Raw* r) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = fmaxf(v[i] - m, kFloor), e = exp2_approx(d * kLog2e);
-    z += e;
-    s = fmaf(e, d, s);
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int h = 0; h < R::kPieces; ++h) r[j].u[h] = __ldcg(p + (j * R::kPieces + h) * 32);
+    p += step;
+  };
+  auto add = [&](const typename R::Raw* r, int i) {
+    float block_most[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const float mine = R::largest(r[j]);
+      lane_top = fmaxf(lane_top, mine);
+      block_most[j] = warp_max(mine);
+    }
+    const int b0 = share.f + kAhead * (share.warp + i * share.warps);
+    if (fine) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+        for (int h = 0; h < R::kPieces; ++h) seg_max[((b0 + j) * R::kPieces + h) * 32 + lane] = R::largest_of(r[j].u[h]);
+    } else if (a.top_n > 0) {
+      float v = block_most[0];
+#pragma unroll
+      for (int j = 1; j < kAhead; ++j) v = lane == j ? block_most[j] : v;
+      if (lane < kAhead) seg_max[b0 + lane] = v;
+    }
+    if (i == 0) {
+      float most = block_most[0];
+#pragma unroll
+      for (int j = 1; j < kAhead; ++j) most = fmaxf(most, block_most[j]);
+      of = fabsf(most) < inf() ? most : 0.0f;  // (no token left in them: any other number)
+      M = Reference(of).M;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      float x[8];
+      R::unpack(r[j], x);
+      sums.template add<kClamp>(x, M);
+    }
+  };
+  fetch(raw);
+#pragma unroll 1
+  for (int i = 0; i < share.mine; i += 2) {
+    if (i + 1 < share.mine) fetch(next);
+    add(raw, i);
+    if (!kClamp && i == 0 && __any_sync(kFullMask, !sums.sound())) return;  // masked tokens
+    if (i + 1 == share.mine) break;
+    if (i + 2 < share.mine) fetch(raw);
+    add(next, i + 1);
   }
 }
 
-template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads) logprob_kernel(LogprobArgs a) {
-  constexpr int kWarps = kThreads / 32;
-  constexpr int kAhead = sizeof(T) == 4 ? 2 : 4;  // blocks that a warp has under way
-  extern __shared__ float seg_max[];              // [segments], the row's first CTA; then the list of segments to read again
-  __shared__ Shared sh;
-  pdl_launch_dependents();
-  cg::cluster_group cluster = cg::this_cluster();
-  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = blockIdx.x / ranks;
-  pdl_wait();
-  const Row<T> row(static_cast<const T*>(a.logits) + t * a.stride_t, a.V);
-  const int blocks = row.blocks();
-  Shared* first = cluster.map_shared_rank(&sh, 0);
-  float* first_max = cluster.map_shared_rank(seg_max, 0);
-
-  float m = -inf(), z = 0.0f, s = 0.0f;
-  bool met = false;  // the row's first CTA has begun, so its shared memory can be written
-  for (int b0 = rank * kWarps + warp; b0 < blocks; b0 += ranks * kWarps * kAhead) {
-    float v[kAhead][8];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int b = b0 + j * ranks * kWarps;
-      if (b < blocks) {
-        row.load(b, lane, v[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = -inf();
-      }
-    }
-    if (!met) {
-      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-      met = true;
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int b = b0 + j * ranks * kWarps;
-      if (b >= blocks) break;
-      float most = -inf();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[j][i] = sane(v[j][i]);
-        most = fmaxf(most, v[j][i]);
-      }
-      const float block_most = warp_max(most);
-      if (a.top_n > 0) {
-        if (a.fine) {
-#pragma unroll
-          for (int h = 0; h < Row<T>::kPieces; ++h) {
-            float piece = v[j][h * Row<T>::kPer];
-#pragma unroll
-            for (int i = 1; i < Row<T>::kPer; ++i) piece = fmaxf(piece, v[j][h * Row<T>::kPer + i]);
-            first_max[(b * Row<T>::kPieces + h) * 32 + lane] = piece;
-          }
-        } else if (lane == 0) {
-          first_max[b] = block_most;
-        }
-      }
-      if (block_most > m) {
-        // A new largest element: what was the largest becomes a term, and the new one, in the
-        // first lane that holds it, is none.
-        const float down = fmaxf(m - block_most, kFloor), f = exp2_approx(down * kLog2e);
-        if (m > -inf()) {
-          s = f * fmaf(down, z, s);
-          z *= f;
-          if (lane == 0) {
-            z += f;
-            s = fmaf(f, down, s);
-          }
-        }
-        m = block_most;
-        const int holder = __ffs(__ballot_sync(kFullMask, most == m)) - 1;
-        if (lane == holder) {
-          bool out = false;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (!out && v[j][i] == m) {
-              v[j][i] = -inf();
-              out = true;
-            }
-        }
-      }
-      if (m > -inf()) add8(v[j], m, z, s);
+// The warp's share of a row: its sums, and its segments' maxima.
+template <typename T>
+__device__ __forceinline__ Part sum_share(const LogprobArgs& a, const Row<T>& row, int warp, int warps, int lane, bool fine, float* seg_max) {
+  using R = Row<T>;
+  constexpr int kAhead = Share<T>::kAhead;
+  const Share<T> share(row, warp, warps);
+  float lane_top = -inf(), top = -inf(), of = -inf();
+  Sums sums;
+  // whether the sums are what they should be: finite, and of terms that are not too small
+  auto good = [&]() {
+    const Reference ref(of);
+    top = warp_max(sane(lane_top));
+    return !ref.far && !(top > -inf() && fabsf(fmaf(top, kLog2e, -ref.M)) > 100.0f) && __all_sync(kFullMask, sums.sound());
+  };
+  if (share.mine > 0) {
+    sum_batches<T, false>(a, row, share, lane, fine, seg_max, sums, of, lane_top);
+    if (!good()) {
+      sums = Sums();
+      sum_batches<T, true>(a, row, share, lane, fine, seg_max, sums, of, lane_top);
     }
   }
-  if (!met) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // One block after another: those at the ends; and where the quick sums did not take a value, all
+  // of them, first for the maximum, then for the sums.
+  const int count = share.count();
+  enum { kEnds, kMaximum, kAll } pass = share.mine == 0 ? kMaximum : kEnds;
+  for (;;) {
+    const Reference ref(pass == kMaximum ? -inf() : of);
+    if (pass != kEnds) {
+      sums = Sums();
+      lane_top = -inf();
+    }
+#pragma unroll 1
+    for (int i = pass == kEnds ? share.mine * kAhead : 0; i < count; ++i) {
+      const int b = share.block(i);
+      const typename R::Raw raw = row.fetch(b, lane);
+      const float mine = R::largest(raw);
+      lane_top = fmaxf(lane_top, mine);
+      if (fine) {
+#pragma unroll
+        for (int h = 0; h < R::kPieces; ++h) seg_max[(b * R::kPieces + h) * 32 + lane] = R::largest_of(raw.u[h]);
+      } else if (a.top_n > 0) {
+        const float most = warp_max(mine);
+        if (lane == 0) seg_max[b] = most;
+      }
+      if (pass != kMaximum) {
+        float v[8];
+        R::unpack(raw, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sums.add_one(ref.term(sane(v[k])));
+      }
+    }
+    const bool done = good();
+    if (pass == kAll || (pass == kEnds && done)) break;
+    if (pass == kMaximum) {
+      of = top;
+      if (of == -inf()) break;
+      pass = kAll;
+    } else {
+      pass = kMaximum;
+    }
+  }
+  Part part;
+  part.m = top;
+  part.of = of;
+  part.lane = __ffs(__ballot_sync(kFullMask, sane(lane_top) == top)) - 1;
+  float z = sums.z.x + sums.z.y, s = sums.s.x + sums.s.y;
+  part.z_lane = __shfl_sync(kFullMask, z, part.lane);
+  part.s_lane = __shfl_sync(kFullMask, s, part.lane);
+  if (lane == part.lane) z = s = 0.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     z += __shfl_xor_sync(kFullMask, z, o);
     s += __shfl_xor_sync(kFullMask, s, o);
   }
-  if (lane == 0) first->part[rank * kWarps + warp] = {m, z, s};
-  cluster.sync();
-  if (rank != 0) return;
+  part.z = z;
+  part.s = s;
+  part.pad = 0;
+  return part;
+}
+
+struct Shared {
+  Part part[kMaxWarps];
+  unsigned long long candidate[kMost];
+  int count, special;  // special: the warp that met the largest element, -1 where its lane's sums do
+  float bound, top, z, s;
+  uint32_t taken[MEMRA_MAX_TOP_LOGPROBS];
+};
+
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(LogprobArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  using R = Row<T>;
+  extern __shared__ float seg_max[];  // the row's first CTA
+  __shared__ Shared sh;
+  pdl_launch_dependents();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  // so that the row's first CTA has begun, and its shared memory can be written, when sums are done
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = ranks * kWarps, my_warp = warp * ranks + rank;
+  const int64_t t = blockIdx.x / ranks;
+  const R row(static_cast<const T*>(a.logits) + t * a.stride_t, a.V);
+  // Segments: blocks, or, where these are too few to tell top_n elements apart, pieces of 16 bytes.
+  const bool fine = a.V <= kFineVocab && a.top_n > 0;
+  const int blocks = row.blocks(), segments = fine ? blocks * 32 * R::kPieces : blocks;
+  if (threadIdx.x == 0) sh.count = 0;
+  pdl_wait();
+  const int32_t token = a.logprobs != nullptr && threadIdx.x == 0 && rank == 0 ? a.tokens[t] : -1;
+  const Part mine = sum_share<T>(a, row, my_warp, warps, lane, fine, seg_max);
+  const bool known = token >= 0 && token < a.V;
+  const float token_x = known ? element<T>(row.base + row.shift + token) : -inf();
+  if (ranks == 1) {
+    if (lane == 0) sh.part[my_warp] = mine;
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const float words[8] = {mine.m, mine.of, mine.z, mine.s, mine.z_lane, mine.s_lane, __int_as_float(mine.lane), 0.0f};
+    const uint32_t at = mapped(&sh.part[my_warp]);
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (lane == i) put(at + 4 * i, words[i]);
+    if (a.top_n > 0 && rank != 0) {
+      const Share<T> share(row, my_warp, warps);
+      const int per = fine ? 32 * R::kPieces : 1, count = share.count() * per;  // per: segments of a block
+      __syncwarp();
+      for (int i = lane; i < count; i += 32) {
+        const int seg = share.block(i / per) * per + i % per;
+        put(mapped(seg_max + seg), seg_max[seg]);
+      }
+    }
+    cluster.sync();
+    if (rank != 0) return;
+  }
 
   // ---- the row's first CTA ----
-  const int segments = a.fine ? blocks * 32 * Row<T>::kPieces : blocks;
   if (warp == 0) {
     float top = -inf();
-    for (int i = lane; i < ranks * kWarps; i += 32) top = fmaxf(top, sh.part[i].m);
-    top = warp_max(top);
-    // the largest element is the first such part's; of others it is a term
-    int own = 0x7fffffff;
-    for (int i = ranks * kWarps - 1 - lane; i >= 0; i -= 32)
-      if (sh.part[i].m == top) own = i;
-    own = __reduce_min_sync(kFullMask, own);
-    float zz = 0.0f, ss = 0.0f;
-    for (int i = lane; i < ranks * kWarps; i += 32) {
-      const Part p = sh.part[i];
+    int special = 0x7fffffff;
+    for (int i = lane; i < warps; i += 32)
+      if (sh.part[i].m > top) {
+        top = sh.part[i].m;
+        special = i;
+      }
+    const float most = warp_max(top);
+    special = __reduce_min_sync(kFullMask, top == most ? special : 0x7fffffff);
+    top = most;
+    const Reference ref(top);
+    const float largest = exp2f(ref.delta);  // the largest element's term
+    float z = 0.0f, s = 0.0f, z_lane = 0.0f, s_lane = 0.0f;
+    for (int i = lane; i < warps; i += 32) {
+      const Part& p = sh.part[i];
       if (p.m == -inf()) continue;
-      const float down = fmaxf(p.m - top, kFloor), f = exp2_approx(down * kLog2e);
-      const float terms = i == own ? p.z : p.z + 1.0f;
-      zz = fmaf(f, terms, zz);
-      ss = fmaf(f, fmaf(down, terms, p.s), ss);
+      const float up = ref.from(Reference(p.of)), e = exp2f(up);
+      z = fmaf(e, p.z, z);
+      s = fmaf(e, fmaf(up, p.z, p.s), s);
+      const float zl = e * p.z_lane, sl = e * fmaf(up, p.z_lane, p.s_lane);
+      if (i == special) {
+        z_lane = zl;
+        s_lane = sl;
+      } else {
+        z += zl;
+        s += sl;
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      zz += __shfl_xor_sync(kFullMask, zz, o);
-      ss += __shfl_xor_sync(kFullMask, ss, o);
+      z += __shfl_xor_sync(kFullMask, z, o);
+      s += __shfl_xor_sync(kFullMask, s, o);
+      z_lane += __shfl_xor_sync(kFullMask, z_lane, o);
+      s_lane += __shfl_xor_sync(kFullMask, s_lane, o);
+    }
+    const bool again = top > -inf() && !(z + z_lane - largest >= 0.25f * largest);
+    if (again) {
+      // the elements of the lane that met the largest, without it
+      const Share<T> share(row, special, warps);
+      const int its_lane = sh.part[special].lane;
+      Sums sums;
+      int equals = 0;
+      for (int i = lane; i < share.count(); i += 32) {
+        float v[8];
+        R::unpack(row.fetch(share.block(i), its_lane), v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float x = sane(v[k]);
+          equals += x == top ? 1 : 0;
+          sums.add_one(x == top ? kFloor : ref.term(x));
+        }
+      }
+      z_lane = sums.z.x;
+      s_lane = sums.s.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        z_lane += __shfl_xor_sync(kFullMask, z_lane, o);
+        s_lane += __shfl_xor_sync(kFullMask, s_lane, o);
+      }
+      const float others = (float)((int)__reduce_add_sync(kFullMask, equals) - 1) * largest;
+      z += z_lane + others;
+      s += s_lane + others * ref.delta;
+    } else {
+      z += z_lane - largest;
+      s += s_lane - largest * ref.delta;
     }
     if (lane == 0) {
-      const bool none = top == -inf();
-      const float log_z = log1pf(zz);
-      sh.m = top;
-      sh.log_z = log_z;
-      if (a.entropy != nullptr) a.entropy[t] = none ? 0.0f : log_z - ss / (1.0f + zz);
+      // relative to the largest element
+      const float up = exp2f(-ref.delta), log_z = log1pf(up * z);
+      const bool none_left = top == -inf();
+      sh.top = top;
+      sh.z = log_z;
+      if (a.entropy != nullptr) {
+        const float terms = kLn2 * up * (s - ref.delta * z);
+        a.entropy[t] = none_left ? 0.0f : log_z - terms / (1.0f + up * z);
+      }
       if (a.logprobs != nullptr) {
-        const int32_t token = a.tokens[t];
         float lp = -inf();
-        if (token >= 0 && token < a.V) {
-          const float x = sane(element<T>(row.base + row.shift + token));
-          if (!none) lp = (x - top) - log_z;
+        if (known) {
+          if (!none_left) lp = (sane(token_x) - top) - log_z;
         } else if (token == -1) {
           lp = 0.0f;
         } else if (a.status != nullptr) {
@@ -294,56 +577,66 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(LogprobArgs a) {
         a.logprobs[t] = lp;
       }
     }
-  } else if (warp == 1 && a.top_n > 0) {
-    // the bound, as the top_n-th largest of the maxima of 32 groups of segments
-    float best = -inf();
-    for (int i = lane; i < segments; i += 32) {
-      best = fmaxf(best, seg_max[i]);
-    }
-    // one lane at a time is struck out, so that equal maxima count each
-    float bound = -inf();
-    for (int n = 0; n < a.top_n; ++n) {
-      bound = warp_max(best);
-      const uint32_t at = __ballot_sync(kFullMask, best == bound);
-      if (lane == __ffs(at) - 1) best = -inf();
-    }
-    if (lane == 0) {
-      sh.bound = bound;
-      sh.count = sh.listed = 0;
-    }
   }
   if (a.top_n == 0) return;
-  __syncthreads();
-  const float bound = sh.bound, top = sh.m, log_z = sh.log_z;
-  const float kMasked = -inf();
-  // the segments to read again, and their elements at or above the bound
-  uint32_t* list = reinterpret_cast<uint32_t*>(seg_max + a.segments);
-  for (int i = threadIdx.x; i < segments; i += kThreads)
-    if (seg_max[i] >= bound && seg_max[i] > kMasked) list[atomicAdd(&sh.listed, 1)] = i;
-  __syncthreads();
-  const int listed = sh.listed;
-  auto consider = [&](float v, int at) {
-    v = sane(v);
-    if (v >= bound && v > kMasked) {
-      const int n = atomicAdd(&sh.count, 1);
-      if (n < kMost)
-        sh.candidate[n] = ((unsigned long long)order_of(v) << 32) | (uint32_t)~(uint32_t)(at - row.shift);
+  if (warp != 0) {
+    constexpr int kLook = kWarps - 1;  // warps that look through the row again
+    if (warp == 1) {
+      const float b = bound_of(seg_max, segments, a.top_n, lane);
+      if (lane == 0) sh.bound = b;
     }
-  };
-  if (a.fine) {
-    for (int i = threadIdx.x; i < listed * Row<T>::kPer; i += kThreads) {
-      const int at = list[i / Row<T>::kPer] * Row<T>::kPer + i % Row<T>::kPer;
-      if (at >= row.shift && at < row.end) consider(element<T>(row.base + at), at);
-    }
-  } else {
-    for (int i = warp; i < listed; i += kWarps) {
+    asm volatile("barrier.sync 1, %0;" ::"n"(kThreads - 32) : "memory");
+    // Segments that reach the bound are read again, and their elements that do so become candidates.
+    const float bound = sh.bound, none = -inf();
+    const int f = row.first_whole();
+    auto consider = [&](float v, int at) {
+      v = sane(v);
+      if (v >= bound && v > none) {
+        const int n = atomicAdd(&sh.count, 1);
+        if (n < kMost) sh.candidate[n] = ((unsigned long long)order_of(v) << 32) | (uint32_t)~(uint32_t)(at - row.shift);
+      }
+    };
+    auto consider_block = [&](const typename R::Raw& raw, int seg) {
       float v[8];
-      row.load(list[i], lane, v);
+      R::unpack(raw, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) consider(v[j], Row<T>::place(list[i], lane, j));
+      for (int j = 0; j < 8; ++j) consider(v[j], R::place(seg, lane, j));
+    };
+    for (int i0 = 0; i0 < segments; i0 += 32 * kLook) {  // neighbouring segments to different warps
+      const int mine = i0 + lane * kLook + warp - 1;
+      const float most = mine < segments ? seg_max[mine] : none;
+      const bool reaches = most >= bound && most > none;
+      if (fine) {
+        if (reaches)
+#pragma unroll 1
+          for (int p = max(mine * R::kPer, row.shift); p < min((mine + 1) * R::kPer, row.end); ++p) consider(element<T>(row.base + p), p);
+        continue;
+      }
+      const bool whole = mine >= f && mine < row.end_whole();
+      uint32_t hits = __ballot_sync(kFullMask, reaches && whole);
+      while (hits != 0) {
+        constexpr int kTogether = 4;
+        int seg[kTogether];
+        typename R::Raw raw[kTogether];
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j) {
+          seg[j] = hits != 0 ? i0 + (__ffs(hits) - 1) * kLook + warp - 1 : -1;
+          hits &= hits - 1;
+          if (seg[j] >= 0) raw[j] = row.fetch_whole(seg[j], lane);
+        }
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j)
+          if (seg[j] >= 0) consider_block(raw[j], seg[j]);
+      }
+#pragma unroll 1
+      for (hits = __ballot_sync(kFullMask, reaches && !whole); hits != 0; hits &= hits - 1) {
+        const int seg = i0 + (__ffs(hits) - 1) * kLook + warp - 1;
+        consider_block(row.fetch(seg, lane), seg);
+      }
     }
   }
   __syncthreads();
+  const float top = sh.top, log_z = sh.z;
   const int count = sh.count;
   int32_t* ids = a.top_ids + t * a.top_n;
   float* out = a.top_logprobs + t * a.top_n;
@@ -369,11 +662,13 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(LogprobArgs a) {
     for (int n = 0; n < a.top_n; ++n) {
       float best = -inf();
       int seg = 0x7fffffff;
-      for (int i = lane; i < segments; i += 32)
-        if (seg_max[i] > best) {
-          best = seg_max[i];
+      for (int i = lane; i < segments; i += 32) {
+        const float v = seg_max[i];
+        if (v > best) {
+          best = v;
           seg = i;
         }
+      }
       const float most = warp_max(best);
       seg = __reduce_min_sync(kFullMask, best == most ? seg : 0x7fffffff);
       Key one = 0, two = 0;  // the lane's two largest of those that are left
@@ -383,16 +678,14 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(LogprobArgs a) {
         two = key > one ? one : (key > two ? key : two);
         one = key > one ? key : one;
       };
-      if (a.fine) {
-        const int at = seg * Row<T>::kPer + lane;
-        if (lane < Row<T>::kPer && at >= row.shift && at < row.end) look(element<T>(row.base + at), at);
+      if (fine) {
+        const int at = seg * R::kPer + lane;
+        if (lane < R::kPer && at >= row.shift && at < row.end) look(element<T>(row.base + at), at);
       } else {
-        float v[8];
-        row.load(seg, lane, v);
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < 8; ++j) {
-          const int at = Row<T>::place(seg, lane, j);
-          if (at >= row.shift && at < row.end) look(v[j], at);
+          const int at = R::place(seg, lane, j);
+          if (at >= row.shift && at < row.end) look(element<T>(row.base + at), at);
         }
       }
 #pragma unroll
@@ -412,14 +705,14 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(LogprobArgs a) {
       __syncwarp();
     }
   }
+  // too few: the lowest indexes not taken, of which there are enough below top_n
   if (chosen == a.top_n) return;
   __syncthreads();
-  // too few: the lowest indexes not taken, of which there are enough below top_n
   if (warp == 0) {
     bool free = lane < a.top_n;
     for (int j = 0; j < chosen; ++j) free = free && sh.taken[j] != (uint32_t)lane;
-    const uint32_t left = __ballot_sync(kFullMask, free);
-    const int to = chosen + __popc(left & ((1u << lane) - 1));
+    const uint32_t left_over = __ballot_sync(kFullMask, free);
+    const int to = chosen + __popc(left_over & ((1u << lane) - 1));
     if (free && to < a.top_n) {
       ids[to] = lane;
       out[to] = -inf();
@@ -437,7 +730,7 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int ranks, cudaStream_t stream
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.T * ranks));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = a.top_n > 0 ? (size_t)a.segments * 8 : 0;
+  cfg.dynamicSmemBytes = a.top_n > 0 ? 4 * (size_t)a.segments : 0;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -451,11 +744,18 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int ranks, cudaStream_t stream
 }
 
 template <typename T>
-cudaError_t launch_logprobs(const LogprobArgs& a, int sms, cudaStream_t stream) {
-  // CTAs to a row: as many as keep the SMs busy, and no more than have four blocks a warp to look at
-  int ranks = 1;
-  while (ranks < 16 && a.T * ranks * 2 <= 2 * sms && (int64_t)ranks * 2 * 16 * 4 * kBlock <= a.V) ranks *= 2;
-  return launch_logprobs<T, 512>(a, ranks, stream);
+cudaError_t launch_logprobs(const LogprobArgs& a, const DeviceInfo& info, cudaStream_t stream) {
+  // 1024 threads an SM.  Up to two rows an SM, CTAs of 512 threads, clusters of them where rows are
+  // fewer (with four blocks a warp at least); up to four, CTAs of 256; CTAs of 128 beyond, which
+  // leave the fewest threads waiting while a row's choice is made.  us for 301 rows of 32,003 bf16
+  // logits, 553 of 114,789 fp32 and 2047 of 151,936 bf16: 512 threads 8.2, 49.1, 118.9; 256 9.1,
+  // 47.9, 118.9; 128 10.8, 59.3, 111.8.
+  if (a.T <= 2 * info.sms) {
+    int ranks = 1;
+    while (ranks < 16 && a.T * ranks * 2 <= 2 * info.sms && (int64_t)ranks * 2 * 16 * 4 * kBlock <= a.V) ranks *= 2;
+    return launch_logprobs<T, 512>(a, ranks, stream);
+  }
+  return a.T <= 4 * info.sms ? launch_logprobs<T, 256>(a, 1, stream) : launch_logprobs<T, 128>(a, 1, stream);
 }
 
 }  // namespace
@@ -489,19 +789,16 @@ extern "C" memra_status memra_token_logprobs(const void* logits, int32_t dtype, 
   a.stride_t = stride_t;
   a.V = (int)V;
   a.top_n = (int)top_n;
-  // Segments of 16 bytes where the vocabulary is small, so that there are many more of them
-  // than top_n; 256 elements else.
-  a.fine = V <= kFineVocab;
   const int64_t blocks = (V + 16 / es - 1 + kBlock - 1) / kBlock;
-  a.segments = (int)(a.fine ? blocks * kBlock * es / 16 : blocks);
+  a.segments = (int)(V <= kFineVocab ? blocks * kBlock * es / 16 : blocks);
   a.tokens = tokens;
   a.logprobs = logprobs;
   a.entropy = entropy;
   a.top_logprobs = top_logprobs;
   a.top_ids = top_ids;
   a.status = dev_status;
-  const cudaError_t e = dtype == MEMRA_BF16 ? launch_logprobs<uint16_t>(a, info.sms, stream)
-                                            : launch_logprobs<float>(a, info.sms, stream);
+  const cudaError_t e = dtype == MEMRA_BF16 ? launch_logprobs<uint16_t>(a, info, stream)
+                                            : launch_logprobs<float>(a, info, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }
