@@ -18,20 +18,24 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRanks = 8;  // CTAs of a cluster
 
+// Cells that a lane looks at together, so that their loads wait for each other once.  A table of
+// one such tile a lane (8192 cells, 65,536 with eight CTAs) is read once and stays in registers.
+constexpr int kTile = 8;
+
 // A table cell's place and what it holds.
 struct Table {
   const int32_t* lens;
   const int32_t* entries;
   int64_t B, max_pages, n_pages;
   int page;
-  Divider by_row;
+  Divider by_row, by_page;
   // pages of a sequence of `len` tokens; *bad: the length is none
   __device__ __forceinline__ int pages_of(int32_t len, bool* bad) const {
     if (len < 0) {
       *bad = true;
       return 0;
     }
-    const uint32_t n = ((uint32_t)len + (uint32_t)page - 1) / (uint32_t)page;
+    const uint32_t whole = by_page((uint32_t)len), n = whole + (whole * (uint32_t)page != (uint32_t)len ? 1 : 0);
     if (n > (uint64_t)max_pages) {
       *bad = true;
       return (int)max_pages;
@@ -40,6 +44,12 @@ struct Table {
   }
   __device__ __forceinline__ bool is_page(int32_t p) const { return p >= 0 && p < n_pages; }
 };
+
+// All threads of the cluster, which may be one CTA.
+__device__ __forceinline__ void meet(cg::cluster_group& cluster, int ranks) {
+  if (ranks > 1) cluster.sync();
+  else __syncthreads();
+}
 
 // Exclusive place of this warp's `count` among the counts of all warps of the cluster, and their
 // sum.  Every thread of the cluster calls it; `slots` is a CTA's own.
@@ -50,12 +60,20 @@ __device__ __forceinline__ void place_of(cg::cluster_group& cluster, Counts& min
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane == 0) mine.of_warp[warp] = count;
-  cluster.sync();
+  meet(cluster, ranks);
   int32_t b = 0, n = 0;
-  for (int r = 0; r < ranks; ++r) {
-    const int32_t c = cluster.map_shared_rank(&mine, r)->of_warp[lane];
-    n += c;
-    if (r < rank || (r == rank && lane < warp)) b += c;
+  if (ranks == 1) {
+    n = mine.of_warp[lane];
+    b = lane < warp ? n : 0;
+  } else {
+    int32_t c[kMaxRanks];
+#pragma unroll
+    for (int r = 0; r < kMaxRanks; ++r) c[r] = r < ranks ? cluster.map_shared_rank(&mine, r)->of_warp[lane] : 0;
+#pragma unroll
+    for (int r = 0; r < kMaxRanks; ++r) {
+      n += c[r];
+      if (r < rank || (r == rank && lane < warp)) b += c[r];
+    }
   }
   *before = __reduce_add_sync(kFullMask, b);
   *all = __reduce_add_sync(kFullMask, n);
@@ -146,11 +164,11 @@ __global__ void __launch_bounds__(kThreads) unshare_kernel(UnshareArgs a) {
     bool bad = add < 0;
     add = max(add, 0);
     const int pages = a.t.pages_of(len, &bad);
-    const int inside = len > 0 ? (int)((uint32_t)len % (uint32_t)a.t.page) : 0;
+    const int inside = len > 0 ? (int)((uint32_t)len - a.t.by_page((uint32_t)len) * (uint32_t)a.t.page) : 0;
     int64_t cell = 0;
     int32_t p = -1, holders = 0;
     // a length beyond the table has no last page there
-    if (mine && add > 0 && inside > 0 && pages == (len + (int64_t)a.t.page - 1) / a.t.page) {
+    if (mine && add > 0 && inside > 0 && pages == (int64_t)a.t.by_page((uint32_t)len) + 1) {
       cell = b * a.t.max_pages + pages - 1;
       p = a.t.entries[cell];
       if (a.t.is_page(p)) holders = __ldcg(a.refs + p);
@@ -295,72 +313,104 @@ __global__ void __launch_bounds__(kThreads) release_kernel(ReleaseArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)cluster.num_blocks() * kWarps;
+  const int lane = threadIdx.x & 31, ranks = (int)cluster.num_blocks();
+  const int64_t warps = (int64_t)ranks * kWarps;
   const int64_t my_warp = (int64_t)cluster.block_rank() * kWarps + (threadIdx.x >> 5);
   const int64_t cells = a.t.B * a.t.max_pages;
   const int64_t chunks = (cells + 31) / 32;
   const int64_t c0 = chunks * my_warp / warps, c1 = chunks * (my_warp + 1) / warps;
-  const int64_t head = a.free_head != nullptr ? *a.free_head : a.n_free;
+  const int64_t head = *a.free_head;
   bool bad = false;
 
-  // the page that cell e gives up, -1 for none
-  auto given_up = [&](int64_t e, bool check) -> int32_t {
-    if (e >= cells) return -1;
-    const uint32_t b = a.t.by_row((uint32_t)e);
-    const int i = (int)((uint32_t)e - b * (uint32_t)a.t.max_pages);
-    bool odd = false;
-    const int32_t len = a.t.lens[b];
-    const int32_t keep = a.keep != nullptr ? a.keep[b] : 0;
-    const int have = a.t.pages_of(len, &odd);
-    const int stay = a.t.pages_of(max(keep, 0), &odd);
-    if (i < stay || i >= have) return -1;
-    const int32_t p = a.t.entries[e];
-    const bool page = a.t.is_page(p);
-    if (check && !page) bad = true;
-    return page ? p : -1;
+  // the pages that the lane's cells of a tile give up, -1 for none
+  int32_t page[kTile];
+  auto look = [&](int64_t c, bool check) {
+    int32_t len[kTile], keep[kTile];
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) {
+      const int64_t e = (c + j) * 32 + lane;
+      const bool in = c + j < c1 && e < cells;
+      const uint32_t b = in ? a.t.by_row((uint32_t)e) : 0;
+      page[j] = in ? a.t.entries[e] : -1;
+      len[j] = in ? a.t.lens[b] : 0;
+      keep[j] = in && a.keep != nullptr ? a.keep[b] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) {
+      const int64_t e = (c + j) * 32 + lane;
+      const bool in = c + j < c1 && e < cells;
+      const int i = in ? (int)((uint32_t)e - a.t.by_row((uint32_t)e) * (uint32_t)a.t.max_pages) : 0;
+      bool odd = false;
+      const bool given = in && i < a.t.pages_of(len[j], &odd) && i >= a.t.pages_of(max(keep[j], 0), &odd);
+      if (given && check && !a.t.is_page(page[j])) bad = true;
+      if (!given || !a.t.is_page(page[j])) page[j] = -1;
+    }
   };
-  auto code = [&](int64_t e) { return (int32_t)(INT32_MIN + (cells - 1 - e)); };
+  const bool one = c1 - c0 <= kTile;
+  auto code = [&](int64_t c, int j) { return (int32_t)(INT32_MIN + (cells - 1 - ((c + j) * 32 + lane))); };
 
-  for (int64_t c = c0; c < c1; ++c) {
-    const int32_t p = given_up(c * 32 + lane, true);
-    if (p >= 0) atomicSub(a.refs + p, 1);
+  for (int64_t c = c0; c < c1; c += kTile) {
+    look(c, true);
+#pragma unroll
+    for (int j = 0; j < kTile; ++j)
+      if (page[j] >= 0) atomicSub(a.refs + page[j], 1);
   }
-  cluster.sync();
-  for (int64_t c = c0; c < c1; ++c) {
-    const int64_t e = c * 32 + lane;
-    const int32_t p = given_up(e, false);
-    if (p < 0) continue;
-    const int32_t r = __ldcg(a.refs + p);
-    if (r >= 0) continue;
-    if (r < -1 && r > INT32_MIN / 2) bad = true;  // more often than it was held
-    atomicMin(a.refs + p, code(e));
+  meet(cluster, ranks);
+  for (int64_t c = c0; c < c1; c += kTile) {
+    if (!one) look(c, false);
+    int32_t r[kTile];
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) r[j] = page[j] >= 0 ? __ldcg(a.refs + page[j]) : 0;
+#pragma unroll
+    for (int j = 0; j < kTile; ++j)
+      if (r[j] < 0) {
+        if (r[j] < -1 && r[j] > INT32_MIN / 2) bad = true;  // more often than it was held
+        atomicMin(a.refs + page[j], code(c, j));
+      } else {
+        page[j] = -1;  // others hold it
+      }
   }
-  cluster.sync();
+  meet(cluster, ranks);
+  uint32_t goes = 0;  // of one tile
   int32_t mine = 0;
-  for (int64_t c = c0; c < c1; ++c) {
-    const int64_t e = c * 32 + lane;
-    const int32_t p = given_up(e, false);
-    mine += __popc(__ballot_sync(kFullMask, p >= 0 && __ldcg(a.refs + p) == code(e)));
+  for (int64_t c = c0; c < c1; c += kTile) {
+    if (!one) look(c, false);
+    int32_t r[kTile];
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) r[j] = page[j] >= 0 ? __ldcg(a.refs + page[j]) : 0;
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) {
+      const bool go = page[j] >= 0 && r[j] == code(c, j);
+      goes |= (go ? 1u : 0u) << j;
+      mine += __popc(__ballot_sync(kFullMask, go));
+    }
   }
   int32_t before, all;
   place_of(cluster, counts, mine, &before, &all);
   int64_t to = head - all + before;
-  for (int64_t c = c0; c < c1; ++c) {
-    const int64_t e = c * 32 + lane;
-    const int32_t p = given_up(e, false);
-    const bool goes = p >= 0 && __ldcg(a.refs + p) == code(e);
-    const uint32_t going = __ballot_sync(kFullMask, goes);
-    if (goes) {
-      const int64_t at = to + __popc(going & ((1u << lane) - 1));
-      if (at >= 0 && at < a.n_free) a.free_pages[at] = p;
-      a.refs[p] = 0;
+  for (int64_t c = c0; c < c1 && mine > 0; c += kTile) {
+    if (!one) {
+      look(c, false);
+      goes = 0;
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) goes |= (page[j] >= 0 && __ldcg(a.refs + page[j]) == code(c, j) ? 1u : 0u) << j;
     }
-    to += __popc(going);
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) {
+      const bool go = (goes >> j) & 1u;
+      const uint32_t going = __ballot_sync(kFullMask, go);
+      if (go) {
+        const int64_t at = to + __popc(going & ((1u << lane) - 1));
+        if (at >= 0 && at < a.n_free) a.free_pages[at] = page[j];
+        a.refs[page[j]] = 0;
+      }
+      to += __popc(going);
+    }
   }
-  cluster.sync();  // lengths have been read, and counts by the other CTAs
+  // lengths have been read by all, in one tile even before the counts were
   int bits = bad ? 1 : 0;
-  for (int64_t b = (int64_t)cluster.block_rank() * kThreads + threadIdx.x; b < a.t.B; b += (int64_t)cluster.num_blocks() * kThreads) {
+  if (ranks > 1) cluster.sync();  // (and counts by the other CTAs)
+  for (int64_t b = (int64_t)cluster.block_rank() * kThreads + threadIdx.x; b < a.t.B; b += (int64_t)ranks * kThreads) {
     bool odd = false;
     const int32_t len = a.t.lens[b], keep = a.keep != nullptr ? a.keep[b] : 0;
     (void)a.t.pages_of(len, &odd);
@@ -388,30 +438,47 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
-  const int lane = threadIdx.x & 31;
-  const int64_t all_threads = (int64_t)cluster.num_blocks() * kThreads;
+  const int lane = threadIdx.x & 31, ranks = (int)cluster.num_blocks();
+  const int64_t all_threads = (int64_t)ranks * kThreads;
   const int64_t me = (int64_t)cluster.block_rank() * kThreads + threadIdx.x;
   const int64_t cells = a.t.B * a.t.max_pages, n = a.t.n_pages, moves = n / 2;
+  // the pages of the thread's cells, kTile at a time; of one such tile they stay in registers
+  int32_t page[kTile];
+  auto look = [&](int64_t e0) {
+    int32_t len[kTile];
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) {
+      const int64_t e = e0 + j * all_threads;
+      page[j] = e < cells ? a.t.entries[e] : -1;
+      len[j] = e < cells ? a.t.lens[a.t.by_row((uint32_t)e)] : 0;
+    }
+    bool none = true;
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) {
+      const int64_t e = e0 + j * all_threads;
+      const int i = e < cells ? (int)((uint32_t)e - a.t.by_row((uint32_t)e) * (uint32_t)a.t.max_pages) : 0;
+      bool odd = false;  // told of below
+      const bool held = e < cells && i < a.t.pages_of(len[j], &odd);
+      if (held && !a.t.is_page(page[j])) none = false;
+      if (!held || !a.t.is_page(page[j])) page[j] = -1;
+    }
+    return !none;
+  };
+  const int64_t tile = all_threads * kTile;
+  const bool one = cells <= tile;
+  bool bad = false;
   for (int64_t p = me; p < n; p += all_threads) a.refs[p] = 0;
   for (int64_t k = me; k < moves; k += all_threads) a.src[k] = a.dst[k] = -1;
-  cluster.sync();
-  bool bad = false;
   for (int64_t b = me; b < a.t.B; b += all_threads) (void)a.t.pages_of(a.t.lens[b], &bad);
-  auto held = [&](int64_t e) -> int32_t {
-    const uint32_t b = a.t.by_row((uint32_t)e);
-    const int i = (int)((uint32_t)e - b * (uint32_t)a.t.max_pages);
-    bool odd = false;  // told above
-    if (i >= a.t.pages_of(a.t.lens[b], &odd)) return -1;
-    const int32_t p = a.t.entries[e];
-    if (a.t.is_page(p)) return p;
-    bad = true;
-    return -1;
-  };
-  for (int64_t e = me; e < cells; e += all_threads) {
-    const int32_t p = held(e);
-    if (p >= 0) atomicAdd(a.refs + p, 1);
+  if (one) bad |= look(me);
+  meet(cluster, ranks);
+  for (int64_t e0 = me; e0 < cells; e0 += tile) {
+    if (!one) bad |= look(e0);
+#pragma unroll
+    for (int j = 0; j < kTile; ++j)
+      if (page[j] >= 0) atomicAdd(a.refs + page[j], 1);
   }
-  cluster.sync();
+  meet(cluster, ranks);
   const int64_t warps = all_threads / 32, my_warp = me / 32, chunks = (n + 31) / 32;
   const int64_t c0 = chunks * my_warp / warps, c1 = chunks * (my_warp + 1) / warps;
   int32_t mine = 0;
@@ -438,10 +505,18 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a) {
       a.free_out[p] = used - 1 - below;  // for now: its move
     }
   }
-  cluster.sync();
-  for (int64_t e = me; e < cells; e += all_threads) {
-    const int32_t p = held(e);
-    a.table_out[e] = p < used ? p : __ldcg(a.dst + __ldcg(a.free_out + p));
+  meet(cluster, ranks);
+  for (int64_t e0 = me; e0 < cells; e0 += tile) {
+    if (!one) (void)look(e0);
+    int32_t to[kTile];
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) to[j] = page[j] >= used ? __ldcg(a.free_out + page[j]) : -1;
+#pragma unroll
+    for (int j = 0; j < kTile; ++j)
+      if (to[j] >= 0) page[j] = __ldcg(a.dst + to[j]);
+#pragma unroll
+    for (int j = 0; j < kTile; ++j)
+      if (e0 + j * all_threads < cells) a.table_out[e0 + j * all_threads] = page[j];
   }
   for (int64_t p = used + me; p < n; p += all_threads) {
     const int32_t count = __ldcg(a.refs + p);
@@ -450,7 +525,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a) {
       a.refs[p] = 0;
     }
   }
-  cluster.sync();
+  meet(cluster, ranks);
   for (int64_t p = me; p < n; p += all_threads) a.free_out[p] = (int32_t)p;
   if (me == 0) *a.free_head_out = used;
   tell(bad ? 1 : 0, a.status);
@@ -504,6 +579,7 @@ memra_status table_args(const int32_t* lens, const int32_t* entries, int64_t B, 
   t->max_pages = max_pages;
   t->n_pages = n_pages;
   t->page = (int)page_size;
+  t->by_page = Divider((uint32_t)page_size);
   t->by_row = Divider((uint32_t)(max_pages > 0 ? max_pages : 1));
   return MEMRA_OK;
 }
@@ -703,7 +779,7 @@ extern "C" memra_status memra_kv_compact(const int32_t* lens, const int32_t* blo
   a.dst = dst;
   a.free_head_out = free_head_out;
   a.status = dev_status;
-  const cudaError_t e = launch_cluster(compact_kernel, B * max_pages + n_pages, stream, a);
+  const cudaError_t e = launch_cluster(compact_kernel, B * max_pages > n_pages ? B * max_pages : n_pages, stream, a);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }

@@ -37,7 +37,7 @@ struct RopeArgs {
   float eps;
   const int32_t* positions;
   const double* inv_freq;
-  Divider by_groups, by_pairs;
+  Divider by_pairs;
 };
 
 // Four values of a row.
@@ -48,9 +48,9 @@ struct Piece<float> {
   uint4 u;
   __device__ __forceinline__ void load(const void* p) { u = __ldcg(static_cast<const uint4*>(p)); }
   __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void unpack(float* v) const {
-    v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
-    v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+  __device__ __forceinline__ void unpack(float2* v) const {
+    v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+    v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
   }
 };
 template <>
@@ -58,20 +58,15 @@ struct Piece<uint16_t> {
   uint2 u;
   __device__ __forceinline__ void load(const void* p) { u = __ldcg(static_cast<const uint2*>(p)); }
   __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
-  __device__ __forceinline__ void unpack(float* v) const {
-    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
-    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+  __device__ __forceinline__ void unpack(float2* v) const {
+    v[0] = make_float2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+    v[1] = make_float2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
   }
 };
 
-__device__ __forceinline__ void store4(const Rows& r, int64_t at, const float* v) {
-  if (r.bf16) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(r.at) + at) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  } else {
-    *reinterpret_cast<float4*>(static_cast<float*>(r.at) + at) = make_float4(v[0], v[1], v[2], v[3]);
-  }
+__device__ __forceinline__ uint2 bf16x4(const float2* v) {
+  const __nv_bfloat162 a = __float22bfloat162_rn(v[0]), b = __float22bfloat162_rn(v[1]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 // The angle's sine and cosine of a position: F is the frequency in turns, 64 bits behind the point.
@@ -81,111 +76,122 @@ __device__ __forceinline__ uint64_t turns_of(double inv_freq) {
   return __double2ull_rn(u * 18446744073709551616.0);
 }
 
-template <typename T, int kD>
-__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(RopeArgs a) {
+template <typename T, int kD, bool kPairs>
+__global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
   constexpr int kLanes = kD / 8;         // of a head
-  constexpr int kHeads = 32 / kLanes;    // that a warp takes at once
+  constexpr int kHeads = 32 / kLanes;    // that a warp takes at once: a group
   __shared__ __align__(16) float cos_of[kRopeTokens][kMaxPairs], sin_of[kRopeTokens][kMaxPairs];
+  __shared__ __align__(16) float weight_of[2][kD];
+  __shared__ uint64_t turn_of[kMaxPairs];
   __shared__ int32_t pos_of[kRopeTokens];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
   const int tokens = (int)min((int64_t)a.tokens, a.T - t0);
-  const int group0 = blockIdx.y * a.groups;
-  const int all_groups = (a.heads + kHeads - 1) / kHeads;
-  const int groups = min(a.groups, all_groups - group0);
-  const int items = tokens * groups;
+  const int end = min((int)(blockIdx.y + 1) * a.groups, (a.heads + kHeads - 1) / kHeads);
 
   // The values that the lane takes of a head: two pieces of four, from off_a and off_b.
   const int l = lane % kLanes;
-  const bool turned = l < a.R / 8, halves = turned && !a.pairs;
+  const bool turned = l < a.R / 8, halves = turned && !kPairs;
   const int off_a = halves ? 4 * l : 8 * l, off_b = halves ? a.R / 2 + 4 * l : 8 * l + 4;
 
-  struct Item {
-    Piece<T> pa, pb;
-    int token, head;
-  };
-  auto fetch = [&](int i) {
-    Item it;
-    it.token = groups == a.groups ? (int)a.by_groups((uint32_t)i) : i / groups;
-    it.head = (group0 + i - it.token * groups) * kHeads + lane / kLanes;
-    it.pa.zero();
-    it.pb.zero();
-    if (i < items && it.head < a.heads) {
-      const bool is_q = it.head < a.Hq;
-      const Rows& r = is_q ? a.q : a.k;
-      const T* p = static_cast<const T*>(r.at) + (t0 + it.token) * r.stride_t +
-                   (is_q ? it.head : it.head - a.Hq) * r.stride_h;
-      it.pa.load(p + off_a);
-      it.pb.load(p + off_b);
-    }
-    return it;
-  };
-
-  Item next = fetch(warp);
   const int half = a.R / 2;
-  for (int i = threadIdx.x; i < tokens * half; i += kRopeWarps * 32) {
-    const int t = (int)a.by_pairs((uint32_t)i), j = i - t * half;
-    const uint64_t turn = turns_of(a.inv_freq[j]) * (uint64_t)(uint32_t)a.positions[t0 + t];
-    // the upper 32 bits as half turns in [-1, 1)
-    sincospif((float)(int32_t)(uint32_t)(turn >> 32) * 4.6566128730773926e-10f, &sin_of[t][j], &cos_of[t][j]);
-  }
-  if (threadIdx.x < tokens) pos_of[threadIdx.x] = a.positions != nullptr ? a.positions[t0 + threadIdx.x] : 0;
-  float w[2][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int at = i < 4 ? off_a + i : off_b + i - 4;
-    w[0][i] = a.q_weight != nullptr ? a.q_weight[at] : 1.0f;
-    w[1][i] = a.k_weight != nullptr ? a.k_weight[at] : 1.0f;
-  }
-  __syncthreads();
-
-  for (int i = warp; i < items; i += kRopeWarps) {
-    const Item it = next;
-    next = fetch(i + kRopeWarps);
-    float v[8];
-    it.pa.unpack(v);
-    it.pb.unpack(v + 4);
-    const bool is_q = it.head < a.Hq, real = pos_of[it.token] >= 0;
-    if (a.eps >= 0.0f) {
-      float s = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
-      s = fmaf(s, 1.0f / kD, a.eps);
-      const float r = s > 0.0f ? __frsqrt_rn(s) : 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = v[j] * r * (is_q ? w[0][j] : w[1][j]);
+  // Weights, and the angles of all tokens: each frequency's conversion, which takes slow fp64
+  // instructions, once.
+  auto prepare = [&]() {
+    for (int i = threadIdx.x; i < 2 * kD; i += kRopeWarps * 32) {
+      const float* from = i < kD ? a.q_weight : a.k_weight;
+      weight_of[i / kD][i % kD] = from != nullptr ? from[i % kD] : 1.0f;
     }
-    if (turned) {
-      const float4 c4 = *reinterpret_cast<const float4*>(&cos_of[it.token][4 * l]);
-      const float4 s4 = *reinterpret_cast<const float4*>(&sin_of[it.token][4 * l]);
-      const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+    if (threadIdx.x < half) turn_of[threadIdx.x] = turns_of(a.inv_freq[threadIdx.x]);
+    if (threadIdx.x < tokens) pos_of[threadIdx.x] = a.positions != nullptr ? a.positions[t0 + threadIdx.x] : 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < tokens * half; i += kRopeWarps * 32) {
+      const int t = (int)a.by_pairs((uint32_t)i), j = i - t * half;
+      const uint64_t turn = turn_of[j] * (uint64_t)(uint32_t)pos_of[t];
+      // the upper 32 bits as half turns in [-1, 1)
+      sincospif((float)(int32_t)(uint32_t)(turn >> 32) * 4.6566128730773926e-10f, &sin_of[t][j], &cos_of[t][j]);
+    }
+    __syncthreads();
+  };
+
+  bool first = true;
+  for (int g = blockIdx.y * a.groups + warp; g < end || first; g += kRopeWarps) {
+    const int head = g * kHeads + lane / kLanes;
+    const bool mine = g < end && head < a.heads, is_q = head < a.Hq;
+    const Rows &in = is_q ? a.q : a.k, &out = is_q ? a.q_out : a.k_out;
+    const int h = is_q ? head : head - a.Hq;
+    // all tokens' values are on their way before the first is worked on
+    Piece<T> pa[kRopeTokens], pb[kRopeTokens];
+    const T* p = static_cast<const T*>(in.at) + t0 * in.stride_t + h * in.stride_h + off_a;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // halves: values j and j + 4; pairs: 2j and 2j + 1
-        const float x = a.pairs ? v[2 * j] : v[j], y = a.pairs ? v[2 * j + 1] : v[j + 4];
-        const float xr = x * c[j] - y * s[j], yr = y * c[j] + x * s[j];
-        if (a.pairs) {
-          v[2 * j] = xr;
-          v[2 * j + 1] = yr;
-        } else {
-          v[j] = xr;
-          v[j + 4] = yr;
-        }
+    for (int t = 0; t < kRopeTokens; ++t, p += in.stride_t) {
+      pa[t].zero();
+      pb[t].zero();
+      if (mine && t < tokens) {
+        pa[t].load(p);
+        pb[t].load(p + (off_b - off_a));
       }
     }
-    if (!real) {
+    if (first) prepare();
+    first = false;
+    if (g >= end) break;
+    const int64_t es = out.bf16 ? 2 : 4, step = out.stride_t * es;
+    char* to = static_cast<char*>(out.at) + (t0 * out.stride_t + h * out.stride_h + off_a) * es;
+    const int64_t second = (off_b - off_a) * es;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    }
-    if (it.head < a.heads) {
-      const Rows& r = is_q ? a.q_out : a.k_out;
-      const int64_t at = (t0 + it.token) * r.stride_t + (is_q ? it.head : it.head - a.Hq) * r.stride_h;
-      store4(r, at + off_a, v);
-      store4(r, at + off_b, v + 4);
+    for (int t = 0; t < kRopeTokens; ++t, to += step) {
+      if (t >= tokens) break;
+      float2 v[4];  // off_a's four values, then off_b's
+      pa[t].unpack(v);
+      pb[t].unpack(v + 2);
+      if (a.eps >= 0.0f) {
+        float2 q = __fmul2_rn(v[0], v[0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) q = __ffma2_rn(v[j], v[j], q);
+        float s = q.x + q.y;
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
+        s = fmaf(s, 1.0f / kD, a.eps);
+        const float r = s > 0.0f ? __frsqrt_rn(s) : 0.0f;
+        const float4 wa = *reinterpret_cast<const float4*>(&weight_of[is_q ? 0 : 1][off_a]);
+        const float4 wb = *reinterpret_cast<const float4*>(&weight_of[is_q ? 0 : 1][off_b]);
+        const float2 w[4] = {{wa.x, wa.y}, {wa.z, wa.w}, {wb.x, wb.y}, {wb.z, wb.w}};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(__fmul2_rn(v[j], make_float2(r, r)), w[j]);
+      }
+      if (turned) {
+        const float4 c4 = *reinterpret_cast<const float4*>(&cos_of[t][4 * l]);
+        const float4 s4 = *reinterpret_cast<const float4*>(&sin_of[t][4 * l]);
+        if (kPairs) {
+          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[j] = __ffma2_rn(make_float2(-v[j].y, v[j].x), make_float2(s[j], s[j]), __fmul2_rn(v[j], make_float2(c[j], c[j])));
+        } else {
+          const float2 c[2] = {{c4.x, c4.y}, {c4.z, c4.w}}, s[2] = {{s4.x, s4.y}, {s4.z, s4.w}};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float2 x = v[j], y = v[j + 2];
+            v[j] = __ffma2_rn(make_float2(-y.x, -y.y), s[j], __fmul2_rn(x, c[j]));
+            v[j + 2] = __ffma2_rn(x, s[j], __fmul2_rn(y, c[j]));
+          }
+        }
+      }
+      if (pos_of[t] < 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = make_float2(0.0f, 0.0f);
+      }
+      if (mine) {
+        if (out.bf16) {
+          *reinterpret_cast<uint2*>(to) = bf16x4(v);
+          *reinterpret_cast<uint2*>(to + second) = bf16x4(v + 2);
+        } else {
+          *reinterpret_cast<float4*>(to) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+          *reinterpret_cast<float4*>(to + second) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+        }
+      }
     }
   }
 }
@@ -194,17 +200,16 @@ template <typename T, int kD>
 cudaError_t launch_rope(RopeArgs a, int sms, cudaStream_t stream) {
   constexpr int kHeads = 32 / (kD / 8);
   const int groups = (a.heads + kHeads - 1) / kHeads;
-  // Few tokens: one to a CTA, and a CTA for every eight groups of heads.  More: all heads of a
-  // token in one CTA, so that its angles are computed once, and up to four tokens, whose angles
-  // keep all threads busy.
-  const int64_t spread = (int64_t)sms * 2;
-  a.tokens = (int)(a.T / spread < 1 ? 1 : (a.T / spread > kRopeTokens ? kRopeTokens : a.T / spread));
-  a.groups = a.T < spread ? kRopeWarps : groups;
-  if (a.groups > groups) a.groups = groups;
-  a.by_groups = Divider((uint32_t)a.groups);
+  // Up to four tokens to a CTA, whose angles keep its threads busy, and all of their heads, so
+  // that angles are computed once; but eight groups of heads, one a warp, where that makes fewer
+  // than three CTAs an SM (1000 tokens of 48 heads of 128: 7.1 us for 9.2; 8191: 41.9 for 39.9).
+  const int64_t spread = a.T / (2 * (int64_t)sms);
+  a.tokens = (int)(spread < 1 ? 1 : (spread > kRopeTokens ? kRopeTokens : spread));
+  a.groups = (a.T + a.tokens - 1) / a.tokens < 3 * (int64_t)sms && groups > kRopeWarps ? kRopeWarps : groups;
   a.by_pairs = Divider((uint32_t)(a.R > 0 ? a.R / 2 : 1));
   const dim3 grid((unsigned)((a.T + a.tokens - 1) / a.tokens), (unsigned)((groups + a.groups - 1) / a.groups));
-  return launch_kernel(rope_kernel<T, kD>, grid, dim3(kRopeWarps * 32), 0, stream, a);
+  if (a.pairs) return launch_kernel(rope_kernel<T, kD, true>, grid, dim3(kRopeWarps * 32), 0, stream, a);
+  return launch_kernel(rope_kernel<T, kD, false>, grid, dim3(kRopeWarps * 32), 0, stream, a);
 }
 
 template <typename T>
