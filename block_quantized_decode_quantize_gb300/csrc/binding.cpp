@@ -104,8 +104,7 @@ PyObject* pack(std::initializer_list<Tensor> ts) {
   return out;
 }
 
-// A contiguous part of a buffer of 4-byte elements, from element `at` on, as a tensor that shares
-// its storage: what views of it would be, at a fraction of their cost.
+// A contiguous part of a buffer, from element `at` (of `type`) on, as a tensor that shares its storage: what views of it would be, at a fraction of their cost.
 Tensor part(const Tensor& buf, int64_t at, at::IntArrayRef shape, at::ScalarType type) {
   Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()), buf.key_set(),
                                                       c10::scalarTypeToTypeMeta(type));
@@ -306,13 +305,15 @@ inline bool optional(PyObject* o, int dev, at::ScalarType type, at::IntArrayRef 
   return dense(*t, type, shape);
 }
 
-// Rows that a call writes: those given, or new ones like x, of the C library's dtype code `want` (-1:
-// the input's).
-inline bool out_rows(PyObject* o, int* dev, const Tensor* x, int64_t want, int32_t code, Tensor* t, int32_t* type) {
-  if (want < 0 && o == Py_None) want = code;
+// Rows that a call writes.  Given ones have to be like x and of the C library's dtype code `want`
+// (-1: any); where there are none (None), their number of bytes is left in *bytes and *type is want,
+// or the input's code.
+inline bool out_rows(PyObject* o, int* dev, const Tensor* x, int64_t want, int32_t code, Tensor* t, int32_t* type,
+                     int64_t* bytes) {
+  *bytes = 0;
   if (o == Py_None) {
-    *t = at::empty(x->sizes(), x->options().dtype(want == MEMRA_BF16 ? at::kBFloat16 : at::kFloat));
-    *type = (int32_t)want;
+    *type = (int32_t)(want < 0 ? code : want);
+    *bytes = x->numel() * (*type == MEMRA_BF16 ? 2 : 4);
     return true;
   }
   const Tensor* given = tensor(o, dev);
@@ -349,8 +350,18 @@ PyObject* rope(PyObject*, PyObject* const* o, Py_ssize_t n) {
   }
   at::AutoDispatchBelowADInplaceOrView guard;
   Tensor qo, ko;
-  if (!out_rows(o[10], &dev, q, q_type, code, &qo, &qo_type) || !out_rows(o[11], &dev, k, k_type, code, &ko, &ko_type))
+  int64_t q_bytes, k_bytes;
+  if (!out_rows(o[10], &dev, q, q_type, code, &qo, &qo_type, &q_bytes) ||
+      !out_rows(o[11], &dev, k, k_type, code, &ko, &ko_type, &k_bytes))
     Py_RETURN_NONE;
+  // one allocation for both; k's rows on a boundary of 16 bytes
+  const int64_t k_at = (q_bytes + 15) / 16 * 16;
+  const auto type_of = [](int32_t t) { return t == MEMRA_BF16 ? at::kBFloat16 : at::kFloat; };
+  if (o[10] == Py_None || o[11] == Py_None) {
+    const Tensor buf = at::empty({k_at + k_bytes}, on(dev, at::kByte));
+    if (o[10] == Py_None) qo = part(buf, 0, q->sizes(), type_of(qo_type));
+    if (o[11] == Py_None) ko = part(buf, k_at / (ko_type == MEMRA_BF16 ? 2 : 4), k->sizes(), type_of(ko_type));
+  }
   const Strides sq(q), sk(k), so(&qo), sko(&ko);
   if (memra_qk_norm_rope(data<void>(q), data<void>(k), code, T, Hq, Hkv, D, sq.t, sq.h, sk.t, sk.h,
                          data<float>(qw), data<float>(kw), eps, data<int32_t>(positions),

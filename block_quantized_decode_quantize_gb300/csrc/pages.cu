@@ -779,7 +779,7 @@ extern "C" memra_status memra_kv_compact(const int32_t* lens, const int32_t* blo
   a.dst = dst;
   a.free_head_out = free_head_out;
   a.status = dev_status;
-  const cudaError_t e = launch_cluster(compact_kernel, B * max_pages > n_pages ? B * max_pages : n_pages, stream, a);
+  const cudaError_t e = launch_cluster(compact_kernel, B * max_pages + n_pages, stream, a);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }
