@@ -333,12 +333,16 @@ __device__ __forceinline__ void sum_batches(const LogprobArgs& a, const Row<T>& 
       of = fabsf(most) < inf() ? most : 0.0f;  // (no token left in them: any other number)
       M = Reference(of).M;
     }
+    // a batch's terms among themselves first, so that long sums of small terms lose less
+    Sums part;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       float x[8];
       R::unpack(r[j], x);
-      sums.template add<kClamp>(x, M);
+      part.template add<kClamp>(x, M);
     }
+    sums.z = __fadd2_rn(sums.z, part.z);
+    sums.s = __fadd2_rn(sums.s, part.s);
   };
   fetch(raw);
 #pragma unroll 1

@@ -137,7 +137,7 @@ struct UnshareArgs {
 };
 
 __global__ void __launch_bounds__(kThreads) unshare_kernel(UnshareArgs a) {
-  __shared__ int32_t page_of[kThreads];     // of the sharers listed
+  __shared__ __align__(16) int32_t page_of[kThreads];  // of the sharers listed
   __shared__ int32_t warp_sum[kWarps];
   __shared__ uint32_t refused_of[kThreads / 32];
   pdl_launch_dependents();
@@ -190,11 +190,16 @@ __global__ void __launch_bounds__(kThreads) unshare_kernel(UnshareArgs a) {
     __syncthreads();
     int before = 0, latest = -1;  // sharers of the same page before this one, and the last of them
     if (shares)
-      for (int i = 0; i < at; ++i)
-        if (page_of[i] == p) {
-          ++before;
-          latest = i;
-        }
+      for (int i = 0; i < at; i += 4) {
+        const int4 q = *reinterpret_cast<const int4*>(page_of + i);
+        const int32_t other[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (other[j] == p && i + j < at) {
+            ++before;
+            latest = i + j;
+          }
+      }
     const bool takes = shares && before < holders;
     int takers;
     const int turn = place(takes, &takers);

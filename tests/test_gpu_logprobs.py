@@ -179,6 +179,59 @@ def test_patterns(mem, V, dtype, n):
             raise AssertionError("%s: %s" % (name, e))
 
 
+@pytest.mark.parametrize("T", [303, 304, 305, 607, 608, 609, 1217])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_on_both_sides_of_the_threads_rule(mem, T, dtype):
+    x, tok = rows(T, 1900, dtype, seed=T)
+    check(mem, x, tok, 6)
+
+
+def staged(T, V, seed):
+    """Rows whose first elements, which a warp's sums refer to, say little about the others."""
+    g = torch.Generator().manual_seed(seed)
+    base = 2.0 * torch.randn(T, V, generator=g)
+    for split in (V // 3, V - V // 5):
+        for low in (-60.0, -95.0, -150.0, -1000.0, -1e30, -math.inf):
+            x = base.clone()
+            x[:, :split] += low
+            yield "rises by %g at %d" % (-low, split), x
+            x = base.clone()
+            x[:, split:] += low
+            yield "falls by %g at %d" % (-low, split), x
+    x = base - 400.0
+    x[:, ::V // 7] = 3.0
+    yield "spikes", x
+    x = torch.full((T, V), -math.inf)
+    x[:, V - 40:] = base[:, V - 40:] - 300.0
+    yield "masked up to a low end", x
+    for level in (2.0 ** 19, 2.0 ** 21, -2.0 ** 21, 1e25, -1e25):
+        yield "at the level %g" % level, base * max(1.0, abs(level) * 2.0 ** -20) + level
+
+
+@pytest.mark.parametrize("V,T", [(1500, 2), (5001, 650), (40000, 310), (70001, 3), (151936, 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_references_far_from_the_maximum(mem, V, T, dtype):
+    """In all kernels' shapes; the rows of a case are the same three, so that the plain form is short."""
+    for name, x in staged(min(T, 3), V, V):
+        x = x.to(DT[dtype])
+        some = x.shape[0]
+        tok = torch.tensor([V - 1, 0, V // 2][:some], dtype=torch.int32)
+        try:
+            lp, H, ids, top = check(mem, x.cuda(), tok.cuda(), 5)
+            if T > some:
+                again = T // some
+                many = mem.memra_token_logprobs(x.cuda().repeat(again, 1), tok.cuda().repeat(again), top_n=5)
+                w_lp, w_H, w_ids, w_top, W = reference(x, tok.numpy(), 5)
+                E = (V / 256 + 2 * W + 80) * 2.0 ** -24
+                for r in (0, again // 2, again - 1):
+                    part = slice(r * some, (r + 1) * some)
+                    assert np.array_equal(many[2][part].cpu().numpy(), w_ids)
+                    near(many[0][part], w_lp, E + 3 * 2.0 ** -24 * np.abs(w_lp), "logprobs")
+                    near(many[1][part], w_H, (1 + W) * E + 3 * 2.0 ** -24 * w_H, "entropy")
+        except AssertionError as e:
+            raise AssertionError("%s: %s" % (name, e))
+
+
 def test_log_probabilities_near_zero_keep_their_digits(mem):
     """-lp of a token that is almost certain is the others' mass, relative to its own size: each of its terms is off by
     (2 * 25 + 4) 2^-24 and the sum by the additions' share, 2 ^-24 (V / 256 + 40)."""
