@@ -3,15 +3,19 @@
 // n = x * w / sqrt(mean x^2 + eps), then (a, b) -> (a cos - b sin, b cos + a sin).  A head's
 // row of D values lies on D / 8 lanes, so the sum of squares takes 3 to 5 exchanges, and each
 // lane holds two pieces of four values that are each other's partners in the rotation:
-// nothing else passes between lanes, and a row is read and written once.  A CTA takes one
-// to four tokens and some or all of their heads; its threads compute the R / 2 angles of a
-// token once, for all heads, and leave cos and sin in shared memory while the first rows are
-// on their way.
+// nothing else passes between lanes, and a row is read and written once.  A warp takes 32 lanes'
+// worth of heads (a group) of one, two or four tokens, all of whose loads are on their way
+// before the first is worked on.  A CTA's threads compute the R / 2 angles of a token once, for
+// all of its heads, and leave cos and sin in shared memory meanwhile.
 //
 // Angles: F = inv_freq / 2 pi as a fraction of a turn in 64-bit fixed point, and
 // position * F modulo 2^64 is the angle of any position, exact to the bits of F.
 //
-// Bytes bound it for many tokens, one launch and one read for few.
+// 8191 tokens of 48 heads of 128 in bf16 (201 MB) take 37.5 us, 79 % of the copy rate: memory and
+// instruction issue (125 a group and token, 0.61 a cycle) together bound it, the angles' beginning
+// of each CTA included.  In fp32 (403 MB) 63.2 us, 94 %.  One token takes 2.1 us, as a kernel that
+// does nothing.  Measured and not kept: one token's loads at a time (51.7 us), fp64 conversion of
+// the frequencies by every thread (+1 us), two tokens a CTA (48.0), eight (47.4).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -20,7 +24,6 @@ namespace memra {
 namespace {
 
 constexpr int kRopeWarps = 8;
-constexpr int kRopeTokens = 4;   // of a CTA, at most
 constexpr int kMaxPairs = 128;   // R / 2, at most
 
 struct Rows {
@@ -76,19 +79,19 @@ __device__ __forceinline__ uint64_t turns_of(double inv_freq) {
   return __double2ull_rn(u * 18446744073709551616.0);
 }
 
-template <typename T, int kD, bool kPairs>
+template <typename T, int kD, bool kPairs, int kTokens>
 __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
   constexpr int kLanes = kD / 8;         // of a head
   constexpr int kHeads = 32 / kLanes;    // that a warp takes at once: a group
-  __shared__ __align__(16) float cos_of[kRopeTokens][kMaxPairs], sin_of[kRopeTokens][kMaxPairs];
+  __shared__ __align__(16) float cos_of[kTokens][kMaxPairs], sin_of[kTokens][kMaxPairs];
   __shared__ __align__(16) float weight_of[2][kD];
   __shared__ uint64_t turn_of[kMaxPairs];
-  __shared__ int32_t pos_of[kRopeTokens];
+  __shared__ int32_t pos_of[kTokens];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
-  const int tokens = (int)min((int64_t)a.tokens, a.T - t0);
+  const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+  const int tokens = (int)min((int64_t)kTokens, a.T - t0);
   const int end = min((int)(blockIdx.y + 1) * a.groups, (a.heads + kHeads - 1) / kHeads);
 
   // The values that the lane takes of a head: two pieces of four, from off_a and off_b.
@@ -105,7 +108,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
       weight_of[i / kD][i % kD] = from != nullptr ? from[i % kD] : 1.0f;
     }
     if (threadIdx.x < half) turn_of[threadIdx.x] = turns_of(a.inv_freq[threadIdx.x]);
-    if (threadIdx.x < tokens) pos_of[threadIdx.x] = a.positions != nullptr ? a.positions[t0 + threadIdx.x] : 0;
+    if (threadIdx.x < kTokens)
+      pos_of[threadIdx.x] = a.positions != nullptr && threadIdx.x < tokens ? a.positions[t0 + threadIdx.x] : 0;
     __syncthreads();
     for (int i = threadIdx.x; i < tokens * half; i += kRopeWarps * 32) {
       const int t = (int)a.by_pairs((uint32_t)i), j = i - t * half;
@@ -123,10 +127,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
     const Rows &in = is_q ? a.q : a.k, &out = is_q ? a.q_out : a.k_out;
     const int h = is_q ? head : head - a.Hq;
     // all tokens' values are on their way before the first is worked on
-    Piece<T> pa[kRopeTokens], pb[kRopeTokens];
+    Piece<T> pa[kTokens], pb[kTokens];
     const T* p = static_cast<const T*>(in.at) + t0 * in.stride_t + h * in.stride_h + off_a;
 #pragma unroll
-    for (int t = 0; t < kRopeTokens; ++t, p += in.stride_t) {
+    for (int t = 0; t < kTokens; ++t, p += in.stride_t) {
       pa[t].zero();
       pb[t].zero();
       if (mine && t < tokens) {
@@ -141,26 +145,24 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
     char* to = static_cast<char*>(out.at) + (t0 * out.stride_t + h * out.stride_h + off_a) * es;
     const int64_t second = (off_b - off_a) * es;
 #pragma unroll
-    for (int t = 0; t < kRopeTokens; ++t, to += step) {
-      if (t >= tokens) break;
+    for (int t = 0; t < kTokens; ++t, to += step) {
       float2 v[4];  // off_a's four values, then off_b's
       pa[t].unpack(v);
       pb[t].unpack(v + 2);
-      if (a.eps >= 0.0f) {
-        float2 q = __fmul2_rn(v[0], v[0]);
+      float2 q = __fmul2_rn(v[0], v[0]);
 #pragma unroll
-        for (int j = 1; j < 4; ++j) q = __ffma2_rn(v[j], v[j], q);
-        float s = q.x + q.y;
+      for (int j = 1; j < 4; ++j) q = __ffma2_rn(v[j], v[j], q);
+      float s = q.x + q.y;
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
-        s = fmaf(s, 1.0f / kD, a.eps);
-        const float r = s > 0.0f ? __frsqrt_rn(s) : 0.0f;
-        const float4 wa = *reinterpret_cast<const float4*>(&weight_of[is_q ? 0 : 1][off_a]);
-        const float4 wb = *reinterpret_cast<const float4*>(&weight_of[is_q ? 0 : 1][off_b]);
-        const float2 w[4] = {{wa.x, wa.y}, {wa.z, wa.w}, {wb.x, wb.y}, {wb.z, wb.w}};
+      for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
+      s = fmaf(s, 1.0f / kD, a.eps);
+      // (2 ulp; without a norm, weights are ones too)
+      const float r = a.eps >= 0.0f ? (s > 0.0f ? rsqrtf(s) : 0.0f) : 1.0f;
+      const float4 wa = *reinterpret_cast<const float4*>(&weight_of[is_q ? 0 : 1][off_a]);
+      const float4 wb = *reinterpret_cast<const float4*>(&weight_of[is_q ? 0 : 1][off_b]);
+      const float2 w[4] = {{wa.x, wa.y}, {wa.z, wa.w}, {wb.x, wb.y}, {wb.z, wb.w}};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(__fmul2_rn(v[j], make_float2(r, r)), w[j]);
-      }
+      for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(__fmul2_rn(v[j], make_float2(r, r)), w[j]);
       if (turned) {
         const float4 c4 = *reinterpret_cast<const float4*>(&cos_of[t][4 * l]);
         const float4 s4 = *reinterpret_cast<const float4*>(&sin_of[t][4 * l]);
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = make_float2(0.0f, 0.0f);
       }
-      if (mine) {
+      if (mine && t < tokens) {
         if (out.bf16) {
           *reinterpret_cast<uint2*>(to) = bf16x4(v);
           *reinterpret_cast<uint2*>(to + second) = bf16x4(v + 2);
@@ -200,16 +202,20 @@ template <typename T, int kD>
 cudaError_t launch_rope(RopeArgs a, int sms, cudaStream_t stream) {
   constexpr int kHeads = 32 / (kD / 8);
   const int groups = (a.heads + kHeads - 1) / kHeads;
-  // Up to four tokens to a CTA, whose angles keep its threads busy, and all of their heads, so
+  // One, two or four tokens to a CTA, whose angles keep its threads busy, and all of their heads, so
   // that angles are computed once; but eight groups of heads, one a warp, where that makes fewer
   // than three CTAs an SM (1000 tokens of 48 heads of 128: 7.1 us for 9.2; 8191: 41.9 for 39.9).
   const int64_t spread = a.T / (2 * (int64_t)sms);
-  a.tokens = (int)(spread < 1 ? 1 : (spread > kRopeTokens ? kRopeTokens : spread));
+  a.tokens = spread < 2 ? 1 : (spread < 4 ? 2 : 4);
   a.groups = (a.T + a.tokens - 1) / a.tokens < 3 * (int64_t)sms && groups > kRopeWarps ? kRopeWarps : groups;
   a.by_pairs = Divider((uint32_t)(a.R > 0 ? a.R / 2 : 1));
   const dim3 grid((unsigned)((a.T + a.tokens - 1) / a.tokens), (unsigned)((groups + a.groups - 1) / a.groups));
-  if (a.pairs) return launch_kernel(rope_kernel<T, kD, true>, grid, dim3(kRopeWarps * 32), 0, stream, a);
-  return launch_kernel(rope_kernel<T, kD, false>, grid, dim3(kRopeWarps * 32), 0, stream, a);
+  const auto run = [&](void (*pairs)(RopeArgs), void (*halves)(RopeArgs)) {
+    return launch_kernel(a.pairs ? pairs : halves, grid, dim3(kRopeWarps * 32), 0, stream, a);
+  };
+  if (a.tokens == 1) return run(rope_kernel<T, kD, true, 1>, rope_kernel<T, kD, false, 1>);
+  if (a.tokens == 2) return run(rope_kernel<T, kD, true, 2>, rope_kernel<T, kD, false, 2>);
+  return run(rope_kernel<T, kD, true, 4>, rope_kernel<T, kD, false, 4>);
 }
 
 template <typename T>

@@ -1,8 +1,9 @@
 """Norm and rotation of queries and keys against the formula in 64 bits.
 
 Tolerances.  n = x r w: the sum of squares of D values is off by 13 roundings at most (8 in a lane, 5 exchanges), its root by
-half of that, and three more follow, so n is off by 11 * 2^-24.  The rotation rounds three times, and sine and cosine are off by
-2 ulp (2^-22) and the angle's 2^-22: together 18 * 2^-24 + 2^-21 < 2^-19 of |n_a| + |n_b|.  bf16 output adds half a step, 2^-8 of the
+half of that, the reciprocal root by 2 ulp (2^-22), and three more roundings follow, so n is off by 11 * 2^-24 + 2^-22.  The rotation
+rounds three times, and sine and cosine are off by 2 ulp (2^-22) and the angle's 2^-22: together 18 * 2^-24 + 3 * 2^-22 = 30 * 2^-24,
+less than 2^-19, of |n_a| + |n_b|.  bf16 output adds half a step, 2^-8 of the
 value."""
 import math
 
