@@ -16,6 +16,16 @@
 //
 // A row is taken by one CTA, or, with few rows, by the CTAs of a cluster, which leave maxima and
 // sums in the first one's shared memory.
+//
+// 2047 rows of 151,936 bf16 logits (622 MB) take 112 us, 82 % of the copy rate: memory, with 0.52
+// instructions a cycle beside it (about 6.5 an element, the exponential's unit 40 % busy) and 10 us
+// of choosing; 640 rows in fp32 (389 MB) 68 us, 84 %.  One row takes 7.4 us: launch 2.1, the read
+// and sums 3.2, the choice 2.1, each a chain of latencies.  Measured and not kept: rescaling sums
+// at every new maximum and keeping it out of them (14 instructions an element, 123 to 169 us);
+// asynchronous copies into a ring of each warp, with the next row's on their way (142 to 198: the
+// ring's own instructions and registers); a second launch for the choice (149 to 196: it reads
+// from DRAM again what L2 no longer holds); maxima stored to the first CTA block by block
+// (addresses of another CTA's memory take four more instructions each).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
