@@ -1,13 +1,14 @@
 // Pages of the cache after they are taken: sequences that share them, copies on write, their
 // return and their compaction.  Rules and orders are stated in memra.h.
 //
-// All but the copy are whole numbers on block tables, 4 bytes an entry, and bound by latency:
-// one launch each.  Where a result depends on all entries (which holder is a page's last, how
-// many pages go before this one) the CTAs of one cluster share the work and meet at the
-// cluster's barrier; counts are atomic, but nothing written depends on their order.  For 256
-// forks of 32 sequences (36,608 cells): fork 1.9 us, copy on write 4, release 12.3; for 4 forks of
-// one 1.5, 1.7, 4.1.  Compaction of 256 pages 6.2, of 6000 pages and 6048 cells 11.1, where one CTA
-// takes 14.9; release with 16 CTAs 14.1.
+// All but the copy are whole numbers on block tables, 4 bytes an entry, and bound by latency: one
+// launch each.  Where a result depends on all entries (which holder is a page's last, how many
+// pages go before this one) either one CTA has the table in its registers and what it counts of
+// each page in its shared memory, or, with more than that, the CTAs of one cluster count in
+// global memory and meet at the cluster's barrier; counts are atomic, but nothing written depends
+// on their order.  For 256 forks of 32 sequences (36,608 cells): fork 1.9 us, copy on write 4,
+// release 12.3 (19.5 of as many random pages); for 4 forks of one 1.5, 1.7, 3.7.  Compaction of 256 pages 3.8, of 6000 pages and 6048 cells 6.8.  Measured and not kept:
+// 16 CTAs for a release (14.1 for 12.3).
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(ReleaseArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Compaction.  Cells and pages in order, cut evenly over the cluster's warps.
+// Compaction.  Cells and pages in order, cut evenly over the cluster's warps: the larger tables.
 // ---------------------------------------------------------------------------
 struct CompactArgs {
   Table t;
@@ -542,6 +543,183 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// Release and compaction of a table of one tile (8192 cells) over a pool of up to 16,384 pages: one
+// CTA, whose shared memory holds what is counted of each page, so that global memory is waited for
+// once or twice instead of at every step.  us, so and with the steps in global memory (by one
+// CTA or a cluster, whichever is faster): a release of all of 1024 pages 4.8 and 7.4, of 8000 8.5
+// and 11.1; compaction of 256 pages 3.8 and 6.2, of 8000 7.4 and 10.5, of 16,384 11.0 and 12.5.
+// ---------------------------------------------------------------------------
+constexpr int kSmallCells = kTile * kThreads, kSmallPages = 16384;
+
+// What the thread's cells of a small table hold: cell tid + 1024 j, -1 for nothing.  `given` says of
+// a cell in use, from its row and place there, whether it counts.
+template <typename Given>
+__device__ __forceinline__ bool cells_of(const Table& t, int32_t* page, Given given) {
+  const int cells = (int)(t.B * t.max_pages);
+  int32_t len[kTile];
+  uint32_t row[kTile];
+#pragma unroll
+  for (int j = 0; j < kTile; ++j) {
+    const int e = threadIdx.x + j * kThreads;
+    row[j] = e < cells ? t.by_row((uint32_t)e) : 0;
+    page[j] = e < cells ? t.entries[e] : -1;
+    len[j] = e < cells ? t.lens[row[j]] : 0;
+  }
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < kTile; ++j) {
+    const int e = threadIdx.x + j * kThreads;
+    const int i = e - (int)row[j] * (int)t.max_pages;
+    bool odd = false;  // lengths are told of elsewhere
+    const bool counts = e < cells && i < t.pages_of(len[j], &odd) && given(row[j], i);
+    if (counts && !t.is_page(page[j])) bad = true;
+    if (!counts || !t.is_page(page[j])) page[j] = -1;
+  }
+  return bad;
+}
+
+__global__ void __launch_bounds__(kThreads) small_release_kernel(ReleaseArgs a) {
+  extern __shared__ int32_t pool[];
+  int32_t *left = pool, *last = pool + a.t.n_pages;  // of a page: its refs, the last cell that gives it up
+  __shared__ int32_t goes_of[kTile][kWarps];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = (int)a.t.n_pages;
+  const int tiles = ((int)(a.t.B * a.t.max_pages) + kThreads - 1) / kThreads;  // of a thread's cells, that are any
+  const int64_t head = *a.free_head;
+  int32_t page[kTile];
+  for (int p = tid; p < n; p += kThreads) {
+    left[p] = __ldcg(a.refs + p);
+    last[p] = -1;
+  }
+  bool bad = cells_of(a.t, page, [&](uint32_t b, int i) {
+    bool odd = false;
+    return a.keep == nullptr || i >= a.t.pages_of(max(a.keep[b], 0), &odd);
+  });
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kTile; ++j)
+    if (page[j] >= 0) {
+      atomicSub(left + page[j], 1);
+      atomicMax(last + page[j], tid + j * kThreads);
+    }
+  __syncthreads();
+  uint32_t goes = 0;
+#pragma unroll
+  for (int j = 0; j < kTile; ++j) {
+    if (j >= tiles) break;
+    const bool go = page[j] >= 0 && last[page[j]] == tid + j * kThreads && left[page[j]] < 0;
+    const uint32_t going = __ballot_sync(kFullMask, go);
+    goes |= (go ? 1u : 0u) << j;
+    if (lane == 0) goes_of[j][warp] = __popc(going);
+  }
+  for (int p = tid; p < n; p += kThreads) {
+    if (last[p] < 0) continue;
+    if (left[p] < -1) bad = true;  // more often than it was held
+    a.refs[p] = max(left[p], 0);
+  }
+  __syncthreads();
+  // cells lie in the order (j, warp, lane)
+  int32_t all = 0;
+  int32_t to[kTile];
+#pragma unroll
+  for (int j = 0; j < kTile; ++j) {
+    if (j >= tiles) break;
+    const int32_t v = goes_of[j][lane];
+    to[j] = all + (int)__reduce_add_sync(kFullMask, lane < warp ? v : 0) +
+            __popc(__ballot_sync(kFullMask, (goes >> j) & 1u) & ((1u << lane) - 1));
+    all += (int)__reduce_add_sync(kFullMask, v);
+  }
+#pragma unroll
+  for (int j = 0; j < kTile; ++j) {
+    const int64_t at = head - all + to[j];
+    if (((goes >> j) & 1u) && at >= 0 && at < a.n_free) a.free_pages[at] = page[j];
+  }
+  int bits = bad ? 1 : 0;
+  for (int64_t b = tid; b < a.t.B; b += kThreads) {
+    bool odd = false;
+    const int32_t len = a.t.lens[b], keep = a.keep != nullptr ? a.keep[b] : 0;
+    (void)a.t.pages_of(len, &odd);
+    if (odd || keep < 0) bits |= 1;
+    const int32_t most = (int32_t)max((int64_t)0, min((int64_t)len, a.t.max_pages * a.t.page));
+    a.lens_out[b] = min(most, max(keep, 0));
+  }
+  if (tid == 0) {
+    if (head - all < 0 || head > a.n_free) bits |= 4;
+    *a.free_head_out = (int32_t)max((int64_t)0, head - all);
+  }
+  tell(bits, a.status);
+}
+
+__global__ void __launch_bounds__(kThreads) small_compact_kernel(CompactArgs a) {
+  extern __shared__ int32_t pool[];
+  const int n = (int)a.t.n_pages, cells = (int)(a.t.B * a.t.max_pages);
+  int32_t *count = pool, *move = pool + n, *hole = pool + 2 * n;  // entries and the move of a page, holes from below
+  __shared__ int32_t used_of[kWarps], moved;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int32_t page[kTile];
+  bool bad = cells_of(a.t, page, [](uint32_t, int) { return true; });
+  for (int64_t b = tid; b < a.t.B; b += kThreads) (void)a.t.pages_of(a.t.lens[b], &bad);
+  for (int p = tid; p < n; p += kThreads) {
+    count[p] = 0;
+    a.free_out[p] = p;
+  }
+  if (tid == 0) moved = 0;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kTile; ++j)
+    if (page[j] >= 0) atomicAdd(count + page[j], 1);
+  __syncthreads();
+  const int chunks = (n + 31) / 32, c0 = chunks * warp / kWarps, c1 = chunks * (warp + 1) / kWarps;
+  int32_t mine = 0;
+  for (int c = c0; c < c1; ++c) mine += __popc(__ballot_sync(kFullMask, c * 32 + lane < n && count[c * 32 + lane] > 0));
+  if (lane == 0) used_of[warp] = mine;
+  __syncthreads();
+  const int32_t used = (int)__reduce_add_sync(kFullMask, used_of[lane]);
+  int32_t before = (int)__reduce_add_sync(kFullMask, lane < warp ? used_of[lane] : 0);
+  for (int c = c0; c < c1; ++c) {
+    const int p = c * 32 + lane;
+    const bool held = p < n && count[p] > 0;
+    const uint32_t in_use = __ballot_sync(kFullMask, held);
+    const int32_t below = before + __popc(in_use & ((1u << lane) - 1));
+    before += __popc(in_use);
+    if (p == used) moved = used - below;
+    if (p >= used) {
+      if (held) {
+        move[p] = used - 1 - below;
+        a.src[used - 1 - below] = p;
+      }
+    } else if (!held) {
+      hole[p - below] = p;
+    }
+  }
+  __syncthreads();
+  const int moves = moved;
+  for (int k = tid; k < n / 2; k += kThreads) {
+    if (k >= moves) a.src[k] = -1;
+    a.dst[k] = k < moves ? hole[k] : -1;
+  }
+  for (int p = tid; p < n; p += kThreads) {
+    const int32_t c = count[p];
+    if (p < used) {
+      if (c > 0) a.refs[p] = c - 1;
+    } else {
+      a.refs[p] = 0;
+      if (c > 0) a.refs[hole[move[p]]] = c - 1;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kTile; ++j) {
+    const int e = tid + j * kThreads;
+    if (e < cells) a.table_out[e] = page[j] >= used ? hole[move[page[j]]] : page[j];
+  }
+  if (tid == 0) *a.free_head_out = used;
+  tell(bad ? 1 : 0, a.status);
+}
+
+// ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
 
@@ -618,6 +796,19 @@ cudaError_t launch_cluster(void (*kernel)(Args), int64_t cells, cudaStream_t str
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
+
+// The one CTA of a small table, with so many bytes of shared memory to a page.
+template <typename Args>
+cudaError_t launch_small(void (*kernel)(Args), int bytes, cudaStream_t stream, const Args& a) {
+  const int smem = bytes * (int)a.t.n_pages;
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes * kSmallPages);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_kernel(kernel, dim3(1), dim3(kThreads), (size_t)smem, stream, a);
+}
+
+bool is_small(const Table& t) { return t.B * t.max_pages <= kSmallCells && t.n_pages <= kSmallPages; }
 
 }  // namespace
 }  // namespace memra
@@ -761,7 +952,8 @@ extern "C" memra_status memra_kv_release(const int32_t* lens, const int32_t* kee
   a.lens_out = lens_out;
   a.free_head_out = free_head_out;
   a.status = dev_status;
-  const cudaError_t e = launch_cluster(release_kernel, B * max_pages, stream, a);
+  const cudaError_t e = is_small(a.t) ? launch_small(small_release_kernel, 8, stream, a)
+                                      : launch_cluster(release_kernel, B * max_pages, stream, a);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }
@@ -789,7 +981,8 @@ extern "C" memra_status memra_kv_compact(const int32_t* lens, const int32_t* blo
   a.dst = dst;
   a.free_head_out = free_head_out;
   a.status = dev_status;
-  const cudaError_t e = launch_cluster(compact_kernel, B * max_pages + n_pages, stream, a);
+  const cudaError_t e = is_small(a.t) ? launch_small(small_compact_kernel, 10, stream, a)
+                                      : launch_cluster(compact_kernel, B * max_pages + n_pages, stream, a);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }

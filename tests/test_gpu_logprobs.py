@@ -186,6 +186,14 @@ def test_on_both_sides_of_the_threads_rule(mem, T, dtype):
     check(mem, x, tok, 6)
 
 
+@pytest.mark.parametrize("T", [310, 620])
+@pytest.mark.parametrize("V,n", [(15359, 5), (15360, 5), (30719, 10), (30720, 10)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_on_both_sides_of_the_rule_for_what_is_read_again(mem, T, V, n, dtype):
+    x, tok = rows(T, V, dtype, seed=n, pad=1)
+    check(mem, x, tok, n)
+
+
 def staged(T, V, seed):
     """Rows whose first elements, which a warp's sums refer to, say little about the others."""
     g = torch.Generator().manual_seed(seed)

@@ -330,6 +330,26 @@ def test_compact_odd_inputs(mem):
     check_compact(mem, np.array([16]), np.array([[1]]), 16, 2)
 
 
+@pytest.mark.parametrize("B,W,n", [(64, 128, 300), (64, 129, 300), (8192, 1, 9000), (8193, 1, 9000), (8, 40, 16384), (8, 40, 16385), (1, 1, 16384),
+                                   (3, 7, 1), (5, 1024, 16383), (1, 8192, 12000)])
+def test_tables_and_pools_on_both_sides_of_the_small_ones(mem, B, W, n):
+    """Any pages at all in the table, many of them shared, and lengths that end anywhere."""
+    rs = np.random.RandomState(B + W + n)
+    P = 16
+    table, lens = rs.randint(0, n, (B, W)), rs.randint(0, P * W + 1, B)
+    lens[0] = P * W
+    held = np.zeros(n, int)
+    for b in range(B):
+        np.add.at(held, table[b, :pages(lens[b], P)], 1)
+    refs, used = np.maximum(held - 1, 0), int((held > 0).sum())
+    check_compact(mem, lens, table, P, n)
+    check_compact(mem, np.where(rs.rand(B) < 0.5, lens, 0), table, P, n, in_place=True)
+    gone = check_release(mem, lens, P, table, refs, rs.permutation(n), used)
+    assert gone[1] == 0 and not gone[2].any()
+    check_release(mem, lens, P, table, refs, rs.permutation(n), used, keep=rs.randint(0, P * W + 1, B), in_place=True)
+    check_release(mem, lens, P, table, refs, rs.permutation(n)[:used // 2], used // 3)
+
+
 # ---------------------------------------------------------------------------
 # Copies.
 # ---------------------------------------------------------------------------
