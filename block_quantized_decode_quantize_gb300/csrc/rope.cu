@@ -4,7 +4,7 @@
 // row of D values lies on D / 8 lanes, so the sum of squares takes 3 to 5 exchanges, and each
 // lane holds two pieces of four values that are each other's partners in the rotation:
 // nothing else passes between lanes, and a row is read and written once.  A warp takes 32 lanes'
-// worth of heads (a group) of one, two or four tokens, all of whose loads are on their way
+// worth of heads (a group) of a set of one, two or four tokens, all of whose loads are on their way
 // before the first is worked on.  A CTA's threads compute the R / 2 angles of a token once, for
 // all of its heads, and leave cos and sin in shared memory meanwhile.
 //
@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kRopeWarps = 8;
 constexpr int kMaxPairs = 128;   // R / 2, at most
+constexpr int kMaxSets = 4;     // of four tokens, that a CTA takes
 
 struct Rows {
   void* at;
@@ -37,12 +38,13 @@ struct Rows {
 struct RopeArgs {
   Rows q, k, q_out, k_out;
   int64_t T;
-  int Hq, heads, R, pairs, tokens, groups;  // groups: warps' shares of heads that a CTA takes
+  int Hq, heads, R, pairs, tokens;
+  int sets, groups;  // what a CTA takes: sets of so many tokens, groups of heads
   const float *q_weight, *k_weight;
   float eps;
   const int32_t* positions;
   const double* inv_freq;
-  Divider by_pairs;
+  Divider by_pairs, by_groups;
 };
 
 // Four values of a row.
@@ -81,20 +83,22 @@ __device__ __forceinline__ uint64_t turns_of(double inv_freq) {
   return __double2ull_rn(u * 18446744073709551616.0);
 }
 
-template <typename T, int kD, bool kPairs, int kTokens>
+template <typename T, int kD, bool kPairs, int kTokens, bool kSets>
 __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
   constexpr int kLanes = kD / 8;         // of a head
   constexpr int kHeads = 32 / kLanes;    // that a warp takes at once: a group
-  __shared__ __align__(16) float cos_of[kTokens][kMaxPairs], sin_of[kTokens][kMaxPairs];
+  constexpr int kAll = kTokens * (kSets ? kMaxSets : 1);
+  __shared__ __align__(16) float cos_of[kAll][kMaxPairs], sin_of[kAll][kMaxPairs];
   __shared__ __align__(16) float weight_of[2][kD];
   __shared__ uint64_t turn_of[kMaxPairs];
-  __shared__ int32_t pos_of[kTokens];
+  __shared__ int32_t pos_of[kAll];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t0 = (int64_t)blockIdx.x * kTokens;
-  const int tokens = (int)min((int64_t)kTokens, a.T - t0);
-  const int end = min((int)(blockIdx.y + 1) * a.groups, (a.heads + kHeads - 1) / kHeads);
+  const int64_t t0 = (int64_t)blockIdx.x * (kSets ? a.sets : 1) * kTokens;
+  const int tokens = (int)min((int64_t)(kSets ? a.sets : 1) * kTokens, a.T - t0);
+  const int end = kSets ? (tokens + kTokens - 1) / kTokens * a.groups
+                        : min((int)(blockIdx.y + 1) * a.groups, (a.heads + kHeads - 1) / kHeads);
 
   // The values that the lane takes of a head: two pieces of four, from off_a and off_b.
   const int l = lane % kLanes;
@@ -110,7 +114,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
       weight_of[i / kD][i % kD] = from != nullptr ? from[i % kD] : 1.0f;
     }
     if (threadIdx.x < half) turn_of[threadIdx.x] = turns_of(a.inv_freq[threadIdx.x]);
-    if (threadIdx.x < kTokens)
+    if (threadIdx.x < kAll)
       pos_of[threadIdx.x] = a.positions != nullptr && threadIdx.x < tokens ? a.positions[t0 + threadIdx.x] : 0;
     __syncthreads();
     for (int i = threadIdx.x; i < tokens * half; i += kRopeWarps * 32) {
@@ -123,28 +127,29 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
   };
 
   bool first = true;
-  for (int g = blockIdx.y * a.groups + warp; g < end || first; g += kRopeWarps) {
-    const int head = g * kHeads + lane / kLanes;
-    const bool mine = g < end && head < a.heads, is_q = head < a.Hq;
+  for (int i = (kSets ? 0 : blockIdx.y * a.groups) + warp; i < end || first; i += kRopeWarps) {
+    const int set = kSets ? (int)a.by_groups((uint32_t)i) : 0, first_t = set * kTokens;
+    const int head = (i - set * a.groups) * kHeads + lane / kLanes;
+    const bool mine = i < end && head < a.heads, is_q = head < a.Hq;
     const Rows &in = is_q ? a.q : a.k, &out = is_q ? a.q_out : a.k_out;
     const int h = is_q ? head : head - a.Hq;
     // all tokens' values are on their way before the first is worked on
     Piece<T> pa[kTokens], pb[kTokens];
-    const T* p = static_cast<const T*>(in.at) + t0 * in.stride_t + h * in.stride_h + off_a;
+    const T* p = static_cast<const T*>(in.at) + (t0 + first_t) * in.stride_t + h * in.stride_h + off_a;
 #pragma unroll
     for (int t = 0; t < kTokens; ++t, p += in.stride_t) {
       pa[t].zero();
       pb[t].zero();
-      if (mine && t < tokens) {
+      if (mine && first_t + t < tokens) {
         pa[t].load(p);
         pb[t].load(p + (off_b - off_a));
       }
     }
     if (first) prepare();
     first = false;
-    if (g >= end) break;
+    if (i >= end) break;
     const int64_t es = out.bf16 ? 2 : 4, step = out.stride_t * es;
-    char* to = static_cast<char*>(out.at) + (t0 * out.stride_t + h * out.stride_h + off_a) * es;
+    char* to = static_cast<char*>(out.at) + ((t0 + first_t) * out.stride_t + h * out.stride_h + off_a) * es;
     const int64_t second = (off_b - off_a) * es;
 #pragma unroll
     for (int t = 0; t < kTokens; ++t, to += step) {
@@ -166,8 +171,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(__fmul2_rn(v[j], make_float2(r, r)), w[j]);
       if (turned) {
-        const float4 c4 = *reinterpret_cast<const float4*>(&cos_of[t][4 * l]);
-        const float4 s4 = *reinterpret_cast<const float4*>(&sin_of[t][4 * l]);
+        const float4 c4 = *reinterpret_cast<const float4*>(&cos_of[first_t + t][4 * l]);
+        const float4 s4 = *reinterpret_cast<const float4*>(&sin_of[first_t + t][4 * l]);
         if (kPairs) {
           const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
@@ -183,11 +188,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
           }
         }
       }
-      if (pos_of[t] < 0) {
+      if (pos_of[first_t + t] < 0) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = make_float2(0.0f, 0.0f);
       }
-      if (mine && t < tokens) {
+      if (mine && first_t + t < tokens) {
         if (out.bf16) {
           *reinterpret_cast<uint2*>(to) = bf16x4(v);
           *reinterpret_cast<uint2*>(to + second) = bf16x4(v + 2);
@@ -211,13 +216,23 @@ cudaError_t launch_rope(RopeArgs a, int sms, cudaStream_t stream) {
   a.tokens = spread < 2 ? 1 : (spread < 4 ? 2 : 4);
   a.groups = (a.T + a.tokens - 1) / a.tokens < 3 * (int64_t)sms && groups > kRopeWarps ? kRopeWarps : groups;
   a.by_pairs = Divider((uint32_t)(a.R > 0 ? a.R / 2 : 1));
-  const dim3 grid((unsigned)((a.T + a.tokens - 1) / a.tokens), (unsigned)((groups + a.groups - 1) / a.groups));
+  a.by_groups = Divider((uint32_t)a.groups);
+  // Few heads, or a number of groups that leaves warps idle: two or four sets of four tokens to a
+  // CTA where that leaves fewer idle, with two CTAs an SM at least (8000 tokens of 2 heads of 128
+  // 4.8 us for 9.6, of 24 of 64 12.7 for 14.4; four CTAs an SM at least 6.5 and 14.4).
+  a.sets = 1;
+  const auto idle = [&](int sets) { return (sets * a.groups + kRopeWarps - 1) / kRopeWarps * (kMaxSets / sets); };
+  for (int sets = 2; sets <= kMaxSets && a.tokens == 4 && a.groups == groups; sets *= 2)
+    if (idle(sets) < idle(a.sets) && a.T >= sets * 4 * 2 * (int64_t)sms) a.sets = sets;
+  const int of_cta = a.sets * a.tokens;
+  const dim3 grid((unsigned)((a.T + of_cta - 1) / of_cta), (unsigned)((groups + a.groups - 1) / a.groups));
   const auto run = [&](void (*pairs)(RopeArgs), void (*halves)(RopeArgs)) {
     return launch_kernel(a.pairs ? pairs : halves, grid, dim3(kRopeWarps * 32), 0, stream, a);
   };
-  if (a.tokens == 1) return run(rope_kernel<T, kD, true, 1>, rope_kernel<T, kD, false, 1>);
-  if (a.tokens == 2) return run(rope_kernel<T, kD, true, 2>, rope_kernel<T, kD, false, 2>);
-  return run(rope_kernel<T, kD, true, 4>, rope_kernel<T, kD, false, 4>);
+  if (a.tokens == 1) return run(rope_kernel<T, kD, true, 1, false>, rope_kernel<T, kD, false, 1, false>);
+  if (a.tokens == 2) return run(rope_kernel<T, kD, true, 2, false>, rope_kernel<T, kD, false, 2, false>);
+  if (a.sets == 1) return run(rope_kernel<T, kD, true, 4, false>, rope_kernel<T, kD, false, 4, false>);
+  return run(rope_kernel<T, kD, true, 4, true>, rope_kernel<T, kD, false, 4, true>);
 }
 
 template <typename T>

@@ -103,6 +103,24 @@ def test_rows_and_heads(mem, T, Hq, Hkv):
         assert bool((o[pos < 0] == 0).all())
 
 
+@pytest.mark.parametrize("T", [2431, 2432, 2437, 4863, 4864, 4866, 4881])
+@pytest.mark.parametrize("Hq,Hkv,D,layout,dtype", [(1, 1, 128, "halves", "bf16"), (4, 4, 128, "pairs", "fp32"), (16, 1, 64, "halves", "fp32"),
+                                                   (8, 1, 128, "halves", "bf16"), (3, 0, 256, "pairs", "bf16")])
+def test_few_heads_of_many_tokens(mem, T, Hq, Hkv, D, layout, dtype):
+    """Several sets of tokens to a CTA, the last of them cut anywhere; beside what is compared, the rows of
+    tokens alone are the same bits."""
+    _, q, k, pos, f, w = case(T, Hq, Hkv, D, D // 2, dtype, seed=T + D)
+    pos[T - 3] = -1
+    norm = dict(q_weight=w[0], k_weight=w[1], eps=1e-5, layout=layout)
+    qo, ko = mem.memra_qk_norm_rope(q, k, pos, f, **norm)
+    for x, o, wt in ((q, qo, w[0]), (k, ko, w[1])):
+        if x.shape[1]:
+            check(o, *reference(x, pos, f, wt, 1e-5, layout), "T %d" % T)
+    for t0, t1 in ((0, 1), (5, 7), (T - 5, T)):
+        a, b = mem.memra_qk_norm_rope(q[t0:t1], k[t0:t1], pos[t0:t1], f, **norm)
+        assert torch.equal(a, qo[t0:t1]) and torch.equal(b, ko[t0:t1])
+
+
 @pytest.mark.parametrize("R", [8, 24, 40, 72, 120, 128])
 @pytest.mark.parametrize("layout", ["halves", "pairs"])
 def test_any_rotated_part(mem, R, layout):
