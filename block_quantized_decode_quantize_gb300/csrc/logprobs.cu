@@ -17,9 +17,9 @@
 // A row is taken by one CTA, or, with few rows, by the CTAs of a cluster, which leave maxima and
 // sums in the first one's shared memory.
 //
-// 2047 rows of 151,936 bf16 logits (622 MB) take 112 us, 82 % of the copy rate: memory, with 0.52
-// instructions a cycle beside it (about 6.5 an element, the exponential's unit 40 % busy) and 10 us
-// of choosing; 640 rows in fp32 (389 MB) 68 us, 84 %.  One row takes 7.4 us: launch 2.1, the read
+// 2047 rows of 151,936 bf16 logits (622 MB) take 106 us, 87 % of the copy rate: memory, with 0.54
+// instructions a cycle beside it (about 6.5 for 32 elements, the exponential's unit 40 % busy) and
+// 5 us of choosing; 640 rows in fp32 (389 MB) 66.5 us, 86 %.  One row takes 7.4 us: launch 2.1, the read
 // and sums 3.2, the choice 2.1, each a chain of latencies.  Measured and not kept: rescaling sums
 // at every new maximum and keeping it out of them (14 instructions an element, 123 to 169 us);
 // asynchronous copies into a ring of each warp, with the next row's on their way (142 to 198: the
@@ -28,6 +28,8 @@
 // (addresses of another CTA's memory take four more instructions each).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -38,8 +40,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kBlock = 256;         // elements a warp looks at together: 8 a lane
 constexpr int kMost = 512;          // candidates that are ranked by counting
-constexpr int kFineVocab = 8192;    // see logprob_kernel
-constexpr int kMaxWarps = 256;      // of a row: 16 CTAs of 16
+constexpr int kFineBytes = 65536;   // of a row with fine segments, at most
+constexpr int kMaxWarps = 256;      // of a row: 16 CTAs of 16 (of smaller CTAs, one has a row)
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 constexpr float kLargest = 3.402823466e38f;
 constexpr float kFloor = -160.0f;   // 2^u is 0 in fp32 below
@@ -57,6 +59,7 @@ struct LogprobArgs {
   int64_t T, stride_t;
   int V, top_n;
   int segments;             // of a row, at most
+  bool fine;                // they are pieces of 16 bytes
   const int32_t* tokens;
   float *logprobs, *entropy, *top_logprobs;
   int32_t *top_ids, *status;
@@ -455,8 +458,9 @@ __device__ __forceinline__ Part sum_share(const LogprobArgs& a, const Row<T>& ro
   return part;
 }
 
+template <int kParts>
 struct Shared {
-  Part part[kMaxWarps];
+  Part part[kParts];
   unsigned long long candidate[kMost];
   int count, special;  // special: the warp that met the largest element, -1 where its lane's sums do
   float bound, top, z, s;
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(Logp
   constexpr int kWarps = kThreads / 32;
   using R = Row<T>;
   extern __shared__ float seg_max[];  // the row's first CTA
-  __shared__ Shared sh;
+  __shared__ Shared<kThreads == 512 ? kMaxWarps : kWarps> sh;
   pdl_launch_dependents();
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(Logp
   const int64_t t = blockIdx.x / ranks;
   const R row(static_cast<const T*>(a.logits) + t * a.stride_t, a.V);
   // Segments: blocks, or, where these are too few to tell top_n elements apart, pieces of 16 bytes.
-  const bool fine = a.V <= kFineVocab && a.top_n > 0;
+  const bool fine = a.fine;
   const int blocks = row.blocks(), segments = fine ? blocks * 32 * R::kPieces : blocks;
   if (threadIdx.x == 0) sh.count = 0;
   pdl_wait();
@@ -616,53 +620,74 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(Logp
       const int n = atomicAdd(&sh.count, 1);
       if (n < kMost) sh.candidate[n] = ((unsigned long long)order_of(sane(v)) << 32) | (uint32_t)~(uint32_t)(at - row.shift);
     };
-    auto consider_block = [&](const typename R::Raw& raw, int seg) {
-      float v[8];
-      R::unpack(raw, v);
+    // kN values that reach the bound or not; place_of: where the j-th lies
+    auto consider = [&](const auto& v, auto n, auto place_of) {
+      constexpr int kN = decltype(n)::value;
       uint32_t reach = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) reach |= v[j] >= bound ? 1u << j : 0u;
+      for (int j = 0; j < kN; ++j) reach |= v[j] >= bound ? 1u << j : 0u;
 #pragma unroll 1
       for (; reach != 0; reach &= reach - 1) {
         const int j = __ffs(reach) - 1;
         float x = v[0];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) x = j == k ? v[k] : x;
-        take(x, R::place(seg, lane, j));
+        for (int k = 1; k < kN; ++k) x = j == k ? v[k] : x;
+        take(x, place_of(j));
       }
     };
-    for (int i0 = 0; i0 < segments; i0 += 32 * kLook) {  // neighbouring segments to different warps
-      const int mine = i0 + lane * kLook + warp - 1;
-      const bool reaches = mine < segments && seg_max[mine] >= bound;
-      if (fine) {
-        if (reaches)
+    auto consider_block = [&](const typename R::Raw& raw, int seg) {
+      float v[8];
+      R::unpack(raw, v);
+      consider(v, std::integral_constant<int, 8>(), [&](int j) { return R::place(seg, lane, j); });
+    };
+    if (fine) {
+      // each lane notes which of its segments reach the bound, up to 32 of them, then reads those
+      for (int i0 = lane * kLook + warp - 1; i0 < segments; i0 += 32 * 32 * kLook) {
+        uint32_t reach = 0;
+        for (int n = 0; n < 32 && i0 + n * 32 * kLook < segments; ++n) reach |= seg_max[i0 + n * 32 * kLook] >= bound ? 1u << n : 0u;
 #pragma unroll 1
-          for (int p = max(mine * R::kPer, row.shift); p < min((mine + 1) * R::kPer, row.end); ++p) {
-            const float v = element<T>(row.base + p);
-            if (v >= bound) take(v, p);
+        for (; reach != 0; reach &= reach - 1) {
+          const int first = (i0 + (__ffs(reach) - 1) * 32 * kLook) * R::kPer;
+          if (first >= row.shift && first + R::kPer <= row.end) {
+            typename R::Raw raw;
+            raw.u[0] = raw.u[R::kPieces - 1] = __ldcg(reinterpret_cast<const uint4*>(row.base + first));
+            float v[8];
+            R::unpack(raw, v);
+            consider(v, std::integral_constant<int, R::kPer>(), [&](int j) { return first + j; });
+          } else {
+#pragma unroll 1
+            for (int p = max(first, row.shift); p < min(first + R::kPer, row.end); ++p) {
+              const float v = element<T>(row.base + p);
+              if (v >= bound) take(v, p);
+            }
           }
-        continue;
-      }
-      const bool whole = mine >= f && mine < row.end_whole();
-      uint32_t hits = __ballot_sync(kFullMask, reaches && whole);
-      while (hits != 0) {
-        constexpr int kTogether = R::kWide && kThreads < 512 ? 4 : 2;  // (1 to 3 % each)
-        int seg[kTogether];
-        typename R::Raw raw[kTogether];
-#pragma unroll
-        for (int j = 0; j < kTogether; ++j) {
-          seg[j] = hits != 0 ? i0 + (__ffs(hits) - 1) * kLook + warp - 1 : -1;
-          hits &= hits - 1;
-          if (seg[j] >= 0) raw[j] = row.fetch_whole(seg[j], lane);
         }
-#pragma unroll
-        for (int j = 0; j < kTogether; ++j)
-          if (seg[j] >= 0) consider_block(raw[j], seg[j]);
       }
+    } else {
+      for (int i0 = 0; i0 < segments; i0 += 32 * kLook) {  // neighbouring segments to different warps
+        const int mine = i0 + lane * kLook + warp - 1;
+        const bool reaches = mine < segments && seg_max[mine] >= bound;
+        const bool whole = mine >= f && mine < row.end_whole();
+        uint32_t hits = __ballot_sync(kFullMask, reaches && whole);
+        while (hits != 0) {
+          constexpr int kTogether = R::kWide && kThreads < 512 ? 4 : 2;  // (1 to 3 % each)
+          int seg[kTogether];
+          typename R::Raw raw[kTogether];
+#pragma unroll
+          for (int j = 0; j < kTogether; ++j) {
+            seg[j] = hits != 0 ? i0 + (__ffs(hits) - 1) * kLook + warp - 1 : -1;
+            hits &= hits - 1;
+            if (seg[j] >= 0) raw[j] = row.fetch_whole(seg[j], lane);
+          }
+#pragma unroll
+          for (int j = 0; j < kTogether; ++j)
+            if (seg[j] >= 0) consider_block(raw[j], seg[j]);
+        }
 #pragma unroll 1
-      for (hits = __ballot_sync(kFullMask, reaches && !whole); hits != 0; hits &= hits - 1) {
-        const int seg = i0 + (__ffs(hits) - 1) * kLook + warp - 1;
-        consider_block(row.fetch(seg, lane), seg);
+        for (hits = __ballot_sync(kFullMask, reaches && !whole); hits != 0; hits &= hits - 1) {
+          const int seg = i0 + (__ffs(hits) - 1) * kLook + warp - 1;
+          consider_block(row.fetch(seg, lane), seg);
+        }
       }
     }
   }
@@ -825,7 +850,11 @@ extern "C" memra_status memra_token_logprobs(const void* logits, int32_t dtype, 
   a.V = (int)V;
   a.top_n = (int)top_n;
   const int64_t blocks = (V + 16 / es - 1 + kBlock - 1) / kBlock;
-  a.segments = (int)(V <= kFineVocab ? blocks * kBlock * es / 16 : blocks);
+  // Fine segments where a sixth of the blocks or more would be read again, as far as shared memory
+  // goes.  us with blocks and with pieces, bf16: 7820 rows of 6885 with 5 alternatives 55 and 52, 4000
+  // of 30,121 with 32 74 and 71, with 5 55 and 63; 301 of 32,003 with 10 8.4 and 8.7.
+  a.fine = V * es <= kFineBytes && V < 6 * kBlock * top_n;
+  a.segments = (int)(a.fine ? blocks * kBlock * es / 16 : blocks);
   a.tokens = tokens;
   a.logprobs = logprobs;
   a.entropy = entropy;

@@ -194,6 +194,18 @@ def test_on_both_sides_of_the_rule_for_what_is_read_again(mem, T, V, n, dtype):
     check(mem, x, tok, n)
 
 
+@pytest.mark.parametrize("dtype,V", [("bf16", 30719), ("bf16", 30720), ("bf16", 32768), ("bf16", 32769), ("fp32", 16384), ("fp32", 16385)])
+@pytest.mark.parametrize("T", [2, 200, 400, 700])
+def test_on_both_sides_of_the_rule_for_segments(mem, dtype, V, T):
+    """Rows at odd places, and in some of them many elements that are equal or lie close together."""
+    for n in (20, 32):
+        x, tok = rows(T, V, dtype, seed=T + n, pad=1)
+        x[0, V // 2:] = 9.0
+        x[1, 100:100 + 600] = x[1, 100:100 + 600] * 0.01 + 20.0
+        x[T // 2, :V - n // 2] = -math.inf
+        check(mem, x, tok, n)
+
+
 def staged(T, V, seed):
     """Rows whose first elements, which a warp's sums refer to, say little about the others."""
     g = torch.Generator().manual_seed(seed)
