@@ -7,8 +7,9 @@
 // each page in its shared memory, or, with more than that, the CTAs of one cluster count in
 // global memory and meet at the cluster's barrier; counts are atomic, but nothing written depends
 // on their order.  For 256 forks of 32 sequences (36,608 cells): fork 1.9 us, copy on write 4,
-// release 12.3 (19.5 of as many random pages); for 4 forks of one 1.5, 1.7, 3.7.  Compaction of 256 pages 3.8, of 6000 pages and 6048 cells 6.8.  Measured and not kept:
-// 16 CTAs for a release (14.1 for 12.3).
+// release 12.3 (19.5 of as many random pages); for 4 forks of one 1.5, 1.7, 3.1.  Compaction of
+// 256 pages 3.1, of 6000 pages and 6048 cells 6.8.  Measured and not kept: 16 CTAs for a release
+// (14.1 for 12.3).
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a) {
 // CTA, whose shared memory holds what is counted of each page, so that global memory is waited for
 // once or twice instead of at every step.  us, so and with the steps in global memory (by one
 // CTA or a cluster, whichever is faster): a release of all of 1024 pages 4.8 and 7.4, of 8000 8.5
-// and 11.1; compaction of 256 pages 3.8 and 6.2, of 8000 7.4 and 10.5, of 16,384 11.0 and 12.5.
+// and 11.1; compaction of 256 pages 3.1 and 6.2, of 8000 7.4 and 10.5, of 16,384 11.0 and 12.5.
 // ---------------------------------------------------------------------------
 constexpr int kSmallCells = kTile * kThreads, kSmallPages = 16384;
 
@@ -559,7 +560,10 @@ __device__ __forceinline__ bool cells_of(const Table& t, int32_t* page, Given gi
   int32_t len[kTile];
   uint32_t row[kTile];
 #pragma unroll
+  for (int j = 0; j < kTile; ++j) page[j] = -1;
+#pragma unroll
   for (int j = 0; j < kTile; ++j) {
+    if (j * kThreads >= cells) break;
     const int e = threadIdx.x + j * kThreads;
     row[j] = e < cells ? t.by_row((uint32_t)e) : 0;
     page[j] = e < cells ? t.entries[e] : -1;
@@ -568,6 +572,7 @@ __device__ __forceinline__ bool cells_of(const Table& t, int32_t* page, Given gi
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < kTile; ++j) {
+    if (j * kThreads >= cells) break;
     const int e = threadIdx.x + j * kThreads;
     const int i = e - (int)row[j] * (int)t.max_pages;
     bool odd = false;  // lengths are told of elsewhere
