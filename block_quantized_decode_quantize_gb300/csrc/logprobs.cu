@@ -804,8 +804,8 @@ cudaError_t launch_logprobs(const LogprobArgs& a, const DeviceInfo& info, cudaSt
   // 1024 threads an SM.  Up to two rows an SM, CTAs of 512 threads, clusters of them where rows are
   // fewer (with four blocks a warp at least); up to four, CTAs of 256; CTAs of 128 beyond, which
   // leave the fewest threads waiting while a row's choice is made.  us for 301 rows of 32,003 bf16
-  // logits, 553 of 114,789 fp32 and 2047 of 151,936 bf16: 512 threads 8.2, 49.1, 118.9; 256 9.1,
-  // 47.9, 118.9; 128 10.8, 59.3, 111.8.
+  // logits, 553 of 114,789 fp32 and 2047 of 151,936 bf16: 512 threads 8.3, 49.4, 113.0; 256 9.2,
+  // 46.0, 112.1; 128 11.0, 57.2, 105.9.
   if (a.T <= 2 * info.sms) {
     int ranks = 1;
     while (ranks < 16 && a.T * ranks * 2 <= 2 * info.sms && (int64_t)ranks * 2 * 16 * 4 * kBlock <= a.V) ranks *= 2;
