@@ -648,19 +648,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(Logp
 #pragma unroll 1
         for (; reach != 0; reach &= reach - 1) {
           const int first = (i0 + (__ffs(reach) - 1) * 32 * kLook) * R::kPer;
-          if (first >= row.shift && first + R::kPer <= row.end) {
-            typename R::Raw raw;
-            raw.u[0] = raw.u[R::kPieces - 1] = __ldcg(reinterpret_cast<const uint4*>(row.base + first));
-            float v[8];
-            R::unpack(raw, v);
-            consider(v, std::integral_constant<int, R::kPer>(), [&](int j) { return first + j; });
-          } else {
-#pragma unroll 1
-            for (int p = max(first, row.shift); p < min(first + R::kPer, row.end); ++p) {
-              const float v = element<T>(row.base + p);
-              if (v >= bound) take(v, p);
-            }
+          float v[R::kPer];
+#pragma unroll
+          for (int j = 0; j < R::kPer; ++j) {
+            const int p = first + j;
+            v[j] = p >= row.shift && p < row.end ? element<T>(row.base + p) : -inf();
           }
+          consider(v, std::integral_constant<int, R::kPer>(), [&](int j) { return first + j; });
         }
       }
     } else {
