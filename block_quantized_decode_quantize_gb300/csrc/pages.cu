@@ -8,8 +8,8 @@
 // global memory and meet at the cluster's barrier; counts are atomic, but nothing written depends
 // on their order.  For 256 forks of 32 sequences (36,608 cells): fork 1.9 us, copy on write 4,
 // release 12.3 (19.5 of as many random pages); for 4 forks of one 1.5, 1.7, 3.1.  Compaction of
-// 256 pages 3.1, of 6000 pages and 6048 cells 6.8.  Measured and not kept: 16 CTAs for a release
-// (14.1 for 12.3).
+// 256 pages 3.1, of 6000 pages and 6048 cells 6.8.  Measured and not kept: for a large release
+// 16 CTAs (14.1 for 12.3), counts in the shared memories of the cluster (13.7).
 #include <cooperative_groups.h>
 
 #include "common.cuh"

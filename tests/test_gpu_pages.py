@@ -333,6 +333,16 @@ def test_compact_odd_inputs(mem):
 @pytest.mark.parametrize("B,W,n", [(64, 128, 300), (64, 129, 300), (8192, 1, 9000), (8193, 1, 9000), (8, 40, 16384), (8, 40, 16385), (1, 1, 16384),
                                    (3, 7, 1), (5, 1024, 16383), (1, 8192, 12000)])
 def test_tables_and_pools_on_both_sides_of_the_small_ones(mem, B, W, n):
+    any_pages(mem, B, W, n)
+
+
+@pytest.mark.parametrize("B,W,n", [(64, 64, 3000), (4097, 1, 3000), (40, 64, 16384), (40, 64, 16385), (70, 100, 131072), (70, 100, 131073), (64, 1024, 9000),
+                                   (65, 1009, 9000), (1, 65536, 70000), (300, 150, 8), (300, 150, 9), (9000, 7, 40000), (2, 1, 100000)])
+def test_larger_tables_and_pools(mem, B, W, n):
+    any_pages(mem, B, W, n)
+
+
+def any_pages(mem, B, W, n):
     """Any pages at all in the table, many of them shared, and lengths that end anywhere."""
     rs = np.random.RandomState(B + W + n)
     P = 16
