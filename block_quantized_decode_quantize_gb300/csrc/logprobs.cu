@@ -255,6 +255,8 @@ __device__ __forceinline__ float bound_of(const float* seg_max, int segments, in
     for (int j = 0; j < 4; ++j)
       if (i + 32 * j < segments) g[j] = fmaxf(g[j], seg_max[i + 32 * j]);
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) g[j] = sane(g[j]);  // what equals +inf may lie in segments without one
   float least = inf(), over = -inf();
   int numbers = 0;
 #pragma unroll
@@ -713,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(Logp
       float best = -inf();
       int seg = 0x7fffffff;
       for (int i = lane; i < segments; i += 32) {
-        const float v = seg_max[i];
+        const float v = sane(seg_max[i]);  // as the keys: +inf ties with the largest finite value
         if (v > best) {
           best = v;
           seg = i;
