@@ -350,11 +350,14 @@ __device__ __forceinline__ void sum_batches(const LogprobArgs& a, const Row<T>& 
       for (int j = 1; j < kAhead; ++j) v = lane == j ? block_most[j] : v;
       if (lane < kAhead) seg_max[b0 + lane] = v;
     }
-    if (i == 0) {
+    // Sums refer to the first batch that has a token left: batches without one add nothing with the
+    // clamp (M is -inf there, u no number), and without it make sums that are not finite.
+    if (kClamp || i == 0) {
       float most = block_most[0];
 #pragma unroll
       for (int j = 1; j < kAhead; ++j) most = fmaxf(most, block_most[j]);
-      of = fabsf(most) < inf() ? most : 0.0f;  // (no token left in them: any other number)
+      if (kClamp) of = of == -inf() ? sane(most) : of;
+      else of = fabsf(most) < inf() ? most : 0.0f;
       M = Reference(of).M;
     }
     // a batch's terms among themselves first, so that long sums of small terms lose less
@@ -388,23 +391,26 @@ __device__ __forceinline__ Part sum_share(const LogprobArgs& a, const Row<T>& ro
   const Share<T> share(row, warp, warps);
   float lane_top = -inf(), top = -inf(), of = -inf();
   Sums sums;
-  // whether the sums are what they should be: finite, and of terms that are not too small
+  // Whether the sums are what they should be: finite, and of terms that are not too small.  What they
+  // refer to is an element of the share, so the largest does not lie below it.
   auto good = [&]() {
     const Reference ref(of);
     top = warp_max(sane(lane_top));
-    return !ref.far && !(top > -inf() && fabsf(fmaf(top, kLog2e, -ref.M)) > 100.0f) && __all_sync(kFullMask, sums.sound());
+    return (top == -inf() || (!ref.far && fmaf(top, kLog2e, -ref.M) <= 100.0f)) && __all_sync(kFullMask, sums.sound());
   };
   if (share.mine > 0) {
     sum_batches<T, kOnce, false>(a, row, share, lane, fine, seg_max, sums, of, lane_top);
     if (!good()) {
       sums = Sums();
+      of = -inf();
       sum_batches<T, kOnce, true>(a, row, share, lane, fine, seg_max, sums, of, lane_top);
     }
   }
-  // One block after another: those at the ends; and where the quick sums did not take a value, all
-  // of them, first for the maximum, then for the sums.
+  // One block after another: those at the ends; and where sums have nothing to refer to yet, or the
+  // quick ones did not take a value, first for the maximum, then for the sums.
   const int count = share.count();
-  enum { kEnds, kMaximum, kAll } pass = share.mine == 0 ? kMaximum : kEnds;
+  const int ends = share.mine * kAhead, start = of == -inf() ? ends : 0;  // (there are no batches, or no token is left in them)
+  enum { kEnds, kMaximum, kAll } pass = of == -inf() ? kMaximum : kEnds;
   for (;;) {
     const Reference ref(pass == kMaximum ? -inf() : of);
     if (pass != kEnds) {
@@ -412,7 +418,7 @@ __device__ __forceinline__ Part sum_share(const LogprobArgs& a, const Row<T>& ro
       lane_top = -inf();
     }
 #pragma unroll 1
-    for (int i = pass == kEnds ? share.mine * kAhead : 0; i < count; ++i) {
+    for (int i = pass == kEnds ? ends : start; i < count; ++i) {
       const int b = share.block(i);
       const typename R::Raw raw = row.fetch(b, lane);
       const float mine = R::largest(raw);

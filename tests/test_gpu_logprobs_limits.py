@@ -2,10 +2,11 @@
 of test_gpu_logprobs.py; every case runs with each number of threads to a row."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_logprobs import DT, HUGE, check, mem  # noqa: F401 (a fixture)
+from test_gpu_logprobs import DT, HUGE, check, mem, reference  # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
 ROWS = (2, 200, 400, 700)   # a cluster or CTAs of 512, 256 and 128 threads to a row
@@ -50,3 +51,33 @@ def test_infinities_tie_with_the_largest_finite_value(mem, V, dtype, n):
                 assert torch.equal(many[2], ids.repeat(T // 2, 1)), "ids of %d rows" % T
         except AssertionError as e:
             raise AssertionError("%s: %s" % (name, e))
+
+
+def tails(mem, name, x, top, dtype):
+    """The log probability and the entropy of rows whose token `top` is almost certain, relative to their own size.  A term 2^u, |u| <= 128
+    from what a warp's sums refer to, is off by ln 2 2^-18 = 45 2^-24 from u's rounding, by 27 2^-24 from log2 e's in fp32 (|d| <= 106, 2^-26 |d|),
+    4 2^-24 from the exponential, and each addition that it takes part in: V / 128 in a lane, 40 in the joins, 10 in what follows: E.  The
+    entropy's terms are these times u, as a difference of two numbers up to 5 times as large: 6 E."""
+    x = x.to(DT[dtype])[None]
+    V = x.shape[1]
+    want = reference(x, np.array([top]), 1)
+    E = (126 + V / 128) * 2.0 ** -24
+    for T in ROWS:
+        tok = torch.full((T,), top, dtype=torch.int32, device="cuda")
+        lp, H, ids, _ = mem.memra_token_logprobs(x.cuda().expand(T, V), tok, top_n=1)
+        assert bool((ids == top).all())
+        for what, got, w, tol in (("log probability", lp, want[0][0], E), ("entropy", H, want[1][0], 6 * E)):
+            off = float((got.double() / w - 1).abs().max())
+            assert off <= tol, "%s, %d rows: %s off by %g of %g, tolerance %g" % (name, T, what, off, w, tol)
+
+
+@pytest.mark.parametrize("V,masked", [(60000, 17000), (151936, 76000), (60000, 59960)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_tails_behind_masked_tokens(mem, V, masked, dtype):
+    """Every warp's first logits, or all but a few, are masked, and those that are left are far below 0."""
+    g = torch.Generator().manual_seed(V)
+    for high, low in ((-69.0, -87.6), (-55.0, -80.0), (-69.0, -94.0), (-3.0, -28.0), (40.0, 20.0), (-160.0, -180.0)):
+        x = low + 0.2 * torch.randn(V, generator=g)
+        x[:masked] = -math.inf
+        x[V - 7] = high
+        tails(mem, "%g over %g" % (high, low), x, V - 7, dtype)
