@@ -3,8 +3,8 @@
 // One pass over the logits.  Each lane sums z = sum 2^u and s = sum 2^u u over its elements, with
 // u = x log2 e - M, M a whole number next to the maximum of its warp's first blocks, so that u is
 // one rounding and the sums of other warps differ by a power of two.  What exceeds that maximum
-// makes terms above 1, which fp32 holds up to 2^127; a warp whose sums are not finite takes its
-// blocks again, with care.  The row is cut into segments whose maxima go to shared memory as the
+// makes terms above 1, which fp32 holds up to 2^127; a warp whose sums are not finite, or whose
+// maximum lies more than 2^60 above, takes its blocks again, with care.  The row is cut into segments whose maxima go to shared memory as the
 // pass goes by.
 //
 // Then the row's sums are joined, and a number is found that the maxima of top_n groups of
@@ -45,6 +45,7 @@ constexpr int kMaxWarps = 256;      // of a row: 16 CTAs of 16 (of smaller CTAs,
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 constexpr float kLargest = 3.402823466e38f;
 constexpr float kFloor = -160.0f;   // 2^u is 0 in fp32 below
+constexpr float kRise = 60.0f;      // of a share's largest term over what its sums refer to, log2
 
 struct alignas(16) Part {  // of a warp
   float m, of;        // its maximum, and what its sums refer to: Reference(of)
@@ -392,11 +393,13 @@ __device__ __forceinline__ Part sum_share(const LogprobArgs& a, const Row<T>& ro
   float lane_top = -inf(), top = -inf(), of = -inf();
   Sums sums;
   // Whether the sums are what they should be: finite, and of terms that are not too small.  What they
-  // refer to is an element of the share, so the largest does not lie below it.
+  // refer to is an element of the share, so the largest does not lie below it.  It may lie 2^kRise
+  // above: with the row's largest 2^d above the share's, the join multiplies sums by
+  // 2^-(kRise + d), which fp32 holds (to 2^-149) for d up to 89, and so 60 below the largest logit.
   auto good = [&]() {
     const Reference ref(of);
     top = warp_max(sane(lane_top));
-    return (top == -inf() || (!ref.far && fmaf(top, kLog2e, -ref.M) <= 100.0f)) && __all_sync(kFullMask, sums.sound());
+    return (top == -inf() || (!ref.far && fmaf(top, kLog2e, -ref.M) <= kRise)) && __all_sync(kFullMask, sums.sound());
   };
   if (share.mine > 0) {
     sum_batches<T, kOnce, false>(a, row, share, lane, fine, seg_max, sums, of, lane_top);

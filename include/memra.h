@@ -796,7 +796,8 @@ memra_status memra_kv_compact(const int32_t* lens, const int32_t* block_table, i
  *   top_ids, top_logprobs [T][top_n]: the top_n largest x, descending, ties to the lowest
  *                  index (-0 equals 0), and their log probabilities.
  * tokens and logprobs may be NULL together.  Sums are fp32 without the largest term (ln Z =
- * log1p of the others), so log probabilities near 0 keep their digits.
+ * log1p of the others), so log probabilities near 0 keep their digits; logits more than 60
+ * below the largest may count as masked in them.
  * A logit of -inf or NaN masks a token (probability 0); +inf counts as the largest finite
  * value of fp32 (for ties too).  Where fewer than top_n tokens are left, the remaining slots hold the lowest indexes
  * not yet taken, with -inf.  A row with no token left has entropy 0 and -inf everywhere.

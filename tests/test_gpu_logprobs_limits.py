@@ -81,3 +81,15 @@ def test_tails_behind_masked_tokens(mem, V, masked, dtype):
         x[:masked] = -math.inf
         x[V - 7] = high
         tails(mem, "%g over %g" % (high, low), x, V - 7, dtype)
+
+
+@pytest.mark.parametrize("V", [60000, 151936])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_tails_far_above_what_their_sums_refer_to(mem, V, dtype):
+    """A warp's first logits are up to 150 powers of two below the row's largest, its others less than 90."""
+    g = torch.Generator().manual_seed(V)
+    for rise, high in ((66.0, 106.0), (60.0, 104.0), (30.0, 60.0), (66.0, 90.0), (39.0, 99.0), (41.0, 95.0), (45.0, 95.0)):
+        x = 0.5 * torch.randn(V, generator=g)
+        x[V // 2:] += rise
+        x[V // 5] = high
+        tails(mem, "%g over %g" % (high, rise), x, V // 5, dtype)
