@@ -823,6 +823,21 @@ cudaError_t launch_logprobs(const LogprobArgs& a, const DeviceInfo& info, cudaSt
   return once ? launch_logprobs<T, 128, true>(a, 1, stream) : launch_logprobs<T, 128, false>(a, 1, stream);
 }
 
+// Bytes at an address: T rows of `width`, `row` apart.
+struct Extent {
+  uintptr_t at;
+  uint64_t row, width, all;
+  Extent(const void* p, uint64_t T, uint64_t row_bytes, uint64_t width_bytes)
+      : at((uintptr_t)p), row(row_bytes), width(width_bytes), all(p != nullptr && T > 0 && width_bytes > 0 ? (T - 1) * row_bytes + width_bytes : 0) {}
+  // o without gaps, which may lie in one of this one's
+  bool meets(const Extent& o) const {
+    if (all == 0 || o.all == 0 || at >= o.at + o.all || o.at >= at + all) return false;
+    if (o.at < at || width >= row) return true;
+    const uint64_t d = (o.at - at) % row;
+    return d < width || d + o.all > row;
+  }
+};
+
 }  // namespace
 }  // namespace memra
 
@@ -846,6 +861,14 @@ extern "C" memra_status memra_token_logprobs(const void* logits, int32_t dtype, 
   const void* words[] = {tokens, logprobs, entropy, top_ids, top_logprobs, dev_status};
   for (const void* p : words)
     if (!aligned(p, 4)) return MEMRA_ERR_ALIGNMENT;
+  const auto list = [](const void* p, int64_t n) { return Extent(p, 1, 0, 4 * (uint64_t)n); };
+  const Extent in[] = {Extent(logits, (uint64_t)T, (uint64_t)stride_t * es, (uint64_t)V * es), list(tokens, T)};
+  const Extent out[] = {list(logprobs, T), list(entropy, T), list(top_ids, T * top_n), list(top_logprobs, T * top_n), list(dev_status, 1)};
+  for (const Extent& o : out) {
+    if (in[0].meets(o) || in[1].meets(o)) return MEMRA_ERR_INVALID_ARG;
+    for (const Extent* p = out; p != &o; ++p)
+      if (p->meets(o)) return MEMRA_ERR_INVALID_ARG;
+  }
   DeviceInfo info;
   if (!device_info(&info)) return MEMRA_ERR_CUDA;
   LogprobArgs a;

@@ -738,7 +738,8 @@ memra_status memra_kv_unshare(const int32_t* lens, const int32_t* new_lens, int6
  * behind them in dst stays.  layers: HOST array of n_layers caches of the same sizes.  An
  * entry with a page of -1, or with src == dst, copies nothing; one with a page outside
  * [0, n_pages), or tokens outside [0, P], neither (status 1).  No page may be the dst of two
- * entries, or of one and the src of another.
+ * entries, or of one and the src of another; the layers' planes, which must not overlap
+ * either, are checked against the lists only.
  */
 typedef struct memra_kv_layer {
   int8_t* kq;
@@ -802,7 +803,9 @@ memra_status memra_kv_compact(const int32_t* lens, const int32_t* block_table, i
  * value of fp32 (for ties too).  Where fewer than top_n tokens are left, the remaining slots hold the lowest indexes
  * not yet taken, with -inf.  A row with no token left has entropy 0 and -inf everywhere.
  * V <= MEMRA_MAX_VOCAB, top_n <= min(MEMRA_MAX_TOP_LOGPROBS, V).  logits are aligned to
- * their type only; rows that start on 16 bytes are no quicker than others.
+ * their type only; rows that start on 16 bytes are no quicker than others.  Outputs and
+ * *dev_status overlap neither each other nor the inputs (MEMRA_ERR_INVALID_ARG), but may lie
+ * between rows of logits.
  */
 #define MEMRA_MAX_VOCAB 1048576
 #define MEMRA_MAX_TOP_LOGPROBS 32
