@@ -159,10 +159,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
       float2 q = __fmul2_rn(v[0], v[0]);
 #pragma unroll
       for (int j = 1; j < 4; ++j) q = __ffma2_rn(v[j], v[j], q);
-      float s = q.x + q.y;
+      // (half of the squares with 256 of them: 2^60 in all of these would sum to 2^128)
+      constexpr float kPart = kD == 256 ? 0.5f : 1.0f;
+      float s = kPart * (q.x + q.y);
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
-      s = fmaf(s, 1.0f / kD, a.eps);
+      s = fmaf(s, 1.0f / (kPart * kD), a.eps);
       // (2 ulp; without a norm, weights are ones too)
       const float r = a.eps >= 0.0f ? (s > 0.0f ? rsqrtf(s) : 0.0f) : 1.0f;
       const float4 wa = *reinterpret_cast<const float4*>(&weight_of[is_q ? 0 : 1][off_a]);
