@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(RopeArgs a) {
       for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
       s = fmaf(s, 1.0f / (kPart * kD), a.eps);
       // (2 ulp; without a norm, weights are ones too)
-      const float r = a.eps >= 0.0f ? (s > 0.0f ? rsqrtf(s) : 0.0f) : 1.0f;
+      const float r = a.eps >= 0.0f ? (s == 0.0f ? 0.0f : rsqrtf(s)) : 1.0f;
       const float4 wa = *reinterpret_cast<const float4*>(&weight_of[is_q ? 0 : 1][off_a]);
       const float4 wb = *reinterpret_cast<const float4*>(&weight_of[is_q ? 0 : 1][off_b]);
       const float2 w[4] = {{wa.x, wa.y}, {wa.z, wa.w}, {wb.x, wb.y}, {wb.z, wb.w}};

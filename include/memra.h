@@ -672,7 +672,8 @@ memra_status memra_moe_route(const void* logits, int32_t dtype, int64_t T, int64
  * of a turn in 64-bit fixed point (inv_freq / 2 pi to 2^-64, times the position modulo one
  * turn), so far positions lose nothing: it is off by position * inv_freq * 2^-52 + 2^-22 at
  * most.  |x| <= 2^60 with a norm; without eps, rows whose largest |x| is below 2^-60 lose
- * digits, and below 2^-75 they are zeros.
+ * digits, and below 2^-75 they are zeros.  A NaN makes all of its head NaN; an infinity makes
+ * itself NaN and the others 0, and what is turned with a NaN is one.
  * Alignment: q, k and outputs 16 bytes, strides keep them; inv_freq 8, else 4.
  * Outputs may be their own inputs (same address, strides and dtype); apart from that they
  * overlap nothing, their own other rows neither (MEMRA_ERR_INVALID_ARG), but rows may lie side by side with equal stride_t
