@@ -152,18 +152,25 @@ CONFIG = {"hidden": 2048, "heads": 32, "kv_heads": 4, "head_dim": 128, "experts"
           "ffn": 768, "vocab": 8192, "page": 64, "block": 16, "layers": 2, "qk_norm": True}
 
 
-def main():
+def arguments(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--layers", type=int, default=CONFIG["layers"])
     ap.add_argument("--sequences", type=int, default=4)
-    ap.add_argument("--samples", type=int, default=2, help="of each sequence")
+    ap.add_argument("--samples", type=int, help="of each sequence; by default 2, or 1 where %d in all are too few for 2" % MAX_ROWS)
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--prompt", type=int, default=21, help="tokens of the longest prompt")
-    a = ap.parse_args()
+    a = ap.parse_args(argv)
+    if a.samples is None:
+        a.samples = 2 if 2 * a.sequences <= MAX_ROWS else 1
     if a.sequences < 1 or a.samples < 1 or a.sequences * a.samples > MAX_ROWS:
         ap.error("1 to %d samples in all" % MAX_ROWS)
     if a.samples > memra.MAX_TOP_LOGPROBS:
         ap.error("up to %d samples of a sequence" % memra.MAX_TOP_LOGPROBS)
+    return a
+
+
+def main():
+    a = arguments()
     model = Decoder(dict(CONFIG, layers=a.layers), a.sequences, a.prompt + a.steps + 1, samples=a.samples)
     gen = torch.Generator().manual_seed(1)
     prompts = [torch.randint(0, CONFIG["vocab"], (max(1, a.prompt - 3 * i),), generator=gen) for i in range(a.sequences)]
