@@ -473,8 +473,8 @@ template <int kParts>
 struct Shared {
   Part part[kParts];
   unsigned long long candidate[kMost];
-  int count, special;  // special: the warp that met the largest element, -1 where its lane's sums do
-  float bound, top, z, s;
+  int count;
+  float bound, top, log_z;
   uint32_t taken[MEMRA_MAX_TOP_LOGPROBS];
 };
 
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(Logp
       const float up = exp2f(-ref.delta), log_z = log1pf(up * z);
       const bool none_left = top == -inf();
       sh.top = top;
-      sh.z = log_z;
+      sh.log_z = log_z;
       if (a.entropy != nullptr) {
         const float terms = kLn2 * up * (s - ref.delta * z);
         a.entropy[t] = none_left ? 0.0f : log_z - terms / (1.0f + up * z);
@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(Logp
     }
   }
   __syncthreads();
-  const float top = sh.top, log_z = sh.z;
+  const float top = sh.top, log_z = sh.log_z;
   const int count = sh.count;
   int32_t* ids = a.top_ids + t * a.top_n;
   float* out = a.top_logprobs + t * a.top_n;

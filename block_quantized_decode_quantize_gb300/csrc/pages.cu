@@ -450,8 +450,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
-  const int lane = threadIdx.x & 31, ranks = (int)cluster.num_blocks();
-  const int64_t all_threads = (int64_t)ranks * kThreads;
+  const int lane = threadIdx.x & 31;
+  constexpr int64_t all_threads = kMaxRanks * kThreads;
   const int64_t me = (int64_t)cluster.block_rank() * kThreads + threadIdx.x;
   const int64_t cells = a.t.B * a.t.max_pages, n = a.t.n_pages, moves = n / 2;
   // the pages of the thread's cells, kTile at a time; of one such tile they stay in registers
@@ -483,14 +483,14 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a) {
   for (int64_t k = me; k < moves; k += all_threads) a.src[k] = a.dst[k] = -1;
   for (int64_t b = me; b < a.t.B; b += all_threads) (void)a.t.pages_of(a.t.lens[b], &bad);
   if (one) bad |= look(me);
-  meet(cluster, ranks);
+  cluster.sync();
   for (int64_t e0 = me; e0 < cells; e0 += tile) {
     if (!one) bad |= look(e0);
 #pragma unroll
     for (int j = 0; j < kTile; ++j)
       if (page[j] >= 0) atomicAdd(a.refs + page[j], 1);
   }
-  meet(cluster, ranks);
+  cluster.sync();
   const int64_t warps = all_threads / 32, my_warp = me / 32, chunks = (n + 31) / 32;
   const int64_t c0 = chunks * my_warp / warps, c1 = chunks * (my_warp + 1) / warps;
   int32_t mine = 0;
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a) {
       a.free_out[p] = used - 1 - below;  // for now: its move
     }
   }
-  meet(cluster, ranks);
+  cluster.sync();
   for (int64_t e0 = me; e0 < cells; e0 += tile) {
     if (!one) (void)look(e0);
     int32_t to[kTile];
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a) {
       a.refs[p] = 0;
     }
   }
-  meet(cluster, ranks);
+  cluster.sync();
   for (int64_t p = me; p < n; p += all_threads) a.free_out[p] = (int32_t)p;
   if (me == 0) *a.free_head_out = used;
   tell(bad ? 1 : 0, a.status);
@@ -783,10 +783,9 @@ bool words_aligned(std::initializer_list<const void*> ps) {
   return true;
 }
 
-// One cluster: a CTA for small tables, eight for others.
+// One cluster of so many CTAs.
 template <typename Args>
-cudaError_t launch_cluster(void (*kernel)(Args), int64_t cells, cudaStream_t stream, const Args& a) {
-  const unsigned ranks = cells <= 8 * kThreads ? 1 : kMaxRanks;
+cudaError_t launch_cluster(void (*kernel)(Args), unsigned ranks, cudaStream_t stream, const Args& a) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks);
   cfg.blockDim = dim3(kThreads);
@@ -958,7 +957,7 @@ extern "C" memra_status memra_kv_release(const int32_t* lens, const int32_t* kee
   a.free_head_out = free_head_out;
   a.status = dev_status;
   const cudaError_t e = is_small(a.t) ? launch_small(small_release_kernel, 8, stream, a)
-                                      : launch_cluster(release_kernel, B * max_pages, stream, a);
+                                      : launch_cluster(release_kernel, B * max_pages <= kSmallCells ? 1 : kMaxRanks, stream, a);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }
@@ -987,7 +986,7 @@ extern "C" memra_status memra_kv_compact(const int32_t* lens, const int32_t* blo
   a.free_head_out = free_head_out;
   a.status = dev_status;
   const cudaError_t e = is_small(a.t) ? launch_small(small_compact_kernel, 10, stream, a)
-                                      : launch_cluster(compact_kernel, B * max_pages + n_pages, stream, a);
+                                      : launch_cluster(compact_kernel, kMaxRanks, stream, a);
   if (e != cudaSuccess) return cuda_fail(e);
   return MEMRA_OK;
 }
