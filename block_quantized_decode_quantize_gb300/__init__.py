@@ -18,6 +18,9 @@ Tensor conventions (all on one CUDA device, contiguous):
   wq  int8 [N, K]          Q8_0 quants            wd  float16 [N, K/32]  Q8_0 scales
   xq  int8 [M, K]          q8_1 quants            xd  float32 [M, K/32]  q8_1 scales
   y   float32 [M, N]       (the GEMV takes and returns 1-D x / y)
+
+New outputs of one call of the cache's and the later operators may share an allocation: one that is kept
+or saved holds the others' memory too (clone it, or hand in tensors of your own).
 """
 import ctypes
 import importlib.util
@@ -1191,7 +1194,8 @@ def memra_qk_norm_rope(q, k, positions=None, inv_freq=None, q_weight=None, k_wei
     the first R values of a head are turned by positions * inv_freq, R 0 (both None) to D.  layout
     "halves" turns value j with j + R / 2, "pairs" 2j with 2j + 1.  eps None: no norm; else every
     head is divided by its root mean square and multiplied by q_weight or k_weight (float32 [D] or
-    None).  Returns q_out, k_out of q_dtype, k_dtype (default: the inputs').  The outputs may be the
+    None).  Returns q_out, k_out of q_dtype, k_dtype (default: the inputs'), which share an allocation
+    where both are new.  The outputs may be the
     inputs themselves: k_out=k leaves k beside v in the projection's rows, with the strides that
     memra_kv_append_q8 wants alike."""
     done = (_fast or _binding()).rope(q, k, positions, inv_freq, q_weight, k_weight, eps,

@@ -17,9 +17,14 @@
 // A row is taken by one CTA, or, with few rows, by the CTAs of a cluster, which leave maxima and
 // sums in the first one's shared memory.
 //
+// A masked token (-inf, NaN) is found at the end of a warp's share, or in its first batch, and the
+// share is then summed again with a clamp: with a few of them in a row, most of it is read twice.
+//
 // 2047 rows of 151,936 bf16 logits (622 MB) take 106 us, 87 % of the copy rate: memory, with 0.54
 // instructions a cycle beside it (about 6.5 for 32 elements, the exponential's unit 40 % busy) and
-// 5 us of choosing; 640 rows in fp32 (389 MB) 66.5 us, 86 %.  One row takes 7.4 us: launch 2.1, the read
+// 5 us of choosing (with 1, 16 and 152 masked tokens a row 151, 194 and 164 us, with half of them 114);
+// 640 rows in fp32 (389 MB) 66.8 us, 86 %.  All instances take 64 registers, the most that 1024 threads
+// an SM leave, and spill 12 to 28 bytes.  One row takes 7.4 us: launch 2.1, the read
 // and sums 3.2, the choice 2.1, each a chain of latencies.  Measured and not kept: rescaling sums
 // at every new maximum and keeping it out of them (14 instructions an element, 123 to 169 us);
 // asynchronous copies into a ring of each warp, with the next row's on their way (142 to 198: the
@@ -92,7 +97,9 @@ __device__ __forceinline__ float value_of(uint32_t r) {
 // A masked token's logit is -inf or no number; +inf counts as the largest finite value.
 __device__ __forceinline__ float sane(float v) { return fminf(fmaxf(v, -inf()), kLargest); }
 
-// A load of the one pass; kOnce: of what will hardly be read again, so that it is first to leave L2.
+// A load of the one pass; kOnce: of what will hardly be read again.  Its lines are not put into L1, and
+// volatile statements keep their order; which of the two makes the rows of 151,936 logits 2 to 4 % faster
+// was not told apart (volatile was needed).
 template <bool kOnce>
 __device__ __forceinline__ uint4 load(const uint4* p) {
   if (!kOnce) return __ldcg(p);
@@ -809,15 +816,15 @@ cudaError_t launch_logprobs(const LogprobArgs& a, const DeviceInfo& info, cudaSt
   // 1024 threads an SM.  Up to two rows an SM, CTAs of 512 threads, clusters of them where rows are
   // fewer (with four blocks a warp at least); up to four, CTAs of 256; CTAs of 128 beyond, which
   // leave the fewest threads waiting while a row's choice is made.  us for 301 rows of 32,003 bf16
-  // logits, 553 of 114,789 fp32 and 2047 of 151,936 bf16: 512 threads 8.3, 49.4, 113.0; 256 9.2,
-  // 46.0, 112.1; 128 11.0, 57.2, 105.9.
+  // logits, 553 of 114,789 fp32 and 2047 of 151,936 bf16: 512 threads 8.3, 49.4, 112.8; 256 9.1,
+  // 46.3, 112.3; 128 11.2, 57.9, 105.9.
   if (a.T <= 2 * info.sms) {
     int ranks = 1;
     while (ranks < 16 && a.T * ranks * 2 <= 2 * info.sms && (int64_t)ranks * 2 * 16 * 4 * kBlock <= a.V) ranks *= 2;
     return launch_logprobs<T, 512, true>(a, ranks, stream);
   }
-  // Where less than a twelfth of the row's blocks is read again, lines leave L2 first after their one
-  // use (2047 rows of 151,936 in bf16, 5 alternatives: 107 us for 109; 4000 of 30,121 with 32: 80 for 75).
+  // Loads of what is hardly read again where less than a twelfth of the row's blocks are (2047 rows of
+  // 151,936 in bf16, 5 alternatives: 105.9 us for 108.1; 4000 of 30,121 with 32: 71.2 for 70.2).
   const bool once = (int64_t)a.top_n * 12 * kBlock <= a.V;
   if (a.T <= 4 * info.sms) return once ? launch_logprobs<T, 256, true>(a, 1, stream) : launch_logprobs<T, 256, false>(a, 1, stream);
   return once ? launch_logprobs<T, 128, true>(a, 1, stream) : launch_logprobs<T, 128, false>(a, 1, stream);
@@ -879,8 +886,8 @@ extern "C" memra_status memra_token_logprobs(const void* logits, int32_t dtype, 
   a.top_n = (int)top_n;
   const int64_t blocks = (V + 16 / es - 1 + kBlock - 1) / kBlock;
   // Fine segments where a sixth of the blocks or more would be read again, as far as shared memory
-  // goes.  us with blocks and with pieces, bf16: 7820 rows of 6885 with 5 alternatives 55 and 52, 4000
-  // of 30,121 with 32 74 and 71, with 5 55 and 63; 301 of 32,003 with 10 8.4 and 8.7.
+  // goes.  us with blocks and with pieces, bf16: 7820 rows of 6885 with 5 alternatives 53 and 52, 4000
+  // of 30,121 with 32 74 and 70, with 5 55 and 63; 301 of 32,003 with 10 8.3 and 8.6.
   a.fine = V * es <= kFineBytes && V < 6 * kBlock * top_n;
   a.segments = (int)(a.fine ? blocks * kBlock * es / 16 : blocks);
   a.tokens = tokens;

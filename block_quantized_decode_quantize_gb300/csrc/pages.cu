@@ -546,9 +546,10 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a) {
 // ---------------------------------------------------------------------------
 // Release and compaction of a table of one tile (8192 cells) over a pool of up to 16,384 pages: one
 // CTA, whose shared memory holds what is counted of each page, so that global memory is waited for
-// once or twice instead of at every step.  us, so and with the steps in global memory (by one
-// CTA or a cluster, whichever is faster): a release of all of 1024 pages 4.8 and 7.4, of 8000 8.5
-// and 11.1; compaction of 256 pages 3.1 and 6.2, of 8000 7.4 and 10.5, of 16,384 11.0 and 12.5.
+// once or twice instead of at every step.  us, so and with the steps in global memory: a release of
+// all of 1024 pages 3.7 and 7.0 (by one CTA; a cluster 8.2), of 8000 8.2 and 10.6 (by a cluster; one CTA
+// 25.1); compaction of 256 pages 2.9 and 8.6 (by a cluster, as the others), of 8000 7.6 and 10.0, of
+// 16,384 11.3 and 11.9.
 // ---------------------------------------------------------------------------
 constexpr int kSmallCells = kTile * kThreads, kSmallPages = 16384;
 

@@ -14,7 +14,7 @@
 // 8191 tokens of 48 heads of 128 in bf16 (201 MB) take 37.5 us, 79 % of the copy rate: each further
 // 2432 tokens (a CTA more for every place on the SMs) take 9.4 us, 94 % of it, so 4 us are the launch, the
 // first CTAs' angles and the last stores, and the rest the last, half-filled round of CTAs.  In fp32
-// (403 MB) 63.2 us, 94 %.  One token takes 2.1 us, as a kernel that does nothing.  Measured and not
+// (403 MB) 63.2 us, 94 %; its instances of four tokens with halves spill 4 to 24 bytes.  One token takes 2.1 us, as a kernel that does nothing.  Measured and not
 // kept: one token's loads at a time (51.7 us), fp64 conversion of the frequencies by every thread
 // (+1 us), two tokens a CTA (48.0), eight (47.4), and 16 bytes to a load (37.0; but 128 tokens of
 // interleaved pairs 2.9 -> 3.6, 2000 of them 12.8 -> 13.8).
@@ -213,7 +213,8 @@ cudaError_t launch_rope(RopeArgs a, int sms, cudaStream_t stream) {
   const int groups = (a.heads + kHeads - 1) / kHeads;
   // One, two or four tokens to a CTA, whose angles keep its threads busy, and all of their heads, so
   // that angles are computed once; but eight groups of heads, one a warp, where that makes fewer
-  // than three CTAs an SM (1000 tokens of 48 heads of 128: 7.1 us for 9.2; 8191: 41.9 for 39.9).
+  // than three CTAs an SM (us of 48 heads of 128 in bf16, so and with all heads: 1 token 2.1 and 3.0, 128
+  // 3.0 and 3.4, 400 5.0 and 4.6, 1500 9.9 and 11.1; where it makes more, 8191 tokens, 38.8 and 37.3).
   const int64_t spread = a.T / (2 * (int64_t)sms);
   a.tokens = spread < 2 ? 1 : (spread < 4 ? 2 : 4);
   a.groups = (a.T + a.tokens - 1) / a.tokens < 3 * (int64_t)sms && groups > kRopeWarps ? kRopeWarps : groups;
@@ -221,7 +222,7 @@ cudaError_t launch_rope(RopeArgs a, int sms, cudaStream_t stream) {
   a.by_groups = Divider((uint32_t)a.groups);
   // Few heads, or a number of groups that leaves warps idle: two or four sets of four tokens to a
   // CTA where that leaves fewer idle, with two CTAs an SM at least (8000 tokens of 2 heads of 128
-  // 4.8 us for 9.6, of 24 of 64 12.7 for 14.4; four CTAs an SM at least 6.5 and 14.4).
+  // 4.8 us for 9.6, of 24 of 64 12.7 for 14.1; four CTAs an SM at least 6.5 and 14.2).
   a.sets = 1;
   const auto idle = [&](int sets) { return (sets * a.groups + kRopeWarps - 1) / kRopeWarps * (kMaxSets / sets); };
   for (int sets = 2; sets <= kMaxSets && a.tokens == 4 && a.groups == groups; sets *= 2)
