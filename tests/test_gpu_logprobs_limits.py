@@ -93,3 +93,21 @@ def test_tails_far_above_what_their_sums_refer_to(mem, V, dtype):
         x[V // 2:] += rise
         x[V // 5] = high
         tails(mem, "%g over %g" % (high, rise), x, V // 5, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", ROWS)
+@pytest.mark.parametrize("level", [1.2345, -7.77])
+def test_sums_of_equal_terms(mem, dtype, T, level):
+    """Equal logits, whose sums round the same way throughout.  A term takes part in 16 additions of its batch (64 bytes a lane, two
+    halves), one for each further batch of a lane (V / 2048 in fp32, V / 4096 in bf16, with the fewest threads, 128, on a row), and 15 in the
+    joins; it is off by 6 2^-24 itself.  The entropy is ln V too; its second sum is 0 but for twice as much."""
+    V = 151936
+    x = torch.full((1, V), level).to(DT[dtype])
+    E = (16 + V / (2048 if dtype == "fp32" else 4096) + 15 + 6) * 2.0 ** -24
+    tok = torch.full((T,), V - 1, dtype=torch.int32, device="cuda")
+    lp, H, ids, top = mem.memra_token_logprobs(x.cuda().expand(T, V), tok, top_n=2)
+    half = 2.0 ** -24 * math.log(V)                      # the result's own rounding
+    assert ids.tolist() == [[0, 1]] * T
+    for got, want, tol in ((lp, -math.log(V), E + half), (top, -math.log(V), E + half), (H, math.log(V), 3 * E + half)):
+        assert float((got.double() - want).abs().max()) <= tol
