@@ -4,8 +4,8 @@
 // u = x log2 e - M, M a whole number next to the maximum of its warp's first blocks, so that u is
 // one rounding and the sums of other warps differ by a power of two.  What exceeds that maximum
 // makes terms above 1, which fp32 holds up to 2^127; a warp whose sums are not finite, or whose
-// maximum lies more than 2^60 above, takes its blocks again, with care.  The row is cut into segments whose maxima go to shared memory as the
-// pass goes by.
+// maximum lies more than 2^60 above, takes its blocks again, with care.  The row is cut into
+// segments whose maxima go to shared memory as the pass goes by.
 //
 // Then the row's sums are joined, and a number is found that the maxima of top_n groups of
 // segments reach, a bound that top_n elements reach: only segments whose maximum reaches it are
