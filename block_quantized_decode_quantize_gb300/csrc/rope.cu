@@ -15,8 +15,8 @@
 // 2432 tokens (a CTA more for every place on the SMs) take 9.4 us, 94 % of it, so 4 us are the launch, the
 // first CTAs' angles and the last stores, and the rest the last, half-filled round of CTAs.  In fp32
 // (403 MB) 63.2 us, 94 %; its instances of four tokens with halves spill 4 to 24 bytes.  One
-// token takes 2.1 us, as a kernel that does nothing.  Measured and not kept: one token's loads at a time (51.7 us), fp64 conversion of the frequencies by every thread
-// (+1 us), two tokens a CTA (48.0), eight (47.4), and 16 bytes to a load (37.0; but 128 tokens of
+// token takes 2.1 us, as a kernel that does nothing.  Measured and not kept: one token's loads at a
+// time (51.7 us), fp64 conversion of the frequencies by every thread (+1 us), two tokens a CTA (48.0), eight (47.4), and 16 bytes to a load (37.0; but 128 tokens of
 // interleaved pairs 2.9 -> 3.6, 2000 of them 12.8 -> 13.8).
 #include <cuda_bf16.h>
 

@@ -802,7 +802,8 @@ memra_status memra_kv_compact(const int32_t* lens, const int32_t* block_table, i
  * below the largest may count as masked in them.
  * A logit of -inf or NaN masks a token (probability 0); +inf counts as the largest finite
  * value of fp32 (for ties too).  Where fewer than top_n tokens are left, the remaining slots
- * hold the lowest indexes not yet taken, with -inf.  A row with no token left has entropy 0 and -inf everywhere.
+ * hold the lowest indexes not yet taken, with -inf.  A row with no token left has entropy 0
+ * and -inf everywhere.
  * V <= MEMRA_MAX_VOCAB, top_n <= min(MEMRA_MAX_TOP_LOGPROBS, V).  logits are aligned to
  * their type only; rows that start on 16 bytes are no quicker than others.  Outputs and
  * *dev_status overlap neither each other nor the inputs (MEMRA_ERR_INVALID_ARG), but may lie
